@@ -25,6 +25,8 @@ CCR_OK, CCR_ERR_INVALID_ARG, CCR_ERR_UNSUPPORTED, CCR_ERR_HIP, CCR_ERR_OOM, CCR_
 CCR_F32, CCR_BF16 = 0, 1
 CCR_COPY_KERNEL, CCR_COPY_SDMA = 0, 1
 CCR_BF16_ACC_PER_HOP, CCR_BF16_ACC_FP32_PARTIALS = 0, 1
+CCR_GATE_CHOSEN, CCR_GATE_ALL = 0, 1
+CCR_GRAD_WORK = 2048  # float64 elements of a gradient call's work tensor
 _STATUS = {1: "invalid argument", 2: "unsupported", 3: "HIP error", 4: "out of memory", 5: "timeout"}
 
 
@@ -86,6 +88,14 @@ _SIGNATURES = {
     "ccr_moe_combine": [_vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _i64, _vp, _vp, _vp, _vp],
     "ccr_moe_dispatch_fused": [_vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _i64, _vp, _vp],
     "ccr_moe_combine_fused": [_vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _i64, _vp, _vp],
+    "ccr_moe_experts": [_vp, _vp, _vp, _vp, _i32, _i32, _i64, _i64, _i32, _vp, _vp],
+    "ccr_moe_experts_dgrad": [_vp, _vp, _vp, _vp, _i32, _i32, _i64, _i64, _i32, _vp, _vp],
+    "ccr_moe_experts_wgrad": [_vp, _vp, _vp, _vp, _i32, _i32, _i64, _i64, _i32, _i32, _i32, _vp, _vp],
+    "ccr_moe_gate_sum": [_vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _i64, _i32, _i32, _vp, _vp],
+    "ccr_moe_gate_sum_bwd": [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _i64, _i32, _i32, _vp,
+                             _vp, _vp],
+    "ccr_grad_norm": [_vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp],
+    "ccr_grad_clip": [_vp, _vp, _vp, _vp, _vp, _i32, ctypes.c_float, _vp, _vp, _vp],
     "ccr_last_error": [],
     "ccr_version": [],
     "ccr_probe_cu_ids": [_vp, _vp, _i32, _vp],
@@ -489,6 +499,175 @@ def ccr_moe_combine_fused(ctx: Context, exp: Sequence, slot: Sequence, ecnt, T: 
     ecnt = np.ascontiguousarray(ecnt, dtype=np.int64)
     _check(_lib.ccr_moe_combine_fused(ctx.handle, _ptrs(exp), _ptrs(slot), ecnt.ctypes.data, R, T,
                                       ecnt.shape[1], K, row_bytes, _ptrs(out), _stream(stream)))
+
+
+def _ctx_stream(ctx: Context, stream):
+    """The stream given, or the current stream of the context's device."""
+    import torch
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(ctx.device)
+    return _stream(torch.cuda.current_stream(ctx.device) if stream is None else stream)
+
+
+def _buffers(ctx: Context, tensors, dtype, shapes, what: str):
+    """Pointer array of contiguous tensors of `dtype` on the context's device,
+    one per entry of `shapes` (each at least that many rows of its shape)."""
+    if len(tensors) != len(shapes):
+        raise ValueError(f"{what}: {len(tensors)} buffers for {len(shapes)} ranks")
+    ptrs = (ctypes.c_void_p * len(tensors))()
+    for i, (t, shape) in enumerate(zip(tensors, shapes)):
+        if t.dtype != dtype:
+            raise TypeError(f"{what}[{i}] is {t.dtype}, not {dtype}")
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{what}[{i}] must be a contiguous device tensor")
+        if t.device.index != ctx.device:
+            raise ValueError(f"{what}[{i}] is on {t.device}, the context on device {ctx.device}")
+        if t.dim() != len(shape) or tuple(t.shape[1:]) != tuple(shape[1:]) or t.shape[0] < shape[0]:
+            raise ValueError(f"{what}[{i}] has shape {tuple(t.shape)}, needs {tuple(shape)}")
+        ptrs[i] = t.data_ptr()
+    return ptrs
+
+
+def _expert_counts(ecnt, R: int):
+    """([R x E] int64 counts, rows of each rank's experts)."""
+    ecnt = np.ascontiguousarray(ecnt, dtype=np.int64)
+    if ecnt.ndim != 2 or ecnt.shape[0] != R or ecnt.shape[1] % R:
+        raise ValueError(f"ecnt has shape {ecnt.shape}, needs [R = {R}, E] with R | E")
+    return ecnt, [int(n) for n in ecnt.sum(axis=0).reshape(R, -1).sum(axis=1)]
+
+
+def ccr_moe_experts(ctx: Context, exp: Sequence, w: Sequence, ecnt, out: Sequence, stream=None):
+    """out[d] row i = w_e @ exp[d] row i, e the expert of the row: exp[d]
+    [rows, H] as the dispatch leaves it, w[d] [E/R, F, H], ecnt [R, E]."""
+    R = len(w)
+    ecnt, rows = _expert_counts(ecnt, R)
+    E = ecnt.shape[1]
+    _, F, H = w[0].shape
+    dt = w[0].dtype
+    code = _dtype_code(w[0])
+    _check(_lib.ccr_moe_experts(
+        ctx.handle, _buffers(ctx, exp, dt, [(n, H) for n in rows], "exp"),
+        _buffers(ctx, w, dt, [(E // R, F, H)] * R, "w"), ecnt.ctypes.data, R, E, H, F, code,
+        _buffers(ctx, out, dt, [(n, F) for n in rows], "out"), _ctx_stream(ctx, stream)))
+
+
+def ccr_moe_experts_dgrad(ctx: Context, dout: Sequence, w: Sequence, ecnt, dexp: Sequence, stream=None):
+    """dexp[d] row i = w_e^T @ dout[d] row i: the gradient of the experts'
+    input rows."""
+    R = len(w)
+    ecnt, rows = _expert_counts(ecnt, R)
+    E = ecnt.shape[1]
+    _, F, H = w[0].shape
+    dt = w[0].dtype
+    code = _dtype_code(w[0])
+    _check(_lib.ccr_moe_experts_dgrad(
+        ctx.handle, _buffers(ctx, dout, dt, [(n, F) for n in rows], "dout"),
+        _buffers(ctx, w, dt, [(E // R, F, H)] * R, "w"), ecnt.ctypes.data, R, E, H, F, code,
+        _buffers(ctx, dexp, dt, [(n, H) for n in rows], "dexp"), _ctx_stream(ctx, stream)))
+
+
+def ccr_moe_experts_wgrad(ctx: Context, exp: Sequence, dout: Sequence, ecnt, dw: Sequence,
+                          accumulate: bool = False, stream=None):
+    """dw[d][e] (+)= dout_e^T @ exp_e over the rows of expert e: the gradient
+    of the experts' weights [E/R, F, H], float32 or the rows' dtype."""
+    R = len(dw)
+    ecnt, rows = _expert_counts(ecnt, R)
+    E = ecnt.shape[1]
+    _, F, H = dw[0].shape
+    dt = exp[0].dtype
+    code, dw_code = _dtype_code(exp[0]), _dtype_code(dw[0])
+    _check(_lib.ccr_moe_experts_wgrad(
+        ctx.handle, _buffers(ctx, exp, dt, [(n, H) for n in rows], "exp"),
+        _buffers(ctx, dout, dt, [(n, F) for n in rows], "dout"), ecnt.ctypes.data, R, E, H, F, code,
+        dw_code, int(bool(accumulate)), _buffers(ctx, dw, dw[0].dtype, [(E // R, F, H)] * R, "dw"),
+        _ctx_stream(ctx, stream)))
+
+
+_GATE_NORM = {"chosen": CCR_GATE_CHOSEN, "all": CCR_GATE_ALL}
+
+
+def _gate_args(ctx, rows, logits, topk, norm):
+    import torch
+    if norm not in _GATE_NORM:
+        raise ValueError(f"norm {norm!r} is not one of {sorted(_GATE_NORM)}")
+    R = len(rows)
+    T, K, H = rows[0].shape
+    E = logits[0].shape[1]
+    code = _dtype_code(rows[0])
+    return (R, T, E, K, H, code, _buffers(ctx, rows, rows[0].dtype, [(T, K, H)] * R, "rows"),
+            _buffers(ctx, logits, torch.float32, [(T, E)] * R, "logits"),
+            _buffers(ctx, topk, torch.int32, [(T, K)] * R, "topk"))
+
+
+def ccr_moe_gate_sum(ctx: Context, rows: Sequence, logits: Sequence, topk: Sequence, y: Sequence,
+                     norm: str = "chosen", stream=None):
+    """y[r][t] = sum_k w_k rows[r][t, k], w the softmax of logits[r][t] at
+    topk[r][t], over the chosen experts or over "all"."""
+    R, T, E, K, H, code, p, l, k = _gate_args(ctx, rows, logits, topk, norm)
+    _check(_lib.ccr_moe_gate_sum(ctx.handle, p, l, k, R, T, E, K, H, code, _GATE_NORM[norm],
+                                 _buffers(ctx, y, rows[0].dtype, [(T, H)] * R, "y"),
+                                 _ctx_stream(ctx, stream)))
+
+
+def ccr_moe_gate_sum_bwd(ctx: Context, dy: Sequence, rows: Sequence, logits: Sequence, topk: Sequence,
+                         drows: Sequence, dlogits: Sequence, norm: str = "chosen", stream=None):
+    """Gradients of ccr_moe_gate_sum: drows[r] [T, K, H] and dlogits[r] [T, E]."""
+    import torch
+    R, T, E, K, H, code, p, l, k = _gate_args(ctx, rows, logits, topk, norm)
+    dt = rows[0].dtype
+    _check(_lib.ccr_moe_gate_sum_bwd(ctx.handle, _buffers(ctx, dy, dt, [(T, H)] * R, "dy"), p, l, k, R, T,
+                                     E, K, H, code, _GATE_NORM[norm],
+                                     _buffers(ctx, drows, dt, [(T, K, H)] * R, "drows"),
+                                     _buffers(ctx, dlogits, torch.float32, [(T, E)] * R, "dlogits"),
+                                     _ctx_stream(ctx, stream)))
+
+
+def _grad_args(ctx, grads, work, norm):
+    import torch
+    n = len(grads)
+    ptrs, counts, codes = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)(), (ctypes.c_int32 * n)()
+    f32, bf16 = torch.float32, torch.bfloat16
+    for i, t in enumerate(grads):
+        dt = t.dtype
+        if dt is not f32:
+            if dt is not bf16:
+                raise TypeError(f"grads[{i}] is {dt}; use float32 or bfloat16")
+            codes[i] = CCR_BF16
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"grads[{i}] must be a contiguous device tensor")
+        ptrs[i] = t.data_ptr()
+        counts[i] = t.numel()
+    _buffers(ctx, [work], torch.float64, [(CCR_GRAD_WORK,)], "work")
+    _buffers(ctx, [norm], f32, [(1,)], "norm")
+    return ptrs, counts, codes, n
+
+
+def ccr_grad_norm(ctx: Context, grads: Sequence, work, norm, stream=None):
+    """norm[0] = the 2-norm over every element of `grads` (float32 and
+    bfloat16 tensors).  work: float64 [CCR_GRAD_WORK], this call's alone while
+    it runs; norm: float32 [1]."""
+    ptrs, counts, codes, n = _grad_args(ctx, grads, work, norm)
+    _check(_lib.ccr_grad_norm(ctx.handle, ptrs, counts, codes, n, work.data_ptr(), norm.data_ptr(),
+                              _ctx_stream(ctx, stream)))
+
+
+def ccr_grad_clip(ctx: Context, grads: Sequence, max_norm: float, work, norm, out=None, stream=None):
+    """norm[0] as ccr_grad_norm, then grads[i] *= min(1, max_norm / (norm +
+    1e-6)), or out[i] = that product."""
+    ptrs, counts, codes, n = _grad_args(ctx, grads, work, norm)
+    optrs = None
+    if out is not None:
+        if len(out) != n:
+            raise ValueError("out needs one tensor per gradient")
+        optrs = (ctypes.c_void_p * n)()
+        for i, (t, o) in enumerate(zip(grads, out)):
+            if o.dtype is not t.dtype or o.numel() != t.numel():
+                raise ValueError(f"out[{i}] differs from grads[{i}] in dtype or element count")
+            if not o.is_cuda or not o.is_contiguous():
+                raise ValueError(f"out[{i}] must be a contiguous device tensor")
+            optrs[i] = o.data_ptr()
+    _check(_lib.ccr_grad_clip(ctx.handle, ptrs, optrs, counts, codes, n, max_norm, work.data_ptr(),
+                              norm.data_ptr(), _ctx_stream(ctx, stream)))
 
 
 def ccr_probe_cu_ids(ctx: Context, nblocks: int, stream=None):

@@ -301,14 +301,24 @@ ccr_status_t check_ctx(ccr_ctx* ctx) {
   return CCR_OK;
 }
 
-// A 16-byte aligned device pointer on this context's device whose next
-// nbytes bytes lie inside one HIP allocation.
-ccr_status_t check_dev_ptr(ccr_ctx* ctx, const void* p, int64_t nbytes, const char* what,
-                           int index) {
+// A device pointer on this context's device, aligned to `align` bytes, whose
+// next nbytes bytes lie inside one HIP allocation.  `known`, if given, is the
+// last allocation that this call found on the device: a pointer inside it
+// needs no further query (a call over hundreds of tensors carved from a few
+// allocations makes a few).
+struct KnownRange {
+  uintptr_t lo = 0, hi = 0;
+};
+
+ccr_status_t check_dev_range(ccr_ctx* ctx, const void* p, int64_t nbytes, int align,
+                             const char* what, int index, KnownRange* known) {
   if (nbytes == 0) return CCR_OK;  // never dereferenced (an empty tensor may even be NULL)
   if (!p) return fail(CCR_ERR_INVALID_ARG, "%s[%d] is NULL", what, index);
-  if (reinterpret_cast<uintptr_t>(p) % 16 != 0)
-    return fail(CCR_ERR_INVALID_ARG, "%s[%d] = %p is not 16-byte aligned", what, index, p);
+  const uintptr_t q = reinterpret_cast<uintptr_t>(p);
+  if (q % (uintptr_t)align != 0)
+    return fail(CCR_ERR_INVALID_ARG, "%s[%d] = %p is not %d-byte aligned", what, index, p, align);
+  if (known && q >= known->lo && q < known->hi && (uint64_t)nbytes <= (uint64_t)(known->hi - q))
+    return CCR_OK;
   hipPointerAttribute_t attr;
   hipError_t e = hipPointerGetAttributes(&attr, p);
   if (e != hipSuccess) {
@@ -327,11 +337,19 @@ ccr_status_t check_dev_ptr(ccr_ctx* ctx, const void* p, int64_t nbytes, const ch
     (void)hipGetLastError();
     return fail(CCR_ERR_INVALID_ARG, "%s[%d] = %p: allocation range unknown", what, index, p);
   }
-  const uintptr_t b = reinterpret_cast<uintptr_t>(base), q = reinterpret_cast<uintptr_t>(p);
+  const uintptr_t b = reinterpret_cast<uintptr_t>(base);
   if (q < b || (uint64_t)nbytes > (uint64_t)(b + size - q))
     return fail(CCR_ERR_INVALID_ARG, "%s[%d] = %p: %lld bytes run past the end of its allocation",
                 what, index, p, (long long)nbytes);
+  if (known) *known = KnownRange{b, b + size};
   return CCR_OK;
+}
+
+// A 16-byte aligned device pointer on this context's device whose next
+// nbytes bytes lie inside one HIP allocation.
+ccr_status_t check_dev_ptr(ccr_ctx* ctx, const void* p, int64_t nbytes, const char* what,
+                           int index) {
+  return check_dev_range(ctx, p, nbytes, 16, what, index, nullptr);
 }
 
 struct Range {
@@ -1126,6 +1144,16 @@ ccr_status_t run_alltoall(ccr_ctx* ctx, const void* const* send, void* const* re
 int64_t env_int(const char* name, int64_t dflt) {
   const char* e = getenv(name);
   return e && *e ? strtoll(e, nullptr, 0) : dflt;
+}
+
+// Host memory that runs out becomes a status, never an exception at a C entry.
+template <typename F>
+ccr_status_t no_throw(F&& f) {
+  try {
+    return f();
+  } catch (const std::bad_alloc&) {
+    return fail(CCR_ERR_OOM, "out of host memory");
+  }
 }
 
 }  // namespace
@@ -2029,6 +2057,367 @@ ccr_status_t ccr_moe_combine_fused(ccr_ctx_t ctx, const void* const* exp, const 
   CCR_TRY(check_writes_disjoint(bufs));
   return moe_gather(ctx, 1, m, h_ecnt, out, slot, const_cast<void* const*>(exp),
                     static_cast<hipStream_t>(stream));
+}
+
+// ------------------------------------------- experts, gated sum, gradients
+// Compute calls of a training or serving step: kernel launches on the
+// caller's stream whose tables travel as kernel arguments, so a call leaves
+// nothing in the context and can be captured.
+
+namespace {
+
+// The calling thread's current device, put back at the end of the call.
+struct KeepDevice {
+  int device = -1;
+  KeepDevice() {
+    if (hipGetDevice(&device) != hipSuccess) device = -1;
+  }
+  ~KeepDevice() {
+    if (device >= 0) (void)hipSetDevice(device);
+  }
+  KeepDevice(const KeepDevice&) = delete;
+  KeepDevice& operator=(const KeepDevice&) = delete;
+};
+
+// As check_writes_disjoint, in n log n: no written range overlaps another.
+struct Touched {
+  uintptr_t lo, hi;
+  bool written;
+  const char* what;
+  int index;
+};
+
+void touch(std::vector<Touched>* v, const void* p, int64_t nbytes, bool written, const char* what,
+           int index) {
+  if (nbytes <= 0) return;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  v->push_back(Touched{a, a + (uintptr_t)nbytes, written, what, index});
+}
+
+ccr_status_t check_touched(std::vector<Touched> v) {
+  std::sort(v.begin(), v.end(), [](const Touched& a, const Touched& b) { return a.lo < b.lo; });
+  // the ranges so far that reach furthest: of all, and of the written ones
+  const Touched *any = nullptr, *written = nullptr;
+  for (const Touched& t : v) {
+    const Touched* o = t.written ? any : written;
+    if (o && t.lo < o->hi)
+      return fail(CCR_ERR_INVALID_ARG, "%s[%d] and %s[%d] overlap", o->what, o->index, t.what, t.index);
+    if (!any || t.hi > any->hi) any = &t;
+    if (t.written && (!written || t.hi > written->hi)) written = &t;
+  }
+  return CCR_OK;
+}
+
+static_assert(kGradSlots <= CCR_GRAD_WORK, "one slot per workgroup");
+constexpr int64_t kMaxExpertDim = int64_t(1) << 20;
+constexpr int kMaxExperts = 65536;
+
+ccr_status_t run_experts(ccr_ctx* ctx, ExpertOp op, const void* const* a, const char* a_name,
+                         const void* const* b, const char* b_name, void* const* c, const char* c_name,
+                         const int64_t* h_ecnt, int R, int E, int64_t H, int64_t F, int dtype,
+                         int out_dtype, bool add, hipStream_t s) {
+  KeepDevice keep;
+  CCR_TRY(check_ctx(ctx));
+  if (R < 1 || R > kMaxRanks || E < 1 || E > kMaxExperts || E % R != 0)
+    return fail(CCR_ERR_INVALID_ARG, "need 1 <= R <= %d, 1 <= E <= %d, R | E", kMaxRanks, kMaxExperts);
+  const int es = dtype_size(dtype), os = dtype_size(out_dtype);
+  if (!es) return fail(CCR_ERR_INVALID_ARG, "dtype %d is not CCR_F32 or CCR_BF16", dtype);
+  if (!os || (es == 4 && os != 4))
+    return fail(CCR_ERR_INVALID_ARG, "dw_dtype %d: CCR_F32, or CCR_BF16 when dtype is", out_dtype);
+  for (int64_t d : {H, F})
+    if (d < 1 || d > kMaxExpertDim || d * es % 16 != 0)
+      return fail(CCR_ERR_INVALID_ARG, "H = %lld, F = %lld: each in [1, %lld], rows a multiple of 16 bytes",
+                  (long long)H, (long long)F, (long long)kMaxExpertDim);
+  if (!h_ecnt) return fail(CCR_ERR_INVALID_ARG, "h_ecnt is NULL");
+  if (!a || !b || !c) return fail(CCR_ERR_INVALID_ARG, "a buffer list is NULL");
+  const int eloc = E / R;
+  std::vector<int64_t> rows((size_t)E, 0), rank_rows((size_t)R, 0);
+  int64_t total = 0, most = 0;
+  for (int e = 0; e < E; e++) {
+    for (int r = 0; r < R; r++) {
+      const int64_t n = h_ecnt[(size_t)r * E + e];
+      if (n < 0) return fail(CCR_ERR_INVALID_ARG, "h_ecnt[%d][%d] < 0", r, e);
+      if (n > INT32_MAX) return fail(CCR_ERR_UNSUPPORTED, "h_ecnt[%d][%d] exceeds 2^31 - 1", r, e);
+      rows[(size_t)e] += n;
+    }
+    rank_rows[(size_t)(e / eloc)] += rows[(size_t)e];
+    total += rows[(size_t)e];
+    most = std::max(most, rows[(size_t)e]);
+  }
+  if (total > INT32_MAX) return fail(CCR_ERR_UNSUPPORTED, "more than 2^31 - 1 rows");
+  const int64_t wsize = F * H;  // one expert's weight, in values
+  std::vector<Touched> t;
+  KnownRange known;
+  for (int d = 0; d < R; d++) {
+    const int64_t n = rank_rows[(size_t)d];
+    int64_t ab, bb, cb;
+    if (op == ExpertOp::kWgrad) {
+      ab = n * F * es;
+      bb = n * H * es;
+      cb = add && n == 0 ? 0 : eloc * wsize * os;
+    } else {
+      ab = n * (op == ExpertOp::kProduct ? H : F) * es;
+      bb = n == 0 ? 0 : eloc * wsize * es;
+      cb = n * (op == ExpertOp::kProduct ? F : H) * es;
+    }
+    CCR_TRY(check_dev_range(ctx, a[d], ab, 16, a_name, d, &known));
+    CCR_TRY(check_dev_range(ctx, b[d], bb, 16, b_name, d, &known));
+    CCR_TRY(check_dev_range(ctx, c[d], cb, 16, c_name, d, &known));
+    touch(&t, a[d], ab, false, a_name, d);
+    touch(&t, b[d], bb, false, b_name, d);
+    touch(&t, c[d], cb, true, c_name, d);
+  }
+  CCR_TRY(check_touched(std::move(t)));
+  const ExpertShape sh{H, F, add};
+  const ExpertTile tile = expert_tile(op, es, sh, most, total);
+  const int64_t N = op == ExpertOp::kProduct ? F : H;
+  auto tiles_of = [&](int64_t n) {
+    return ceil_div(op == ExpertOp::kWgrad ? F : n, tile.m) * ceil_div(N, tile.n);
+  };
+  // one launch's grid, in work-items, is counted in 32 bits
+  constexpr int64_t kMaxTiles = int64_t(UINT32_MAX) / 512;
+  if (tiles_of(most) > kMaxTiles) return fail(CCR_ERR_UNSUPPORTED, "an expert's product is too large for one launch");
+  ExpertTable tab;
+  tab.n = 0;
+  int64_t tiles = 0;
+  auto flush = [&]() -> ccr_status_t {
+    HIP_TRY(launch_experts(op, es, os, tab, sh, tile, (int)tiles, s));
+    tab.n = 0;
+    tiles = 0;
+    return CCR_OK;
+  };
+  for (int d = 0; d < R; d++) {
+    int64_t row = 0;
+    for (int l = 0; l < eloc; l++) {
+      const int64_t n = rows[(size_t)d * eloc + l];
+      if (n > 0 || (op == ExpertOp::kWgrad && !add)) {
+        const int64_t more = tiles_of(n);
+        if (tab.n == kExpertGroups || tiles + more > kMaxTiles) CCR_TRY(flush());
+        ExpertGroup& g = tab.g[tab.n];
+        const char *pa = static_cast<const char*>(a[d]), *pb = static_cast<const char*>(b[d]);
+        char* pc = static_cast<char*>(c[d]);
+        g.rows = (int32_t)n;
+        if (op == ExpertOp::kWgrad) {
+          g.a = pa + row * F * es;
+          g.b = pb + row * H * es;
+          g.c = pc + l * wsize * os;
+        } else {
+          g.a = pa + row * (op == ExpertOp::kProduct ? H : F) * es;
+          g.b = pb + l * wsize * es;
+          g.c = pc + row * N * es;
+        }
+        tab.tile0[tab.n++] = (int32_t)tiles;
+        tiles += more;
+      }
+      row += n;
+    }
+  }
+  return tab.n > 0 ? flush() : CCR_OK;
+}
+
+ccr_status_t run_gate(ccr_ctx* ctx, bool bwd, const void* const* dy, const void* const* rows,
+                      const float* const* logits, const int32_t* const* topk, void* const* y,
+                      void* const* drows, float* const* dlogits, int R, int64_t T, int E, int K,
+                      int64_t H, int dtype, int norm, hipStream_t s) {
+  KeepDevice keep;
+  CCR_TRY(check_ctx(ctx));
+  if (R < 1 || R > kMaxRanks || T < 0 || T > INT32_MAX || E < 1 || E > 1024 || K < 1 || K > 16 || K > E)
+    return fail(CCR_ERR_INVALID_ARG, "need 1 <= R <= %d, 0 <= T < 2^31, 1 <= E <= 1024, 1 <= K <= min(E, 16)",
+                kMaxRanks);
+  const int es = dtype_size(dtype);
+  if (!es) return fail(CCR_ERR_INVALID_ARG, "dtype %d is not CCR_F32 or CCR_BF16", dtype);
+  if (norm != CCR_GATE_CHOSEN && norm != CCR_GATE_ALL)
+    return fail(CCR_ERR_INVALID_ARG, "norm %d is not CCR_GATE_CHOSEN (0) or CCR_GATE_ALL (1)", norm);
+  if (H < 1 || H > kMaxExpertDim || H * es % 16 != 0)
+    return fail(CCR_ERR_INVALID_ARG, "H = %lld: in [1, %lld], a row a multiple of 16 bytes", (long long)H,
+                (long long)kMaxExpertDim);
+  if (!rows || !logits || !topk || (bwd ? !dy || !drows || !dlogits : !y))
+    return fail(CCR_ERR_INVALID_ARG, "a buffer list is NULL");
+  if (T == 0) return CCR_OK;
+  const int64_t rb = T * K * H * es, yb = T * H * es, lb = T * E * 4, kb = T * K * 4;
+  std::vector<Touched> t;
+  KnownRange known;
+  GateArgs args{};
+  auto add = [&](const void* p, int64_t n, bool written, const char* what, int r) -> ccr_status_t {
+    CCR_TRY(check_dev_range(ctx, p, n, 16, what, r, &known));
+    touch(&t, p, n, written, what, r);
+    return CCR_OK;
+  };
+  for (int r = 0; r < R; r++) {
+    CCR_TRY(add(rows[r], rb, false, "rows", r));
+    CCR_TRY(add(logits[r], lb, false, "logits", r));
+    CCR_TRY(add(topk[r], kb, false, "topk", r));
+    args.rows[r] = static_cast<const char*>(rows[r]);
+    args.logits[r] = logits[r];
+    args.topk[r] = topk[r];
+    if (bwd) {
+      CCR_TRY(add(dy[r], yb, false, "dy", r));
+      CCR_TRY(add(drows[r], rb, true, "drows", r));
+      CCR_TRY(add(dlogits[r], lb, true, "dlogits", r));
+      args.dy[r] = static_cast<const char*>(dy[r]);
+      args.drows[r] = static_cast<char*>(drows[r]);
+      args.dlogits[r] = dlogits[r];
+    } else {
+      CCR_TRY(add(y[r], yb, true, "y", r));
+      args.y[r] = static_cast<char*>(y[r]);
+    }
+  }
+  CCR_TRY(check_touched(std::move(t)));
+  if (T > kMaxGridWorkgroups / R) return fail(CCR_ERR_UNSUPPORTED, "R x T is too large for one launch");
+  HIP_TRY(launch_gate_sum(bwd, norm == CCR_GATE_ALL, es, args, R, T, E, K, H * es, s));
+  return CCR_OK;
+}
+
+// The norm over `grads`; with `clip`, the scaled values to out (NULL: in place).
+ccr_status_t run_grads(ccr_ctx* ctx, bool clip, const void* const* grads, void* const* out,
+                       const int64_t* counts, const int32_t* dtypes, int n, float max_norm, double* work,
+                       float* norm, hipStream_t s) {
+  KeepDevice keep;
+  CCR_TRY(check_ctx(ctx));
+  if (n < 0) return fail(CCR_ERR_INVALID_ARG, "n = %d < 0", n);
+  if (n > 0 && (!grads || !counts || !dtypes))
+    return fail(CCR_ERR_INVALID_ARG, "grads, counts or dtypes is NULL");
+  if (clip && !(max_norm >= 0.0f)) return fail(CCR_ERR_INVALID_ARG, "max_norm %g is not >= 0", max_norm);
+  std::vector<Touched> t;
+  t.reserve((size_t)n * 2 + 2);
+  KnownRange known, known_out;
+  if (!work || !norm) return fail(CCR_ERR_INVALID_ARG, "work or norm is NULL");
+  CCR_TRY(check_dev_range(ctx, work, CCR_GRAD_WORK * 8, 8, "work", 0, nullptr));
+  CCR_TRY(check_dev_range(ctx, norm, 4, 4, "norm", 0, nullptr));
+  touch(&t, work, CCR_GRAD_WORK * 8, true, "work", 0);
+  touch(&t, norm, 4, true, "norm", 0);
+  int64_t most = 1;  // tiles of the largest launch
+  int64_t tiles = 0;
+  int held = 0;
+  for (int i = 0; i < n; i++) {
+    const int es = dtype_size(dtypes[i]);
+    if (!es) return fail(CCR_ERR_INVALID_ARG, "dtypes[%d] = %d is not CCR_F32 or CCR_BF16", i, dtypes[i]);
+    if (counts[i] < 0) return fail(CCR_ERR_INVALID_ARG, "counts[%d] < 0", i);
+    if (counts[i] > (int64_t(1) << 40)) return fail(CCR_ERR_UNSUPPORTED, "counts[%d] exceeds 2^40", i);
+    if (counts[i] == 0) continue;
+    const int64_t bytes = counts[i] * es;
+    CCR_TRY(check_dev_range(ctx, grads[i], bytes, es, "grads", i, &known));
+    const bool apart = clip && out && out[i] != grads[i];
+    if (apart) CCR_TRY(check_dev_range(ctx, out[i], bytes, es, "out", i, &known_out));
+    touch(&t, grads[i], bytes, clip && !apart, "grads", i);
+    if (apart) touch(&t, out[i], bytes, true, "out", i);
+    const int64_t k = grad_tiles(grads[i], counts[i], es);
+    if (held == kGradTensors || tiles + k > INT32_MAX) {
+      held = 0;
+      tiles = 0;
+    }
+    if (k > INT32_MAX) return fail(CCR_ERR_UNSUPPORTED, "counts[%d] is too large", i);
+    held++;
+    tiles += k;
+    most = std::max(most, tiles);
+  }
+  CCR_TRY(check_touched(std::move(t)));
+  // every launch uses at most the first launch's slots, which it sets
+  const int slots = (int)std::min<int64_t>(kGradSlots, most);
+  GradTable tab;
+  for (int pass = 0; pass < (clip ? 2 : 1); pass++) {
+    bool first = true;
+    auto flush = [&]() -> ccr_status_t {
+      tab.tile0[tab.n] = (int32_t)tab.ntiles;
+      const int grid = first && pass == 0 ? slots : (int)std::min<int64_t>(slots, std::max<int64_t>(1, tab.ntiles));
+      if (pass == 0) HIP_TRY(launch_grad_squares(tab, grid, work, !first, s));
+      else HIP_TRY(launch_grad_clip(tab, grid, work, slots, max_norm, first ? norm : nullptr, s));
+      first = false;
+      tab.n = 0;
+      tab.ntiles = 0;
+      return CCR_OK;
+    };
+    tab.n = 0;
+    tab.ntiles = 0;
+    for (int i = 0; i < n; i++) {
+      if (counts[i] == 0) continue;
+      const int es = dtype_size(dtypes[i]);
+      const int64_t k = grad_tiles(grads[i], counts[i], es);
+      if (tab.n == kGradTensors || tab.ntiles + k > INT32_MAX) CCR_TRY(flush());
+      tab.tile0[tab.n] = (int32_t)tab.ntiles;
+      tab.t[tab.n++] = GradTensor{static_cast<const char*>(grads[i]),
+                                  const_cast<char*>(static_cast<const char*>(clip && out ? out[i] : grads[i])),
+                                  counts[i], es};
+      tab.ntiles += k;
+    }
+    if (tab.n > 0 || first) CCR_TRY(flush());
+  }
+  if (!clip) HIP_TRY(launch_grad_norm(work, slots, norm, s));
+  return CCR_OK;
+}
+
+}  // namespace
+
+ccr_status_t ccr_moe_experts(ccr_ctx_t ctx, const void* const* exp, const void* const* w,
+                             const int64_t* h_ecnt, int R, int E, int64_t H, int64_t F, int dtype,
+                             void* const* out, void* stream) {
+  CCR_MARK("ccr_moe_experts");
+  return no_throw([&] {
+    return run_experts(ctx, ExpertOp::kProduct, exp, "exp", w, "w", out, "out", h_ecnt, R, E, H, F, dtype,
+                       dtype, false, static_cast<hipStream_t>(stream));
+  });
+}
+
+ccr_status_t ccr_moe_experts_dgrad(ccr_ctx_t ctx, const void* const* dout, const void* const* w,
+                                   const int64_t* h_ecnt, int R, int E, int64_t H, int64_t F, int dtype,
+                                   void* const* dexp, void* stream) {
+  CCR_MARK("ccr_moe_experts_dgrad");
+  return no_throw([&] {
+    return run_experts(ctx, ExpertOp::kDgrad, dout, "dout", w, "w", dexp, "dexp", h_ecnt, R, E, H, F, dtype,
+                       dtype, false, static_cast<hipStream_t>(stream));
+  });
+}
+
+ccr_status_t ccr_moe_experts_wgrad(ccr_ctx_t ctx, const void* const* exp, const void* const* dout,
+                                   const int64_t* h_ecnt, int R, int E, int64_t H, int64_t F, int dtype,
+                                   int dw_dtype, int accumulate, void* const* dw, void* stream) {
+  CCR_MARK("ccr_moe_experts_wgrad");
+  return no_throw([&]() -> ccr_status_t {
+    if (accumulate != 0 && accumulate != 1)
+      return fail(CCR_ERR_INVALID_ARG, "accumulate %d is not 0 or 1", accumulate);
+    return run_experts(ctx, ExpertOp::kWgrad, dout, "dout", exp, "exp", dw, "dw", h_ecnt, R, E, H, F, dtype,
+                       dw_dtype, accumulate == 1, static_cast<hipStream_t>(stream));
+  });
+}
+
+ccr_status_t ccr_moe_gate_sum(ccr_ctx_t ctx, const void* const* rows, const float* const* logits,
+                              const int32_t* const* topk, int R, int64_t T, int E, int K, int64_t H,
+                              int dtype, int norm, void* const* y, void* stream) {
+  CCR_MARK("ccr_moe_gate_sum");
+  return no_throw([&] {
+    return run_gate(ctx, false, nullptr, rows, logits, topk, y, nullptr, nullptr, R, T, E, K, H, dtype, norm,
+                    static_cast<hipStream_t>(stream));
+  });
+}
+
+ccr_status_t ccr_moe_gate_sum_bwd(ccr_ctx_t ctx, const void* const* dy, const void* const* rows,
+                                  const float* const* logits, const int32_t* const* topk, int R, int64_t T,
+                                  int E, int K, int64_t H, int dtype, int norm, void* const* drows,
+                                  float* const* dlogits, void* stream) {
+  CCR_MARK("ccr_moe_gate_sum_bwd");
+  return no_throw([&] {
+    return run_gate(ctx, true, dy, rows, logits, topk, nullptr, drows, dlogits, R, T, E, K, H, dtype, norm,
+                    static_cast<hipStream_t>(stream));
+  });
+}
+
+ccr_status_t ccr_grad_norm(ccr_ctx_t ctx, const void* const* grads, const int64_t* counts,
+                           const int32_t* dtypes, int n, double* work, float* norm, void* stream) {
+  CCR_MARK("ccr_grad_norm");
+  return no_throw([&] {
+    return run_grads(ctx, false, grads, nullptr, counts, dtypes, n, 0.0f, work, norm,
+                     static_cast<hipStream_t>(stream));
+  });
+}
+
+ccr_status_t ccr_grad_clip(ccr_ctx_t ctx, const void* const* grads, void* const* out,
+                           const int64_t* counts, const int32_t* dtypes, int n, float max_norm,
+                           double* work, float* norm, void* stream) {
+  CCR_MARK("ccr_grad_clip");
+  return no_throw([&] {
+    return run_grads(ctx, true, grads, out, counts, dtypes, n, max_norm, work, norm,
+                     static_cast<hipStream_t>(stream));
+  });
 }
 
 ccr_status_t ccr_profile_enable(ccr_ctx_t ctx, int on) {

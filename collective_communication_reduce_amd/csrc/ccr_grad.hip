@@ -1,0 +1,273 @@
+// Device kernels of the global gradient norm and of clipping, written for
+// gfx950 (CDNA4: wave64, 256 CUs in 8 XCDs, HBM3E).
+//
+//   norm = sqrt(sum over every tensor, over every element, of g^2)
+//   out  = g * min(1, max_norm / (norm + 1e-6))
+//
+// Both are streaming passes bound by HBM.  The tensors of a call are cut into
+// tiles and the tiles dealt to a fixed number of workgroups in contiguous
+// runs, so a call over hundreds of small tensors is still one launch per
+// kGradTensors of them.  Each workgroup leaves one fp64 partial in its own
+// slot of the caller's work array; the slots are added in a fixed order, so
+// the norm has the same bits on every run.  Squares are taken and added in
+// fp64: the square of any fp32 value is exact in it and neither overflows nor
+// underflows, and at HBM rate its cost does not show.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ccr_device.h"
+#include "ccr_internal.h"
+
+namespace ccr {
+namespace {
+
+using dev::u32x4;
+
+constexpr int kVecs = 8;                         // 16-byte vectors per thread and tile
+constexpr int64_t kTileVecs = kBlock * kVecs;    // 32 KiB
+
+// A tensor as the kernels walk it: `head` elements up to the first 16-byte
+// boundary, then whole vectors, then a tail shorter than one.
+struct Span {
+  const char* src;
+  char* dst;
+  int64_t count, nvec;
+  int head, tail;
+};
+
+template <int ES>
+__device__ __forceinline__ Span span_of(const GradTensor& t) {
+  Span s;
+  s.src = t.src;
+  s.dst = t.dst;
+  s.count = t.count;
+  const int64_t to_edge = ((16 - (int)(reinterpret_cast<uintptr_t>(t.src) & 15)) & 15) / ES;
+  s.head = (int)(to_edge < t.count ? to_edge : t.count);
+  s.nvec = (t.count - s.head) * ES >> 4;
+  s.tail = (int)(t.count - s.head - s.nvec * (16 / ES));
+  return s;
+}
+
+template <int ES>
+__device__ __forceinline__ float element(const char* p, int64_t i) {
+  if constexpr (ES == 4) return reinterpret_cast<const float*>(p)[i];
+  else return dev::bf16_lo(reinterpret_cast<const uint16_t*>(p)[i]);
+}
+
+__device__ __forceinline__ double square(float x) { return (double)x * (double)x; }
+
+template <int ES>
+__device__ __forceinline__ double squares(u32x4 v, double acc) {
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    if constexpr (ES == 4) {
+      acc += square(__builtin_bit_cast(float, (uint32_t)v[j]));
+    } else {
+      acc += square(dev::bf16_lo(v[j]));
+      acc += square(dev::bf16_hi(v[j]));
+    }
+  }
+  return acc;
+}
+
+template <int ES>
+__device__ __forceinline__ double tile_squares(const GradTensor& t, int64_t tile, double acc) {
+  const Span s = span_of<ES>(t);
+  const u32x4* v = reinterpret_cast<const u32x4*>(s.src + (int64_t)s.head * ES);
+  const int64_t first = tile * kTileVecs + threadIdx.x;
+  u32x4 x[kVecs];
+#pragma unroll
+  for (int u = 0; u < kVecs; u++) {
+    const int64_t i = first + u * kBlock;
+    x[u] = i < s.nvec ? v[i] : u32x4{0, 0, 0, 0};
+  }
+#pragma unroll
+  for (int u = 0; u < kVecs; u++) acc = squares<ES>(x[u], acc);
+  if (tile == 0 && (int)threadIdx.x < s.head)
+    acc += square(element<ES>(s.src, threadIdx.x));
+  if (tile == 0 && (int)threadIdx.x < s.tail)
+    acc += square(element<ES>(s.src, s.count - s.tail + threadIdx.x));
+  return acc;
+}
+
+__device__ __forceinline__ double wave_sum(double x) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) x += __shfl_xor(x, off);
+  return x;
+}
+
+// The sum over the workgroup, in every thread; `part` holds a double per wave.
+__device__ __forceinline__ double block_sum(double x, double* part) {
+  x = wave_sum(x);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
+  __syncthreads();
+  double s = 0;
+#pragma unroll
+  for (int w = 0; w < kBlock / 64; w++) s += part[w];
+  return s;
+}
+
+// Tiles [lo, hi) of workgroup b of g, and the tensor that holds tile lo.
+__device__ __forceinline__ void my_tiles(const GradTable& tab, int64_t* lo, int64_t* hi, int* at) {
+  const int64_t b = blockIdx.x, g = gridDim.x, per = tab.ntiles / g, rem = tab.ntiles % g;
+  *lo = b * per + (b < rem ? b : rem);
+  *hi = *lo + per + (b < rem ? 1 : 0);
+  int i = 0;
+  if (*lo < *hi) {
+    int a = 0, z = tab.n - 1;
+    while (a < z) {
+      const int mid = (a + z + 1) >> 1;
+      if (tab.tile0[mid] <= *lo) a = mid; else z = mid - 1;
+    }
+    i = a;
+  }
+  *at = i;
+}
+
+// One partial per workgroup: work[b] = (add ? work[b] : 0) + its tiles' sum.
+__global__ __launch_bounds__(kBlock) void grad_squares_kernel(const GradTable tab, double* work,
+                                                              int add) {
+  __shared__ double part[kBlock / 64];
+  int64_t lo, hi;
+  int at;
+  my_tiles(tab, &lo, &hi, &at);
+  double acc = 0;
+  for (int64_t tile = lo; tile < hi; tile++) {
+    while (tile >= tab.tile0[at + 1]) at++;
+    const GradTensor& t = tab.t[at];
+    if (t.es == 4) acc = tile_squares<4>(t, tile - tab.tile0[at], acc);
+    else acc = tile_squares<2>(t, tile - tab.tile0[at], acc);
+  }
+  const double s = block_sum(acc, part);
+  if (threadIdx.x == 0) work[blockIdx.x] = add ? work[blockIdx.x] + s : s;
+}
+
+// The sum of the slots, the same additions in the same order in every
+// workgroup that makes it.
+__device__ __forceinline__ double total_of(const double* work, int slots, double* part) {
+  double acc = 0;
+  for (int i = threadIdx.x; i < slots; i += kBlock) acc += work[i];
+  return block_sum(acc, part);
+}
+
+__global__ __launch_bounds__(kBlock) void grad_norm_kernel(const double* work, int slots, float* norm) {
+  __shared__ double part[kBlock / 64];
+  const double s = total_of(work, slots, part);
+  if (threadIdx.x == 0) *norm = (float)sqrt(s);
+}
+
+// Each result is rounded once more than the fp32 product: to its own type.
+template <int ES>
+__device__ __forceinline__ u32x4 scaled(u32x4 v, float c) {
+  u32x4 r;
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    if constexpr (ES == 4) {
+      r[j] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, (uint32_t)v[j]) * c);
+    } else {
+      dev::f32x2 f = {dev::bf16_lo(v[j]) * c, dev::bf16_hi(v[j]) * c};
+      r[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, dev::bf16x2));
+    }
+  }
+  return r;
+}
+
+template <int ES>
+__device__ __forceinline__ void scale_element(const Span& s, int64_t i, float c) {
+  const float r = element<ES>(s.src, i) * c;
+  if constexpr (ES == 4) reinterpret_cast<float*>(s.dst)[i] = r;
+  else reinterpret_cast<__bf16*>(s.dst)[i] = static_cast<__bf16>(r);
+}
+
+template <int ES>
+__device__ __forceinline__ void tile_scale(const GradTensor& t, int64_t tile, float c) {
+  const Span s = span_of<ES>(t);
+  const u32x4* v = reinterpret_cast<const u32x4*>(s.src + (int64_t)s.head * ES);
+  char* const out = s.dst + (int64_t)s.head * ES;
+  const int64_t first = tile * kTileVecs + threadIdx.x;
+  u32x4 x[kVecs];
+#pragma unroll
+  for (int u = 0; u < kVecs; u++) {
+    const int64_t i = first + u * kBlock;
+    if (i < s.nvec) x[u] = v[i];
+  }
+  if ((reinterpret_cast<uintptr_t>(out) & 15) == 0) {
+#pragma unroll
+    for (int u = 0; u < kVecs; u++) {
+      const int64_t i = first + u * kBlock;
+      if (i < s.nvec) reinterpret_cast<u32x4*>(out)[i] = scaled<ES>(x[u], c);
+    }
+  } else {  // the result's buffer starts at another offset within 16 bytes
+#pragma unroll
+    for (int u = 0; u < kVecs; u++) {
+      const int64_t i = first + u * kBlock;
+      if (i >= s.nvec) continue;
+      const u32x4 r = scaled<ES>(x[u], c);
+      if constexpr (ES == 4) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) reinterpret_cast<uint32_t*>(out)[4 * i + j] = r[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+          reinterpret_cast<uint16_t*>(out)[8 * i + j] = (uint16_t)(r[j >> 1] >> (16 * (j & 1)));
+      }
+    }
+  }
+  if (tile == 0 && (int)threadIdx.x < s.head) scale_element<ES>(s, threadIdx.x, c);
+  if (tile == 0 && (int)threadIdx.x < s.tail)
+    scale_element<ES>(s, s.count - s.tail + threadIdx.x, c);
+}
+
+// out = g * min(1, max_norm / (norm + 1e-6)) over the tiles, the last tile
+// first: the pass before left the end of the gradients in the last-level
+// cache.  Every workgroup adds the slots itself (16 KiB from L2), which saves
+// a launch between the two passes.  In place, a factor of 1 writes nothing.
+__global__ __launch_bounds__(kBlock) void grad_clip_kernel(const GradTable tab, const double* work,
+                                                           int slots, float max_norm, float* norm) {
+  __shared__ double part[kBlock / 64];
+  const float nv = (float)sqrt(total_of(work, slots, part));
+  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = nv;
+  const float q = max_norm / (nv + 1e-6f);
+  const float c = q > 1.0f ? 1.0f : q;  // a NaN stays
+  int64_t lo, hi;
+  int at;
+  my_tiles(tab, &lo, &hi, &at);
+  if (lo >= hi) return;
+  while (hi - 1 >= tab.tile0[at + 1]) at++;
+  for (int64_t tile = hi - 1; tile >= lo; tile--) {
+    while (tile < tab.tile0[at]) at--;
+    const GradTensor& t = tab.t[at];
+    if (c == 1.0f && t.src == t.dst) continue;
+    if (t.es == 4) tile_scale<4>(t, tile - tab.tile0[at], c);
+    else tile_scale<2>(t, tile - tab.tile0[at], c);
+  }
+}
+
+}  // namespace
+
+int64_t grad_tiles(const void* p, int64_t count, int es) {
+  const int64_t to_edge = ((16 - (int)(reinterpret_cast<uintptr_t>(p) & 15)) & 15) / es;
+  const int64_t nvec = count > to_edge ? (count - to_edge) * es >> 4 : 0;
+  const int64_t t = (nvec + kTileVecs - 1) / kTileVecs;
+  return t > 0 ? t : 1;
+}
+
+hipError_t launch_grad_squares(const GradTable& tab, int grid, double* work, bool add,
+                               hipStream_t stream) {
+  grad_squares_kernel<<<(unsigned)grid, kBlock, 0, stream>>>(tab, work, add ? 1 : 0);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_norm(const double* work, int slots, float* norm, hipStream_t stream) {
+  grad_norm_kernel<<<1, kBlock, 0, stream>>>(work, slots, norm);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_clip(const GradTable& tab, int grid, const double* work, int slots,
+                            float max_norm, float* norm, hipStream_t stream) {
+  grad_clip_kernel<<<(unsigned)grid, kBlock, 0, stream>>>(tab, work, slots, max_norm, norm);
+  return hipGetLastError();
+}
+
+}  // namespace ccr

@@ -190,6 +190,81 @@ hipError_t launch_moe_topk(const float* logits, int32_t* topk, int64_t T, int E,
 hipError_t launch_moe_plan(const int32_t* topk, int64_t T, int E, int K, int eloc,
                            int64_t* ecnt, int32_t* src_tok, int32_t* slot, hipStream_t stream);
 
+// The experts' products (ccr_experts.hip).  A group is one expert's work of a
+// launch: its first operand a (x, dout, dout), second operand b (W, W, x) and
+// output c (out, dexp, dw), and its rows.
+enum class ExpertOp : int { kProduct = 0, kDgrad = 1, kWgrad = 2 };
+struct ExpertGroup {
+  const char* a;
+  const char* b;
+  char* c;
+  int32_t rows;
+};
+// Up to kExpertGroups experts go into one launch, passed by value as kernel
+// arguments (4 KiB at most); tile0[i] = first tile of group i.
+constexpr int kExpertGroups = 96;
+struct ExpertTable {
+  int32_t n;
+  int32_t tile0[kExpertGroups];
+  ExpertGroup g[kExpertGroups];
+};
+static_assert(sizeof(ExpertTable) <= 3584, "fits the kernel argument segment");
+struct ExpertShape {
+  int64_t H, F;
+  bool add;  // wgrad: add to what c holds
+};
+// Output tile of the kernel variant that a launch takes.
+struct ExpertTile {
+  int m, n;
+};
+// The variant for groups of `max_rows` rows at most and `rows` in all.
+ExpertTile expert_tile(ExpertOp op, int es, const ExpertShape& sh, int64_t max_rows, int64_t rows);
+// es, os: bytes per input and output value; tiles: in all, numbered group by group.
+hipError_t launch_experts(ExpertOp op, int es, int os, const ExpertTable& tab, const ExpertShape& sh,
+                          ExpertTile tile, int tiles, hipStream_t stream);
+
+// The gated sum and its gradients (ccr_gate.hip).  Per rank, device pointers.
+struct GateArgs {
+  const char* rows[kRingHopMaxRanks];
+  const float* logits[kRingHopMaxRanks];
+  const int32_t* topk[kRingHopMaxRanks];
+  const char* dy[kRingHopMaxRanks];
+  char* y[kRingHopMaxRanks];
+  char* drows[kRingHopMaxRanks];
+  float* dlogits[kRingHopMaxRanks];
+};
+static_assert(sizeof(GateArgs) <= 3584, "fits the kernel argument segment");
+hipError_t launch_gate_sum(bool bwd, bool over_all, int es, const GateArgs& a, int R, int64_t T,
+                           int E, int K, int64_t row_bytes, hipStream_t stream);
+
+// The gradient norm and clipping (ccr_grad.hip).  Up to kGradTensors tensors
+// go into one launch; tile0[i] = first tile of tensor i, tile0[n] = ntiles.
+constexpr int kGradTensors = 112;
+struct GradTensor {
+  const char* src;
+  char* dst;
+  int64_t count;
+  int32_t es;
+};
+struct GradTable {
+  int32_t n;
+  int64_t ntiles;
+  int32_t tile0[kGradTensors + 1];
+  GradTensor t[kGradTensors];
+};
+static_assert(sizeof(GradTable) <= 4056, "fits the kernel argument segment");
+// Slots of the work array, one per workgroup at most.
+constexpr int kGradSlots = 2048;
+// Tiles of a tensor of `count` > 0 elements of es bytes at p.
+int64_t grad_tiles(const void* p, int64_t count, int es);
+// work[b] (+)= the sum of squares of workgroup b's tiles.
+hipError_t launch_grad_squares(const GradTable& tab, int grid, double* work, bool add,
+                               hipStream_t stream);
+hipError_t launch_grad_norm(const double* work, int slots, float* norm, hipStream_t stream);
+// norm may be NULL (a later launch of the same call).
+hipError_t launch_grad_clip(const GradTable& tab, int grid, const double* work, int slots,
+                            float max_norm, float* norm, hipStream_t stream);
+
 // One wave64 workgroup per block; writes (XCC id, SE id, CU id) per block.
 hipError_t launch_probe_cu_ids(int32_t* out, int nblocks, hipStream_t stream);
 

@@ -52,7 +52,8 @@
  *     capturing stream and replayed (the ring collectives with kernel copies
  *     and per-hop bf16, with or without slices or overlap; ccr_alltoall,
  *     ccr_alltoall_rows, ccr_moe_dispatch and ccr_moe_combine with kernel
- *     copies; ccr_permute_rows; ccr_moe_topk).  A replay reuses the device
+ *     copies; ccr_permute_rows; ccr_moe_topk; the experts' products, the
+ *     gated sum, ccr_grad_norm and ccr_grad_clip).  A replay reuses the device
  *     pointers given at capture time.  Calls that would depend on context
  *     scratch that may be reallocated, on host memory copied at launch, or
  *     on the DMA proxy (SDMA copies, fp32 partials, ccr_sendrecv,
@@ -61,6 +62,10 @@
  *     so does every call of a context with a CU budget, because a replay
  *     runs the captured kernels on the replaying stream's hardware queue,
  *     without the budget's CU mask.
+ *   - The experts' products, the gated sum and the gradient calls are
+ *     compute, not communication: like ccr_moe_topk they run on the caller's
+ *     stream, whatever the context's CU budget, and keep no device state in
+ *     the context.
  */
 #ifndef CCR_H
 #define CCR_H
@@ -486,6 +491,104 @@ ccr_status_t ccr_moe_combine_fused(ccr_ctx_t ctx, const void *const *exp,
                                    const int32_t *const *slot, const int64_t *h_ecnt, int R,
                                    int64_t T, int E, int K, int64_t row_bytes, void *const *out,
                                    void *stream);
+
+/* ----------------------------------------------------------------------
+ * The experts' matrix products, between ccr_moe_dispatch and ccr_moe_combine
+ * (HOCCL §2.1: dispatch brings tokens to their experts, combine returns what
+ * the experts make of them; the pages describe the exchange only, so the
+ * products are the plain linear layer).  Expert e of rank d = e / (E/R) owns
+ * the run of rows that dispatch placed for it in exp[d] (experts in order,
+ * sum over r of h_ecnt[r*E + e] rows), and a weight w_e [F x H], the
+ * (e mod E/R)-th of w[d] [E/R x F x H].
+ *
+ * ccr_moe_experts:       out[d][i, f]  = sum_h exp[d][i, h] w_e[f, h]
+ * ccr_moe_experts_dgrad: dexp[d][i, h] = sum_f dout[d][i, f] w_e[f, h]
+ * ccr_moe_experts_wgrad: dw[d][e][f, h] (+)= sum_i dout[d][i, f] exp[d][i, h]
+ *   over e's rows; an expert without a row gets zeros.  dw_dtype: CCR_F32, or
+ *   CCR_BF16 when dtype is.  accumulate = 1 adds to what dw holds (and leaves
+ *   an expert without a row as it is).
+ *
+ * Products are summed in fp32 whatever the dtype, and each result is rounded
+ * once.  h_ecnt: host int64 [R*E], the array of the dispatch call; its rows
+ * need not have equal sums.  exp, dout, out, dexp [d]: the rows of rank d's
+ * experts, contiguous, H or F values each; rows behind the last are left as
+ * they are.  A rank without a row has none of its buffers read (its dw is
+ * written).  H and F: 1 .. 2^20, rows a multiple of 16 bytes; E <= 65536; at
+ * most 2^31 - 1 rows in all.  Written buffers must not overlap any other
+ * buffer of the call.
+ * ---------------------------------------------------------------------- */
+ccr_status_t ccr_moe_experts(ccr_ctx_t ctx, const void *const *exp, const void *const *w,
+                             const int64_t *h_ecnt, int R, int E, int64_t H, int64_t F, int dtype,
+                             void *const *out, void *stream);
+ccr_status_t ccr_moe_experts_dgrad(ccr_ctx_t ctx, const void *const *dout, const void *const *w,
+                                   const int64_t *h_ecnt, int R, int E, int64_t H, int64_t F,
+                                   int dtype, void *const *dexp, void *stream);
+ccr_status_t ccr_moe_experts_wgrad(ccr_ctx_t ctx, const void *const *exp, const void *const *dout,
+                                   const int64_t *h_ecnt, int R, int E, int64_t H, int64_t F,
+                                   int dtype, int dw_dtype, int accumulate, void *const *dw,
+                                   void *stream);
+
+/* ----------------------------------------------------------------------
+ * The gated sum that ends an expert-parallel layer (HOCCL §2.1: combine
+ * returns each token's K expert rows; the router's softmax weighs them), and
+ * its gradients.  Per rank, rows[r] [T x K x H] as ccr_moe_combine leaves
+ * them, logits[r] (fp32 [T x E]) and topk[r] (int32 [T x K]) as given to and
+ * by ccr_moe_topk.
+ *
+ * ccr_moe_gate_sum: y[r][t] = sum_k w_k rows[r][t, k], w_k the softmax of the
+ *   token's logits taken at its k-th choice: over its K choices
+ *   (CCR_GATE_CHOSEN: the weights sum to 1) or over all E experts
+ *   (CCR_GATE_ALL).  A choice is absent when its topk entry is outside
+ *   [0, E) or its logit is -infinity: it has weight 0 and its row is not
+ *   read.  A token without a choice gets zeros.
+ * ccr_moe_gate_sum_bwd: from dy[r] [T x H], drows[r][t, k] = w_k dy[r][t]
+ *   (zeros for an absent choice) and dlogits[r] (fp32 [T x E], every entry
+ *   written): the gradient through the softmax of g_k = <dy[r][t],
+ *   rows[r][t, k]>.  An expert chosen twice by a token collects both parts.
+ *
+ * Weights and sums are fp32; each result is rounded once.  dtype: of rows, y,
+ * dy and drows.  1 <= E <= 1024, 1 <= K <= min(E, 16), H 1 .. 2^20 with rows a
+ * multiple of 16 bytes.  Written buffers must not overlap any other buffer.
+ * ---------------------------------------------------------------------- */
+typedef enum { CCR_GATE_CHOSEN = 0, CCR_GATE_ALL = 1 } ccr_gate_norm_t;
+ccr_status_t ccr_moe_gate_sum(ccr_ctx_t ctx, const void *const *rows, const float *const *logits,
+                              const int32_t *const *topk, int R, int64_t T, int E, int K, int64_t H,
+                              int dtype, int norm, void *const *y, void *stream);
+ccr_status_t ccr_moe_gate_sum_bwd(ccr_ctx_t ctx, const void *const *dy, const void *const *rows,
+                                  const float *const *logits, const int32_t *const *topk, int R,
+                                  int64_t T, int E, int K, int64_t H, int dtype, int norm,
+                                  void *const *drows, float *const *dlogits, void *stream);
+
+/* ----------------------------------------------------------------------
+ * The global norm of gradients and clipping, after the bucket's all-reduce
+ * (or over the owned chunks after a reduce-scatter; HOCCL §5: reductions
+ * stay on the GPU cores).
+ *
+ * ccr_grad_norm: *norm (device fp32) = sqrt(sum of the squares of every
+ *   element of every tensor).  Squares and sums are fp64, in a fixed order:
+ *   the norm of any fp32 or bf16 values neither overflows on the way nor
+ *   changes from run to run.  An infinity or a NaN in a tensor shows in it.
+ * ccr_grad_clip: the norm, then out[i] = grads[i] * min(1, max_norm / (norm +
+ *   1e-6)) in fp32, rounded once to the tensor's type.  out NULL, or out[i] =
+ *   grads[i]: in place, and nothing is written when the factor is 1.  A
+ *   non-finite norm follows the formula (infinite: finite values become 0
+ *   and infinite ones NaN; NaN: every value NaN).  max_norm >= 0; infinity
+ *   only measures.
+ *
+ * grads: host array of n device pointers, each to counts[i] >= 0 contiguous
+ * elements of dtypes[i]; pointers need their element's alignment only (views
+ * into a bucket).  work: device fp64 [CCR_GRAD_WORK], the call's alone until
+ * it completes, contents of no meaning before and after: two calls that may
+ * run at the same time, captured graphs included, need a work array and a
+ * norm each.  Tensors may overlap in ccr_grad_norm (shared ones count twice);
+ * a buffer that is written must not overlap any other.
+ * ---------------------------------------------------------------------- */
+#define CCR_GRAD_WORK 2048
+ccr_status_t ccr_grad_norm(ccr_ctx_t ctx, const void *const *grads, const int64_t *counts,
+                           const int32_t *dtypes, int n, double *work, float *norm, void *stream);
+ccr_status_t ccr_grad_clip(ccr_ctx_t ctx, const void *const *grads, void *const *out,
+                           const int64_t *counts, const int32_t *dtypes, int n, float max_norm,
+                           double *work, float *norm, void *stream);
 
 /* ----------------------------------------------------------------------
  * Diagnostics.

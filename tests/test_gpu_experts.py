@@ -1,0 +1,299 @@
+"""GPU parity of the experts' products with a 64-bit reference.
+
+Whole-number inputs small enough that every sum is exact in fp32 have one
+right answer, whatever the order of the sums: those cases compare bit for bit.
+Random inputs compare within the error of the sums, derived at the test."""
+import numpy as np
+import pytest
+
+from gpu_helpers import say, torch_cuda
+from operator_helpers import Guarded, HALF, counts_of, experts_ref, inside_nan, tdtype
+
+pytestmark = pytest.mark.gpu
+
+OPS = ["product", "dgrad", "wgrad"]
+
+
+@pytest.fixture(scope="module")
+def ccr_mod():
+    torch_cuda()
+    import collective_communication_reduce_amd as ccr
+    return ccr
+
+
+def make(op, dt, rows, R, H, F, seed, whole):
+    """(ecnt, first operand, second operand, output shapes) per rank."""
+    import torch
+    E = len(rows)
+    eloc = E // R
+    rng = np.random.default_rng(seed)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+
+    def values(*shape):
+        if whole:
+            v = torch.randint(-3, 4, shape, generator=g, device="cuda").float()
+        else:
+            v = torch.randn(shape, generator=g, device="cuda")
+        return inside_nan(v.to(tdtype(dt)))
+
+    tot = [int(sum(rows[d * eloc:(d + 1) * eloc])) for d in range(R)]
+    a = [values(t, H if op == "product" else F) for t in tot]
+    if op == "wgrad":
+        b = [values(t, H) for t in tot]
+        shapes = [(eloc, F, H)] * R
+    else:
+        b = [values(eloc, F, H) for _ in range(R)]
+        shapes = [(t, F if op == "product" else H) for t in tot]
+    return counts_of(rows, R, E, rng), a, b, shapes
+
+
+def call(ccr, c, op, a, b, ecnt, out, **kw):
+    if op == "product":
+        ccr.ccr_moe_experts(c, a, b, ecnt, out, **kw)
+    elif op == "dgrad":
+        ccr.ccr_moe_experts_dgrad(c, a, b, ecnt, out, **kw)
+    else:
+        ccr.ccr_moe_experts_wgrad(c, b, a, ecnt, out, **kw)
+
+
+def check(ccr, op, dt, rows, R, H, F, seed=0, whole=True, out_dt=None, accumulate=False):
+    import torch
+    out_dt = out_dt or dt
+    say(f"experts {op} {dt}->{out_dt} rows={list(rows)[:12]} R={R} H={H} F={F} whole={whole} acc={accumulate}")
+    ecnt, a, b, shapes = make(op, dt, rows, R, H, F, seed, whole)
+    fill = 3.0 if accumulate else float("nan")
+    outs = [Guarded(s, tdtype(out_dt), fill) for s in shapes]
+    with ccr.Context(0) as c:
+        call(ccr, c, op, a, b, ecnt, [o.t for o in outs], **({"accumulate": True} if accumulate else {}))
+        torch.cuda.synchronize()
+    ref, mag = experts_ref(op, a, b, rows, R, len(rows))
+    inner = {"product": H, "dgrad": F, "wgrad": max(list(rows) + [1])}[op]
+    for d in range(R):
+        assert outs[d].intact(), f"rank {d}: a guard byte changed"
+        want = ref[d] + (3.0 if accumulate else 0.0)
+        got = outs[d].t
+        if whole:
+            assert torch.equal(got, want.to(tdtype(out_dt))), f"rank {d} differs"
+        else:
+            # each of the `inner` fp32 additions and the adding of the old value is
+            # off by at most one unit (2^-23) of a partial sum, which the sum of the
+            # products' magnitudes bounds; then one rounding to the output type
+            tol = HALF[out_dt] * want.abs() + (inner + 1) * 2.0 ** -23 * (mag[d] + 3.0 * accumulate) * 1.01
+            assert bool(((got.double() - want).abs() <= tol).all()), f"rank {d} out of tolerance"
+    return outs
+
+
+ROWS = {
+    "one row": [1],
+    "no row at all": [0, 0],
+    "one expert of four": [0, 0, 5, 0],
+    "single tokens": [1, 0, 1, 1, 0, 0, 1, 2],
+    "around sixteen": [15, 16, 17, 0],
+    "around thirty-two": [31, 32, 33, 48],
+    "around a tile": [63, 64, 65, 127, 128, 129],
+    "ragged": [300, 0, 1, 257, 77, 512, 0, 9],
+}
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", ROWS.values(), ids=ROWS.keys())
+@pytest.mark.parametrize("H,F", [(8, 8), (72, 136), (264, 520), (1032, 200)])
+def test_whole_numbers_bitwise(ccr_mod, op, dt, rows, H, F):
+    check(ccr_mod, op, dt, rows, 1, H, F, seed=H + F + len(rows))
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_several_ranks_bitwise(ccr_mod, op, dt):
+    check(ccr_mod, op, dt, [5, 0, 130, 64, 0, 0, 33, 200], 4, 136, 264, seed=3)  # rank 2 has no row
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_fp32_rows_of_four_values(ccr_mod, op):
+    check(ccr_mod, op, "f32", [3, 70, 0, 129], 2, 4, 12)
+    check(ccr_mod, op, "f32", [3, 70, 0, 129], 2, 132, 68)
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_more_experts_than_one_launch_lists(ccr_mod, op):
+    rng = np.random.default_rng(9)
+    check(ccr_mod, op, "bf16", list(rng.integers(0, 20, 250)), 2, 40, 24)
+
+
+@pytest.mark.parametrize("op,dt,rows,H,F", [
+    ("product", "bf16", [700, 1300, 0, 2500], 1024, 768),
+    ("dgrad", "bf16", [700, 1300, 0, 2500], 768, 1024),
+    ("wgrad", "bf16", [700, 1300, 0, 2500], 512, 1024),
+    ("product", "bf16", [2, 9, 0, 1], 2048, 1024),
+    ("product", "f32", [300, 900], 512, 260),
+    ("dgrad", "f32", [300, 900], 260, 512),
+    ("wgrad", "f32", [300, 900], 260, 516),
+    ("wgrad", "bf16", [40000, 3], 88, 176),
+])
+def test_random_values_within_the_sums_error(ccr_mod, op, dt, rows, H, F):
+    check(ccr_mod, op, dt, rows, 1, H, F, whole=False, seed=H)
+
+
+@pytest.mark.parametrize("dt,out_dt", [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("whole", [True, False])
+def test_wgrad_types_and_accumulation(ccr_mod, dt, out_dt, whole):
+    rows = [50, 0, 1, 300]
+    check(ccr_mod, "wgrad", dt, rows, 2, 136, 72, whole=whole, out_dt=out_dt)
+    check(ccr_mod, "wgrad", dt, rows, 2, 136, 72, whole=whole, out_dt=out_dt, accumulate=True)
+
+
+def test_gradients_against_differences(ccr_mod):
+    """<dout, experts(x)> is linear in x and in w: moving one entry of either
+    by a step changes it by step times that entry's gradient, exactly in
+    whole numbers."""
+    import torch
+    rows, R, H, F = [5, 0, 37], 1, 16, 24
+    ecnt, x, w, _ = make("product", "f32", rows, R, H, F, 1, True)
+    n = sum(rows)
+    dout = [torch.randint(-3, 4, (n, F), device="cuda").float()]
+    with ccr_mod.Context(0) as c:
+        dx, dw, y = torch.empty(n, H, device="cuda"), torch.empty(3, F, H, device="cuda"), torch.empty(n, F, device="cuda")
+        ccr_mod.ccr_moe_experts_dgrad(c, dout, w, ecnt, [dx])
+        ccr_mod.ccr_moe_experts_wgrad(c, x, dout, ecnt, [dw])
+
+        def loss(xs, ws):
+            ccr_mod.ccr_moe_experts(c, [xs], [ws], ecnt, [y])
+            return float((y.double() * dout[0].double()).sum())
+
+        base = loss(x[0], w[0])
+        for i, h in [(0, 0), (4, 15), (5, 3), (41, 9)]:
+            moved = x[0].clone()
+            moved[i, h] += 2
+            assert loss(moved, w[0]) - base == 2 * float(dx[i, h])
+        for e, f, h in [(0, 0, 0), (2, 23, 15), (2, 7, 1), (1, 3, 3)]:
+            moved = w[0].clone()
+            moved[e, f, h] += 2
+            assert loss(x[0], moved) - base == 2 * float(dw[e, f, h])
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_values_of_other_rows_do_not_leak(ccr_mod, op):
+    """A NaN or an infinity in one expert's rows stays with that expert."""
+    import torch
+    rows, H, F = [70, 3, 130], 72, 136
+    ecnt, a, b, shapes = make(op, "bf16", rows, 1, H, F, 2, True)
+    a[0][70:73] = float("nan")
+    a[0][72] = float("inf")
+    out = torch.empty(shapes[0], dtype=torch.bfloat16, device="cuda")
+    with ccr_mod.Context(0) as c:
+        call(ccr_mod, c, op, a, b, ecnt, [out])
+        torch.cuda.synchronize()
+    ref, _ = experts_ref(op, a, b, rows, 1, 3)
+    keep = [0, 2] if op == "wgrad" else list(range(70)) + list(range(73, 203))
+    assert torch.equal(out[keep], ref[0][keep].to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_rows_behind_the_last_are_left(ccr_mod, op):
+    import torch
+    rows, H, F = [9, 40], 24, 40
+    ecnt, a, b, shapes = make(op, "bf16", rows, 1, H, F, 4, True)
+    pad = lambda t: torch.cat([t, torch.full((7,) + tuple(t.shape[1:]), float("nan"), dtype=t.dtype, device="cuda")])
+    a = [pad(t) for t in a]
+    b = [pad(t) for t in b] if op == "wgrad" else b
+    n = shapes[0][0]
+    extra = 0 if op == "wgrad" else 7
+    out = torch.full((n + extra,) + tuple(shapes[0][1:]), 5.0, dtype=torch.bfloat16, device="cuda")
+    with ccr_mod.Context(0) as c:
+        call(ccr_mod, c, op, a, b, ecnt, [out])
+        torch.cuda.synchronize()
+    ref, _ = experts_ref(op, a, b, rows, 1, 2)
+    assert torch.equal(out[:n], ref[0].to(torch.bfloat16))
+    assert bool((out[n:] == 5.0).all())
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_another_stream_and_graph_replays(ccr_mod, op):
+    import torch
+    rows, H, F = [33, 0, 200, 1], 136, 72
+    ecnt, a, b, shapes = make(op, "bf16", rows, 1, H, F, 5, True)
+    out = torch.zeros(shapes[0], dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    with ccr_mod.Context(0) as c:
+        side.wait_stream(torch.cuda.current_stream())
+        call(ccr_mod, c, op, a, b, ecnt, [out], stream=side)
+        side.synchronize()
+        want = experts_ref(op, a, b, rows, 1, 4)[0][0].to(torch.bfloat16)
+        assert torch.equal(out, want)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(ccr_mod, c, op, a, b, ecnt, [out])
+        for step in range(3):
+            a[0].copy_(torch.randint(-3, 4, a[0].shape, device="cuda").to(a[0].dtype))
+            out.fill_(float("nan"))
+            graph.replay()
+            torch.cuda.synchronize()
+            want = experts_ref(op, a, b, rows, 1, 4)[0][0].to(torch.bfloat16)
+            assert torch.equal(out, want), f"replay {step}"
+
+
+def test_runs_with_a_cu_budget_and_under_capture(ccr_mod):
+    import torch
+    ecnt, a, b, shapes = make("product", "bf16", [40, 5], 1, 72, 40, 6, True)
+    out = torch.zeros(shapes[0], dtype=torch.bfloat16, device="cuda")
+    with ccr_mod.Context(0, ccr_mod.Config(cu_budget=16)) as c:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            ccr_mod.ccr_moe_experts(c, a, b, ecnt, [out])
+        graph.replay()
+        torch.cuda.synchronize()
+    assert torch.equal(out, experts_ref("product", a, b, [40, 5], 1, 2)[0][0].to(torch.bfloat16))
+
+
+def test_same_bits_every_run(ccr_mod):
+    import torch
+    for op in OPS:
+        ecnt, a, b, shapes = make(op, "bf16", [500, 3, 0, 129], 1, 264, 200, 7, False)
+        got = []
+        with ccr_mod.Context(0) as c:
+            for _ in range(3):
+                out = torch.empty(shapes[0], dtype=torch.bfloat16, device="cuda")
+                call(ccr_mod, c, op, a, b, ecnt, [out])
+                got.append(out)
+            torch.cuda.synchronize()
+        assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+
+
+def test_refusals(ccr_mod):
+    import ctypes
+
+    import torch
+    bad = ccr_mod.CCR_ERR_INVALID_ARG
+    x = torch.ones(8, 16, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(2, 24, 16, dtype=torch.bfloat16, device="cuda")
+    y = torch.full((8, 24), 7.0, dtype=torch.bfloat16, device="cuda")
+    ecnt = np.array([[5, 3]], np.int64)
+    lib = ccr_mod._lib
+    with ccr_mod.Context(0) as c:
+        def raw(px=x.data_ptr(), pw=w.data_ptr(), py=y.data_ptr(), counts=ecnt, R=1, E=2, H=16, F=24, dt=1):
+            one = lambda p: (ctypes.c_void_p * 1)(p)
+            return lib.ccr_moe_experts(c.handle, one(px), one(pw), counts.ctypes.data, R, E, H, F, dt,
+                                       one(py), None)
+
+        for kw, word in [(dict(px=0), "NULL"), (dict(px=x.data_ptr() + 2), "aligned"),
+                         (dict(counts=np.array([[5, -1]], np.int64)), "< 0"),
+                         (dict(counts=np.array([[5, 1 << 30]], np.int64)), "past the end"),
+                         (dict(H=12), "16 bytes"), (dict(F=1 << 21), "F ="), (dict(H=0), "H ="),
+                         (dict(dt=2), "dtype"), (dict(R=0), "R"), (dict(R=2, E=3), "R"),
+                         (dict(py=x.data_ptr()), "overlap")]:
+            assert raw(**kw) == bad and word in ccr_mod.ccr_last_error(), (kw, ccr_mod.ccr_last_error())
+        assert raw(counts=np.array([[1 << 31, 0]], np.int64)) == ccr_mod.CCR_ERR_UNSUPPORTED
+        torch.cuda.synchronize()
+        assert bool((y == 7.0).all())
+        with pytest.raises(TypeError):
+            ccr_mod.ccr_moe_experts(c, [x.float()], [w], ecnt, [y])
+        with pytest.raises(ValueError):
+            ccr_mod.ccr_moe_experts(c, [x[:7]], [w], ecnt, [y])
+        with pytest.raises(ValueError):
+            ccr_mod.ccr_moe_experts(c, [x], [w.transpose(1, 2)], ecnt, [y])
+        with pytest.raises(ValueError):
+            ccr_mod.ccr_moe_experts(c, [x], [w], ecnt[0], [y])
+        with pytest.raises(ccr_mod.CcrError):  # bf16 gradients of fp32 rows
+            ccr_mod.ccr_moe_experts_wgrad(c, [x.float()], [y.float()], ecnt, [w.clone()])

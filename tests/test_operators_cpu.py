@@ -1,0 +1,72 @@
+"""Host-side refusals of the experts' products, the gated sum and the gradient
+calls: what the binding and the C entries turn away before any device is
+touched.  No GPU is used."""
+import types
+
+import numpy as np
+import pytest
+import torch
+
+import collective_communication_reduce_amd as ccr
+
+CTX = types.SimpleNamespace(device=0, handle=None)
+BF16 = torch.bfloat16
+
+
+def test_a_null_context_is_refused():
+    n = np.zeros((1, 2), np.int64).ctypes.data
+    lib = ccr._lib
+    calls = [lib.ccr_moe_experts(None, None, None, n, 1, 2, 8, 8, 1, None, None),
+             lib.ccr_moe_experts_dgrad(None, None, None, n, 1, 2, 8, 8, 1, None, None),
+             lib.ccr_moe_experts_wgrad(None, None, None, n, 1, 2, 8, 8, 1, 0, 0, None, None),
+             lib.ccr_moe_gate_sum(None, None, None, None, 1, 1, 2, 1, 8, 1, 0, None, None),
+             lib.ccr_moe_gate_sum_bwd(None, None, None, None, None, 1, 1, 2, 1, 8, 1, 0, None, None, None),
+             lib.ccr_grad_norm(None, None, None, None, 0, None, None, None),
+             lib.ccr_grad_clip(None, None, None, None, None, 0, 1.0, None, None, None)]
+    assert calls == [ccr.CCR_ERR_INVALID_ARG] * len(calls)
+    assert "ctx" in ccr.ccr_last_error()
+    assert lib.ccr_moe_experts_wgrad(None, None, None, n, 1, 2, 8, 8, 1, 0, 2, None, None) == \
+        ccr.CCR_ERR_INVALID_ARG
+    assert "accumulate" in ccr.ccr_last_error()
+
+
+def test_host_tensors_are_refused():
+    x, w, y = torch.ones(3, 16), torch.ones(2, 8, 16), torch.ones(3, 8)
+    ecnt = [[1, 2]]
+    with pytest.raises(ValueError, match="device tensor"):
+        ccr.ccr_moe_experts(CTX, [x], [w], ecnt, [y])
+    with pytest.raises(ValueError, match="device tensor"):
+        ccr.ccr_moe_experts_dgrad(CTX, [y], [w], ecnt, [x])
+    with pytest.raises(ValueError, match="device tensor"):
+        ccr.ccr_moe_experts_wgrad(CTX, [x], [y], ecnt, [w])
+    rows, logits, topk = torch.ones(3, 2, 8), torch.ones(3, 4), torch.zeros(3, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="device tensor"):
+        ccr.ccr_moe_gate_sum(CTX, [rows], [logits], [topk], [torch.ones(3, 8)])
+    with pytest.raises(ValueError, match="device tensor"):
+        ccr.ccr_grad_norm(CTX, [x], None, None)
+
+
+def test_types_and_shapes_are_refused():
+    x, w, y = torch.ones(3, 16, dtype=BF16), torch.ones(2, 8, 16, dtype=BF16), torch.ones(3, 8, dtype=BF16)
+    with pytest.raises(TypeError):  # operands of two types
+        ccr.ccr_moe_experts(CTX, [x.float()], [w], [[1, 2]], [y])
+    with pytest.raises(TypeError):
+        ccr.ccr_moe_experts(CTX, [x.half()], [w.half()], [[1, 2]], [y.half()])
+    with pytest.raises(ValueError, match="ecnt"):
+        ccr.ccr_moe_experts(CTX, [x], [w], [1, 2], [y])
+    with pytest.raises(ValueError, match="ecnt"):
+        ccr.ccr_moe_experts(CTX, [x] * 2, [w] * 2, [[1, 2, 0], [0, 0, 0]], [y] * 2)
+    with pytest.raises(ValueError, match="buffers"):
+        ccr.ccr_moe_experts(CTX, [x, x], [w], [[1, 2]], [y])
+    with pytest.raises(TypeError):
+        ccr.ccr_grad_clip(CTX, [torch.ones(4).double()], 1.0, None, None)
+    with pytest.raises(ValueError, match="norm"):
+        ccr.ccr_moe_gate_sum(CTX, [], [], [], [], norm="some")
+
+
+def test_work_constant_matches_the_header():
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(ccr.__file__)))
+    text = open(os.path.join(root, "include", "ccr.h")).read()
+    assert int(re.search(r"#define CCR_GRAD_WORK (\d+)", text).group(1)) == ccr.CCR_GRAD_WORK
