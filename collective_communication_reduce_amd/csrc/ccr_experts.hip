@@ -271,32 +271,217 @@ __global__ __launch_bounds__(WM * WN * 64) void experts_kernel(const ExpertTable
   }
 }
 
+// ------------------------------------------------------------- large tiles
+// bf16 products of 256 x 256 tiles: four waves, one to a SIMD, each with a
+// 128 x 128 part of the tile in its accumulators.  Per K-step of 64 a wave
+// reads 32 KiB from LDS for 128 MFMAs.
+//
+// Two LDS buffers of one K-step each, two register sets of half a step each:
+// while a half's products run, the other half's fragments are read, and while
+// the second half's run, the loads of the step after the next go out into the
+// buffer just read empty.  So loads have a whole K-step to arrive, and there
+// is one barrier per K-step, in its middle.
+//
+// The loads are written in assembly (they have no result register, only LDS)
+// because the compiler would otherwise wait for all of them before any later
+// LDS read.
+__device__ __forceinline__ void load_lds(uint32_t lds, uint32_t off, const char* base) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               ::"s"(lds), "v"(off), "s"(base) : "memory");
+}
+__device__ __forceinline__ void load_lds(uint32_t lds, const char* p) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               ::"s"(lds), "v"(p) : "memory");
+}
+
+// D += a b^T with D held in accumulation registers.  Written in assembly
+// because all 256 of them are accumulators here, which the compiler's own
+// allocation mixes with the fragments and moves about in the loop.  No two
+// products in a row touch the same D, so no wait states are due between them;
+// drain() provides those before D is read.
+__device__ __forceinline__ void mma_acc(u32x4 a, u32x4 b, f32x4& d) {
+  asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(d) : "v"(a), "v"(b));
+}
+__device__ __forceinline__ void drain(f32x4* d) {
+  asm volatile("s_nop 15\n\ts_nop 15"
+               : "+a"(d[0]), "+a"(d[1]), "+a"(d[2]), "+a"(d[3]), "+a"(d[4]), "+a"(d[5]), "+a"(d[6]),
+                 "+a"(d[7]));
+}
+
+template <ExpertOp OP, int OS>
+__global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable tab, const ExpertShape sh) {
+  constexpr int ES = 2, BM = 256, BN = 256, NT = 256, T = 8;
+  constexpr bool kACol = OP == ExpertOp::kWgrad;
+  constexpr bool kBCol = OP != ExpertOp::kProduct;
+  constexpr int kABytes = BM * 128, kBuf = (BM + BN) * 128;
+  using LoadA = Loader<ES, BM, kACol, NT>;
+  using LoadB = Loader<ES, BN, kBCol, NT>;
+  __shared__ __align__(1024) char lds[2 * kBuf];
+  const int t = xcd_tile(blockIdx.x, gridDim.x);
+  const int gi = __builtin_amdgcn_readfirstlane(group_of(tab, t));
+  const ExpertGroup g = tab.g[gi];
+  const int64_t M = OP == ExpertOp::kWgrad ? sh.F : g.rows;
+  const int64_t N = OP == ExpertOp::kProduct ? sh.F : sh.H;
+  const int64_t C = OP == ExpertOp::kProduct ? sh.H : OP == ExpertOp::kDgrad ? sh.F : g.rows;
+  const int mt = (int)((M + BM - 1) / BM);
+  const int in = t - tab.tile0[gi];
+  const int64_t m0 = (int64_t)(in % mt) * BM, n0 = (int64_t)(in / mt) * BN;
+  const int64_t lda = (OP == ExpertOp::kProduct ? sh.H : sh.F) * ES;
+  const int64_t ldb = sh.H * ES;
+  const int l = threadIdx.x & 63;
+  if (OP == ExpertOp::kWgrad && C == 0) {  // an expert without a row
+    for (int i = threadIdx.x; i < BM * (BN / 4); i += NT) {
+      const int64_t m = m0 + i / (BN / 4), n = n0 + i % (BN / 4) * 4;
+      if (m < M && n < N) store4<OS>(g.c + (m * N + n) * OS, f32x4{0, 0, 0, 0}, sh.add);
+    }
+    return;
+  }
+  LoadA la;
+  LoadB lb;
+  la.init(g.a, lda, m0, M);
+  lb.init(g.b, ldb, n0, N);
+  const int nk = (int)((C + kStep<ES> - 1) / kStep<ES>);
+  const int rest = (int)(C - (int64_t)(nk - 1) * kStep<ES>);
+  f32x4 acc[T][T];
+#pragma unroll
+  for (int i = 0; i < T; i++)
+#pragma unroll
+    for (int j = 0; j < T; j++) acc[i][j] = f32x4{0, 0, 0, 0};
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = (w >> 1) * 128, wn = (w & 1) * 128;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(CCR_LDS char*)lds + w * 1024;
+
+  // K-step 0 is the partial one (rest values, then zeros), so that every later
+  // step is whole: step s > 0 starts at k = rest + 64 (s - 1).
+  const char* pa = la.base + (kACol ? rest * la.ld : rest * ES);
+  const char* pb = lb.base + (kBCol ? rest * lb.ld : rest * ES);
+  const int64_t da = kACol ? kStep<ES> * la.ld : 128, db = kBCol ? kStep<ES> * lb.ld : 128;
+  constexpr int kLoads = LoadA::kLoads + LoadB::kLoads;
+  auto load_first = [&]() {
+    const char* zero = reinterpret_cast<const char*>(&zero_vector);
+#pragma unroll
+    for (int i = 0; i < LoadA::kLoads; i++)
+      load_lds(lds0 + i * NT * 16, la.k[i] < rest ? la.base + la.off[i] : zero);
+#pragma unroll
+    for (int i = 0; i < LoadB::kLoads; i++)
+      load_lds(lds0 + kABytes + i * NT * 16, lb.k[i] < rest ? lb.base + lb.off[i] : zero);
+  };
+  // load i (a's, then b's) of the step at pa, pb
+  auto load = [&](int i, uint32_t to) {
+    if (i < LoadA::kLoads) load_lds(to + i * NT * 16, (uint32_t)la.off[i], pa);
+    else load_lds(to + kABytes + (i - LoadA::kLoads) * NT * 16, (uint32_t)lb.off[i - LoadA::kLoads], pb);
+  };
+
+  u32x4 a[2][T], b[2][T];
+  // fragment i of half h from the buffer at cur: b's, then a's
+  auto read = [&](int i, int h, const char* cur) {
+    if (i < T) b[h][i] = fragment<ES, BN, kBCol>(cur + kABytes, wn + i * 16, h);
+    else a[h][i - T] = fragment<ES, BM, kACol>(cur, wm + (i - T) * 16, h);
+  };
+
+  {
+    load_first();
+    if (nk > 1) {
+#pragma unroll
+      for (int i = 0; i < kLoads; i++) load(i, lds0 + kBuf);
+      pa += da;
+      pb += db;
+      asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
+      static_assert(kLoads == 16, "the second step's loads may be in flight");
+    } else {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    asm volatile("s_barrier" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 2 * T; i++) read(i, 0, lds);
+    int cur = 0;  // byte offset of step s's buffer
+    int s = 0;
+#pragma unroll 1
+    do {
+#pragma unroll
+      for (int i = 0; i < T; i++) {
+        if (i < 6) {
+#pragma unroll
+          for (int x = 0; x < 3; x++)
+            if (i * 3 + x < 2 * T) read(i * 3 + x, 1, lds + cur);
+        }
+#pragma unroll
+        for (int j = 0; j < T; j++) mma_acc(b[0][j], a[0][i], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // step s is read by every wave; step s + 1 is in LDS
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      const uint32_t to = lds0 + cur;
+      cur ^= kBuf;
+      const bool more = s + 2 < nk;
+#pragma unroll
+      for (int i = 0; i < T; i++) {
+        // after the last step this reads what the buffer held before; unused
+        if (i < 6) {
+#pragma unroll
+          for (int x = 0; x < 3; x++)
+            if (i * 3 + x < 2 * T) read(i * 3 + x, 0, lds + cur);
+        }
+        if (more) {
+#pragma unroll
+          for (int x = 0; x < kLoads / T; x++) load(i * (kLoads / T) + x, to);
+        }
+#pragma unroll
+        for (int j = 0; j < T; j++) mma_acc(b[1][j], a[1][i], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      pa += da;
+      pb += db;
+    } while (++s < nk);
+    drain(acc[T - 1]);
+  }
+
+#pragma unroll
+  for (int i = 0; i < T; i++) {
+    const int64_t m = m0 + wm + i * 16 + (l & 15);
+#pragma unroll
+    for (int j = 0; j < T; j++) {
+      asm volatile("" : "+a"(acc[i][j]));  // read out row by row, not all at once
+      const int64_t n = n0 + wn + j * 16 + (l >> 4) * 4;
+      if (m < M && n < N) store4<OS>(g.c + (m * N + n) * OS, acc[i][j], sh.add);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
 template <ExpertOp OP, int ES, int OS>
-hipError_t launch_as(const ExpertTable& tab, const ExpertShape& sh, int tiles, hipStream_t stream) {
+hipError_t launch_as(const ExpertTable& tab, const ExpertShape& sh, ExpertTile tile, int tiles,
+                     hipStream_t stream) {
+  if constexpr (ES == 2)
+    if (tile.m == 256) {
+      experts_big_kernel<OP, OS><<<(unsigned)tiles, 256, 0, stream>>>(tab, sh);
+      return hipGetLastError();
+    }
   experts_kernel<OP, ES, OS, 128, 128, 2, 2><<<(unsigned)tiles, 256, 0, stream>>>(tab, sh);
   return hipGetLastError();
 }
 
 }  // namespace
 
-ExpertTile expert_tile(ExpertOp, int, const ExpertShape&, int64_t, int64_t) {
+ExpertTile expert_tile(ExpertOp op, int es, const ExpertShape& sh, int64_t max_rows, int64_t rows) {
+  if (es == 2 && rows >= 4096) return ExpertTile{256, 256};
   return ExpertTile{128, 128};
 }
 
 hipError_t launch_experts(ExpertOp op, int es, int os, const ExpertTable& tab, const ExpertShape& sh,
-                          ExpertTile, int tiles, hipStream_t stream) {
+                          ExpertTile tile, int tiles, hipStream_t stream) {
   if (tiles <= 0) return hipSuccess;
   switch (op) {
     case ExpertOp::kProduct:
-      return es == 4 ? launch_as<ExpertOp::kProduct, 4, 4>(tab, sh, tiles, stream)
-                     : launch_as<ExpertOp::kProduct, 2, 2>(tab, sh, tiles, stream);
+      return es == 4 ? launch_as<ExpertOp::kProduct, 4, 4>(tab, sh, tile, tiles, stream)
+                     : launch_as<ExpertOp::kProduct, 2, 2>(tab, sh, tile, tiles, stream);
     case ExpertOp::kDgrad:
-      return es == 4 ? launch_as<ExpertOp::kDgrad, 4, 4>(tab, sh, tiles, stream)
-                     : launch_as<ExpertOp::kDgrad, 2, 2>(tab, sh, tiles, stream);
+      return es == 4 ? launch_as<ExpertOp::kDgrad, 4, 4>(tab, sh, tile, tiles, stream)
+                     : launch_as<ExpertOp::kDgrad, 2, 2>(tab, sh, tile, tiles, stream);
     default:
-      if (es == 4) return launch_as<ExpertOp::kWgrad, 4, 4>(tab, sh, tiles, stream);
-      return os == 4 ? launch_as<ExpertOp::kWgrad, 2, 4>(tab, sh, tiles, stream)
-                     : launch_as<ExpertOp::kWgrad, 2, 2>(tab, sh, tiles, stream);
+      if (es == 4) return launch_as<ExpertOp::kWgrad, 4, 4>(tab, sh, tile, tiles, stream);
+      return os == 4 ? launch_as<ExpertOp::kWgrad, 2, 4>(tab, sh, tile, tiles, stream)
+                     : launch_as<ExpertOp::kWgrad, 2, 2>(tab, sh, tile, tiles, stream);
   }
 }
 
