@@ -34,22 +34,24 @@ using dev::u32x4;
 // Source of the lanes that lie past the end of the contraction.
 __device__ const u32x4 zero_vector = {0, 0, 0, 0};
 
-// What one K-step of a tile holds of one operand, 128 bytes of K per row:
-// 64 bf16 or 32 fp32.
-template <int ES>
-constexpr int kStep = 128 / ES;
-
-// LDS image of an operand tile of X rows (the tile's m or n) by one K-step,
-// in 16-byte vectors.  Loads go straight from memory to LDS, which fixes each
-// lane's LDS place (its wave's base + 16 x lane), so the bank swizzle is
-// applied to the address a lane reads from.
+// LDS image of an operand tile of X rows (the tile's m or n) by one K-step of
+// KB bytes per row (128: 64 bf16 or 32 fp32; 64: half of that), in 16-byte
+// vectors.  Loads go straight from memory to LDS, which fixes each lane's LDS
+// place (its wave's base + 16 x lane), so the bank swizzle is applied to the
+// address a lane reads from.
 //
-// Row image (K contiguous in memory): X rows of 8 vectors; vector c of row r
-// sits at c ^ ((r >> 1) & 7), so 16 lanes that read the same vector of 16
-// consecutive rows touch all 64 banks once.
-// Column image (the tile's X contiguous): kStep rows of X / (16 / ES)
-// vectors; vector c of row k sits at c ^ swz(k), which spreads the rows that
-// one transposing read touches over the banks.
+// Row image (K contiguous in memory): X rows of KB / 16 vectors; vector c of
+// row r sits at c ^ row_swz(r).  A 16-byte read serves 16 lanes at a time, of
+// two 16-lane groups (0-3, 12-15 of the one, 4-11 of the other): the swizzle
+// puts the 16 vectors they ask for, of 16 rows, on all 64 banks once.
+// Column image (the tile's X contiguous): KB / ES rows of X / (16 / ES)
+// vectors; vector c of row k sits at c ^ col_swz(k), which spreads the rows
+// that one transposing read touches over the banks.
+template <int KB>
+__device__ __forceinline__ int row_swz(int r) {
+  if constexpr (KB == 128) return (r >> 1) & 7;
+  else return (r >> 3 & 1) * 3;
+}
 template <int ES, int X>
 __device__ __forceinline__ int col_swz(int k) {
   constexpr int kPerRow = X * ES / 16;
@@ -57,12 +59,13 @@ __device__ __forceinline__ int col_swz(int k) {
   else return (((k >> 2) & 3) << 2) & (kPerRow - 1);
 }
 
-// One operand's loads of a K-step: NT threads bring X x 128 bytes.  Lanes
-// past the tile's last row (or column) read a row inside it: their products
-// are not stored.  Lanes past the contraction's end read zeros.
-template <int ES, int X, bool COL, int NT>
+// One operand's loads of a K-step: NT threads bring X x KB bytes.  Lanes past
+// the tile's last row (or column) read a row inside it: their products are
+// not stored.  Lanes past the contraction's end read zeros.
+template <int ES, int X, bool COL, int KB, int NT>
 struct Loader {
-  static constexpr int kLoads = X * 8 / NT;
+  static constexpr int kLoads = X * (KB / 16) / NT;
+  static constexpr int kStep = KB / ES;        // k values per step
   static constexpr int kPerRow = X * ES / 16;  // vectors per row of a column image
   const char* base;  // the tile's first row (row image) or column (column image)
   int64_t ld;        // bytes from one memory row to the next
@@ -84,17 +87,20 @@ struct Loader {
         off[i] = (int)(kr * ld) + (c * (16 / ES) < left ? c * 16 : 0);
         k[i] = kr;
       } else {
-        const int r = q >> 3;
-        const int c = (q & 7) ^ ((r >> 1) & 7);
+        const int r = q / (KB / 16);
+        const int c = (q % (KB / 16)) ^ row_swz<KB>(r);
         off[i] = (int)((r < left ? r : left - 1) * ld) + c * 16;
         k[i] = c * (16 / ES);
       }
     }
   }
 
+  // bytes from one K-step to the next
+  __device__ __forceinline__ int64_t stride() const { return COL ? kStep * ld : KB; }
+
   // K-step s of nk; `rest` = k values the last step holds.
   __device__ __forceinline__ void issue(char* lds, int64_t s, int rest, bool last) const {
-    const char* from = base + (COL ? s * kStep<ES> * ld : s * 128);
+    const char* from = base + s * stride();
     char* const to = lds + (threadIdx.x & ~63) * 16;
 #pragma unroll
     for (int i = 0; i < kLoads; i++) {
@@ -106,27 +112,30 @@ struct Loader {
   }
 };
 
-// A 16-row fragment of half a K-step: 4 registers per lane.  Lane l holds row
-// l % 16 and, with g = l / 16, k = 32 h + 8 g + (0..7) in bf16 or
-// k = 16 h + 4 g + (0..3) in fp32.  Both operands use the same k for the same
-// lane and register, which is all a product needs.
-template <int ES, int X, bool COL>
+// Half of a bf16 fragment from a column image: a transposing read of 4 k x 16
+// columns per 16 lanes.  Lane j gives the address of 4 columns of row j / 4 and
+// receives column j of the 4 rows.
+template <int X>
+__device__ __forceinline__ s16x4 fragment_half(const char* lds, int x0, int h, int u) {
+  const int l = threadIdx.x & 63, j = l & 15, g = l >> 4;
+  const int k = h * 32 + g * 8 + u * 4 + (j >> 2);
+  const int c = (x0 >> 3) + ((j & 3) >> 1);
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (CCR_LDS s16x4*)(lds + k * (X * 2) + ((c ^ col_swz<2, X>(k)) << 4) + (j & 1) * 8));
+}
+
+// A 16-row fragment of 64 bytes of K (part h of the step): 4 registers per
+// lane.  Lane l holds row l % 16 and, with g = l / 16, k = 32 h + 8 g + (0..7)
+// in bf16 or k = 16 h + 4 g + (0..3) in fp32.  Both operands use the same k for
+// the same lane and register, which is all a product needs.
+template <int ES, int X, bool COL, int KB>
 __device__ __forceinline__ u32x4 fragment(const char* lds, int x0, int h) {
   const int l = threadIdx.x & 63, j = l & 15, g = l >> 4;
   if constexpr (!COL) {
     const int r = x0 + j;
-    return *reinterpret_cast<const u32x4*>(lds + r * 128 + (((h * 4 + g) ^ ((r >> 1) & 7)) << 4));
+    return *reinterpret_cast<const u32x4*>(lds + r * KB + (((h * 4 + g) ^ row_swz<KB>(r)) << 4));
   } else if constexpr (ES == 2) {
-    // two transposing reads of 4 k x 16 columns per 16 lanes: lane j gives the
-    // address of 4 columns of row j / 4 and receives column j of the 4 rows
-    s16x4 v[2];
-#pragma unroll
-    for (int u = 0; u < 2; u++) {
-      const int k = h * 32 + g * 8 + u * 4 + (j >> 2);
-      const int c = (x0 >> 3) + ((j & 3) >> 1);
-      v[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (CCR_LDS s16x4*)(lds + k * (X * 2) + ((c ^ col_swz<ES, X>(k)) << 4) + (j & 1) * 8));
-    }
+    const s16x4 v[2] = {fragment_half<X>(lds, x0, h, 0), fragment_half<X>(lds, x0, h, 1)};
     u32x4 r;
     __builtin_memcpy(&r, v, 16);
     return r;
@@ -191,6 +200,17 @@ __device__ __forceinline__ int group_of(const ExpertTable& tab, int t) {
   return n - 1;
 }
 
+// Tile `in` of a group of mt x nt tiles: strips of 8 tiles in m, column after
+// column, so the 32 tiles that an XCD's compute units hold at a time are about
+// 8 x 4 and share their operands in its L2.
+__device__ __forceinline__ void tile_at(int in, int mt, int nt, int* m, int* n) {
+  constexpr int kStrip = 8;
+  const int strip = in / (kStrip * nt), r = in - strip * kStrip * nt;
+  const int left = mt - strip * kStrip, h = left < kStrip ? left : kStrip;
+  *n = r / h;
+  *m = strip * kStrip + (r - *n * h);
+}
+
 // OP as in the table above.  Tile BM x BN of the output, WM x WN waves.
 template <ExpertOp OP, int ES, int OS, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM * WN * 64) void experts_kernel(const ExpertTable tab,
@@ -207,17 +227,19 @@ __global__ __launch_bounds__(WM * WN * 64) void experts_kernel(const ExpertTable
   const int64_t M = OP == ExpertOp::kWgrad ? sh.F : g.rows;
   const int64_t N = OP == ExpertOp::kProduct ? sh.F : sh.H;
   const int64_t C = OP == ExpertOp::kProduct ? sh.H : OP == ExpertOp::kDgrad ? sh.F : g.rows;
-  const int mt = (int)((M + BM - 1) / BM);
-  const int in = t - tab.tile0[gi];
-  const int64_t m0 = (int64_t)(in % mt) * BM, n0 = (int64_t)(in / mt) * BN;
+  int tm, tn;
+  tile_at(t - tab.tile0[gi], (int)((M + BM - 1) / BM), (int)((N + BN - 1) / BN), &tm, &tn);
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const int64_t lda = (OP == ExpertOp::kProduct ? sh.H : sh.F) * ES;
   const int64_t ldb = sh.H * ES;
-  Loader<ES, BM, kACol, NT> la;
-  Loader<ES, BN, kBCol, NT> lb;
+  constexpr int KB = 128;
+  Loader<ES, BM, kACol, KB, NT> la;
+  Loader<ES, BN, kBCol, KB, NT> lb;
   la.init(g.a, lda, m0, M);
   lb.init(g.b, ldb, n0, N);
-  const int64_t nk = (C + kStep<ES> - 1) / kStep<ES>;
-  const int rest = (int)(C - (nk - 1) * kStep<ES>);
+  constexpr int kStep = KB / ES;
+  const int64_t nk = (C + kStep - 1) / kStep;
+  const int rest = (int)(C - (nk - 1) * kStep);
   f32x4 acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; i++)
@@ -239,9 +261,9 @@ __global__ __launch_bounds__(WM * WN * 64) void experts_kernel(const ExpertTable
 #pragma unroll
     for (int h = 0; h < 2; h++) {
 #pragma unroll
-      for (int i = 0; i < TM; i++) a[h][i] = fragment<ES, BM, kACol>(cur, wm + i * 16, h);
+      for (int i = 0; i < TM; i++) a[h][i] = fragment<ES, BM, kACol, KB>(cur, wm + i * 16, h);
 #pragma unroll
-      for (int j = 0; j < TN; j++) b[h][j] = fragment<ES, BN, kBCol>(cur + kABytes, wn + j * 16, h);
+      for (int j = 0; j < TN; j++) b[h][j] = fragment<ES, BN, kBCol, KB>(cur + kABytes, wn + j * 16, h);
     }
     if (s + 1 < nk) {
       char* next = lds + ((s + 1) & 1) * kBuf;
@@ -273,14 +295,15 @@ __global__ __launch_bounds__(WM * WN * 64) void experts_kernel(const ExpertTable
 
 // ------------------------------------------------------------- large tiles
 // bf16 products of 256 x 256 tiles: four waves, one to a SIMD, each with a
-// 128 x 128 part of the tile in its accumulators.  Per K-step of 64 a wave
-// reads 32 KiB from LDS for 128 MFMAs.
+// 128 x 128 part of the tile in its accumulators.  Per K-step of 32 a wave
+// reads 16 KiB from LDS for 64 MFMAs.
 //
-// Two LDS buffers of one K-step each, two register sets of half a step each:
-// while a half's products run, the other half's fragments are read, and while
-// the second half's run, the loads of the step after the next go out into the
-// buffer just read empty.  So loads have a whole K-step to arrive, and there
-// is one barrier per K-step, in its middle.
+// Four LDS buffers of one K-step each, two register sets.  While step s runs
+// from one set, step s + 1 is read into the other, and the loads of step s + 4
+// go out into the buffer that step s was read from, one load to eight MFMAs,
+// so that the loads, the LDS reads and the products each keep their unit busy
+// and none waits in another's queue.  A step's loads have two whole steps to
+// arrive; one barrier per step.
 //
 // The loads are written in assembly (they have no result register, only LDS)
 // because the compiler would otherwise wait for all of them before any later
@@ -293,6 +316,28 @@ __device__ __forceinline__ void load_lds(uint32_t lds, const char* p) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                ::"s"(lds), "v"(p) : "memory");
 }
+
+// A fragment as fragment() gives it, read in parts.
+template <bool COL>
+struct Frag {
+  static constexpr int kReads = COL ? 2 : 1;
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  u32x4 whole;
+  u32x2 half[2];
+
+  template <int X, int KB>
+  __device__ __forceinline__ void read(const char* lds, int x0, int part) {
+    if constexpr (!COL) {
+      whole = fragment<2, X, false, KB>(lds, x0, 0);
+    } else {
+      half[part] = __builtin_bit_cast(u32x2, fragment_half<X>(lds, x0, 0, part));
+    }
+  }
+  __device__ __forceinline__ u32x4 v() const {
+    if constexpr (COL) return __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3);
+    else return whole;
+  }
+};
 
 // D += a b^T with D held in accumulation registers.  Written in assembly
 // because all 256 of them are accumulators here, which the compiler's own
@@ -310,22 +355,22 @@ __device__ __forceinline__ void drain(f32x4* d) {
 
 template <ExpertOp OP, int OS>
 __global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable tab, const ExpertShape sh) {
-  constexpr int ES = 2, BM = 256, BN = 256, NT = 256, T = 8;
+  constexpr int ES = 2, BM = 256, BN = 256, NT = 256, T = 8, KB = 64;
   constexpr bool kACol = OP == ExpertOp::kWgrad;
   constexpr bool kBCol = OP != ExpertOp::kProduct;
-  constexpr int kABytes = BM * 128, kBuf = (BM + BN) * 128;
-  using LoadA = Loader<ES, BM, kACol, NT>;
-  using LoadB = Loader<ES, BN, kBCol, NT>;
-  __shared__ __align__(1024) char lds[2 * kBuf];
+  constexpr int kABytes = BM * KB, kBuf = (BM + BN) * KB, kBufs = 4;
+  using LoadA = Loader<ES, BM, kACol, KB, NT>;
+  using LoadB = Loader<ES, BN, kBCol, KB, NT>;
+  __shared__ __align__(1024) char lds[kBufs * kBuf];
   const int t = xcd_tile(blockIdx.x, gridDim.x);
   const int gi = __builtin_amdgcn_readfirstlane(group_of(tab, t));
   const ExpertGroup g = tab.g[gi];
   const int64_t M = OP == ExpertOp::kWgrad ? sh.F : g.rows;
   const int64_t N = OP == ExpertOp::kProduct ? sh.F : sh.H;
   const int64_t C = OP == ExpertOp::kProduct ? sh.H : OP == ExpertOp::kDgrad ? sh.F : g.rows;
-  const int mt = (int)((M + BM - 1) / BM);
-  const int in = t - tab.tile0[gi];
-  const int64_t m0 = (int64_t)(in % mt) * BM, n0 = (int64_t)(in / mt) * BN;
+  int tm, tn;
+  tile_at(t - tab.tile0[gi], (int)((M + BM - 1) / BM), (int)((N + BN - 1) / BN), &tm, &tn);
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const int64_t lda = (OP == ExpertOp::kProduct ? sh.H : sh.F) * ES;
   const int64_t ldb = sh.H * ES;
   const int l = threadIdx.x & 63;
@@ -340,101 +385,140 @@ __global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable t
   LoadB lb;
   la.init(g.a, lda, m0, M);
   lb.init(g.b, ldb, n0, N);
-  const int nk = (int)((C + kStep<ES> - 1) / kStep<ES>);
-  const int rest = (int)(C - (int64_t)(nk - 1) * kStep<ES>);
+  constexpr int kStep = LoadA::kStep;
+  // The steps run in pairs: step 0 holds the contraction's odd end (`rest`
+  // values, then zeros), step 1 is whole, or all zeros where the steps are odd
+  // in number, and every later one is whole.
+  const int whole = (int)((C - 1) / kStep);
+  const int rest = (int)(C - (int64_t)whole * kStep);
+  const bool blank = (whole & 1) == 0;
+  const int nk = whole + 1 + (blank ? 1 : 0);
   f32x4 acc[T][T];
-#pragma unroll
-  for (int i = 0; i < T; i++)
-#pragma unroll
-    for (int j = 0; j < T; j++) acc[i][j] = f32x4{0, 0, 0, 0};
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = (w >> 1) * 128, wn = (w & 1) * 128;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(CCR_LDS char*)lds + w * 1024;
 
-  // K-step 0 is the partial one (rest values, then zeros), so that every later
-  // step is whole: step s > 0 starts at k = rest + 64 (s - 1).
   const char* pa = la.base + (kACol ? rest * la.ld : rest * ES);
   const char* pb = lb.base + (kBCol ? rest * lb.ld : rest * ES);
-  const int64_t da = kACol ? kStep<ES> * la.ld : 128, db = kBCol ? kStep<ES> * lb.ld : 128;
+  const int64_t da = la.stride(), db = lb.stride();
   constexpr int kLoads = LoadA::kLoads + LoadB::kLoads;
-  auto load_first = [&]() {
+  static_assert(kLoads == T, "one load to a row of products");
+  // a step's loads from the operands' beginning, zeros from value `until` on
+  auto load_part = [&](int until, uint32_t to) {
     const char* zero = reinterpret_cast<const char*>(&zero_vector);
 #pragma unroll
     for (int i = 0; i < LoadA::kLoads; i++)
-      load_lds(lds0 + i * NT * 16, la.k[i] < rest ? la.base + la.off[i] : zero);
+      load_lds(to + i * NT * 16, la.k[i] < until ? la.base + la.off[i] : zero);
 #pragma unroll
     for (int i = 0; i < LoadB::kLoads; i++)
-      load_lds(lds0 + kABytes + i * NT * 16, lb.k[i] < rest ? lb.base + lb.off[i] : zero);
+      load_lds(to + kABytes + i * NT * 16, lb.k[i] < until ? lb.base + lb.off[i] : zero);
   };
-  // load i (a's, then b's) of the step at pa, pb
-  auto load = [&](int i, uint32_t to) {
-    if (i < LoadA::kLoads) load_lds(to + i * NT * 16, (uint32_t)la.off[i], pa);
-    else load_lds(to + kABytes + (i - LoadA::kLoads) * NT * 16, (uint32_t)lb.off[i - LoadA::kLoads], pb);
+  // A step's loads, one at a time: its LDS place (in m0, advanced from one
+  // load to the next), then load i (a's, then b's) of the step at pa, pb.
+  static_assert(kABytes == LoadA::kLoads * NT * 16, "b's first load follows a's last");
+  auto place = [&](int i, uint32_t to) {
+    if (i == 0) asm volatile("s_mov_b32 m0, %0" ::"s"(to));
+    else asm volatile("s_add_u32 m0, m0, %0" ::"n"(NT * 16) : "scc");
+  };
+  auto load = [&](int i) {
+    if (i < LoadA::kLoads)
+      asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(la.off[i]), "s"(pa) : "memory");
+    else
+      asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(lb.off[i - LoadA::kLoads]), "s"(pb) : "memory");
   };
 
-  u32x4 a[2][T], b[2][T];
-  // fragment i of half h from the buffer at cur: b's, then a's
-  auto read = [&](int i, int h, const char* cur) {
-    if (i < T) b[h][i] = fragment<ES, BN, kBCol>(cur + kABytes, wn + i * 16, h);
-    else a[h][i - T] = fragment<ES, BM, kACol>(cur, wm + (i - T) * 16, h);
-  };
-
-  {
-    load_first();
-    if (nk > 1) {
-#pragma unroll
-      for (int i = 0; i < kLoads; i++) load(i, lds0 + kBuf);
-      pa += da;
-      pb += db;
-      asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
-      static_assert(kLoads == 16, "the second step's loads may be in flight");
+  // Fragments are read in units: one LDS read each, two to a fragment from a
+  // column image.
+  constexpr int kUnitsB = T * Frag<kBCol>::kReads, kUnits = kUnitsB + T * Frag<kACol>::kReads;
+  Frag<kACol> a[2][T];
+  Frag<kBCol> b[2][T];
+  auto read = [&](int u, int x, const char* cur) {  // b's first, then a's
+    if (u < kUnitsB) {
+      constexpr int n = Frag<kBCol>::kReads;
+      b[x][u / n].template read<BN, KB>(cur + kABytes, wn + u / n * 16, u % n);
     } else {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      constexpr int n = Frag<kACol>::kReads;
+      a[x][(u - kUnitsB) / n].template read<BM, KB>(cur, wm + (u - kUnitsB) / n * 16, (u - kUnitsB) % n);
     }
-    asm volatile("s_barrier" ::: "memory");
+  };
+
+  load_part(rest, lds0);
+  if (blank) load_part(0, lds0 + kBuf);
+  for (int s = blank ? 2 : 1; s < kBufs && s < nk; s++) {
 #pragma unroll
-    for (int i = 0; i < 2 * T; i++) read(i, 0, lds);
-    int cur = 0;  // byte offset of step s's buffer
-    int s = 0;
-#pragma unroll 1
-    do {
-#pragma unroll
-      for (int i = 0; i < T; i++) {
-        if (i < 6) {
-#pragma unroll
-          for (int x = 0; x < 3; x++)
-            if (i * 3 + x < 2 * T) read(i * 3 + x, 1, lds + cur);
-        }
-#pragma unroll
-        for (int j = 0; j < T; j++) mma_acc(b[0][j], a[0][i], acc[i][j]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      // step s is read by every wave; step s + 1 is in LDS
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      const uint32_t to = lds0 + cur;
-      cur ^= kBuf;
-      const bool more = s + 2 < nk;
-#pragma unroll
-      for (int i = 0; i < T; i++) {
-        // after the last step this reads what the buffer held before; unused
-        if (i < 6) {
-#pragma unroll
-          for (int x = 0; x < 3; x++)
-            if (i * 3 + x < 2 * T) read(i * 3 + x, 0, lds + cur);
-        }
-        if (more) {
-#pragma unroll
-          for (int x = 0; x < kLoads / T; x++) load(i * (kLoads / T) + x, to);
-        }
-#pragma unroll
-        for (int j = 0; j < T; j++) mma_acc(b[1][j], a[1][i], acc[i][j]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      pa += da;
-      pb += db;
-    } while (++s < nk);
-    drain(acc[T - 1]);
+    for (int i = 0; i < kLoads; i++) {
+      place(i, lds0 + s * kBuf);
+      asm volatile("s_nop 0");
+      load(i);
+    }
+    pa += da;
+    pb += db;
   }
+  // the accumulators are cleared while the loads arrive
+#pragma unroll
+  for (int i = 0; i < T; i++)
+#pragma unroll
+    for (int j = 0; j < T; j++) {
+      acc[i][j] = f32x4{0, 0, 0, 0};
+      asm volatile("" : "+a"(acc[i][j]));
+    }
+  if (nk >= kBufs) asm volatile("s_waitcnt vmcnt(16)" ::: "memory");  // all but steps 2 and 3
+  else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  asm volatile("s_barrier" ::: "memory");
+#pragma unroll
+  for (int u = 0; u < kUnits; u++) read(u, 0, lds);
+  int s = 0, cur = 0;  // the step that runs, and the byte offset of its buffer
+  // The last four steps have nothing to load: they bring the last whole step
+  // again (or, where there is none, each operand's first vector) into buffers
+  // that are not read any more.  That keeps the loop without a branch and the
+  // count of loads on their way the same.
+  if (whole == 0) {
+    pa = la.base;
+    pb = lb.base;
+#pragma unroll
+    for (int i = 0; i < LoadA::kLoads; i++) la.off[i] = 0;
+#pragma unroll
+    for (int i = 0; i < LoadB::kLoads; i++) lb.off[i] = 0;
+  } else if (nk <= kBufs) {
+    pa -= da;
+    pb -= db;
+  }
+  auto step = [&](auto set) {
+    constexpr int X = decltype(set)::value;
+    const uint32_t to = lds0 + cur;
+    cur = (cur + kBuf) & (kBufs * kBuf - 1);
+    const char* next = lds + cur;
+#pragma unroll
+    for (int n = 0; n < T * T; n++) {
+      mma_acc(b[X][n % T].v(), a[X][n / T].v(), acc[n / T][n % T]);
+      // Behind each product at most a read or two, or a part of a load: the
+      // next product is issued before this one is done.
+      // (After the last step the reads bring what the buffer held; unused.)
+      constexpr int kReadSlots = 48;
+      if (n < kReadSlots) {
+#pragma unroll
+        for (int u = n * kUnits / kReadSlots; u < (n + 1) * kUnits / kReadSlots; u++) read(u, X ^ 1, next);
+      }
+      if (n % T == T - 3) place(n / T, to);
+      if (n % T == T - 2) load(n / T);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    const bool more = s + kBufs + 1 < nk;
+    pa += more ? da : 0;
+    pb += more ? db : 0;
+    // step s + 1 is read by every wave; step s + 2 is in LDS, s + 3 and s + 4
+    // may be on their way
+    asm volatile("s_waitcnt vmcnt(16) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    s++;
+  };
+  static_assert((kBufs & (kBufs - 1)) == 0, "buffers wrap by a mask");
+#pragma unroll 1
+  do {
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
+  } while (s < nk);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  drain(acc[T - 1]);
 
 #pragma unroll
   for (int i = 0; i < T; i++) {
