@@ -295,15 +295,22 @@ __global__ __launch_bounds__(WM * WN * 64) void experts_kernel(const ExpertTable
 
 // ------------------------------------------------------------- large tiles
 // bf16 products of 256 x 256 tiles: four waves, one to a SIMD, each with a
-// 128 x 128 part of the tile in its accumulators.  Per K-step of 32 a wave
-// reads 16 KiB from LDS for 64 MFMAs.
+// 128 x 128 part of the tile in its accumulators.  Per K-step of 64 a wave
+// reads 32 KiB from LDS for 128 MFMAs.
 //
-// Four LDS buffers of one K-step each, two register sets.  While step s runs
-// from one set, step s + 1 is read into the other, and the loads of step s + 4
-// go out into the buffer that step s was read from, one load to eight MFMAs,
-// so that the loads, the LDS reads and the products each keep their unit busy
-// and none waits in another's queue.  A step's loads have two whole steps to
-// arrive; one barrier per step.
+// All of the CU's LDS is a ring of five 32 KiB slots, each one operand's part
+// of one K-step (whole 128-byte lines of memory).  A step runs in two phases
+// of 32 k: in the first, the fragments of its second half are read; then a
+// barrier, after which its slots are free and the next step's are full; in the
+// second, the fragments of the next step's first half are read.  The loads of
+// the slots set free go out in the second phase and the beginning of the next
+// step's first: b of step s + 2, needed one step later, then a of step s + 3,
+// needed two steps later.
+//
+// With one wave to a SIMD nothing hides an instruction that stalls, so reads
+// and loads are placed one by one between the products.  Measured at 8192^3
+// against reads and loads in groups of three before every eight products:
+// 1283 -> 1433 TFLOP/s (dgrad).
 //
 // The loads are written in assembly (they have no result register, only LDS)
 // because the compiler would otherwise wait for all of them before any later
@@ -326,12 +333,9 @@ struct Frag {
   u32x2 half[2];
 
   template <int X, int KB>
-  __device__ __forceinline__ void read(const char* lds, int x0, int part) {
-    if constexpr (!COL) {
-      whole = fragment<2, X, false, KB>(lds, x0, 0);
-    } else {
-      half[part] = __builtin_bit_cast(u32x2, fragment_half<X>(lds, x0, 0, part));
-    }
+  __device__ __forceinline__ void read(const char* lds, int x0, int h, int part) {
+    if constexpr (!COL) whole = fragment<2, X, false, KB>(lds, x0, h);
+    else half[part] = __builtin_bit_cast(u32x2, fragment_half<X>(lds, x0, h, part));
   }
   __device__ __forceinline__ u32x4 v() const {
     if constexpr (COL) return __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3);
@@ -355,13 +359,14 @@ __device__ __forceinline__ void drain(f32x4* d) {
 
 template <ExpertOp OP, int OS>
 __global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable tab, const ExpertShape sh) {
-  constexpr int ES = 2, BM = 256, BN = 256, NT = 256, T = 8, KB = 64;
+  constexpr int ES = 2, BM = 256, BN = 256, NT = 256, T = 8, KB = 128;
   constexpr bool kACol = OP == ExpertOp::kWgrad;
   constexpr bool kBCol = OP != ExpertOp::kProduct;
-  constexpr int kABytes = BM * KB, kBuf = (BM + BN) * KB, kBufs = 4;
+  constexpr int kSlot = BM * KB, kSlots = 5;
+  static_assert(BM == BN, "both operands fill a slot");
   using LoadA = Loader<ES, BM, kACol, KB, NT>;
   using LoadB = Loader<ES, BN, kBCol, KB, NT>;
-  __shared__ __align__(1024) char lds[kBufs * kBuf];
+  __shared__ __align__(1024) char lds[kSlots * kSlot];
   const int t = xcd_tile(blockIdx.x, gridDim.x);
   const int gi = __builtin_amdgcn_readfirstlane(group_of(tab, t));
   const ExpertGroup g = tab.g[gi];
@@ -386,13 +391,10 @@ __global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable t
   la.init(g.a, lda, m0, M);
   lb.init(g.b, ldb, n0, N);
   constexpr int kStep = LoadA::kStep;
-  // The steps run in pairs: step 0 holds the contraction's odd end (`rest`
-  // values, then zeros), step 1 is whole, or all zeros where the steps are odd
-  // in number, and every later one is whole.
-  const int whole = (int)((C - 1) / kStep);
+  // Step 0 holds the contraction's odd end (`rest` values, then zeros), so that
+  // every later step is whole.
+  const int whole = (int)((C - 1) / kStep), nk = whole + 1;
   const int rest = (int)(C - (int64_t)whole * kStep);
-  const bool blank = (whole & 1) == 0;
-  const int nk = whole + 1 + (blank ? 1 : 0);
   f32x4 acc[T][T];
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = (w >> 1) * 128, wn = (w & 1) * 128;
@@ -401,30 +403,46 @@ __global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable t
   const char* pa = la.base + (kACol ? rest * la.ld : rest * ES);
   const char* pb = lb.base + (kBCol ? rest * lb.ld : rest * ES);
   const int64_t da = la.stride(), db = lb.stride();
-  constexpr int kLoads = LoadA::kLoads + LoadB::kLoads;
-  static_assert(kLoads == T, "one load to a row of products");
-  // a step's loads from the operands' beginning, zeros from value `until` on
-  auto load_part = [&](int until, uint32_t to) {
+  constexpr int kLoads = LoadA::kLoads;  // of one slot
+  static_assert(kLoads == 8 && LoadB::kLoads == 8, "the wait counts below");
+  // The first step's loads, zeros from value `rest` on.
+  {
     const char* zero = reinterpret_cast<const char*>(&zero_vector);
 #pragma unroll
-    for (int i = 0; i < LoadA::kLoads; i++)
-      load_lds(to + i * NT * 16, la.k[i] < until ? la.base + la.off[i] : zero);
+    for (int i = 0; i < kLoads; i++)
+      load_lds(lds0 + i * NT * 16, la.k[i] < rest ? la.base + la.off[i] : zero);
 #pragma unroll
-    for (int i = 0; i < LoadB::kLoads; i++)
-      load_lds(to + kABytes + i * NT * 16, lb.k[i] < until ? lb.base + lb.off[i] : zero);
+    for (int i = 0; i < kLoads; i++)
+      load_lds(lds0 + kSlot + i * NT * 16, lb.k[i] < rest ? lb.base + lb.off[i] : zero);
+  }
+  // Past the last step the loads bring the last whole step again (or, where
+  // there is none, each operand's first vector) into slots that are not read
+  // any more: the loop keeps no branch, and the count of loads on their way
+  // stays the same.
+  int ja = 1, jb = 1;  // the step at pa, pb
+  if (whole == 0) {
+    pa = la.base;
+    pb = lb.base;
+#pragma unroll
+    for (int i = 0; i < kLoads; i++) la.off[i] = lb.off[i] = 0;
+  }
+  auto next_a = [&]() {
+    pa += ja < whole ? da : 0;
+    ja++;
   };
-  // A step's loads, one at a time: its LDS place (in m0, advanced from one
-  // load to the next), then load i (a's, then b's) of the step at pa, pb.
-  static_assert(kABytes == LoadA::kLoads * NT * 16, "b's first load follows a's last");
+  auto next_b = [&]() {
+    pb += jb < whole ? db : 0;
+    jb++;
+  };
+  // A slot's loads, one at a time: the LDS place in m0, then load i.
   auto place = [&](int i, uint32_t to) {
-    if (i == 0) asm volatile("s_mov_b32 m0, %0" ::"s"(to));
-    else asm volatile("s_add_u32 m0, m0, %0" ::"n"(NT * 16) : "scc");
+    asm volatile("s_add_u32 m0, %0, %1" ::"s"(to), "n"(i * NT * 16) : "scc");
   };
-  auto load = [&](int i) {
-    if (i < LoadA::kLoads)
-      asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(la.off[i]), "s"(pa) : "memory");
-    else
-      asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(lb.off[i - LoadA::kLoads]), "s"(pb) : "memory");
+  auto load_a = [&](int i) {
+    asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(la.off[i]), "s"(pa) : "memory");
+  };
+  auto load_b = [&](int i) {
+    asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(lb.off[i]), "s"(pb) : "memory");
   };
 
   // Fragments are read in units: one LDS read each, two to a fragment from a
@@ -432,28 +450,29 @@ __global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable t
   constexpr int kUnitsB = T * Frag<kBCol>::kReads, kUnits = kUnitsB + T * Frag<kACol>::kReads;
   Frag<kACol> a[2][T];
   Frag<kBCol> b[2][T];
-  auto read = [&](int u, int x, const char* cur) {  // b's first, then a's
+  auto read = [&](int u, int h, const char* at_a, const char* at_b) {  // b's first, then a's
     if (u < kUnitsB) {
       constexpr int n = Frag<kBCol>::kReads;
-      b[x][u / n].template read<BN, KB>(cur + kABytes, wn + u / n * 16, u % n);
+      b[h][u / n].template read<BN, KB>(at_b, wn + u / n * 16, h, u % n);
     } else {
       constexpr int n = Frag<kACol>::kReads;
-      a[x][(u - kUnitsB) / n].template read<BM, KB>(cur, wm + (u - kUnitsB) / n * 16, (u - kUnitsB) % n);
+      a[h][(u - kUnitsB) / n].template read<BM, KB>(at_a, wm + (u - kUnitsB) / n * 16, h, (u - kUnitsB) % n);
     }
   };
-
-  load_part(rest, lds0);
-  if (blank) load_part(0, lds0 + kBuf);
-  for (int s = blank ? 2 : 1; s < kBufs && s < nk; s++) {
+  constexpr int kEarlyA = 5;  // loads of a that go out in the second phase
+  auto load_whole = [&](auto& load, uint32_t to, int n) {
 #pragma unroll
-    for (int i = 0; i < kLoads; i++) {
-      place(i, lds0 + s * kBuf);
+    for (int i = 0; i < n; i++) {
+      place(i, to);
       asm volatile("s_nop 0");
       load(i);
     }
-    pa += da;
-    pb += db;
-  }
+  };
+  load_whole(load_a, lds0 + 2 * kSlot, kLoads);
+  next_a();
+  load_whole(load_b, lds0 + 3 * kSlot, kLoads);
+  next_b();
+  load_whole(load_a, lds0 + 4 * kSlot, kEarlyA);
   // the accumulators are cleared while the loads arrive
 #pragma unroll
   for (int i = 0; i < T; i++)
@@ -462,61 +481,71 @@ __global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable t
       acc[i][j] = f32x4{0, 0, 0, 0};
       asm volatile("" : "+a"(acc[i][j]));
     }
-  if (nk >= kBufs) asm volatile("s_waitcnt vmcnt(16)" ::: "memory");  // all but steps 2 and 3
-  else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  asm volatile("s_barrier" ::: "memory");
+  // step 0 is in LDS, step 1 and part of a's step 2 may be on their way
+  asm volatile("s_waitcnt vmcnt(21)\n\ts_barrier" ::: "memory");
+  static_assert(2 * kLoads + kEarlyA == 21, "as waited for");
 #pragma unroll
-  for (int u = 0; u < kUnits; u++) read(u, 0, lds);
-  int s = 0, cur = 0;  // the step that runs, and the byte offset of its buffer
-  // The last four steps have nothing to load: they bring the last whole step
-  // again (or, where there is none, each operand's first vector) into buffers
-  // that are not read any more.  That keeps the loop without a branch and the
-  // count of loads on their way the same.
-  if (whole == 0) {
-    pa = la.base;
-    pb = lb.base;
-#pragma unroll
-    for (int i = 0; i < LoadA::kLoads; i++) la.off[i] = 0;
-#pragma unroll
-    for (int i = 0; i < LoadB::kLoads; i++) lb.off[i] = 0;
-  } else if (nk <= kBufs) {
-    pa -= da;
-    pb -= db;
-  }
-  auto step = [&](auto set) {
-    constexpr int X = decltype(set)::value;
-    const uint32_t to = lds0 + cur;
-    cur = (cur + kBuf) & (kBufs * kBuf - 1);
-    const char* next = lds + cur;
-#pragma unroll
-    for (int n = 0; n < T * T; n++) {
-      mma_acc(b[X][n % T].v(), a[X][n / T].v(), acc[n / T][n % T]);
-      // Behind each product at most a read or two, or a part of a load: the
-      // next product is issued before this one is done.
-      // (After the last step the reads bring what the buffer held; unused.)
-      constexpr int kReadSlots = 48;
-      if (n < kReadSlots) {
-#pragma unroll
-        for (int u = n * kUnits / kReadSlots; u < (n + 1) * kUnits / kReadSlots; u++) read(u, X ^ 1, next);
-      }
-      if (n % T == T - 3) place(n / T, to);
-      if (n % T == T - 2) load(n / T);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    const bool more = s + kBufs + 1 < nk;
-    pa += more ? da : 0;
-    pb += more ? db : 0;
-    // step s + 1 is read by every wave; step s + 2 is in LDS, s + 3 and s + 4
-    // may be on their way
-    asm volatile("s_waitcnt vmcnt(16) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    s++;
+  for (int u = 0; u < kUnits; u++) read(u, 0, lds, lds + kSlot);
+  int s = 0, slot = 0;  // the step that runs, and the slot of its a
+  auto ahead = [&](int n) {  // the slot n places on
+    const int x = slot + n;
+    return x < kSlots ? x : x - kSlots;
   };
-  static_assert((kBufs & (kBufs - 1)) == 0, "buffers wrap by a mask");
+  constexpr int kReadSlots = 48;  // a phase's reads are done after this many of its products
+  constexpr int kLoadEvery = 5;   // products from one load to the next
 #pragma unroll 1
   do {
-    step(std::integral_constant<int, 0>{});
-    step(std::integral_constant<int, 1>{});
-  } while (s < nk);
+    {
+      const char* at_a = lds + slot * kSlot;
+      const char* at_b = lds + ahead(1) * kSlot;
+      const uint32_t to = lds0 + ahead(4) * kSlot;
+#pragma unroll
+      for (int n = 0; n < T * T; n++) {
+        mma_acc(b[0][n % T].v(), a[0][n / T].v(), acc[n / T][n % T]);
+        if (n < kReadSlots) {
+#pragma unroll
+          for (int u = n * kUnits / kReadSlots; u < (n + 1) * kUnits / kReadSlots; u++)
+            read(u, 1, at_a, at_b);
+        }
+        if (n / kLoadEvery < kLoads - kEarlyA) {  // the rest of a's step s + 2
+          if (n % kLoadEvery == 1) place(kEarlyA + n / kLoadEvery, to);
+          if (n % kLoadEvery == 2) load_a(kEarlyA + n / kLoadEvery);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      next_a();
+    }
+    // step s is read by every wave; step s + 1 is in LDS, a's step s + 2 may be
+    // on its way
+    asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    {
+      const char* at_a = lds + ahead(2) * kSlot;
+      const char* at_b = lds + ahead(3) * kSlot;
+      const uint32_t to_b = lds0 + slot * kSlot, to_a = lds0 + ahead(1) * kSlot;
+#pragma unroll
+      for (int n = 0; n < T * T; n++) {
+        mma_acc(b[1][n % T].v(), a[1][n / T].v(), acc[n / T][n % T]);
+        // (after the last step this reads what the slots held; unused)
+        if (n < kReadSlots) {
+#pragma unroll
+          for (int u = n * kUnits / kReadSlots; u < (n + 1) * kUnits / kReadSlots; u++)
+            read(u, 0, at_a, at_b);
+        }
+        const int i = n / kLoadEvery;
+        if (i < kLoads) {
+          if (n % kLoadEvery == 1) place(i, to_b);
+          if (n % kLoadEvery == 2) load_b(i);
+        } else if (i < kLoads + kEarlyA) {
+          if (n % kLoadEvery == 1) place(i - kLoads, to_a);
+          if (n % kLoadEvery == 2) load_a(i - kLoads);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      static_assert((kLoads + kEarlyA - 1) * kLoadEvery + 2 < T * T, "a phase holds its loads");
+      next_b();
+    }
+    slot = ahead(2);
+  } while (++s < nk);
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   drain(acc[T - 1]);
 
