@@ -14,7 +14,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <type_traits>
+#include <cstdlib>
 
 #include "ccr_device.h"
 #include "ccr_internal.h"
@@ -35,34 +35,40 @@ using dev::u32x4;
 __device__ const u32x4 zero_vector = {0, 0, 0, 0};
 
 // LDS image of an operand tile of X rows (the tile's m or n) by one K-step of
-// KB bytes per row (128: 64 bf16 or 32 fp32; 64: half of that), in 16-byte
-// vectors.  Loads go straight from memory to LDS, which fixes each lane's LDS
+// KB = 128 bytes per row (64 bf16 or 32 fp32), in 16-byte vectors.  Loads go straight from memory to LDS, which fixes each lane's LDS
 // place (its wave's base + 16 x lane), so the bank swizzle is applied to the
 // address a lane reads from.
 //
-// Row image (K contiguous in memory): X rows of KB / 16 vectors; vector c of
+// Row image (K contiguous in memory): X rows of 8 vectors; vector c of
 // row r sits at c ^ row_swz(r).  A 16-byte read serves 16 lanes at a time, of
 // two 16-lane groups (0-3, 12-15 of the one, 4-11 of the other): the swizzle
 // puts the 16 vectors they ask for, of 16 rows, on all 64 banks once.
 // Column image (the tile's X contiguous): KB / ES rows of X / (16 / ES)
 // vectors; vector c of row k sits at c ^ col_swz(k), which spreads the rows
 // that one transposing read touches over the banks.
-template <int KB>
+//
+// PAIRED: how a fragment's 16 rows (or columns) lie in the tile.  Plain, they
+// are 16 neighbours.  Paired, fragments 2 i and 2 i + 1 share 32 neighbours, in
+// turns of four: row q of fragment 2 i + u is 8 (q / 4) + 4 u + q % 4 of them,
+// so that the four results a lane holds of each are eight neighbours.
+template <bool PAIRED>
 __device__ __forceinline__ int row_swz(int r) {
-  if constexpr (KB == 128) return (r >> 1) & 7;
-  else return (r >> 3 & 1) * 3;
+  return PAIRED ? ((r >> 1) & 1) | ((r >> 2) & 6) : (r >> 1) & 7;
 }
-template <int ES, int X>
+template <int ES, int X, bool PAIRED>
 __device__ __forceinline__ int col_swz(int k) {
   constexpr int kPerRow = X * ES / 16;
-  if constexpr (ES == 2) return ((((k & 3) | ((k >> 1) & 4)) << 1)) & (kPerRow - 1);
-  else return (((k >> 2) & 3) << 2) & (kPerRow - 1);
+  if constexpr (ES == 4) return (((k >> 2) & 3) << 2) & (kPerRow - 1);
+  else if constexpr (PAIRED) return ((k & 3) << 2) & (kPerRow - 1);
+  else return ((((k & 3) | ((k >> 1) & 4)) << 1)) & (kPerRow - 1);
 }
 
 // One operand's loads of a K-step: NT threads bring X x KB bytes.  Lanes past
 // the tile's last row (or column) read a row inside it: their products are
 // not stored.  Lanes past the contraction's end read zeros.
-template <int ES, int X, bool COL, int KB, int NT>
+constexpr int KB = 128;
+
+template <int ES, int X, bool COL, bool PAIRED, int NT>
 struct Loader {
   static constexpr int kLoads = X * (KB / 16) / NT;
   static constexpr int kStep = KB / ES;        // k values per step
@@ -83,12 +89,12 @@ struct Loader {
       const int q = i * NT + threadIdx.x;
       if constexpr (COL) {
         const int kr = q / kPerRow;
-        const int c = (q % kPerRow) ^ col_swz<ES, X>(kr);
+        const int c = (q % kPerRow) ^ col_swz<ES, X, PAIRED>(kr);
         off[i] = (int)(kr * ld) + (c * (16 / ES) < left ? c * 16 : 0);
         k[i] = kr;
       } else {
         const int r = q / (KB / 16);
-        const int c = (q % (KB / 16)) ^ row_swz<KB>(r);
+        const int c = (q % (KB / 16)) ^ row_swz<PAIRED>(r);
         off[i] = (int)((r < left ? r : left - 1) * ld) + c * 16;
         k[i] = c * (16 / ES);
       }
@@ -97,56 +103,46 @@ struct Loader {
 
   // bytes from one K-step to the next
   __device__ __forceinline__ int64_t stride() const { return COL ? kStep * ld : KB; }
-
-  // K-step s of nk; `rest` = k values the last step holds.
-  __device__ __forceinline__ void issue(char* lds, int64_t s, int rest, bool last) const {
-    const char* from = base + s * stride();
-    char* const to = lds + (threadIdx.x & ~63) * 16;
-#pragma unroll
-    for (int i = 0; i < kLoads; i++) {
-      const char* g = from + off[i];
-      if (last && k[i] >= rest) g = reinterpret_cast<const char*>(&zero_vector);
-      __builtin_amdgcn_global_load_lds((const CCR_GLOBAL unsigned*)g,
-                                       (CCR_LDS unsigned*)(to + i * NT * 16), 16, 0, 0);
-    }
-  }
 };
 
 // Half of a bf16 fragment from a column image: a transposing read of 4 k x 16
 // columns per 16 lanes.  Lane j gives the address of 4 columns of row j / 4 and
-// receives column j of the 4 rows.
-template <int X>
-__device__ __forceinline__ s16x4 fragment_half(const char* lds, int x0, int h, int u) {
+// receives column j of the 4 rows.  The fragment is the i-th from column x0 on.
+template <int X, bool PAIRED>
+__device__ __forceinline__ s16x4 fragment_half(const char* lds, int x0, int i, int h, int u) {
   const int l = threadIdx.x & 63, j = l & 15, g = l >> 4;
   const int k = h * 32 + g * 8 + u * 4 + (j >> 2);
-  const int c = (x0 >> 3) + ((j & 3) >> 1);
+  const int x = PAIRED ? x0 + (i >> 1) * 32 + (j & 3) * 8 + (i & 1) * 4 : x0 + i * 16 + (j & 3) * 4;
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-      (CCR_LDS s16x4*)(lds + k * (X * 2) + ((c ^ col_swz<2, X>(k)) << 4) + (j & 1) * 8));
+      (CCR_LDS s16x4*)(lds + k * (X * 2) + (((x >> 3) ^ col_swz<2, X, PAIRED>(k)) << 4) + (x & 4) * 2));
 }
 
-// A 16-row fragment of 64 bytes of K (part h of the step): 4 registers per
-// lane.  Lane l holds row l % 16 and, with g = l / 16, k = 32 h + 8 g + (0..7)
-// in bf16 or k = 16 h + 4 g + (0..3) in fp32.  Both operands use the same k for
-// the same lane and register, which is all a product needs.
-template <int ES, int X, bool COL, int KB>
-__device__ __forceinline__ u32x4 fragment(const char* lds, int x0, int h) {
+// A 16-row fragment (the i-th from row x0 on) of 64 bytes of K (part h of the
+// step): 4 registers per lane.  Lane l holds row l % 16 and, with g = l / 16,
+// k = 32 h + 8 g + (0..7) in bf16 or k = 16 h + 4 g + (0..3) in fp32.  Both
+// operands use the same k for the same lane and register, which is all a
+// product needs.
+template <int ES, int X, bool COL, bool PAIRED>
+__device__ __forceinline__ u32x4 fragment(const char* lds, int x0, int i, int h) {
+  static_assert(ES == 2 || !PAIRED, "fp32 results are 16 bytes by fours");
   const int l = threadIdx.x & 63, j = l & 15, g = l >> 4;
   if constexpr (!COL) {
-    const int r = x0 + j;
-    return *reinterpret_cast<const u32x4*>(lds + r * KB + (((h * 4 + g) ^ row_swz<KB>(r)) << 4));
+    const int r = PAIRED ? x0 + (i >> 1) * 32 + (j >> 2) * 8 + (i & 1) * 4 + (j & 3) : x0 + i * 16 + j;
+    return *reinterpret_cast<const u32x4*>(lds + r * KB + (((h * 4 + g) ^ row_swz<PAIRED>(r)) << 4));
   } else if constexpr (ES == 2) {
-    const s16x4 v[2] = {fragment_half<X>(lds, x0, h, 0), fragment_half<X>(lds, x0, h, 1)};
+    const s16x4 v[2] = {fragment_half<X, PAIRED>(lds, x0, i, h, 0),
+                        fragment_half<X, PAIRED>(lds, x0, i, h, 1)};
     u32x4 r;
     __builtin_memcpy(&r, v, 16);
     return r;
   } else {
     u32x4 r;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int k = h * 16 + g * 4 + i;
-      const int c = (x0 + j) >> 2;
-      r[i] = *reinterpret_cast<const uint32_t*>(lds + k * (X * 4) + ((c ^ col_swz<ES, X>(k)) << 4) +
-                                                (j & 3) * 4);
+    for (int e = 0; e < 4; e++) {
+      const int k = h * 16 + g * 4 + e;
+      const int c = (x0 + i * 16 + j) >> 2;
+      r[e] = *reinterpret_cast<const uint32_t*>(
+          lds + k * (X * 4) + ((c ^ col_swz<4, X, false>(k)) << 4) + (j & 3) * 4);
     }
     return r;
   }
@@ -211,84 +207,150 @@ __device__ __forceinline__ void tile_at(int in, int mt, int nt, int* m, int* n) 
   *m = strip * kStrip + (r - *n * h);
 }
 
-// OP as in the table above.  Tile BM x BN of the output, WM x WN waves.
-template <ExpertOp OP, int ES, int OS, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM * WN * 64) void experts_kernel(const ExpertTable tab,
-                                                               const ExpertShape sh) {
+// What a workgroup computes: its expert's operands and sizes (output M x N,
+// contraction C) and its tile's corner.
+struct Where {
+  const char *a, *b;
+  char* c;
+  int64_t M, N, C, m0, n0;
+};
+template <ExpertOp OP, int BM, int BN>
+__device__ __forceinline__ Where place_of(const ExpertTable& tab, const ExpertShape& sh, int t) {
+  const int gi = __builtin_amdgcn_readfirstlane(group_of(tab, t));
+  const ExpertGroup& g = tab.g[gi];
+  Where at;
+  at.a = g.a;
+  at.b = g.b;
+  at.c = g.c;
+  at.M = OP == ExpertOp::kWgrad ? sh.F : g.rows;
+  at.N = OP == ExpertOp::kProduct ? sh.F : sh.H;
+  at.C = OP == ExpertOp::kProduct ? sh.H : OP == ExpertOp::kDgrad ? sh.F : g.rows;
+  int tm, tn;
+  tile_at(t - tab.tile0[gi], (int)((at.M + BM - 1) / BM), (int)((at.N + BN - 1) / BN), &tm, &tn);
+  at.m0 = (int64_t)tm * BM;
+  at.n0 = (int64_t)tn * BN;
+  return at;
+}
+
+// The loads are written in assembly (they have no result register, only LDS)
+// because the compiler would otherwise wait for all of them before any later
+// LDS read.
+__device__ __forceinline__ void load_lds(uint32_t lds, uint32_t off, const char* base) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               ::"s"(lds), "v"(off), "s"(base) : "memory");
+}
+__device__ __forceinline__ void load_lds(uint32_t lds, const char* p) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               ::"s"(lds), "v"(p) : "memory");
+}
+
+// ------------------------------------------------------- small and mid tiles
+// OP as in the table above.  Tile BM x BN of the output, WM x WN waves, a ring
+// of NBUF K-steps in LDS.  Per step one barrier: behind it the step's vectors
+// are in LDS and the step before is read by every wave, so its buffer takes
+// the loads of the step NBUF - 1 ahead.
+template <ExpertOp OP, int ES, int OS, int BM, int BN, int WM, int WN, int NBUF>
+__global__ __launch_bounds__(WM * WN * 64) void experts_ring_kernel(const ExpertTable tab,
+                                                                    const ExpertShape sh) {
   constexpr bool kACol = OP == ExpertOp::kWgrad;       // a: x, dout, dout
   constexpr bool kBCol = OP != ExpertOp::kProduct;     // b: W, W, x
   constexpr int NT = WM * WN * 64;
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 blocks per wave
-  constexpr int kABytes = BM * 128, kBuf = (BM + BN) * 128;
-  __shared__ __align__(1024) char lds[2 * kBuf];
-  const int t = xcd_tile(blockIdx.x, gridDim.x);
-  const int gi = __builtin_amdgcn_readfirstlane(group_of(tab, t));
-  const ExpertGroup g = tab.g[gi];
-  const int64_t M = OP == ExpertOp::kWgrad ? sh.F : g.rows;
-  const int64_t N = OP == ExpertOp::kProduct ? sh.F : sh.H;
-  const int64_t C = OP == ExpertOp::kProduct ? sh.H : OP == ExpertOp::kDgrad ? sh.F : g.rows;
-  int tm, tn;
-  tile_at(t - tab.tile0[gi], (int)((M + BM - 1) / BM), (int)((N + BN - 1) / BN), &tm, &tn);
-  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
-  const int64_t lda = (OP == ExpertOp::kProduct ? sh.H : sh.F) * ES;
-  const int64_t ldb = sh.H * ES;
-  constexpr int KB = 128;
-  Loader<ES, BM, kACol, KB, NT> la;
-  Loader<ES, BN, kBCol, KB, NT> lb;
-  la.init(g.a, lda, m0, M);
-  lb.init(g.b, ldb, n0, N);
-  constexpr int kStep = KB / ES;
-  const int64_t nk = (C + kStep - 1) / kStep;
-  const int rest = (int)(C - (nk - 1) * kStep);
+  constexpr int kABytes = BM * KB, kBuf = (BM + BN) * KB;
+  using LoadA = Loader<ES, BM, kACol, false, NT>;
+  using LoadB = Loader<ES, BN, kBCol, false, NT>;
+  constexpr int kLoads = LoadA::kLoads + LoadB::kLoads;
+  static_assert(LoadA::kLoads * NT == BM * 8 && LoadB::kLoads * NT == BN * 8, "whole loads");
+  static_assert((NBUF - 2) * kLoads <= 63, "the wait count has 6 bits");
+  __shared__ __align__(1024) char lds[NBUF * kBuf];
+  const Where at = place_of<OP, BM, BN>(tab, sh, xcd_tile(blockIdx.x, gridDim.x));
+  LoadA la;
+  LoadB lb;
+  la.init(at.a, (OP == ExpertOp::kProduct ? sh.H : sh.F) * ES, at.m0, at.M);
+  lb.init(at.b, sh.H * ES, at.n0, at.N);
+  constexpr int kStep = LoadA::kStep;
+  // Step 0 holds the contraction's odd end (`rest` values, then zeros; no value
+  // for a weight gradient without rows), so that every later step is whole.
+  // Past the last step the loads bring the last whole step again (or, where
+  // there is none, each operand's first vector): the count of loads on their
+  // way stays the same.
+  const int whole = (int)((at.C - 1) / kStep), nk = whole + 1;
+  const int rest = (int)(at.C - (int64_t)whole * kStep);
+  const char* pa = la.base + (kACol ? rest * la.ld : rest * ES);
+  const char* pb = lb.base + (kBCol ? rest * lb.ld : rest * ES);
+  const int64_t da = la.stride(), db = lb.stride();
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = (w / WN) * (BM / WM), wn = (w % WN) * (BN / WN);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(CCR_LDS char*)lds + w * 1024;
+  {
+    const char* zero = reinterpret_cast<const char*>(&zero_vector);
+#pragma unroll
+    for (int i = 0; i < LoadA::kLoads; i++)
+      load_lds(lds0 + i * NT * 16, la.k[i] < rest ? la.base + la.off[i] : zero);
+#pragma unroll
+    for (int i = 0; i < LoadB::kLoads; i++)
+      load_lds(lds0 + kABytes + i * NT * 16, lb.k[i] < rest ? lb.base + lb.off[i] : zero);
+  }
+  if (whole == 0) {
+    pa = rest ? la.base : reinterpret_cast<const char*>(&zero_vector);
+    pb = rest ? lb.base : reinterpret_cast<const char*>(&zero_vector);
+#pragma unroll
+    for (int i = 0; i < LoadA::kLoads; i++) la.off[i] = 0;
+#pragma unroll
+    for (int i = 0; i < LoadB::kLoads; i++) lb.off[i] = 0;
+  }
+  int j = 1;  // the step at pa, pb
+  auto issue = [&](uint32_t to) {
+#pragma unroll
+    for (int i = 0; i < LoadA::kLoads; i++) load_lds(to + i * NT * 16, (uint32_t)la.off[i], pa);
+#pragma unroll
+    for (int i = 0; i < LoadB::kLoads; i++)
+      load_lds(to + kABytes + i * NT * 16, (uint32_t)lb.off[i], pb);
+    pa += j < whole ? da : 0;
+    pb += j < whole ? db : 0;
+    j++;
+  };
+#pragma unroll
+  for (int i = 1; i < NBUF - 1; i++) issue(lds0 + i * kBuf);
   f32x4 acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; i++)
 #pragma unroll
-    for (int j = 0; j < TN; j++) acc[i][j] = f32x4{0, 0, 0, 0};
-  const int w = threadIdx.x >> 6;
-  const int wm = (w / WN) * (BM / WM), wn = (w % WN) * (BN / WN);
-
-  if (nk > 0) {
-    la.issue(lds, 0, rest, nk == 1);
-    lb.issue(lds + kABytes, 0, rest, nk == 1);
-  }
-  for (int64_t s = 0; s < nk; s++) {
-    // this step's vectors are in LDS for every wave, and every wave has read
-    // the step before
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    const char* cur = lds + (s & 1) * kBuf;
+    for (int n = 0; n < TN; n++) acc[i][n] = f32x4{0, 0, 0, 0};
+  int cur = 0, free = (NBUF - 1) * kBuf;  // byte offsets of this step's buffer and of the one read before
+#pragma unroll 1
+  for (int s = 0; s < nk; s++) {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NBUF - 2) * kLoads) : "memory");
     u32x4 a[2][TM], b[2][TN];
 #pragma unroll
     for (int h = 0; h < 2; h++) {
 #pragma unroll
-      for (int i = 0; i < TM; i++) a[h][i] = fragment<ES, BM, kACol, KB>(cur, wm + i * 16, h);
+      for (int i = 0; i < TM; i++) a[h][i] = fragment<ES, BM, kACol, false>(lds + cur, wm, i, h);
 #pragma unroll
-      for (int j = 0; j < TN; j++) b[h][j] = fragment<ES, BN, kBCol, KB>(cur + kABytes, wn + j * 16, h);
+      for (int n = 0; n < TN; n++) b[h][n] = fragment<ES, BN, kBCol, false>(lds + cur + kABytes, wn, n, h);
     }
-    if (s + 1 < nk) {
-      char* next = lds + ((s + 1) & 1) * kBuf;
-      la.issue(next, s + 1, rest, s + 2 == nk);
-      lb.issue(next + kABytes, s + 1, rest, s + 2 == nk);
-    }
+    issue(lds0 + free);
+    free = cur;
+    cur = cur + kBuf == NBUF * kBuf ? 0 : cur + kBuf;
 #pragma unroll
     for (int h = 0; h < 2; h++)
 #pragma unroll
       for (int i = 0; i < TM; i++)
 #pragma unroll
-        for (int j = 0; j < TN; j++) acc[i][j] = mma<ES>(b[h][j], a[h][i], acc[i][j]);
+        for (int n = 0; n < TN; n++) acc[i][n] = mma<ES>(b[h][n], a[h][i], acc[i][n]);
   }
-
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   // D holds b's rows (the output's columns) down its registers: lane l has
   // output row l % 16 and columns 4 (l / 16) + (0..3) of each 16 x 16 block.
   const int l = threadIdx.x & 63;
 #pragma unroll
   for (int i = 0; i < TM; i++) {
-    const int64_t m = m0 + wm + i * 16 + (l & 15);
-    if (m >= M) continue;
+    const int64_t m = at.m0 + wm + i * 16 + (l & 15);
+    if (m >= at.M) continue;
 #pragma unroll
-    for (int j = 0; j < TN; j++) {
-      const int64_t n = n0 + wn + j * 16 + (l >> 4) * 4;
-      if (n < N) store4<OS>(g.c + (m * N + n) * OS, acc[i][j], sh.add);
+    for (int n = 0; n < TN; n++) {
+      const int64_t c = at.n0 + wn + n * 16 + (l >> 4) * 4;
+      if (c < at.N) store4<OS>(at.c + (m * at.N + c) * OS, acc[i][n], sh.add);
     }
   }
 }
@@ -311,31 +373,18 @@ __global__ __launch_bounds__(WM * WN * 64) void experts_kernel(const ExpertTable
 // and loads are placed one by one between the products.  Measured at 8192^3
 // against reads and loads in groups of three before every eight products:
 // 1283 -> 1433 TFLOP/s (dgrad).
-//
-// The loads are written in assembly (they have no result register, only LDS)
-// because the compiler would otherwise wait for all of them before any later
-// LDS read.
-__device__ __forceinline__ void load_lds(uint32_t lds, uint32_t off, const char* base) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-               ::"s"(lds), "v"(off), "s"(base) : "memory");
-}
-__device__ __forceinline__ void load_lds(uint32_t lds, const char* p) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-               ::"s"(lds), "v"(p) : "memory");
-}
-
 // A fragment as fragment() gives it, read in parts.
-template <bool COL>
+template <bool COL, bool PAIRED>
 struct Frag {
   static constexpr int kReads = COL ? 2 : 1;
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
   u32x4 whole;
   u32x2 half[2];
 
-  template <int X, int KB>
-  __device__ __forceinline__ void read(const char* lds, int x0, int h, int part) {
-    if constexpr (!COL) whole = fragment<2, X, false, KB>(lds, x0, h);
-    else half[part] = __builtin_bit_cast(u32x2, fragment_half<X>(lds, x0, h, part));
+  template <int X>
+  __device__ __forceinline__ void read(const char* lds, int x0, int i, int h, int part) {
+    if constexpr (!COL) whole = fragment<2, X, false, PAIRED>(lds, x0, i, h);
+    else half[part] = __builtin_bit_cast(u32x2, fragment_half<X, PAIRED>(lds, x0, i, h, part));
   }
   __device__ __forceinline__ u32x4 v() const {
     if constexpr (COL) return __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3);
@@ -357,83 +406,47 @@ __device__ __forceinline__ void drain(f32x4* d) {
                  "+a"(d[7]));
 }
 
+// Eight neighbouring values of an output row.
+template <int OS>
+__device__ __forceinline__ void store8(char* p, f32x4 lo, f32x4 hi) {
+  if constexpr (OS == 4) {
+    reinterpret_cast<f32x4*>(p)[0] = lo;
+    reinterpret_cast<f32x4*>(p)[1] = hi;
+  } else {
+    const bf16x4 a = __builtin_convertvector(lo, bf16x4), b = __builtin_convertvector(hi, bf16x4);
+    *reinterpret_cast<bf16x8*>(p) = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+}
+
+// One workgroup to a compute unit, each taking every gridDim.x-th tile.  The
+// first loads of its next tile go out before this tile's results are written,
+// so that neither their latency nor the launch of a workgroup lies between two
+// tiles.
 template <ExpertOp OP, int OS>
-__global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable tab, const ExpertShape sh) {
-  constexpr int ES = 2, BM = 256, BN = 256, NT = 256, T = 8, KB = 128;
+__global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable tab, const ExpertShape sh,
+                                                             int tiles) {
+  constexpr int ES = 2, BM = 256, BN = 256, NT = 256, T = 8;
   constexpr bool kACol = OP == ExpertOp::kWgrad;
   constexpr bool kBCol = OP != ExpertOp::kProduct;
   constexpr int kSlot = BM * KB, kSlots = 5;
   static_assert(BM == BN, "both operands fill a slot");
-  using LoadA = Loader<ES, BM, kACol, KB, NT>;
-  using LoadB = Loader<ES, BN, kBCol, KB, NT>;
-  __shared__ __align__(1024) char lds[kSlots * kSlot];
-  const int t = xcd_tile(blockIdx.x, gridDim.x);
-  const int gi = __builtin_amdgcn_readfirstlane(group_of(tab, t));
-  const ExpertGroup g = tab.g[gi];
-  const int64_t M = OP == ExpertOp::kWgrad ? sh.F : g.rows;
-  const int64_t N = OP == ExpertOp::kProduct ? sh.F : sh.H;
-  const int64_t C = OP == ExpertOp::kProduct ? sh.H : OP == ExpertOp::kDgrad ? sh.F : g.rows;
-  int tm, tn;
-  tile_at(t - tab.tile0[gi], (int)((M + BM - 1) / BM), (int)((N + BN - 1) / BN), &tm, &tn);
-  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
-  const int64_t lda = (OP == ExpertOp::kProduct ? sh.H : sh.F) * ES;
-  const int64_t ldb = sh.H * ES;
-  const int l = threadIdx.x & 63;
-  if (OP == ExpertOp::kWgrad && C == 0) {  // an expert without a row
-    for (int i = threadIdx.x; i < BM * (BN / 4); i += NT) {
-      const int64_t m = m0 + i / (BN / 4), n = n0 + i % (BN / 4) * 4;
-      if (m < M && n < N) store4<OS>(g.c + (m * N + n) * OS, f32x4{0, 0, 0, 0}, sh.add);
-    }
-    return;
-  }
-  LoadA la;
-  LoadB lb;
-  la.init(g.a, lda, m0, M);
-  lb.init(g.b, ldb, n0, N);
+  using LoadA = Loader<ES, BM, kACol, false, NT>;
+  using LoadB = Loader<ES, BN, kBCol, true, NT>;
   constexpr int kStep = LoadA::kStep;
-  // Step 0 holds the contraction's odd end (`rest` values, then zeros), so that
-  // every later step is whole.
-  const int whole = (int)((C - 1) / kStep), nk = whole + 1;
-  const int rest = (int)(C - (int64_t)whole * kStep);
-  f32x4 acc[T][T];
+  constexpr int kLoads = LoadA::kLoads;  // of one slot
+  static_assert(kLoads == 8 && LoadB::kLoads == 8, "the wait counts below");
+  constexpr int kEarlyA = 5;  // loads of a that go out in a step's second phase
+  __shared__ __align__(1024) char lds[kSlots * kSlot];
+  const int l = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = (w >> 1) * 128, wn = (w & 1) * 128;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(CCR_LDS char*)lds + w * 1024;
 
-  const char* pa = la.base + (kACol ? rest * la.ld : rest * ES);
-  const char* pb = lb.base + (kBCol ? rest * lb.ld : rest * ES);
-  const int64_t da = la.stride(), db = lb.stride();
-  constexpr int kLoads = LoadA::kLoads;  // of one slot
-  static_assert(kLoads == 8 && LoadB::kLoads == 8, "the wait counts below");
-  // The first step's loads, zeros from value `rest` on.
-  {
-    const char* zero = reinterpret_cast<const char*>(&zero_vector);
-#pragma unroll
-    for (int i = 0; i < kLoads; i++)
-      load_lds(lds0 + i * NT * 16, la.k[i] < rest ? la.base + la.off[i] : zero);
-#pragma unroll
-    for (int i = 0; i < kLoads; i++)
-      load_lds(lds0 + kSlot + i * NT * 16, lb.k[i] < rest ? lb.base + lb.off[i] : zero);
-  }
-  // Past the last step the loads bring the last whole step again (or, where
-  // there is none, each operand's first vector) into slots that are not read
-  // any more: the loop keeps no branch, and the count of loads on their way
-  // stays the same.
-  int ja = 1, jb = 1;  // the step at pa, pb
-  if (whole == 0) {
-    pa = la.base;
-    pb = lb.base;
-#pragma unroll
-    for (int i = 0; i < kLoads; i++) la.off[i] = lb.off[i] = 0;
-  }
-  auto next_a = [&]() {
-    pa += ja < whole ? da : 0;
-    ja++;
-  };
-  auto next_b = [&]() {
-    pb += jb < whole ? db : 0;
-    jb++;
-  };
+  LoadA la;
+  LoadB lb;
+  const char *pa, *pb;  // the step whose loads are next, of a and of b
+  int64_t da, db;
+  int ja, jb, whole;
   // A slot's loads, one at a time: the LDS place in m0, then load i.
   auto place = [&](int i, uint32_t to) {
     asm volatile("s_add_u32 m0, %0, %1" ::"s"(to), "n"(i * NT * 16) : "scc");
@@ -444,22 +457,18 @@ __global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable t
   auto load_b = [&](int i) {
     asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(lb.off[i]), "s"(pb) : "memory");
   };
-
-  // Fragments are read in units: one LDS read each, two to a fragment from a
-  // column image.
-  constexpr int kUnitsB = T * Frag<kBCol>::kReads, kUnits = kUnitsB + T * Frag<kACol>::kReads;
-  Frag<kACol> a[2][T];
-  Frag<kBCol> b[2][T];
-  auto read = [&](int u, int h, const char* at_a, const char* at_b) {  // b's first, then a's
-    if (u < kUnitsB) {
-      constexpr int n = Frag<kBCol>::kReads;
-      b[h][u / n].template read<BN, KB>(at_b, wn + u / n * 16, h, u % n);
-    } else {
-      constexpr int n = Frag<kACol>::kReads;
-      a[h][(u - kUnitsB) / n].template read<BM, KB>(at_a, wm + (u - kUnitsB) / n * 16, h, (u - kUnitsB) % n);
-    }
+  // Past the last step the loads bring the last whole step again (or, where
+  // there is none, each operand's first vector) into slots that are not read
+  // any more: the loop keeps no branch, and the count of loads on their way
+  // stays the same.
+  auto next_a = [&]() {
+    pa += ja < whole ? da : 0;
+    ja++;
   };
-  constexpr int kEarlyA = 5;  // loads of a that go out in the second phase
+  auto next_b = [&]() {
+    pb += jb < whole ? db : 0;
+    jb++;
+  };
   auto load_whole = [&](auto& load, uint32_t to, int n) {
 #pragma unroll
     for (int i = 0; i < n; i++) {
@@ -468,97 +477,185 @@ __global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable t
       load(i);
     }
   };
-  load_whole(load_a, lds0 + 2 * kSlot, kLoads);
-  next_a();
-  load_whole(load_b, lds0 + 3 * kSlot, kLoads);
-  next_b();
-  load_whole(load_a, lds0 + 4 * kSlot, kEarlyA);
-  // the accumulators are cleared while the loads arrive
+  // A tile's first loads: step 0, which holds the contraction's odd end (`rest`
+  // values, then zeros; no value for a weight gradient without rows), so that
+  // every later step is whole; step 1; the first of a's step 2.
+  auto begin = [&](const Where& at) {
+    la.init(at.a, (OP == ExpertOp::kProduct ? sh.H : sh.F) * ES, at.m0, at.M);
+    lb.init(at.b, sh.H * ES, at.n0, at.N);
+    whole = (int)((at.C - 1) / kStep);
+    const int rest = (int)(at.C - (int64_t)whole * kStep);
+    const char* zero = reinterpret_cast<const char*>(&zero_vector);
 #pragma unroll
-  for (int i = 0; i < T; i++)
+    for (int i = 0; i < kLoads; i++)
+      load_lds(lds0 + i * NT * 16, la.k[i] < rest ? la.base + la.off[i] : zero);
 #pragma unroll
-    for (int j = 0; j < T; j++) {
-      acc[i][j] = f32x4{0, 0, 0, 0};
-      asm volatile("" : "+a"(acc[i][j]));
+    for (int i = 0; i < kLoads; i++)
+      load_lds(lds0 + kSlot + i * NT * 16, lb.k[i] < rest ? lb.base + lb.off[i] : zero);
+    pa = la.base + (kACol ? rest * la.ld : rest * ES);
+    pb = lb.base + (kBCol ? rest * lb.ld : rest * ES);
+    da = la.stride();
+    db = lb.stride();
+    ja = jb = 1;
+    if (whole == 0) {
+      pa = rest ? la.base : zero;
+      pb = rest ? lb.base : zero;
+#pragma unroll
+      for (int i = 0; i < kLoads; i++) la.off[i] = lb.off[i] = 0;
     }
-  // step 0 is in LDS, step 1 and part of a's step 2 may be on their way
+    load_whole(load_a, lds0 + 2 * kSlot, kLoads);
+    next_a();
+    load_whole(load_b, lds0 + 3 * kSlot, kLoads);
+    next_b();
+    load_whole(load_a, lds0 + 4 * kSlot, kEarlyA);
+  };
+
+  // Fragments are read in units: one LDS read each, two to a fragment from a
+  // column image.
+  using FragA = Frag<kACol, false>;
+  using FragB = Frag<kBCol, true>;
+  constexpr int kUnitsB = T * FragB::kReads, kUnits = kUnitsB + T * FragA::kReads;
+  FragA a[2][T];
+  FragB b[2][T];
+  auto read = [&](int u, int h, const char* at_a, const char* at_b) {  // b's first, then a's
+    if (u < kUnitsB) {
+      constexpr int n = FragB::kReads;
+      b[h][u / n].template read<BN>(at_b, wn, u / n, h, u % n);
+    } else {
+      constexpr int n = FragA::kReads;
+      a[h][(u - kUnitsB) / n].template read<BM>(at_a, wm, (u - kUnitsB) / n, h, (u - kUnitsB) % n);
+    }
+  };
+
+  int t = blockIdx.x;
+  Where at = place_of<OP, BM, BN>(tab, sh, xcd_tile(t, tiles));
+  begin(at);
+  // all but step 1 and part of a's step 2
   asm volatile("s_waitcnt vmcnt(21)\n\ts_barrier" ::: "memory");
   static_assert(2 * kLoads + kEarlyA == 21, "as waited for");
-#pragma unroll
-  for (int u = 0; u < kUnits; u++) read(u, 0, lds, lds + kSlot);
-  int s = 0, slot = 0;  // the step that runs, and the slot of its a
-  auto ahead = [&](int n) {  // the slot n places on
-    const int x = slot + n;
-    return x < kSlots ? x : x - kSlots;
-  };
-  constexpr int kReadSlots = 48;  // a phase's reads are done after this many of its products
-  constexpr int kLoadEvery = 5;   // products from one load to the next
 #pragma unroll 1
-  do {
-    {
-      const char* at_a = lds + slot * kSlot;
-      const char* at_b = lds + ahead(1) * kSlot;
-      const uint32_t to = lds0 + ahead(4) * kSlot;
+  for (;;) {
+    const int nk = whole + 1;
+    t += gridDim.x;
+    const bool again = t < tiles;
+    const Where next = place_of<OP, BM, BN>(tab, sh, xcd_tile(again ? t : blockIdx.x, tiles));
 #pragma unroll
-      for (int n = 0; n < T * T; n++) {
-        mma_acc(b[0][n % T].v(), a[0][n / T].v(), acc[n / T][n % T]);
-        if (n < kReadSlots) {
+    for (int u = 0; u < kUnits; u++) read(u, 0, lds, lds + kSlot);
+    f32x4 acc[T][T];
 #pragma unroll
-          for (int u = n * kUnits / kReadSlots; u < (n + 1) * kUnits / kReadSlots; u++)
-            read(u, 1, at_a, at_b);
-        }
-        if (n / kLoadEvery < kLoads - kEarlyA) {  // the rest of a's step s + 2
-          if (n % kLoadEvery == 1) place(kEarlyA + n / kLoadEvery, to);
-          if (n % kLoadEvery == 2) load_a(kEarlyA + n / kLoadEvery);
-        }
-        __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < T; i++)
+#pragma unroll
+      for (int j = 0; j < T; j++) {
+        acc[i][j] = f32x4{0, 0, 0, 0};
+        asm volatile("" : "+a"(acc[i][j]));
       }
-      next_a();
-    }
-    // step s is read by every wave; step s + 1 is in LDS, a's step s + 2 may be
-    // on its way
-    asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    {
-      const char* at_a = lds + ahead(2) * kSlot;
-      const char* at_b = lds + ahead(3) * kSlot;
-      const uint32_t to_b = lds0 + slot * kSlot, to_a = lds0 + ahead(1) * kSlot;
+    int s = 0, slot = 0;  // the step that runs, and the slot of its a
+    auto ahead = [&](int n) {  // the slot n places on
+      const int x = slot + n;
+      return x < kSlots ? x : x - kSlots;
+    };
+    // A phase's reads are done after kReadSlots of its 64 products; a load goes
+    // out every kLoadEvery products.  (Between 32 and 56, and at 4, the rate
+    // stays within 1%.)
+    constexpr int kReadSlots = 48, kLoadEvery = 5;
+#pragma unroll 1
+    do {
+      {
+        const char* at_a = lds + slot * kSlot;
+        const char* at_b = lds + ahead(1) * kSlot;
+        const uint32_t to = lds0 + ahead(4) * kSlot;
 #pragma unroll
-      for (int n = 0; n < T * T; n++) {
-        mma_acc(b[1][n % T].v(), a[1][n / T].v(), acc[n / T][n % T]);
-        // (after the last step this reads what the slots held; unused)
-        if (n < kReadSlots) {
+        for (int n = 0; n < T * T; n++) {
+          mma_acc(b[0][n % T].v(), a[0][n / T].v(), acc[n / T][n % T]);
+          if (n < kReadSlots) {
 #pragma unroll
-          for (int u = n * kUnits / kReadSlots; u < (n + 1) * kUnits / kReadSlots; u++)
-            read(u, 0, at_a, at_b);
+            for (int u = n * kUnits / kReadSlots; u < (n + 1) * kUnits / kReadSlots; u++)
+              read(u, 1, at_a, at_b);
+          }
+          if (n / kLoadEvery < kLoads - kEarlyA) {  // the rest of a's step s + 2
+            if (n % kLoadEvery == 1) place(kEarlyA + n / kLoadEvery, to);
+            if (n % kLoadEvery == 2) load_a(kEarlyA + n / kLoadEvery);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
-        const int i = n / kLoadEvery;
-        if (i < kLoads) {
-          if (n % kLoadEvery == 1) place(i, to_b);
-          if (n % kLoadEvery == 2) load_b(i);
-        } else if (i < kLoads + kEarlyA) {
-          if (n % kLoadEvery == 1) place(i - kLoads, to_a);
-          if (n % kLoadEvery == 2) load_a(i - kLoads);
-        }
-        __builtin_amdgcn_sched_barrier(0);
+        next_a();
       }
-      static_assert((kLoads + kEarlyA - 1) * kLoadEvery + 2 < T * T, "a phase holds its loads");
-      next_b();
-    }
-    slot = ahead(2);
-  } while (++s < nk);
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  drain(acc[T - 1]);
+      // step s is read by every wave; step s + 1 is in LDS, a's step s + 2 may be
+      // on its way
+      asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      {
+        const char* at_a = lds + ahead(2) * kSlot;
+        const char* at_b = lds + ahead(3) * kSlot;
+        const uint32_t to_b = lds0 + slot * kSlot, to_a = lds0 + ahead(1) * kSlot;
+#pragma unroll
+        for (int n = 0; n < T * T; n++) {
+          mma_acc(b[1][n % T].v(), a[1][n / T].v(), acc[n / T][n % T]);
+          // (after the last step this reads what the slots held; unused)
+          if (n < kReadSlots) {
+#pragma unroll
+            for (int u = n * kUnits / kReadSlots; u < (n + 1) * kUnits / kReadSlots; u++)
+              read(u, 0, at_a, at_b);
+          }
+          const int i = n / kLoadEvery;
+          if (i < kLoads) {
+            if (n % kLoadEvery == 1) place(i, to_b);
+            if (n % kLoadEvery == 2) load_b(i);
+          } else if (i < kLoads + kEarlyA) {
+            if (n % kLoadEvery == 1) place(i - kLoads, to_a);
+            if (n % kLoadEvery == 2) load_a(i - kLoads);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        static_assert((kLoads + kEarlyA - 1) * kLoadEvery + 2 < T * T, "a phase holds its loads");
+        next_b();
+      }
+      slot = ahead(2);
+    } while (++s < nk);
+    drain(acc[T - 1]);
+    // The last loads of this tile are done, and every wave has read what it
+    // needs of the slots (at the last step's barrier): the next tile's go out.
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    if (again) begin(next);
 
+    // D holds b's rows (the output's columns) down its registers: lane l has
+    // output row l % 16 of each block and, of a pair of blocks, columns
+    // 8 (l / 16) + (0..7).
+    const bool full = at.m0 + BM <= at.M && at.n0 + BN <= at.N && !sh.add;
+    char* out = at.c + ((at.m0 + wm + (l & 15)) * at.N + at.n0 + wn + (l >> 4) * 8) * OS;
+    const int64_t down = 16 * at.N * OS;
+    if (full) {
 #pragma unroll
-  for (int i = 0; i < T; i++) {
-    const int64_t m = m0 + wm + i * 16 + (l & 15);
+      for (int i = 0; i < T; i++) {
 #pragma unroll
-    for (int j = 0; j < T; j++) {
-      asm volatile("" : "+a"(acc[i][j]));  // read out row by row, not all at once
-      const int64_t n = n0 + wn + j * 16 + (l >> 4) * 4;
-      if (m < M && n < N) store4<OS>(g.c + (m * N + n) * OS, acc[i][j], sh.add);
+        for (int j = 0; j < T; j += 2) {
+          asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i][j + 1]));  // read out row by row
+          store8<OS>(out + j * 16 * OS, acc[i][j], acc[i][j + 1]);
+        }
+        out += down;
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < T; i++) {
+        const bool in = at.m0 + wm + i * 16 + (l & 15) < at.M;
+#pragma unroll
+        for (int j = 0; j < T; j++) {
+          asm volatile("" : "+a"(acc[i][j]));
+          const int c = (j >> 1) * 32 + (j & 1) * 4;
+          if (in && at.n0 + wn + (l >> 4) * 8 + c < at.N) store4<OS>(out + c * OS, acc[i][j], sh.add);
+        }
+        out += down;
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
-    __builtin_amdgcn_sched_barrier(0);
+    if (!again) return;
+    at = next;
+    // the next tile's step 0; its step 1 and part of a's step 2, and in a full
+    // tile the results' stores, may be on their way
+    constexpr int kStores = T * T * OS / 4;
+    if (full) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(21 + kStores < 63 ? 21 + kStores : 63) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    asm volatile("s_barrier" ::: "memory");
   }
 }
 
@@ -567,16 +664,33 @@ hipError_t launch_as(const ExpertTable& tab, const ExpertShape& sh, ExpertTile t
                      hipStream_t stream) {
   if constexpr (ES == 2)
     if (tile.m == 256) {
-      experts_big_kernel<OP, OS><<<(unsigned)tiles, 256, 0, stream>>>(tab, sh);
+      // one workgroup for each of the 256 compute units, which its LDS fills
+      experts_big_kernel<OP, OS><<<(unsigned)(tiles < 256 ? tiles : 256), 256, 0, stream>>>(tab, sh, tiles);
       return hipGetLastError();
     }
-  experts_kernel<OP, ES, OS, 128, 128, 2, 2><<<(unsigned)tiles, 256, 0, stream>>>(tab, sh);
+  if (tile.m == 128) {
+    experts_ring_kernel<OP, ES, OS, 128, 128, 2, 2, 2><<<(unsigned)tiles, 256, 0, stream>>>(tab, sh);
+    return hipGetLastError();
+  }
+  if constexpr (OP != ExpertOp::kWgrad)
+    if (tile.m == 16) {
+      experts_ring_kernel<OP, ES, OS, 16, 64, 1, 2, 6><<<(unsigned)tiles, 128, 0, stream>>>(tab, sh);
+      return hipGetLastError();
+    }
+  experts_ring_kernel<OP, ES, OS, 64, 64, 2, 2, 5><<<(unsigned)tiles, 256, 0, stream>>>(tab, sh);
   return hipGetLastError();
 }
 
 }  // namespace
 
 ExpertTile expert_tile(ExpertOp op, int es, const ExpertShape& sh, int64_t max_rows, int64_t rows) {
+  const char* e = getenv("CCR_TILE");
+  if (e) {
+    int m = atoi(e);
+    if (m == 16 && op == ExpertOp::kWgrad) m = 64;
+    if (m == 256 && es == 4) m = 128;
+    return m == 16 ? ExpertTile{16, 64} : ExpertTile{m, m};
+  }
   if (es == 2 && rows >= 4096) return ExpertTile{256, 256};
   return ExpertTile{128, 128};
 }
