@@ -2186,31 +2186,37 @@ ccr_status_t run_experts(ccr_ctx* ctx, ExpertOp op, const void* const* a, const 
     tiles = 0;
     return CCR_OK;
   };
-  for (int d = 0; d < R; d++) {
-    int64_t row = 0;
-    for (int l = 0; l < eloc; l++) {
-      const int64_t n = rows[(size_t)d * eloc + l];
-      if (n > 0 || (op == ExpertOp::kWgrad && !add)) {
-        const int64_t more = tiles_of(n);
-        if (tab.n == kExpertGroups || tiles + more > kMaxTiles) CCR_TRY(flush());
-        ExpertGroup& g = tab.g[tab.n];
-        const char *pa = static_cast<const char*>(a[d]), *pb = static_cast<const char*>(b[d]);
-        char* pc = static_cast<char*>(c[d]);
-        g.rows = (int32_t)n;
-        if (op == ExpertOp::kWgrad) {
-          g.a = pa + row * F * es;
-          g.b = pb + row * H * es;
-          g.c = pc + l * wsize * os;
-        } else {
-          g.a = pa + row * (op == ExpertOp::kProduct ? H : F) * es;
-          g.b = pb + l * wsize * es;
-          g.c = pc + row * N * es;
-        }
-        tab.tile0[tab.n++] = (int32_t)tiles;
-        tiles += more;
-      }
-      row += n;
+  // the experts with work, and each one's first row in its rank's buffers
+  std::vector<int64_t> first((size_t)E);
+  std::vector<int> listed;
+  for (int e = 0; e < E; e++) {
+    first[(size_t)e] = e % eloc ? first[(size_t)e - 1] + rows[(size_t)e - 1] : 0;
+    if (rows[(size_t)e] > 0 || (op == ExpertOp::kWgrad && !add)) listed.push_back(e);
+  }
+  // a weight gradient's tiles take as long as its expert has rows: longest first
+  if (op == ExpertOp::kWgrad)
+    std::stable_sort(listed.begin(), listed.end(),
+                     [&](int x, int y) { return rows[(size_t)x] > rows[(size_t)y]; });
+  for (const int e : listed) {
+    const int d = e / eloc, l = e % eloc;
+    const int64_t n = rows[(size_t)e], row = first[(size_t)e];
+    const int64_t more = tiles_of(n);
+    if (tab.n == kExpertGroups || tiles + more > kMaxTiles) CCR_TRY(flush());
+    ExpertGroup& g = tab.g[tab.n];
+    const char *pa = static_cast<const char*>(a[d]), *pb = static_cast<const char*>(b[d]);
+    char* pc = static_cast<char*>(c[d]);
+    g.rows = (int32_t)n;
+    if (op == ExpertOp::kWgrad) {
+      g.a = pa + row * F * es;
+      g.b = pb + row * H * es;
+      g.c = pc + l * wsize * os;
+    } else {
+      g.a = pa + row * (op == ExpertOp::kProduct ? H : F) * es;
+      g.b = pb + l * wsize * es;
+      g.c = pc + row * N * es;
     }
+    tab.tile0[tab.n++] = (int32_t)tiles;
+    tiles += more;
   }
   return tab.n > 0 ? flush() : CCR_OK;
 }
