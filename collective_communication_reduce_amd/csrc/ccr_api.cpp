@@ -2169,11 +2169,20 @@ ccr_status_t run_experts(ccr_ctx* ctx, ExpertOp op, const void* const* a, const 
   }
   CCR_TRY(check_touched(std::move(t)));
   const ExpertShape sh{H, F, add};
-  const ExpertTile tile = expert_tile(op, es, sh, most, total);
+  // the experts with work, and each one's first row in its rank's buffers
+  std::vector<int64_t> first((size_t)E), work;
+  std::vector<int> listed;
+  for (int e = 0; e < E; e++) {
+    first[(size_t)e] = e % eloc ? first[(size_t)e - 1] + rows[(size_t)e - 1] : 0;
+    if (rows[(size_t)e] > 0 || (op == ExpertOp::kWgrad && !add)) {
+      listed.push_back(e);
+      work.push_back(rows[(size_t)e]);
+    }
+  }
+  const ExpertTile tile = expert_tile(op, es, os, sh, work.data(), (int)work.size());
+  const int side = expert_tile_size(tile);
   const int64_t N = op == ExpertOp::kProduct ? F : H;
-  auto tiles_of = [&](int64_t n) {
-    return ceil_div(op == ExpertOp::kWgrad ? F : n, tile.m) * ceil_div(N, tile.n);
-  };
+  auto tiles_of = [&](int64_t n) { return ceil_div(op == ExpertOp::kWgrad ? F : n, side) * ceil_div(N, side); };
   // one launch's grid, in work-items, is counted in 32 bits
   constexpr int64_t kMaxTiles = int64_t(UINT32_MAX) / 512;
   if (tiles_of(most) > kMaxTiles) return fail(CCR_ERR_UNSUPPORTED, "an expert's product is too large for one launch");
@@ -2186,13 +2195,6 @@ ccr_status_t run_experts(ccr_ctx* ctx, ExpertOp op, const void* const* a, const 
     tiles = 0;
     return CCR_OK;
   };
-  // the experts with work, and each one's first row in its rank's buffers
-  std::vector<int64_t> first((size_t)E);
-  std::vector<int> listed;
-  for (int e = 0; e < E; e++) {
-    first[(size_t)e] = e % eloc ? first[(size_t)e - 1] + rows[(size_t)e - 1] : 0;
-    if (rows[(size_t)e] > 0 || (op == ExpertOp::kWgrad && !add)) listed.push_back(e);
-  }
   // a weight gradient's tiles take as long as its expert has rows: longest first
   if (op == ExpertOp::kWgrad)
     std::stable_sort(listed.begin(), listed.end(),

@@ -14,7 +14,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <cstdlib>
+#include <cmath>
 
 #include "ccr_device.h"
 #include "ccr_internal.h"
@@ -191,7 +191,7 @@ __device__ __forceinline__ int xcd_tile(int b, int n) {
 // gradients, whose tiles take as long as their expert has rows and are listed
 // from the longest on: each round's tiles are dealt out in one piece, the later
 // rounds in reverse, so that who had a long tile gets a short one (a training
-// layer of 16 experts of 518 to 5999 rows: 323 us with contiguous runs, 259 us so).
+// layer of 16 experts of 518 to 5999 rows: 323 us with contiguous runs, 274 us so).
 constexpr int kCus = 256;
 template <bool UNEQUAL>
 __device__ __forceinline__ int tile_of(int b, int r, int n) {
@@ -678,37 +678,76 @@ __global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable t
 template <ExpertOp OP, int ES, int OS>
 hipError_t launch_as(const ExpertTable& tab, const ExpertShape& sh, ExpertTile tile, int tiles,
                      hipStream_t stream) {
-  if constexpr (ES == 2)
-    if (tile.m == 256) {
-      // one workgroup for each compute unit, which its LDS fills
-      experts_big_kernel<OP, OS><<<(unsigned)(tiles < kCus ? tiles : kCus), 256, 0, stream>>>(tab, sh, tiles);
-      return hipGetLastError();
-    }
-  if (tile.m == 128) {
-    experts_ring_kernel<OP, ES, OS, 128, 128, 2, 2, 2><<<(unsigned)tiles, 256, 0, stream>>>(tab, sh);
-    return hipGetLastError();
+  switch (tile) {
+    case ExpertTile::k64:  // 48 KiB of LDS: three workgroups to a compute unit
+      experts_ring_kernel<OP, ES, OS, 64, 64, 2, 2, 3><<<(unsigned)tiles, 256, 0, stream>>>(tab, sh);
+      break;
+    case ExpertTile::k128:  // 128 KiB: one
+      experts_ring_kernel<OP, ES, OS, 128, 128, 2, 4, 4><<<(unsigned)tiles, 512, 0, stream>>>(tab, sh);
+      break;
+    case ExpertTile::k256:
+      if constexpr (ES == 2)
+        experts_big_kernel<OP, OS><<<(unsigned)(tiles < kCus ? tiles : kCus), 256, 0, stream>>>(tab, sh,
+                                                                                              tiles);
+      else
+        return hipErrorInvalidValue;
+      break;
   }
-  if constexpr (OP != ExpertOp::kWgrad)
-    if (tile.m == 16) {
-      experts_ring_kernel<OP, ES, OS, 16, 64, 1, 2, 6><<<(unsigned)tiles, 128, 0, stream>>>(tab, sh);
-      return hipGetLastError();
-    }
-  experts_ring_kernel<OP, ES, OS, 64, 64, 2, 2, 5><<<(unsigned)tiles, 256, 0, stream>>>(tab, sh);
   return hipGetLastError();
 }
 
 }  // namespace
 
-ExpertTile expert_tile(ExpertOp op, int es, const ExpertShape& sh, int64_t max_rows, int64_t rows) {
-  const char* e = getenv("CCR_TILE");
-  if (e) {
-    int m = atoi(e);
-    if (m == 16 && op == ExpertOp::kWgrad) m = 64;
-    if (m == 256 && es == 4) m = 128;
-    return m == 16 ? ExpertTile{16, 64} : ExpertTile{m, m};
+int expert_tile_size(ExpertTile tile) {
+  return tile == ExpertTile::k64 ? 64 : tile == ExpertTile::k128 ? 128 : 256;
+}
+
+// The variant with the shortest estimated time.  A tile of s K-steps is taken
+// to cost c0 + c1 s + its output at an even share of 4.9 TB/s, and tiles to
+// run in rounds of one to a compute unit (of the 64-tiles, of which a unit
+// holds three, in fractions of a round).  c0 and c1 in us were fitted to all
+// three products of 22 shapes from 1 to 16000 rows; where the choice matters:
+//   bf16 product, us at tile          64    128    256
+//   8 x 16 rows, 512 x 512           4.4    6.0   13.9
+//   8 x 200 rows, 2048 x 2048       31.2   21.7   44.2
+//   8 x 2000 rows, 1024 x 1024      62.6   50.6   35.7
+//   4 x 1500 rows, 2048 x 2048      80.4   62.4   50.4
+// and weight gradients (fp32 out) of 64 x 4 rows, 2048 x 1024: 161, 181, 109.
+// fp32 products run at the rate of the matrix units with either tile.
+ExpertTile expert_tile(ExpertOp op, int es, int os, const ExpertShape& sh, const int64_t* rows, int n) {
+  struct Cost {
+    ExpertTile tile;
+    double c0, c1;
+  };
+  const Cost costs[] = {{ExpertTile::k64, 0.4, es == 2 ? 0.2 : 0.5},
+                        {ExpertTile::k128, 2.0, es == 2 ? 0.5 : 2.0},
+                        {ExpertTile::k256, 2.0, 1.42}};
+  ExpertTile best = ExpertTile::k64;
+  double least = 0;
+  for (const Cost& c : costs) {
+    if (c.tile == ExpertTile::k256 && es == 4) continue;
+    const int x = expert_tile_size(c.tile), step = KB / es;
+    const double fixed = c.c0 + (double)x * x * os / 19000.0;
+    const int64_t across = ((op == ExpertOp::kProduct ? sh.F : sh.H) + x - 1) / x;
+    double tiles = 0, work = 0, longest = 0;
+    for (int i = 0; i < n; i++) {
+      const int64_t down = ((op == ExpertOp::kWgrad ? sh.F : rows[i]) + x - 1) / x;
+      const int64_t k = op == ExpertOp::kProduct ? sh.H : op == ExpertOp::kDgrad ? sh.F : rows[i];
+      const double t = fixed + c.c1 * (double)((k + step - 1) / step);
+      tiles += (double)(down * across);
+      work += t * (double)(down * across);
+      longest = t > longest ? t : longest;
+    }
+    double est = work / kCus;
+    if (c.tile != ExpertTile::k64 && op != ExpertOp::kWgrad) est = longest * ceil(tiles / kCus);
+    else if (est > longest && op == ExpertOp::kWgrad) est += longest / 2;  // the last round's unevenness
+    if (est < longest) est = longest;
+    if (least == 0 || est < least) {
+      least = est;
+      best = c.tile;
+    }
   }
-  if (es == 2 && rows >= 4096) return ExpertTile{256, 256};
-  return ExpertTile{128, 128};
+  return best;
 }
 
 hipError_t launch_experts(ExpertOp op, int es, int os, const ExpertTable& tab, const ExpertShape& sh,

@@ -213,12 +213,11 @@ struct ExpertShape {
   int64_t H, F;
   bool add;  // wgrad: add to what c holds
 };
-// Output tile of the kernel variant that a launch takes.
-struct ExpertTile {
-  int m, n;
-};
-// The variant for groups of `max_rows` rows at most and `rows` in all.
-ExpertTile expert_tile(ExpertOp op, int es, const ExpertShape& sh, int64_t max_rows, int64_t rows);
+// Kernel variants, by the side of their output tile.
+enum class ExpertTile : int { k64, k128, k256 };
+int expert_tile_size(ExpertTile tile);
+// The variant for n experts of rows[i] rows.
+ExpertTile expert_tile(ExpertOp op, int es, int os, const ExpertShape& sh, const int64_t* rows, int n);
 // es, os: bytes per input and output value; tiles: in all, numbered group by group.
 hipError_t launch_experts(ExpertOp op, int es, int os, const ExpertTable& tab, const ExpertShape& sh,
                           ExpertTile tile, int tiles, hipStream_t stream);
