@@ -679,7 +679,10 @@ template <ExpertOp OP, int ES, int OS>
 hipError_t launch_as(const ExpertTable& tab, const ExpertShape& sh, ExpertTile tile, int tiles,
                      hipStream_t stream) {
   switch (tile) {
-    case ExpertTile::k64:  // 48 KiB of LDS: three workgroups to a compute unit
+    case ExpertTile::k32:  // 32 KiB of LDS: five workgroups to a compute unit
+      experts_ring_kernel<OP, ES, OS, 32, 32, 2, 2, 4><<<(unsigned)tiles, 256, 0, stream>>>(tab, sh);
+      break;
+    case ExpertTile::k64:  // 48 KiB: three
       experts_ring_kernel<OP, ES, OS, 64, 64, 2, 2, 3><<<(unsigned)tiles, 256, 0, stream>>>(tab, sh);
       break;
     case ExpertTile::k128:  // 128 KiB: one
@@ -699,30 +702,34 @@ hipError_t launch_as(const ExpertTable& tab, const ExpertShape& sh, ExpertTile t
 }  // namespace
 
 int expert_tile_size(ExpertTile tile) {
-  return tile == ExpertTile::k64 ? 64 : tile == ExpertTile::k128 ? 128 : 256;
+  return tile == ExpertTile::k32 ? 32 : tile == ExpertTile::k64 ? 64 : tile == ExpertTile::k128 ? 128 : 256;
 }
 
 // The variant with the shortest estimated time.  A tile of s K-steps is taken
 // to cost c0 + c1 s + its output at an even share of 4.9 TB/s, and tiles to
-// run in rounds of one to a compute unit (of the 64-tiles, of which a unit
-// holds three, in fractions of a round).  c0 and c1 in us were fitted to all
-// three products of 22 shapes from 1 to 16000 rows; where the choice matters:
-//   bf16 product, us at tile          64    128    256
-//   8 x 16 rows, 512 x 512           4.4    6.0   13.9
-//   8 x 200 rows, 2048 x 2048       31.2   21.7   44.2
-//   8 x 2000 rows, 1024 x 1024      62.6   50.6   35.7
-//   4 x 1500 rows, 2048 x 2048      80.4   62.4   50.4
-// and weight gradients (fp32 out) of 64 x 4 rows, 2048 x 1024: 161, 181, 109.
-// fp32 products run at the rate of the matrix units with either tile.
+// run in rounds of one to a compute unit (of the smaller tiles, of which a unit
+// holds several, in fractions of a round).  c0 and c1 in us were fitted to all
+// three products of 24 shapes from 1 to 16000 rows; where the choice matters:
+//   bf16 product, us at tile          32     64    128    256
+//   1 row, 2048 x 1024               5.8    9.3   14.6   36.7
+//   8 x 16 rows, 512 x 512           3.4    4.4    6.0   13.9
+//   4 x 500 rows, 1024 x 1024       13.2    9.1   11.4   26.7
+//   8 x 200 rows, 2048 x 2048       41.3   30.5   21.7   44.2
+//   8 x 2000 rows, 1024 x 1024      95.3   59.4   50.6   35.7
+//   4 x 1500 rows, 2048 x 2048       131   77.7   62.4   50.4
+// fp32 products of 8 x 16 rows, 512 x 512: 5.5, 11.2, 32.3; weight gradients
+// (fp32 out) of 64 x 4 rows, 2048 x 1024: 268, 161, 181, 109.  Large fp32
+// products run at the rate of the matrix units from tile 64 on.
 ExpertTile expert_tile(ExpertOp op, int es, int os, const ExpertShape& sh, const int64_t* rows, int n) {
   struct Cost {
     ExpertTile tile;
     double c0, c1;
   };
-  const Cost costs[] = {{ExpertTile::k64, 0.4, es == 2 ? 0.2 : 0.5},
+  const Cost costs[] = {{ExpertTile::k32, 0.25, es == 2 ? 0.09 : 0.15},
+                        {ExpertTile::k64, 0.4, es == 2 ? 0.2 : 0.5},
                         {ExpertTile::k128, 2.0, es == 2 ? 0.5 : 2.0},
-                        {ExpertTile::k256, 2.0, 1.42}};
-  ExpertTile best = ExpertTile::k64;
+                        {ExpertTile::k256, 1.0, 1.42}};
+  ExpertTile best = ExpertTile::k32;
   double least = 0;
   for (const Cost& c : costs) {
     if (c.tile == ExpertTile::k256 && es == 4) continue;
@@ -739,8 +746,8 @@ ExpertTile expert_tile(ExpertOp op, int es, int os, const ExpertShape& sh, const
       longest = t > longest ? t : longest;
     }
     double est = work / kCus;
-    if (c.tile != ExpertTile::k64 && op != ExpertOp::kWgrad) est = longest * ceil(tiles / kCus);
-    else if (est > longest && op == ExpertOp::kWgrad) est += longest / 2;  // the last round's unevenness
+    if (x >= 128 && op != ExpertOp::kWgrad) est = longest * ceil(tiles / kCus);
+    else if (x >= 128 && est > longest) est += longest / 4;  // the last round's unevenness
     if (est < longest) est = longest;
     if (least == 0 || est < least) {
       least = est;
