@@ -302,23 +302,34 @@ ccr_status_t check_ctx(ccr_ctx* ctx) {
 }
 
 // A device pointer on this context's device, aligned to `align` bytes, whose
-// next nbytes bytes lie inside one HIP allocation.  `known`, if given, is the
-// last allocation that this call found on the device: a pointer inside it
+// next nbytes bytes lie inside one HIP allocation.  `known`, if given, holds
+// the allocations that this call has found on the device: a pointer inside one
 // needs no further query (a call over hundreds of tensors carved from a few
 // allocations makes a few).
-struct KnownRange {
-  uintptr_t lo = 0, hi = 0;
+struct KnownRanges {
+  static constexpr int kHeld = 8;
+  uintptr_t lo[kHeld] = {}, hi[kHeld] = {};
+  int next = 0;
+  bool hold(uintptr_t q, int64_t nbytes) const {
+    for (int i = 0; i < kHeld; i++)
+      if (q >= lo[i] && q < hi[i] && (uint64_t)nbytes <= (uint64_t)(hi[i] - q)) return true;
+    return false;
+  }
+  void add(uintptr_t a, uintptr_t b) {
+    lo[next] = a;
+    hi[next] = b;
+    next = (next + 1) % kHeld;
+  }
 };
 
 ccr_status_t check_dev_range(ccr_ctx* ctx, const void* p, int64_t nbytes, int align,
-                             const char* what, int index, KnownRange* known) {
+                             const char* what, int index, KnownRanges* known) {
   if (nbytes == 0) return CCR_OK;  // never dereferenced (an empty tensor may even be NULL)
   if (!p) return fail(CCR_ERR_INVALID_ARG, "%s[%d] is NULL", what, index);
   const uintptr_t q = reinterpret_cast<uintptr_t>(p);
   if (q % (uintptr_t)align != 0)
     return fail(CCR_ERR_INVALID_ARG, "%s[%d] = %p is not %d-byte aligned", what, index, p, align);
-  if (known && q >= known->lo && q < known->hi && (uint64_t)nbytes <= (uint64_t)(known->hi - q))
-    return CCR_OK;
+  if (known && known->hold(q, nbytes)) return CCR_OK;
   hipPointerAttribute_t attr;
   hipError_t e = hipPointerGetAttributes(&attr, p);
   if (e != hipSuccess) {
@@ -341,7 +352,7 @@ ccr_status_t check_dev_range(ccr_ctx* ctx, const void* p, int64_t nbytes, int al
   if (q < b || (uint64_t)nbytes > (uint64_t)(b + size - q))
     return fail(CCR_ERR_INVALID_ARG, "%s[%d] = %p: %lld bytes run past the end of its allocation",
                 what, index, p, (long long)nbytes);
-  if (known) *known = KnownRange{b, b + size};
+  if (known) known->add(b, b + size);
   return CCR_OK;
 }
 
@@ -2147,7 +2158,7 @@ ccr_status_t run_experts(ccr_ctx* ctx, ExpertOp op, const void* const* a, const 
   if (total > INT32_MAX) return fail(CCR_ERR_UNSUPPORTED, "more than 2^31 - 1 rows");
   const int64_t wsize = F * H;  // one expert's weight, in values
   std::vector<Touched> t;
-  KnownRange known;
+  KnownRanges known;
   for (int d = 0; d < R; d++) {
     const int64_t n = rank_rows[(size_t)d];
     int64_t ab, bb, cb;
@@ -2244,7 +2255,7 @@ ccr_status_t run_gate(ccr_ctx* ctx, bool bwd, const void* const* dy, const void*
   if (T == 0) return CCR_OK;
   const int64_t rb = T * K * H * es, yb = T * H * es, lb = T * E * 4, kb = T * K * 4;
   std::vector<Touched> t;
-  KnownRange known;
+  KnownRanges known;
   GateArgs args{};
   auto add = [&](const void* p, int64_t n, bool written, const char* what, int r) -> ccr_status_t {
     CCR_TRY(check_dev_range(ctx, p, n, 16, what, r, &known));
@@ -2286,71 +2297,106 @@ ccr_status_t run_grads(ccr_ctx* ctx, bool clip, const void* const* grads, void* 
   if (n > 0 && (!grads || !counts || !dtypes))
     return fail(CCR_ERR_INVALID_ARG, "grads, counts or dtypes is NULL");
   if (clip && !(max_norm >= 0.0f)) return fail(CCR_ERR_INVALID_ARG, "max_norm %g is not >= 0", max_norm);
-  std::vector<Touched> t;
-  t.reserve((size_t)n * 2 + 2);
-  KnownRange known, known_out;
   if (!work || !norm) return fail(CCR_ERR_INVALID_ARG, "work or norm is NULL");
-  CCR_TRY(check_dev_range(ctx, work, CCR_GRAD_WORK * 8, 8, "work", 0, nullptr));
-  CCR_TRY(check_dev_range(ctx, norm, 4, 4, "norm", 0, nullptr));
-  touch(&t, work, CCR_GRAD_WORK * 8, true, "work", 0);
-  touch(&t, norm, 4, true, "norm", 0);
-  int64_t most = 1;  // tiles of the largest launch
-  int64_t tiles = 0;
-  int held = 0;
+  KnownRanges known;
+  CCR_TRY(check_dev_range(ctx, work, CCR_GRAD_WORK * 8, 8, "work", 0, &known));
+  CCR_TRY(check_dev_range(ctx, norm, 4, 4, "norm", 0, &known));
+  // The tensors with elements; neighbours in memory (views that fill a bucket
+  // one after the other) become one.
+  constexpr int64_t kMaxCount = int64_t(1) << 40;
+  std::vector<GradTensor> list;
+  std::vector<int> index;  // of the caller's tensor that each one starts with
+  list.reserve((size_t)n);
+  index.reserve((size_t)n);
+  int64_t bytes = 0;
   for (int i = 0; i < n; i++) {
     const int es = dtype_size(dtypes[i]);
     if (!es) return fail(CCR_ERR_INVALID_ARG, "dtypes[%d] = %d is not CCR_F32 or CCR_BF16", i, dtypes[i]);
     if (counts[i] < 0) return fail(CCR_ERR_INVALID_ARG, "counts[%d] < 0", i);
-    if (counts[i] > (int64_t(1) << 40)) return fail(CCR_ERR_UNSUPPORTED, "counts[%d] exceeds 2^40", i);
+    if (counts[i] > kMaxCount) return fail(CCR_ERR_UNSUPPORTED, "counts[%d] exceeds 2^40", i);
     if (counts[i] == 0) continue;
-    const int64_t bytes = counts[i] * es;
-    CCR_TRY(check_dev_range(ctx, grads[i], bytes, es, "grads", i, &known));
-    const bool apart = clip && out && out[i] != grads[i];
-    if (apart) CCR_TRY(check_dev_range(ctx, out[i], bytes, es, "out", i, &known_out));
-    touch(&t, grads[i], bytes, clip && !apart, "grads", i);
-    if (apart) touch(&t, out[i], bytes, true, "out", i);
-    const int64_t k = grad_tiles(grads[i], counts[i], es);
-    if (held == kGradTensors || tiles + k > INT32_MAX) {
-      held = 0;
-      tiles = 0;
+    const GradTensor t{static_cast<const char*>(grads[i]),
+                       const_cast<char*>(static_cast<const char*>(clip && out ? out[i] : grads[i])),
+                       counts[i], es};
+    CCR_TRY(check_dev_range(ctx, t.src, t.count * es, es, "grads", i, &known));
+    if (t.dst != t.src) CCR_TRY(check_dev_range(ctx, t.dst, t.count * es, es, "out", i, &known));
+    bytes += t.count * es;
+    if (!list.empty()) {
+      GradTensor& last = list.back();
+      const int64_t lb = last.count * es;
+      if (last.es == es && last.src + lb == t.src && last.dst + lb == t.dst &&
+          last.count + t.count <= kMaxCount) {
+        last.count += t.count;
+        continue;
+      }
     }
-    if (k > INT32_MAX) return fail(CCR_ERR_UNSUPPORTED, "counts[%d] is too large", i);
-    held++;
-    tiles += k;
-    most = std::max(most, tiles);
+    list.push_back(t);
+    index.push_back(i);
   }
-  CCR_TRY(check_touched(std::move(t)));
+  std::vector<Touched> touched;
+  touched.reserve(list.size() * 2 + 2);
+  touch(&touched, work, CCR_GRAD_WORK * 8, true, "work", 0);
+  touch(&touched, norm, 4, true, "norm", 0);
+  for (size_t i = 0; i < list.size(); i++) {
+    const GradTensor& t = list[i];
+    touch(&touched, t.src, t.count * t.es, clip && t.src == t.dst, "grads", index[i]);
+    if (t.src != t.dst) touch(&touched, t.dst, t.count * t.es, true, "out", index[i]);
+  }
+  CCR_TRY(check_touched(std::move(touched)));
+  // One launch per kGradTensors tensors and per 2^31 - 1 tiles: each is the
+  // run of tensors [first, last) with its tiles in all.
+  struct Launch {
+    size_t first, last;
+    int64_t tiles;
+  };
+  std::vector<Launch> launches{{0, 0, 0}};
+  int64_t most = 1, total = 0;
+  for (size_t i = 0; i < list.size(); i++) {
+    const int64_t k = grad_tiles(list[i].src, list[i].count, list[i].es);
+    if (k > INT32_MAX) return fail(CCR_ERR_UNSUPPORTED, "counts[%d] is too large", index[i]);
+    Launch* l = &launches.back();
+    if (l->last - l->first == kGradTensors || l->tiles + k > INT32_MAX) {
+      launches.push_back(Launch{i, i, 0});
+      l = &launches.back();
+    }
+    l->last = i + 1;
+    l->tiles += k;
+    total += k;
+    most = std::max(most, l->tiles);
+  }
   // every launch uses at most the first launch's slots, which it sets
   const int slots = (int)std::min<int64_t>(kGradSlots, most);
+  // What is read once is loaded non-temporally: everything for a norm; of a
+  // clipping that exceeds the last-level cache all but the last three quarters
+  // of a cache, which the second pass begins with.
+  const bool large = bytes * (clip && out ? 2 : 1) > kMallBytes;
+  const int64_t kept = clip ? (large ? kMallBytes / 4 * 3 / grad_tile_bytes() : total) : 0;
   GradTable tab;
-  for (int pass = 0; pass < (clip ? 2 : 1); pass++) {
-    bool first = true;
-    auto flush = [&]() -> ccr_status_t {
-      tab.tile0[tab.n] = (int32_t)tab.ntiles;
-      const int grid = first && pass == 0 ? slots : (int)std::min<int64_t>(slots, std::max<int64_t>(1, tab.ntiles));
-      if (pass == 0) HIP_TRY(launch_grad_squares(tab, grid, work, !first, s));
-      else HIP_TRY(launch_grad_clip(tab, grid, work, slots, max_norm, first ? norm : nullptr, s));
-      first = false;
-      tab.n = 0;
-      tab.ntiles = 0;
-      return CCR_OK;
-    };
+  auto fill = [&](const Launch& l) {
     tab.n = 0;
     tab.ntiles = 0;
-    for (int i = 0; i < n; i++) {
-      if (counts[i] == 0) continue;
-      const int es = dtype_size(dtypes[i]);
-      const int64_t k = grad_tiles(grads[i], counts[i], es);
-      if (tab.n == kGradTensors || tab.ntiles + k > INT32_MAX) CCR_TRY(flush());
+    for (size_t i = l.first; i < l.last; i++) {
       tab.tile0[tab.n] = (int32_t)tab.ntiles;
-      tab.t[tab.n++] = GradTensor{static_cast<const char*>(grads[i]),
-                                  const_cast<char*>(static_cast<const char*>(clip && out ? out[i] : grads[i])),
-                                  counts[i], es};
-      tab.ntiles += k;
+      tab.t[tab.n++] = list[i];
+      tab.ntiles += grad_tiles(list[i].src, list[i].count, list[i].es);
     }
-    if (tab.n > 0 || first) CCR_TRY(flush());
+    tab.tile0[tab.n] = (int32_t)tab.ntiles;
+    return (int)std::min<int64_t>(slots, std::max<int64_t>(1, tab.ntiles));
+  };
+  int64_t before = 0;  // tiles of the launches so far
+  for (size_t i = 0; i < launches.size(); i++) {
+    const int grid = fill(launches[i]);
+    HIP_TRY(launch_grad_squares(tab, i == 0 ? slots : grid, total - kept - before, work, i > 0, s));
+    before += tab.ntiles;
   }
-  if (!clip) HIP_TRY(launch_grad_norm(work, slots, norm, s));
+  if (!clip) {
+    HIP_TRY(launch_grad_norm(work, slots, norm, s));
+    return CCR_OK;
+  }
+  for (size_t i = launches.size(); i-- > 0;) {  // the last gradients first
+    const int grid = fill(launches[i]);
+    HIP_TRY(launch_grad_clip(tab, grid, large, work, slots, max_norm, i == 0 ? norm : nullptr, s));
+  }
   return CCR_OK;
 }
 

@@ -5,9 +5,9 @@
 //   out  = g * min(1, max_norm / (norm + 1e-6))
 //
 // Both are streaming passes bound by HBM.  The tensors of a call are cut into
-// tiles and the tiles dealt to a fixed number of workgroups in contiguous
-// runs, so a call over hundreds of small tensors is still one launch per
-// kGradTensors of them.  Each workgroup leaves one fp64 partial in its own
+// tiles and the tiles dealt round robin to at most kGradSlots workgroups, so a
+// call over hundreds of small tensors is still one launch per kGradTensors of
+// them.  Each workgroup leaves one fp64 partial in its own
 // slot of the caller's work array; the slots are added in a fixed order, so
 // the norm has the same bits on every run.  Squares are taken and added in
 // fp64: the square of any fp32 value is exact in it and neither overflows nor
@@ -24,8 +24,10 @@ namespace {
 
 using dev::u32x4;
 
-constexpr int kVecs = 8;                         // 16-byte vectors per thread and tile
-constexpr int64_t kTileVecs = kBlock * kVecs;    // 32 KiB
+// 16-byte vectors per thread and tile.  Clipping 200 Mi values of both types:
+// 8: 432 us, 4: 335, 2: 348, 1: 411.
+constexpr int kVecs = 4;
+constexpr int64_t kTileVecs = kBlock * kVecs;  // 16 KiB
 
 // A tensor as the kernels walk it: `head` elements up to the first 16-byte
 // boundary, then whole vectors, then a tail shorter than one.
@@ -71,7 +73,7 @@ __device__ __forceinline__ double squares(u32x4 v, double acc) {
   return acc;
 }
 
-template <int ES>
+template <int ES, bool NT>
 __device__ __forceinline__ double tile_squares(const GradTensor& t, int64_t tile, double acc) {
   const Span s = span_of<ES>(t);
   const u32x4* v = reinterpret_cast<const u32x4*>(s.src + (int64_t)s.head * ES);
@@ -80,7 +82,7 @@ __device__ __forceinline__ double tile_squares(const GradTensor& t, int64_t tile
 #pragma unroll
   for (int u = 0; u < kVecs; u++) {
     const int64_t i = first + u * kBlock;
-    x[u] = i < s.nvec ? v[i] : u32x4{0, 0, 0, 0};
+    x[u] = i < s.nvec ? dev::load16<NT>(v + i) : u32x4{0, 0, 0, 0};
   }
 #pragma unroll
   for (int u = 0; u < kVecs; u++) acc = squares<ES>(x[u], acc);
@@ -108,36 +110,33 @@ __device__ __forceinline__ double block_sum(double x, double* part) {
   return s;
 }
 
-// Tiles [lo, hi) of workgroup b of g, and the tensor that holds tile lo.
-__device__ __forceinline__ void my_tiles(const GradTable& tab, int64_t* lo, int64_t* hi, int* at) {
-  const int64_t b = blockIdx.x, g = gridDim.x, per = tab.ntiles / g, rem = tab.ntiles % g;
-  *lo = b * per + (b < rem ? b : rem);
-  *hi = *lo + per + (b < rem ? 1 : 0);
-  int i = 0;
-  if (*lo < *hi) {
-    int a = 0, z = tab.n - 1;
-    while (a < z) {
-      const int mid = (a + z + 1) >> 1;
-      if (tab.tile0[mid] <= *lo) a = mid; else z = mid - 1;
-    }
-    i = a;
+// The tensor that holds tile `tile`: the last whose first tile is at or before
+// it.  Every lane looks at one or two first tiles.
+__device__ __forceinline__ int tensor_of(const GradTable& tab, int64_t tile) {
+  const int lane = threadIdx.x & 63;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kGradTensors; i += 64) {
+    const int j = i + lane < tab.n ? i + lane : 0;
+    n += __popcll(__ballot(i + lane < tab.n && tab.tile0[j] <= tile));
   }
-  *at = i;
+  return __builtin_amdgcn_readfirstlane(n - 1);
 }
 
 // One partial per workgroup: work[b] = (add ? work[b] : 0) + its tiles' sum.
-__global__ __launch_bounds__(kBlock) void grad_squares_kernel(const GradTable tab, double* work,
-                                                              int add) {
+// Tiles below `stream` are loaded non-temporally.
+__global__ __launch_bounds__(kBlock) void grad_squares_kernel(const GradTable tab, int64_t stream,
+                                                              double* work, int add) {
   __shared__ double part[kBlock / 64];
-  int64_t lo, hi;
-  int at;
-  my_tiles(tab, &lo, &hi, &at);
   double acc = 0;
-  for (int64_t tile = lo; tile < hi; tile++) {
-    while (tile >= tab.tile0[at + 1]) at++;
+  for (int64_t tile = blockIdx.x; tile < tab.ntiles; tile += gridDim.x) {
+    const int at = tensor_of(tab, tile);
     const GradTensor& t = tab.t[at];
-    if (t.es == 4) acc = tile_squares<4>(t, tile - tab.tile0[at], acc);
-    else acc = tile_squares<2>(t, tile - tab.tile0[at], acc);
+    const int64_t in = tile - tab.tile0[at];
+    if (tile < stream)
+      acc = t.es == 4 ? tile_squares<4, true>(t, in, acc) : tile_squares<2, true>(t, in, acc);
+    else
+      acc = t.es == 4 ? tile_squares<4, false>(t, in, acc) : tile_squares<2, false>(t, in, acc);
   }
   const double s = block_sum(acc, part);
   if (threadIdx.x == 0) work[blockIdx.x] = add ? work[blockIdx.x] + s : s;
@@ -180,7 +179,7 @@ __device__ __forceinline__ void scale_element(const Span& s, int64_t i, float c)
   else reinterpret_cast<__bf16*>(s.dst)[i] = static_cast<__bf16>(r);
 }
 
-template <int ES>
+template <int ES, bool NT>
 __device__ __forceinline__ void tile_scale(const GradTensor& t, int64_t tile, float c) {
   const Span s = span_of<ES>(t);
   const u32x4* v = reinterpret_cast<const u32x4*>(s.src + (int64_t)s.head * ES);
@@ -190,13 +189,13 @@ __device__ __forceinline__ void tile_scale(const GradTensor& t, int64_t tile, fl
 #pragma unroll
   for (int u = 0; u < kVecs; u++) {
     const int64_t i = first + u * kBlock;
-    if (i < s.nvec) x[u] = v[i];
+    if (i < s.nvec) x[u] = dev::load16<NT>(v + i);
   }
   if ((reinterpret_cast<uintptr_t>(out) & 15) == 0) {
 #pragma unroll
     for (int u = 0; u < kVecs; u++) {
       const int64_t i = first + u * kBlock;
-      if (i < s.nvec) reinterpret_cast<u32x4*>(out)[i] = scaled<ES>(x[u], c);
+      if (i < s.nvec) dev::store16<NT>(reinterpret_cast<u32x4*>(out) + i, scaled<ES>(x[u], c));
     }
   } else {  // the result's buffer starts at another offset within 16 bytes
 #pragma unroll
@@ -223,6 +222,8 @@ __device__ __forceinline__ void tile_scale(const GradTensor& t, int64_t tile, fl
 // first: the pass before left the end of the gradients in the last-level
 // cache.  Every workgroup adds the slots itself (16 KiB from L2), which saves
 // a launch between the two passes.  In place, a factor of 1 writes nothing.
+// NT: loads and stores are non-temporal.
+template <bool NT>
 __global__ __launch_bounds__(kBlock) void grad_clip_kernel(const GradTable tab, const double* work,
                                                            int slots, float max_norm, float* norm) {
   __shared__ double part[kBlock / 64];
@@ -230,21 +231,19 @@ __global__ __launch_bounds__(kBlock) void grad_clip_kernel(const GradTable tab, 
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = nv;
   const float q = max_norm / (nv + 1e-6f);
   const float c = q > 1.0f ? 1.0f : q;  // a NaN stays
-  int64_t lo, hi;
-  int at;
-  my_tiles(tab, &lo, &hi, &at);
-  if (lo >= hi) return;
-  while (hi - 1 >= tab.tile0[at + 1]) at++;
-  for (int64_t tile = hi - 1; tile >= lo; tile--) {
-    while (tile < tab.tile0[at]) at--;
+  for (int64_t tile = tab.ntiles - 1 - blockIdx.x; tile >= 0; tile -= gridDim.x) {
+    const int at = tensor_of(tab, tile);
     const GradTensor& t = tab.t[at];
     if (c == 1.0f && t.src == t.dst) continue;
-    if (t.es == 4) tile_scale<4>(t, tile - tab.tile0[at], c);
-    else tile_scale<2>(t, tile - tab.tile0[at], c);
+    const int64_t in = tile - tab.tile0[at];
+    if (t.es == 4) tile_scale<4, NT>(t, in, c);
+    else tile_scale<2, NT>(t, in, c);
   }
 }
 
 }  // namespace
+
+int64_t grad_tile_bytes() { return kTileVecs * 16; }
 
 int64_t grad_tiles(const void* p, int64_t count, int es) {
   const int64_t to_edge = ((16 - (int)(reinterpret_cast<uintptr_t>(p) & 15)) & 15) / es;
@@ -253,9 +252,9 @@ int64_t grad_tiles(const void* p, int64_t count, int es) {
   return t > 0 ? t : 1;
 }
 
-hipError_t launch_grad_squares(const GradTable& tab, int grid, double* work, bool add,
-                               hipStream_t stream) {
-  grad_squares_kernel<<<(unsigned)grid, kBlock, 0, stream>>>(tab, work, add ? 1 : 0);
+hipError_t launch_grad_squares(const GradTable& tab, int grid, int64_t stream_tiles, double* work,
+                               bool add, hipStream_t stream) {
+  grad_squares_kernel<<<(unsigned)grid, kBlock, 0, stream>>>(tab, stream_tiles, work, add ? 1 : 0);
   return hipGetLastError();
 }
 
@@ -264,9 +263,12 @@ hipError_t launch_grad_norm(const double* work, int slots, float* norm, hipStrea
   return hipGetLastError();
 }
 
-hipError_t launch_grad_clip(const GradTable& tab, int grid, const double* work, int slots,
-                            float max_norm, float* norm, hipStream_t stream) {
-  grad_clip_kernel<<<(unsigned)grid, kBlock, 0, stream>>>(tab, work, slots, max_norm, norm);
+hipError_t launch_grad_clip(const GradTable& tab, int grid, bool nontemporal, const double* work,
+                            int slots, float max_norm, float* norm, hipStream_t stream) {
+  if (nontemporal)
+    grad_clip_kernel<true><<<(unsigned)grid, kBlock, 0, stream>>>(tab, work, slots, max_norm, norm);
+  else
+    grad_clip_kernel<false><<<(unsigned)grid, kBlock, 0, stream>>>(tab, work, slots, max_norm, norm);
   return hipGetLastError();
 }
 

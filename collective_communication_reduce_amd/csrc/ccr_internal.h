@@ -256,13 +256,15 @@ static_assert(sizeof(GradTable) <= 4056, "fits the kernel argument segment");
 constexpr int kGradSlots = 2048;
 // Tiles of a tensor of `count` > 0 elements of es bytes at p.
 int64_t grad_tiles(const void* p, int64_t count, int es);
-// work[b] (+)= the sum of squares of workgroup b's tiles.
-hipError_t launch_grad_squares(const GradTable& tab, int grid, double* work, bool add,
-                               hipStream_t stream);
+int64_t grad_tile_bytes();
+// work[b] (+)= the sum of squares of workgroup b's tiles; tiles below
+// stream_tiles are loaded non-temporally.
+hipError_t launch_grad_squares(const GradTable& tab, int grid, int64_t stream_tiles, double* work,
+                               bool add, hipStream_t stream);
 hipError_t launch_grad_norm(const double* work, int slots, float* norm, hipStream_t stream);
 // norm may be NULL (a later launch of the same call).
-hipError_t launch_grad_clip(const GradTable& tab, int grid, const double* work, int slots,
-                            float max_norm, float* norm, hipStream_t stream);
+hipError_t launch_grad_clip(const GradTable& tab, int grid, bool nontemporal, const double* work,
+                            int slots, float max_norm, float* norm, hipStream_t stream);
 
 // One wave64 workgroup per block; writes (XCC id, SE id, CU id) per block.
 hipError_t launch_probe_cu_ids(int32_t* out, int nblocks, hipStream_t stream);
