@@ -2283,7 +2283,8 @@ ccr_status_t run_gate(ccr_ctx* ctx, bool bwd, const void* const* dy, const void*
   }
   CCR_TRY(check_touched(std::move(t)));
   if (T > kMaxGridWorkgroups / R) return fail(CCR_ERR_UNSUPPORTED, "R x T is too large for one launch");
-  HIP_TRY(launch_gate_sum(bwd, norm == CCR_GATE_ALL, es, args, R, T, E, K, H * es, s));
+  HIP_TRY(launch_gate_sum(bwd, norm == CCR_GATE_ALL, es, args, R, T, E, K, H * es,
+                          R * (rb + yb) > kMallBytes, s));
   return CCR_OK;
 }
 

@@ -233,8 +233,9 @@ struct GateArgs {
   float* dlogits[kRingHopMaxRanks];
 };
 static_assert(sizeof(GateArgs) <= 3584, "fits the kernel argument segment");
+// large: rows and results exceed the last-level cache.
 hipError_t launch_gate_sum(bool bwd, bool over_all, int es, const GateArgs& a, int R, int64_t T,
-                           int E, int K, int64_t row_bytes, hipStream_t stream);
+                           int E, int K, int64_t row_bytes, bool large, hipStream_t stream);
 
 // The gradient norm and clipping (ccr_grad.hip).  Up to kGradTensors tensors
 // go into one launch; tile0[i] = first tile of tensor i, tile0[n] = ntiles.
