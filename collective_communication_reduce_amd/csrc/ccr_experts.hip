@@ -332,27 +332,45 @@ __global__ __launch_bounds__(WM * WN * 64) void experts_ring_kernel(const Expert
   for (int i = 0; i < TM; i++)
 #pragma unroll
     for (int n = 0; n < TN; n++) acc[i][n] = f32x4{0, 0, 0, 0};
+  // fp32 results are summed in chains of 64 products, and the chains' sums
+  // apart: the error grows with the length of a chain of additions.  Over 4096
+  // values it is 2e-7 of the result, 1e-6 in one chain; the cost is 2%.
+  constexpr int kChain = ES == 4 ? 8 : 32;  // K-steps
+  f32x4 sum[OS == 4 ? TM : 1][OS == 4 ? TN : 1] = {};
+  auto collect = [&]() {
+#pragma unroll
+    for (int i = 0; i < TM; i++)
+#pragma unroll
+      for (int n = 0; n < TN; n++) {
+        sum[i][n] += acc[i][n];
+        acc[i][n] = f32x4{0, 0, 0, 0};
+      }
+  };
   int cur = 0, free = (NBUF - 1) * kBuf;  // byte offsets of this step's buffer and of the one read before
+  for (int s = 0; s < nk;) {
+    const int until = OS == 4 && s + kChain < nk ? s + kChain : nk;
 #pragma unroll 1
-  for (int s = 0; s < nk; s++) {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NBUF - 2) * kLoads) : "memory");
-    u32x4 a[2][TM], b[2][TN];
+    for (; s < until; s++) {
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NBUF - 2) * kLoads) : "memory");
+      u32x4 a[2][TM], b[2][TN];
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
+      for (int h = 0; h < 2; h++) {
 #pragma unroll
-      for (int i = 0; i < TM; i++) a[h][i] = fragment<ES, BM, kACol, false>(lds + cur, wm, i, h);
+        for (int i = 0; i < TM; i++) a[h][i] = fragment<ES, BM, kACol, false>(lds + cur, wm, i, h);
 #pragma unroll
-      for (int n = 0; n < TN; n++) b[h][n] = fragment<ES, BN, kBCol, false>(lds + cur + kABytes, wn, n, h);
+        for (int n = 0; n < TN; n++) b[h][n] = fragment<ES, BN, kBCol, false>(lds + cur + kABytes, wn, n, h);
+      }
+      issue(lds0 + free);
+      free = cur;
+      cur = cur + kBuf == NBUF * kBuf ? 0 : cur + kBuf;
+#pragma unroll
+      for (int h = 0; h < 2; h++)
+#pragma unroll
+        for (int i = 0; i < TM; i++)
+#pragma unroll
+          for (int n = 0; n < TN; n++) acc[i][n] = mma<ES>(b[h][n], a[h][i], acc[i][n]);
     }
-    issue(lds0 + free);
-    free = cur;
-    cur = cur + kBuf == NBUF * kBuf ? 0 : cur + kBuf;
-#pragma unroll
-    for (int h = 0; h < 2; h++)
-#pragma unroll
-      for (int i = 0; i < TM; i++)
-#pragma unroll
-        for (int n = 0; n < TN; n++) acc[i][n] = mma<ES>(b[h][n], a[h][i], acc[i][n]);
+    if constexpr (OS == 4) collect();
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   // D holds b's rows (the output's columns) down its registers: lane l has
@@ -365,7 +383,7 @@ __global__ __launch_bounds__(WM * WN * 64) void experts_ring_kernel(const Expert
 #pragma unroll
     for (int n = 0; n < TN; n++) {
       const int64_t c = at.n0 + wn + n * 16 + (l >> 4) * 4;
-      if (c < at.N) store4<OS>(at.c + (m * at.N + c) * OS, acc[i][n], sh.add);
+      if (c < at.N) store4<OS>(at.c + (m * at.N + c) * OS, OS == 4 ? sum[i][n] : acc[i][n], sh.add);
     }
   }
 }
