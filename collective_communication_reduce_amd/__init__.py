@@ -13,7 +13,9 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from dataclasses import dataclass
+from operator import attrgetter
 from typing import Optional, Sequence
 
 import numpy as np
@@ -509,45 +511,57 @@ def _ctx_stream(ctx: Context, stream):
     return _stream(torch.cuda.current_stream(ctx.device) if stream is None else stream)
 
 
+def _refuse(ctx: Context, t, i, dtype, shape, what: str):
+    """Say why tensor i of `what` is not what the call takes."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{what}[{i}] is {t.dtype}, not {dtype}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}[{i}] must be a contiguous device tensor")
+    if t.get_device() != ctx.device:
+        raise ValueError(f"{what}[{i}] is on {t.device}, the context on device {ctx.device}")
+    raise ValueError(f"{what}[{i}] has shape {tuple(t.shape)}, needs {tuple(shape)}")
+
+
 def _buffers(ctx: Context, tensors, dtype, shapes, what: str):
     """Pointer array of contiguous tensors of `dtype` on the context's device,
-    one per entry of `shapes` (each at least that many rows of its shape)."""
-    if len(tensors) != len(shapes):
-        raise ValueError(f"{what}: {len(tensors)} buffers for {len(shapes)} ranks")
-    ptrs = (ctypes.c_void_p * len(tensors))()
-    for i, (t, shape) in enumerate(zip(tensors, shapes)):
-        if t.dtype != dtype:
-            raise TypeError(f"{what}[{i}] is {t.dtype}, not {dtype}")
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{what}[{i}] must be a contiguous device tensor")
-        if t.device.index != ctx.device:
-            raise ValueError(f"{what}[{i}] is on {t.device}, the context on device {ctx.device}")
-        if t.dim() != len(shape) or tuple(t.shape[1:]) != tuple(shape[1:]) or t.shape[0] < shape[0]:
-            raise ValueError(f"{what}[{i}] has shape {tuple(t.shape)}, needs {tuple(shape)}")
-        ptrs[i] = t.data_ptr()
-    return ptrs
+    one per entry of `shapes` (each of at least as many rows)."""
+    n = len(tensors)
+    if n != len(shapes):
+        raise ValueError(f"{what}: {n} buffers for {len(shapes)} ranks")
+    device, ptrs = ctx.device, []
+    for t, shape in zip(tensors, shapes):
+        s = t.shape
+        if (t.dtype is not dtype or t.get_device() != device or not t.is_contiguous() or
+                s != shape and (len(s) != len(shape) or s[1:] != shape[1:] or s[0] < shape[0])):
+            _refuse(ctx, t, len(ptrs), dtype, shape, what)
+        ptrs.append(t.data_ptr())
+    return (ctypes.c_void_p * n)(*ptrs)
 
 
 def _expert_counts(ecnt, R: int):
-    """([R x E] int64 counts, rows of each rank's experts)."""
+    """([R x E] int64 counts, their address, rows of each rank's experts)."""
     ecnt = np.ascontiguousarray(ecnt, dtype=np.int64)
     if ecnt.ndim != 2 or ecnt.shape[0] != R or ecnt.shape[1] % R:
         raise ValueError(f"ecnt has shape {ecnt.shape}, needs [R = {R}, E] with R | E")
-    return ecnt, [int(n) for n in ecnt.sum(axis=0).reshape(R, -1).sum(axis=1)]
+    if R == 1:
+        rows = [int(np.add.reduce(ecnt[0]))]
+    else:
+        rows = np.add.reduce(np.add.reduce(ecnt, 0).reshape(R, -1), 1).tolist()
+    return ecnt, ecnt.__array_interface__["data"][0], rows
 
 
 def ccr_moe_experts(ctx: Context, exp: Sequence, w: Sequence, ecnt, out: Sequence, stream=None):
     """out[d] row i = w_e @ exp[d] row i, e the expert of the row: exp[d]
     [rows, H] as the dispatch leaves it, w[d] [E/R, F, H], ecnt [R, E]."""
     R = len(w)
-    ecnt, rows = _expert_counts(ecnt, R)
+    ecnt, counts, rows = _expert_counts(ecnt, R)
     E = ecnt.shape[1]
     _, F, H = w[0].shape
     dt = w[0].dtype
     code = _dtype_code(w[0])
     _check(_lib.ccr_moe_experts(
         ctx.handle, _buffers(ctx, exp, dt, [(n, H) for n in rows], "exp"),
-        _buffers(ctx, w, dt, [(E // R, F, H)] * R, "w"), ecnt.ctypes.data, R, E, H, F, code,
+        _buffers(ctx, w, dt, [(E // R, F, H)] * R, "w"), counts, R, E, H, F, code,
         _buffers(ctx, out, dt, [(n, F) for n in rows], "out"), _ctx_stream(ctx, stream)))
 
 
@@ -555,14 +569,14 @@ def ccr_moe_experts_dgrad(ctx: Context, dout: Sequence, w: Sequence, ecnt, dexp:
     """dexp[d] row i = w_e^T @ dout[d] row i: the gradient of the experts'
     input rows."""
     R = len(w)
-    ecnt, rows = _expert_counts(ecnt, R)
+    ecnt, counts, rows = _expert_counts(ecnt, R)
     E = ecnt.shape[1]
     _, F, H = w[0].shape
     dt = w[0].dtype
     code = _dtype_code(w[0])
     _check(_lib.ccr_moe_experts_dgrad(
         ctx.handle, _buffers(ctx, dout, dt, [(n, F) for n in rows], "dout"),
-        _buffers(ctx, w, dt, [(E // R, F, H)] * R, "w"), ecnt.ctypes.data, R, E, H, F, code,
+        _buffers(ctx, w, dt, [(E // R, F, H)] * R, "w"), counts, R, E, H, F, code,
         _buffers(ctx, dexp, dt, [(n, H) for n in rows], "dexp"), _ctx_stream(ctx, stream)))
 
 
@@ -571,14 +585,14 @@ def ccr_moe_experts_wgrad(ctx: Context, exp: Sequence, dout: Sequence, ecnt, dw:
     """dw[d][e] (+)= dout_e^T @ exp_e over the rows of expert e: the gradient
     of the experts' weights [E/R, F, H], float32 or the rows' dtype."""
     R = len(dw)
-    ecnt, rows = _expert_counts(ecnt, R)
+    ecnt, counts, rows = _expert_counts(ecnt, R)
     E = ecnt.shape[1]
     _, F, H = dw[0].shape
     dt = exp[0].dtype
     code, dw_code = _dtype_code(exp[0]), _dtype_code(dw[0])
     _check(_lib.ccr_moe_experts_wgrad(
         ctx.handle, _buffers(ctx, exp, dt, [(n, H) for n in rows], "exp"),
-        _buffers(ctx, dout, dt, [(n, F) for n in rows], "dout"), ecnt.ctypes.data, R, E, H, F, code,
+        _buffers(ctx, dout, dt, [(n, F) for n in rows], "dout"), counts, R, E, H, F, code,
         dw_code, int(bool(accumulate)), _buffers(ctx, dw, dw[0].dtype, [(E // R, F, H)] * R, "dw"),
         _ctx_stream(ctx, stream)))
 
@@ -622,52 +636,63 @@ def ccr_moe_gate_sum_bwd(ctx: Context, dy: Sequence, rows: Sequence, logits: Seq
                                      _ctx_stream(ctx, stream)))
 
 
-def _grad_args(ctx, grads, work, norm):
+_dtype_of, _is_cuda = attrgetter("dtype"), attrgetter("is_cuda")
+
+
+def _grad_codes():
     import torch
-    n = len(grads)
-    ptrs, counts, codes = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)(), (ctypes.c_int32 * n)()
-    f32, bf16 = torch.float32, torch.bfloat16
-    for i, t in enumerate(grads):
-        dt = t.dtype
-        if dt is not f32:
-            if dt is not bf16:
-                raise TypeError(f"grads[{i}] is {dt}; use float32 or bfloat16")
-            codes[i] = CCR_BF16
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"grads[{i}] must be a contiguous device tensor")
-        ptrs[i] = t.data_ptr()
-        counts[i] = t.numel()
+    return {torch.float32: CCR_F32, torch.bfloat16: CCR_BF16}
+
+
+_GRAD_CODE = _grad_codes()
+
+
+def _grad_list(ctx, tensors, what: str):
+    """(pointers, element counts, dtype codes) of contiguous float32 and
+    bfloat16 tensors, as arrays; one pass of C-level calls per property, since
+    a call may list hundreds of them."""
+    import torch
+    T = torch.Tensor
+    try:
+        codes = array("i", map(_GRAD_CODE.__getitem__, map(_dtype_of, tensors)))
+    except KeyError as e:
+        raise TypeError(f"{what} holds a tensor of {e.args[0]}; use float32 or bfloat16") from None
+    if not all(map(T.is_contiguous, tensors)) or not all(map(_is_cuda, tensors)):
+        raise ValueError(f"{what} must be contiguous device tensors")
+    return array("Q", map(T.data_ptr, tensors)), array("q", map(T.numel, tensors)), codes
+
+
+def _grad_scratch(ctx, work, norm):
+    import torch
     _buffers(ctx, [work], torch.float64, [(CCR_GRAD_WORK,)], "work")
-    _buffers(ctx, [norm], f32, [(1,)], "norm")
-    return ptrs, counts, codes, n
+    _buffers(ctx, [norm], torch.float32, [(1,)], "norm")
 
 
 def ccr_grad_norm(ctx: Context, grads: Sequence, work, norm, stream=None):
     """norm[0] = the 2-norm over every element of `grads` (float32 and
     bfloat16 tensors).  work: float64 [CCR_GRAD_WORK], this call's alone while
     it runs; norm: float32 [1]."""
-    ptrs, counts, codes, n = _grad_args(ctx, grads, work, norm)
-    _check(_lib.ccr_grad_norm(ctx.handle, ptrs, counts, codes, n, work.data_ptr(), norm.data_ptr(),
+    ptrs, counts, codes = _grad_list(ctx, grads, "grads")
+    _grad_scratch(ctx, work, norm)
+    _check(_lib.ccr_grad_norm(ctx.handle, ptrs.buffer_info()[0], counts.buffer_info()[0],
+                              codes.buffer_info()[0], len(ptrs), work.data_ptr(), norm.data_ptr(),
                               _ctx_stream(ctx, stream)))
 
 
 def ccr_grad_clip(ctx: Context, grads: Sequence, max_norm: float, work, norm, out=None, stream=None):
     """norm[0] as ccr_grad_norm, then grads[i] *= min(1, max_norm / (norm +
     1e-6)), or out[i] = that product."""
-    ptrs, counts, codes, n = _grad_args(ctx, grads, work, norm)
+    ptrs, counts, codes = _grad_list(ctx, grads, "grads")
+    _grad_scratch(ctx, work, norm)
     optrs = None
     if out is not None:
-        if len(out) != n:
-            raise ValueError("out needs one tensor per gradient")
-        optrs = (ctypes.c_void_p * n)()
-        for i, (t, o) in enumerate(zip(grads, out)):
-            if o.dtype is not t.dtype or o.numel() != t.numel():
-                raise ValueError(f"out[{i}] differs from grads[{i}] in dtype or element count")
-            if not o.is_cuda or not o.is_contiguous():
-                raise ValueError(f"out[{i}] must be a contiguous device tensor")
-            optrs[i] = o.data_ptr()
-    _check(_lib.ccr_grad_clip(ctx.handle, ptrs, optrs, counts, codes, n, max_norm, work.data_ptr(),
-                              norm.data_ptr(), _ctx_stream(ctx, stream)))
+        optrs, ocounts, ocodes = _grad_list(ctx, out, "out")
+        if ocounts != counts or ocodes != codes:
+            raise ValueError("out needs a tensor of each gradient's dtype and element count")
+    _check(_lib.ccr_grad_clip(ctx.handle, ptrs.buffer_info()[0],
+                              None if optrs is None else optrs.buffer_info()[0],
+                              counts.buffer_info()[0], codes.buffer_info()[0], len(ptrs), max_norm,
+                              work.data_ptr(), norm.data_ptr(), _ctx_stream(ctx, stream)))
 
 
 def ccr_probe_cu_ids(ctx: Context, nblocks: int, stream=None):

@@ -744,7 +744,7 @@ ExpertTile expert_tile(ExpertOp op, int es, int os, const ExpertShape& sh, const
     double c0, c1;
   };
   const Cost costs[] = {{ExpertTile::k32, 0.25, es == 2 ? 0.09 : 0.15},
-                        {ExpertTile::k64, 0.4, es == 2 ? 0.2 : 0.5},
+                        {ExpertTile::k64, 0.4, es == 2 ? 0.2 : 0.52},
                         {ExpertTile::k128, 2.0, es == 2 ? 0.5 : 2.0},
                         {ExpertTile::k256, 1.0, 1.42}};
   ExpertTile best = ExpertTile::k32;

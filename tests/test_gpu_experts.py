@@ -104,6 +104,66 @@ def test_whole_numbers_bitwise(ccr_mod, op, dt, rows, H, F):
     check(ccr_mod, op, dt, rows, 1, H, F, seed=H + F + len(rows))
 
 
+MID = [200, 129, 255, 0, 190, 199, 256, 250, 240]
+LONG = [2000, 1999, 1801, 2048, 2001, 1793, 1900, 2047]
+MANY = [4096, 4000, 0, 3999, 1, 4095, 257, 4097, 255, 3000]
+
+
+@pytest.mark.parametrize("op,dt,out_dt,rows,H,F", [
+    # tiles of 128 and of 256, the last of a row of tiles and of a contraction partial
+    ("product", "bf16", "bf16", MID, 2056, 2040), ("dgrad", "bf16", "bf16", MID, 2040, 2056),
+    ("product", "bf16", "bf16", LONG, 1032, 1000), ("dgrad", "bf16", "bf16", LONG, 1000, 1032),
+    # more than one round of tiles, a contraction of few steps
+    ("product", "bf16", "bf16", MANY, 264, 2056), ("dgrad", "bf16", "bf16", MANY, 2056, 264),
+    ("product", "bf16", "bf16", MANY, 8, 2056), ("dgrad", "bf16", "bf16", MANY, 2056, 72),
+    ("wgrad", "bf16", "f32", LONG, 1000, 1032), ("wgrad", "bf16", "bf16", LONG + [0, 1], 1032, 1032),
+    # unequal weight gradients in several rounds
+    ("wgrad", "bf16", "f32", [400, 399, 0, 1, 64, 65, 700, 128] * 2, 2040, 1400),
+    ("wgrad", "bf16", "bf16", [400, 399, 0, 1, 64, 65, 700, 128] * 2, 2040, 1400),
+    ("product", "f32", "f32", [4095, 4090], 1028, 2044), ("dgrad", "f32", "f32", [4095, 4090], 2044, 1028),
+    ("wgrad", "f32", "f32", [2000, 2009, 1000], 2044, 2040),
+])
+def test_large_tiles_bitwise(ccr_mod, op, dt, out_dt, rows, H, F):
+    check(ccr_mod, op, dt, rows, 1, H, F, out_dt=out_dt, seed=H + F)
+
+
+@pytest.mark.parametrize("out_dt", ["f32", "bf16"])
+def test_large_accumulation_bitwise(ccr_mod, out_dt):
+    check(ccr_mod, "wgrad", "bf16", [400, 399, 0, 1, 64, 65, 700, 128] * 2, 2, 2040, 1400, out_dt=out_dt,
+          accumulate=True)
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_offsets_past_32_bits(ccr_mod, op):
+    """Rows, weights and results that lie past 2^32 bytes from their buffer's
+    first byte: expert 1's are compared, expert 0's are many."""
+    import torch
+    H, F, n0, n1 = 2048, 2048, 1100000, 300
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GiB")
+    say(f"experts {op} past 32-bit offsets")
+    x = torch.zeros(n0 + n1, H if op == "product" else F, dtype=torch.bfloat16, device="cuda")
+    x[n0:] = torch.randint(-3, 4, (n1, x.shape[1]), device="cuda").to(torch.bfloat16)
+    ecnt = np.array([[n0, n1]], np.int64)
+    with ccr_mod.Context(0) as c:
+        if op == "wgrad":
+            y = torch.ones(n0 + n1, H, dtype=torch.bfloat16, device="cuda")
+            y[n0:] = torch.randint(-3, 4, (n1, H), device="cuda").to(torch.bfloat16)
+            dw = torch.empty(2, F, H, device="cuda")
+            ccr_mod.ccr_moe_experts_wgrad(c, [y], [x], ecnt, [dw])
+            torch.cuda.synchronize()
+            assert torch.equal(dw[1], (x[n0:].double().t() @ y[n0:].double()).float())
+            assert not bool(dw[0].any())
+            return
+        w = torch.randint(-3, 4, (2, F, H), device="cuda").to(torch.bfloat16)
+        out = torch.empty(n0 + n1, F if op == "product" else H, dtype=torch.bfloat16, device="cuda")
+        call(ccr_mod, c, op, [x], [w], ecnt, [out])
+        torch.cuda.synchronize()
+        w1 = w[1].double().t() if op == "product" else w[1].double()
+        assert torch.equal(out[n0:], (x[n0:].double() @ w1).to(torch.bfloat16))
+        assert not bool(out[:n0].any())
+
+
 @pytest.mark.parametrize("op", OPS)
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_several_ranks_bitwise(ccr_mod, op, dt):
@@ -131,6 +191,8 @@ def test_more_experts_than_one_launch_lists(ccr_mod, op):
     ("dgrad", "f32", [300, 900], 260, 512),
     ("wgrad", "f32", [300, 900], 260, 516),
     ("wgrad", "bf16", [40000, 3], 88, 176),
+    ("product", "bf16", LONG, 1032, 1000),
+    ("wgrad", "bf16", LONG, 1000, 1032),
 ])
 def test_random_values_within_the_sums_error(ccr_mod, op, dt, rows, H, F):
     check(ccr_mod, op, dt, rows, 1, H, F, whole=False, seed=H)

@@ -207,6 +207,32 @@ def test_streams_and_graph_replays(ccr_mod):
             assert all(torch.equal(a, b) for a, b in zip((y, dr, dl), want)), f"replay {step}"
 
 
+def test_offsets_past_32_bits(ccr_mod):
+    """The last tokens' rows lie past 2^32 bytes from the first."""
+    import torch
+    T, E, K, H = 70000, 8, 4, 8192
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GiB")
+    say("gate past 32-bit offsets")
+    rows = torch.zeros(T, K, H, dtype=torch.bfloat16, device="cuda")
+    rows[-3:] = torch.randn(3, K, H, device="cuda").to(torch.bfloat16)
+    logits = torch.randn(T, E, device="cuda")
+    topk = torch.topk(logits, K, dim=1).indices.to(torch.int32)
+    dy = torch.randn(T, H, device="cuda").to(torch.bfloat16)
+    y = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    dr, dl = torch.empty_like(rows), torch.empty_like(logits)
+    small = [t[-3:].contiguous() for t in (rows, logits, topk, dy)]
+    sy, sdr, sdl = (torch.empty_like(t) for t in (small[3], small[0], small[1]))
+    with ccr_mod.Context(0) as c:
+        ccr_mod.ccr_moe_gate_sum(c, [rows], [logits], [topk], [y])
+        ccr_mod.ccr_moe_gate_sum_bwd(c, [dy], [rows], [logits], [topk], [dr], [dl])
+        ccr_mod.ccr_moe_gate_sum(c, [small[0]], [small[1]], [small[2]], [sy])
+        ccr_mod.ccr_moe_gate_sum_bwd(c, [small[3]], [small[0]], [small[1]], [small[2]], [sdr], [sdl])
+        torch.cuda.synchronize()
+    assert torch.equal(y[-3:], sy) and torch.equal(dr[-3:], sdr) and torch.equal(dl[-3:], sdl)
+    assert not bool(y[:-3].any()) and not bool(dl[:-3].any())
+
+
 def test_empty_and_refusals(ccr_mod):
     import torch
     rows, logits, topk, dy = inputs(4, 8, 2, 16, "bf16", 1)

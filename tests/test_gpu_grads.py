@@ -125,6 +125,51 @@ def test_squares_beyond_fp32(ccr_mod, scale):
     assert close_norm(float(norm), norm64(grads)) and 0 < float(norm) < float("inf")
 
 
+def test_a_tensor_past_32_bits(ccr_mod):
+    """2^32 + 99 bf16 values, the last few of them not zero, clipped in place."""
+    import torch
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GiB")
+    n = 2 ** 32 + 99
+    say("grads past 32-bit counts")
+    x = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    tail = torch.randn(5000, device="cuda").to(torch.bfloat16)
+    x[-5000:] = tail
+    x[0] = 3.0
+    work, norm = scratch(ccr_mod)
+    with ccr_mod.Context(0) as c:
+        ccr_mod.ccr_grad_clip(c, [x[1:]], 0.5, work, norm)
+        torch.cuda.synchronize()
+    want = norm64([tail])
+    assert close_norm(float(norm), want) and float(x[0]) == 3.0
+    q = 0.5 / (want + 1e-6)
+    err = (x[-5000:].double() - tail.double() * q).abs()
+    assert bool((err <= (HALF["bf16"] + 4 * U) * 1.01 * (tail.double() * q).abs()).all())
+
+
+def test_neighbours_in_memory(ccr_mod):
+    """Views that fill a bucket one after the other, in order, out of order,
+    with gaps and of two types, give the same as separate tensors."""
+    import torch
+    work, norm = scratch(ccr_mod)
+    flat = inside_nan(torch.randn(100_000, device="cuda").to(torch.bfloat16), 3)
+    cuts = [0, 1, 2, 10, 5000, 5003, 5003, 60_001, 99_999, 100_000]
+    views = [flat[a:b] for a, b in zip(cuts, cuts[1:])]
+    other = torch.randn(77, device="cuda")
+    for grads in (views, views[::-1], views[::2], views[:4] + [other] + views[4:]):
+        want = norm64(grads)
+        outs = [torch.empty_like(g) for g in grads]
+        with ccr_mod.Context(0) as c:
+            ccr_mod.ccr_grad_norm(c, grads, work, norm)
+            assert close_norm(float(norm), want)
+            ccr_mod.ccr_grad_clip(c, grads, 0.5, work, norm, out=outs)
+            torch.cuda.synchronize()
+        q = 0.5 / (want + 1e-6)
+        for g, o in zip(grads, outs):
+            half = HALF["f32" if g.dtype == torch.float32 else "bf16"]
+            assert bool(((o.double() - g.double() * q).abs() <= (half + 4 * U) * 1.01 * (g.double() * q).abs()).all())
+
+
 def test_nothing_to_measure(ccr_mod):
     import torch
     work, norm = scratch(ccr_mod)
