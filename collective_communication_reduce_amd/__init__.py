@@ -3,6 +3,8 @@
 A thin ctypes layer over the C ABI in ``include/ccr.h``: every function here
 only marshals arguments (torch tensors -> device pointers, sizes, dtype
 codes, the current HIP stream) and calls the C entry point of the same name.
+(Lists of tensors that can be long are read by a small compiled module,
+``_ccr_torch``, built with the library.)
 All of the work runs in the library's HIP kernels and SDMA copies; there is
 no Python or CPU fallback, and importing this package fails loudly if the
 library has not been built (``python collective_communication_reduce_amd/build.py``).
@@ -13,15 +15,14 @@ from __future__ import annotations
 
 import ctypes
 import os
-from array import array
 from dataclasses import dataclass
-from operator import attrgetter
 from typing import Optional, Sequence
 
 import numpy as np
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libccr.so")
+MARSHAL_PATH = os.path.join(_HERE, "_ccr_torch.so")
 
 CCR_OK, CCR_ERR_INVALID_ARG, CCR_ERR_UNSUPPORTED, CCR_ERR_HIP, CCR_ERR_OOM, CCR_ERR_TIMEOUT = range(6)
 CCR_F32, CCR_BF16 = 0, 1
@@ -134,6 +135,9 @@ def _load():
         raise ImportError(
             f"{LIB_PATH} is missing: build it with "
             "`python collective_communication_reduce_amd/build.py` (hipcc, gfx950)")
+    if not os.path.exists(MARSHAL_PATH):
+        raise ImportError(f"{MARSHAL_PATH} is missing: build it with "
+                          "`python collective_communication_reduce_amd/build.py`")
     lib = ctypes.CDLL(LIB_PATH)
     if len(_hip_runtimes()) > 1:
         raise ImportError(f"two HIP runtimes are loaded ({sorted(_hip_runtimes())}); import "
@@ -146,6 +150,7 @@ def _load():
 
 
 _lib = _load()
+from . import _ccr_torch  # noqa: E402  (needs torch loaded, which _load does)
 
 
 def _raw_stream_getter():
@@ -522,40 +527,33 @@ def _refuse(ctx: Context, t, i, dtype, shape, what: str):
     raise ValueError(f"{what}[{i}] has shape {tuple(t.shape)}, needs {tuple(shape)}")
 
 
-def _buffers(ctx: Context, tensors, dtype, shapes, what: str):
+def _buffers(ctx: Context, tensors, dtype, shapes, what: str) -> bytes:
     """Pointer array of contiguous tensors of `dtype` on the context's device,
     one per entry of `shapes` (each of at least as many rows)."""
-    n = len(tensors)
-    if n != len(shapes):
-        raise ValueError(f"{what}: {n} buffers for {len(shapes)} ranks")
-    device, ptrs = ctx.device, []
-    for t, shape in zip(tensors, shapes):
-        s = t.shape
-        if (t.dtype is not dtype or t.get_device() != device or not t.is_contiguous() or
-                s != shape and (len(s) != len(shape) or s[1:] != shape[1:] or s[0] < shape[0])):
-            _refuse(ctx, t, len(ptrs), dtype, shape, what)
-        ptrs.append(t.data_ptr())
-    return (ctypes.c_void_p * n)(*ptrs)
+    if len(tensors) != len(shapes):
+        raise ValueError(f"{what}: {len(tensors)} buffers for {len(shapes)} ranks")
+    p = _ccr_torch.pointers(tensors, dtype, ctx.device, shapes)
+    if type(p) is int:
+        _refuse(ctx, tensors[p], p, dtype, shapes[p], what)
+    return p
 
 
 def _expert_counts(ecnt, R: int):
-    """([R x E] int64 counts, their address, rows of each rank's experts)."""
-    ecnt = np.ascontiguousarray(ecnt, dtype=np.int64)
-    if ecnt.ndim != 2 or ecnt.shape[0] != R or ecnt.shape[1] % R:
-        raise ValueError(f"ecnt has shape {ecnt.shape}, needs [R = {R}, E] with R | E")
-    if R == 1:
-        rows = [int(np.add.reduce(ecnt[0]))]
-    else:
-        rows = np.add.reduce(np.add.reduce(ecnt, 0).reshape(R, -1), 1).tolist()
-    return ecnt, ecnt.__array_interface__["data"][0], rows
+    """([R x E] int64 counts, their address, E, rows of each rank's experts)."""
+    r = _ccr_torch.expert_rows(ecnt, R)
+    if r is None:
+        ecnt = np.ascontiguousarray(ecnt, dtype=np.int64)
+        r = _ccr_torch.expert_rows(ecnt, R)
+        if r is None:
+            raise ValueError(f"ecnt has shape {ecnt.shape}, needs [R = {R}, E] with R | E")
+    return (ecnt, *r)
 
 
 def ccr_moe_experts(ctx: Context, exp: Sequence, w: Sequence, ecnt, out: Sequence, stream=None):
     """out[d] row i = w_e @ exp[d] row i, e the expert of the row: exp[d]
     [rows, H] as the dispatch leaves it, w[d] [E/R, F, H], ecnt [R, E]."""
     R = len(w)
-    ecnt, counts, rows = _expert_counts(ecnt, R)
-    E = ecnt.shape[1]
+    ecnt, counts, E, rows = _expert_counts(ecnt, R)
     _, F, H = w[0].shape
     dt = w[0].dtype
     code = _dtype_code(w[0])
@@ -569,8 +567,7 @@ def ccr_moe_experts_dgrad(ctx: Context, dout: Sequence, w: Sequence, ecnt, dexp:
     """dexp[d] row i = w_e^T @ dout[d] row i: the gradient of the experts'
     input rows."""
     R = len(w)
-    ecnt, counts, rows = _expert_counts(ecnt, R)
-    E = ecnt.shape[1]
+    ecnt, counts, E, rows = _expert_counts(ecnt, R)
     _, F, H = w[0].shape
     dt = w[0].dtype
     code = _dtype_code(w[0])
@@ -585,8 +582,7 @@ def ccr_moe_experts_wgrad(ctx: Context, exp: Sequence, dout: Sequence, ecnt, dw:
     """dw[d][e] (+)= dout_e^T @ exp_e over the rows of expert e: the gradient
     of the experts' weights [E/R, F, H], float32 or the rows' dtype."""
     R = len(dw)
-    ecnt, counts, rows = _expert_counts(ecnt, R)
-    E = ecnt.shape[1]
+    ecnt, counts, E, rows = _expert_counts(ecnt, R)
     _, F, H = dw[0].shape
     dt = exp[0].dtype
     code, dw_code = _dtype_code(exp[0]), _dtype_code(dw[0])
@@ -636,30 +632,15 @@ def ccr_moe_gate_sum_bwd(ctx: Context, dy: Sequence, rows: Sequence, logits: Seq
                                      _ctx_stream(ctx, stream)))
 
 
-_dtype_of, _is_cuda = attrgetter("dtype"), attrgetter("is_cuda")
-
-
-def _grad_codes():
-    import torch
-    return {torch.float32: CCR_F32, torch.bfloat16: CCR_BF16}
-
-
-_GRAD_CODE = _grad_codes()
-
-
-def _grad_list(ctx, tensors, what: str):
+def _grad_list(tensors, what: str):
     """(pointers, element counts, dtype codes) of contiguous float32 and
-    bfloat16 tensors, as arrays; one pass of C-level calls per property, since
-    a call may list hundreds of them."""
-    import torch
-    T = torch.Tensor
-    try:
-        codes = array("i", map(_GRAD_CODE.__getitem__, map(_dtype_of, tensors)))
-    except KeyError as e:
-        raise TypeError(f"{what} holds a tensor of {e.args[0]}; use float32 or bfloat16") from None
-    if not all(map(T.is_contiguous, tensors)) or not all(map(_is_cuda, tensors)):
-        raise ValueError(f"{what} must be contiguous device tensors")
-    return array("Q", map(T.data_ptr, tensors)), array("q", map(T.numel, tensors)), codes
+    bfloat16 tensors, as arrays."""
+    r = _ccr_torch.grad_list(tensors)
+    if type(r) is int:
+        t = tensors[r]
+        _dtype_code(t)
+        raise ValueError(f"{what}[{r}] must be a contiguous device tensor")
+    return r
 
 
 def _grad_scratch(ctx, work, norm):
@@ -672,26 +653,23 @@ def ccr_grad_norm(ctx: Context, grads: Sequence, work, norm, stream=None):
     """norm[0] = the 2-norm over every element of `grads` (float32 and
     bfloat16 tensors).  work: float64 [CCR_GRAD_WORK], this call's alone while
     it runs; norm: float32 [1]."""
-    ptrs, counts, codes = _grad_list(ctx, grads, "grads")
+    ptrs, counts, codes = _grad_list(grads, "grads")
     _grad_scratch(ctx, work, norm)
-    _check(_lib.ccr_grad_norm(ctx.handle, ptrs.buffer_info()[0], counts.buffer_info()[0],
-                              codes.buffer_info()[0], len(ptrs), work.data_ptr(), norm.data_ptr(),
-                              _ctx_stream(ctx, stream)))
+    _check(_lib.ccr_grad_norm(ctx.handle, ptrs, counts, codes, len(grads), work.data_ptr(),
+                              norm.data_ptr(), _ctx_stream(ctx, stream)))
 
 
 def ccr_grad_clip(ctx: Context, grads: Sequence, max_norm: float, work, norm, out=None, stream=None):
     """norm[0] as ccr_grad_norm, then grads[i] *= min(1, max_norm / (norm +
     1e-6)), or out[i] = that product."""
-    ptrs, counts, codes = _grad_list(ctx, grads, "grads")
+    ptrs, counts, codes = _grad_list(grads, "grads")
     _grad_scratch(ctx, work, norm)
     optrs = None
     if out is not None:
-        optrs, ocounts, ocodes = _grad_list(ctx, out, "out")
+        optrs, ocounts, ocodes = _grad_list(out, "out")
         if ocounts != counts or ocodes != codes:
             raise ValueError("out needs a tensor of each gradient's dtype and element count")
-    _check(_lib.ccr_grad_clip(ctx.handle, ptrs.buffer_info()[0],
-                              None if optrs is None else optrs.buffer_info()[0],
-                              counts.buffer_info()[0], codes.buffer_info()[0], len(ptrs), max_norm,
+    _check(_lib.ccr_grad_clip(ctx.handle, ptrs, optrs, counts, codes, len(grads), max_norm,
                               work.data_ptr(), norm.data_ptr(), _ctx_stream(ctx, stream)))
 
 

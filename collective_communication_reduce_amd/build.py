@@ -1,16 +1,19 @@
-"""Build libccr.so (the C-ABI library) in place with hipcc for gfx950.
+"""Build libccr.so (the C-ABI library) in place with hipcc for gfx950, and
+_ccr_torch.so (the Python binding's marshalling of tensor lists) with g++.
 
     python collective_communication_reduce_amd/build.py
 
-The library is built in-tree next to this file so it travels with the
-source tree; nothing is installed.
+Both are built in-tree next to this file so they travel with the source
+tree; nothing is installed.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +21,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libccr.so")
+MARSHAL = os.path.join(PKG, "_ccr_torch.so")
 SOURCES = ["ccr_api.cpp", "ccr_dma.cpp", "ccr_schedule.cpp", "ccr_kernels.hip", "ccr_ring.hip",
            "ccr_moe_kernels.hip", "ccr_experts.hip", "ccr_gate.hip", "ccr_grad.hip", "ccr_scratch.hip"]
 # Per-source additions: the ring-hop kernels take their leading scalar
@@ -44,6 +48,24 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found; the HIP library cannot be built")
 
 
+def build_marshal() -> str:
+    """Compile _ccr_torch.so, the binding's marshalling of tensor lists: host
+    code against torch's C++ headers (found without importing torch)."""
+    root = importlib.util.find_spec("torch").submodule_search_locations[0]
+    inc = [os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include")]
+    tmp = MARSHAL + ".tmp"
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", "-D_GLIBCXX_USE_CXX11_ABI=1",
+           *[a for i in inc for a in ("-isystem", i)], "-I" + sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "ccr_torch.cpp"), "-o", tmp, "-L" + os.path.join(root, "lib"),
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on ccr_torch.cpp:\n{r.stdout}{r.stderr}")
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cc = hipcc()
@@ -60,8 +82,10 @@ def build(verbose: bool = False) -> str:
             print(err, file=sys.stderr)
         return obj
 
-    with ThreadPoolExecutor(len(SOURCES)) as ex:
+    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        marshal = ex.submit(build_marshal)
         objs = list(ex.map(compile_one, SOURCES))
+        marshal.result()
     tmp = LIB + ".tmp"
     # libhsa-runtime64 (SDMA engine copies): resolved at load time to the HSA
     # runtime already in the process (torch's), like libamdhip64.  The roctx

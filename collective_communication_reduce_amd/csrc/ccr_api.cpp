@@ -2077,17 +2077,25 @@ ccr_status_t ccr_moe_combine_fused(ccr_ctx_t ctx, const void* const* exp, const 
 
 namespace {
 
-// The calling thread's current device, put back at the end of the call.
-struct KeepDevice {
-  int device = -1;
-  KeepDevice() {
-    if (hipGetDevice(&device) != hipSuccess) device = -1;
+// The context's device, current for the length of a call; the calling thread's
+// own is put back at its end.
+struct OnDevice {
+  int before = -1;  // -1: nothing to put back
+  ccr_status_t enter(ccr_ctx* ctx) {
+    if (!ctx) return fail(CCR_ERR_INVALID_ARG, "ctx is NULL");
+    int now = -1;
+    HIP_TRY(hipGetDevice(&now));
+    if (now == ctx->device) return CCR_OK;
+    HIP_TRY(hipSetDevice(ctx->device));
+    before = now;
+    return CCR_OK;
   }
-  ~KeepDevice() {
-    if (device >= 0) (void)hipSetDevice(device);
+  OnDevice() = default;
+  ~OnDevice() {
+    if (before >= 0) (void)hipSetDevice(before);
   }
-  KeepDevice(const KeepDevice&) = delete;
-  KeepDevice& operator=(const KeepDevice&) = delete;
+  OnDevice(const OnDevice&) = delete;
+  OnDevice& operator=(const OnDevice&) = delete;
 };
 
 // As check_writes_disjoint, in n log n: no written range overlaps another.
@@ -2105,11 +2113,14 @@ void touch(std::vector<Touched>* v, const void* p, int64_t nbytes, bool written,
   v->push_back(Touched{a, a + (uintptr_t)nbytes, written, what, index});
 }
 
-ccr_status_t check_touched(std::vector<Touched> v) {
-  std::sort(v.begin(), v.end(), [](const Touched& a, const Touched& b) { return a.lo < b.lo; });
+ccr_status_t check_touched(const std::vector<Touched>& v) {
+  std::vector<std::pair<uintptr_t, uint32_t>> order(v.size());
+  for (size_t i = 0; i < v.size(); i++) order[i] = {v[i].lo, (uint32_t)i};
+  std::sort(order.begin(), order.end());
   // the ranges so far that reach furthest: of all, and of the written ones
   const Touched *any = nullptr, *written = nullptr;
-  for (const Touched& t : v) {
+  for (const auto& x : order) {
+    const Touched& t = v[x.second];
     const Touched* o = t.written ? any : written;
     if (o && t.lo < o->hi)
       return fail(CCR_ERR_INVALID_ARG, "%s[%d] and %s[%d] overlap", o->what, o->index, t.what, t.index);
@@ -2127,8 +2138,8 @@ ccr_status_t run_experts(ccr_ctx* ctx, ExpertOp op, const void* const* a, const 
                          const void* const* b, const char* b_name, void* const* c, const char* c_name,
                          const int64_t* h_ecnt, int R, int E, int64_t H, int64_t F, int dtype,
                          int out_dtype, bool add, hipStream_t s) {
-  KeepDevice keep;
-  CCR_TRY(check_ctx(ctx));
+  OnDevice on;
+  CCR_TRY(on.enter(ctx));
   if (R < 1 || R > kMaxRanks || E < 1 || E > kMaxExperts || E % R != 0)
     return fail(CCR_ERR_INVALID_ARG, "need 1 <= R <= %d, 1 <= E <= %d, R | E", kMaxRanks, kMaxExperts);
   const int es = dtype_size(dtype), os = dtype_size(out_dtype);
@@ -2178,7 +2189,7 @@ ccr_status_t run_experts(ccr_ctx* ctx, ExpertOp op, const void* const* a, const 
     touch(&t, b[d], bb, false, b_name, d);
     touch(&t, c[d], cb, true, c_name, d);
   }
-  CCR_TRY(check_touched(std::move(t)));
+  CCR_TRY(check_touched(t));
   const ExpertShape sh{H, F, add};
   // the experts with work, and each one's first row in its rank's buffers
   std::vector<int64_t> first((size_t)E), work;
@@ -2238,8 +2249,8 @@ ccr_status_t run_gate(ccr_ctx* ctx, bool bwd, const void* const* dy, const void*
                       const float* const* logits, const int32_t* const* topk, void* const* y,
                       void* const* drows, float* const* dlogits, int R, int64_t T, int E, int K,
                       int64_t H, int dtype, int norm, hipStream_t s) {
-  KeepDevice keep;
-  CCR_TRY(check_ctx(ctx));
+  OnDevice on;
+  CCR_TRY(on.enter(ctx));
   if (R < 1 || R > kMaxRanks || T < 0 || T > INT32_MAX || E < 1 || E > 1024 || K < 1 || K > 16 || K > E)
     return fail(CCR_ERR_INVALID_ARG, "need 1 <= R <= %d, 0 <= T < 2^31, 1 <= E <= 1024, 1 <= K <= min(E, 16)",
                 kMaxRanks);
@@ -2281,7 +2292,7 @@ ccr_status_t run_gate(ccr_ctx* ctx, bool bwd, const void* const* dy, const void*
       args.y[r] = static_cast<char*>(y[r]);
     }
   }
-  CCR_TRY(check_touched(std::move(t)));
+  CCR_TRY(check_touched(t));
   if (T > kMaxGridWorkgroups / R) return fail(CCR_ERR_UNSUPPORTED, "R x T is too large for one launch");
   HIP_TRY(launch_gate_sum(bwd, norm == CCR_GATE_ALL, es, args, R, T, E, K, H * es,
                           R * (rb + yb) > kMallBytes, s));
@@ -2292,8 +2303,8 @@ ccr_status_t run_gate(ccr_ctx* ctx, bool bwd, const void* const* dy, const void*
 ccr_status_t run_grads(ccr_ctx* ctx, bool clip, const void* const* grads, void* const* out,
                        const int64_t* counts, const int32_t* dtypes, int n, float max_norm, double* work,
                        float* norm, hipStream_t s) {
-  KeepDevice keep;
-  CCR_TRY(check_ctx(ctx));
+  OnDevice on;
+  CCR_TRY(on.enter(ctx));
   if (n < 0) return fail(CCR_ERR_INVALID_ARG, "n = %d < 0", n);
   if (n > 0 && (!grads || !counts || !dtypes))
     return fail(CCR_ERR_INVALID_ARG, "grads, counts or dtypes is NULL");
@@ -2343,7 +2354,7 @@ ccr_status_t run_grads(ccr_ctx* ctx, bool clip, const void* const* grads, void* 
     touch(&touched, t.src, t.count * t.es, clip && t.src == t.dst, "grads", index[i]);
     if (t.src != t.dst) touch(&touched, t.dst, t.count * t.es, true, "out", index[i]);
   }
-  CCR_TRY(check_touched(std::move(touched)));
+  CCR_TRY(check_touched(touched));
   // One launch per kGradTensors tensors and per 2^31 - 1 tiles: each is the
   // run of tensors [first, last) with its tiles in all.
   struct Launch {
