@@ -230,7 +230,8 @@ __global__ __launch_bounds__(kBlock) void grad_clip_kernel(const GradTable tab, 
   const float nv = (float)sqrt(total_of(work, slots, part));
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = nv;
   const float q = max_norm / (nv + 1e-6f);
-  const float c = q > 1.0f ? 1.0f : q;  // a NaN stays
+  // a NaN stays; an infinite max_norm only measures, whatever the norm
+  const float c = q > 1.0f || max_norm == __builtin_inff() ? 1.0f : q;
   for (int64_t tile = tab.ntiles - 1 - blockIdx.x; tile >= 0; tile -= gridDim.x) {
     const int at = tensor_of(tab, tile);
     const GradTensor& t = tab.t[at];

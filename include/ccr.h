@@ -548,7 +548,7 @@ ccr_status_t ccr_moe_experts_wgrad(ccr_ctx_t ctx, const void *const *exp, const 
  *
  * Weights and sums are fp32; each result is rounded once.  dtype: of rows, y,
  * dy and drows.  1 <= E <= 1024, 1 <= K <= min(E, 16), H 1 .. 2^20 with rows a
- * multiple of 16 bytes.  Written buffers must not overlap any other buffer.
+ * multiple of 16 bytes, R x T < 2^24.  Written buffers must not overlap any other buffer.
  * ---------------------------------------------------------------------- */
 typedef enum { CCR_GATE_CHOSEN = 0, CCR_GATE_ALL = 1 } ccr_gate_norm_t;
 ccr_status_t ccr_moe_gate_sum(ccr_ctx_t ctx, const void *const *rows, const float *const *logits,
@@ -572,8 +572,8 @@ ccr_status_t ccr_moe_gate_sum_bwd(ccr_ctx_t ctx, const void *const *dy, const vo
  *   1e-6)) in fp32, rounded once to the tensor's type.  out NULL, or out[i] =
  *   grads[i]: in place, and nothing is written when the factor is 1.  A
  *   non-finite norm follows the formula (infinite: finite values become 0
- *   and infinite ones NaN; NaN: every value NaN).  max_norm >= 0; infinity
- *   only measures.
+ *   and infinite ones NaN; NaN: every value NaN).  max_norm >= 0; an
+ *   infinite max_norm only measures (the factor is 1 whatever the norm).
  *
  * grads: host array of n device pointers, each to counts[i] >= 0 contiguous
  * elements of dtypes[i]; pointers need their element's alignment only (views

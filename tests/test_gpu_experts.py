@@ -309,6 +309,41 @@ def test_runs_with_a_cu_budget_and_under_capture(ccr_mod):
     assert torch.equal(out, experts_ref("product", a, b, [40, 5], 1, 2)[0][0].to(torch.bfloat16))
 
 
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_subnormal_values(ccr_mod, op, dt):
+    """Products of subnormal and ordinary values keep their bits: 2^-130 times
+    whole numbers, summed exactly, is a multiple of 2^-130 still."""
+    import torch
+    rows, H, F = [40, 3], 72, 40
+    ecnt, a, b, shapes = make(op, dt, rows, 1, H, F, 11, True)
+    a[0].mul_(2.0 ** -65).mul_(2.0 ** -65)
+    out = torch.empty(shapes[0], device="cuda", dtype=tdtype(dt))
+    with ccr_mod.Context(0) as c:
+        call(ccr_mod, c, op, a, b, ecnt, [out])
+        torch.cuda.synchronize()
+    ref = experts_ref(op, a, b, rows, 1, 2)[0][0]
+    assert bool((ref != 0).any()) and torch.equal(out, ref.to(tdtype(dt)))
+
+
+def test_two_streams_at_once(ccr_mod):
+    """One context, two streams, calls in flight together: each its own result."""
+    import torch
+    sets = [make(op, "bf16", rows, 1, 264, 392, 12 + i, True)
+            for i, (op, rows) in enumerate([("product", [300, 0, 77]), ("dgrad", [1, 512, 65])])]
+    ops = ["product", "dgrad"]
+    outs = [torch.zeros(s[3][0], dtype=torch.bfloat16, device="cuda") for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    with ccr_mod.Context(0) as c:
+        for _ in range(20):
+            for op, (ecnt, a, b, _), o, st in zip(ops, sets, outs, streams):
+                call(ccr_mod, c, op, a, b, ecnt, [o], stream=st)
+        torch.cuda.synchronize()
+    for op, (ecnt, a, b, _), o, rows in zip(ops, sets, outs, ([300, 0, 77], [1, 512, 65])):
+        assert torch.equal(o, experts_ref(op, a, b, rows, 1, 3)[0][0].to(torch.bfloat16))
+
+
 def test_same_bits_every_run(ccr_mod):
     import torch
     for op in OPS:

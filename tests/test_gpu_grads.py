@@ -201,6 +201,10 @@ def test_non_finite_norms_follow_the_formula(ccr_mod):
         assert close_norm(float(norm), math.sqrt(1000)) and bool((grads[0] == 1).all())
         ccr_mod.ccr_grad_clip(c, grads, 0.0, work, norm)
         assert bool((grads[0] == 0).all())
+        for bad in (float("inf"), float("nan")):  # only measured
+            grads = [torch.tensor([1.0, bad, 2.0], device="cuda")]
+            ccr_mod.ccr_grad_clip(c, grads, float("inf"), work, norm)
+            assert not bool(norm.isfinite()) and float(grads[0][0]) == 1.0 and float(grads[0][2]) == 2.0
 
 
 def test_shared_tensors_count_twice_in_the_norm_only(ccr_mod):
