@@ -439,16 +439,10 @@ __device__ __forceinline__ void drain(f32x4* d) {
                  "+a"(d[7]));
 }
 
-// Eight neighbouring values of an output row.
-template <int OS>
+// Eight neighbouring bf16 values of an output row.
 __device__ __forceinline__ void store8(char* p, f32x4 lo, f32x4 hi) {
-  if constexpr (OS == 4) {
-    reinterpret_cast<f32x4*>(p)[0] = lo;
-    reinterpret_cast<f32x4*>(p)[1] = hi;
-  } else {
-    const bf16x4 a = __builtin_convertvector(lo, bf16x4), b = __builtin_convertvector(hi, bf16x4);
-    *reinterpret_cast<bf16x8*>(p) = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-  }
+  const bf16x4 a = __builtin_convertvector(lo, bf16x4), b = __builtin_convertvector(hi, bf16x4);
+  *reinterpret_cast<bf16x8*>(p) = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
 // One workgroup to a compute unit, each taking every gridDim.x-th tile.  The
@@ -464,7 +458,11 @@ __global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable t
   constexpr int kSlot = BM * KB, kSlots = 5;
   static_assert(BM == BN, "both operands fill a slot");
   using LoadA = Loader<ES, BM, kACol, false, NT>;
-  using LoadB = Loader<ES, BN, kBCol, true, NT>;
+  // Paired fragments of b give 16-byte stores of bf16 (dgrad of 8 x 4096 rows,
+  // 2048 x 1024: 119 us, unpaired 130), though in a column image their reads meet
+  // on half of the banks.  fp32 results are stored by 16 bytes either way.
+  constexpr bool kPaired = OS == 2;
+  using LoadB = Loader<ES, BN, kBCol, kPaired, NT>;
   constexpr int kStep = LoadA::kStep;
   constexpr int kLoads = LoadA::kLoads;  // of one slot
   static_assert(kLoads == 8 && LoadB::kLoads == 8, "the wait counts below");
@@ -546,7 +544,7 @@ __global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable t
   // Fragments are read in units: one LDS read each, two to a fragment from a
   // column image.
   using FragA = Frag<kACol, false>;
-  using FragB = Frag<kBCol, true>;
+  using FragB = Frag<kBCol, kPaired>;
   constexpr int kUnitsB = T * FragB::kReads, kUnits = kUnitsB + T * FragA::kReads;
   FragA a[2][T];
   FragB b[2][T];
@@ -652,18 +650,25 @@ __global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable t
     if (again) begin(next);
 
     // D holds b's rows (the output's columns) down its registers: lane l has
-    // output row l % 16 of each block and, of a pair of blocks, columns
-    // 8 (l / 16) + (0..7).
+    // output row l % 16 of each block and columns 4 (l / 16) + (0..3) of it, or of
+    // a pair of blocks columns 8 (l / 16) + (0..7).
     const bool full = at.m0 + BM <= at.M && at.n0 + BN <= at.N && !sh.add;
-    char* out = at.c + ((at.m0 + wm + (l & 15)) * at.N + at.n0 + wn + (l >> 4) * 8) * OS;
+    const int64_t n = at.n0 + wn + (l >> 4) * (kPaired ? 8 : 4);
+    char* out = at.c + ((at.m0 + wm + (l & 15)) * at.N + n) * OS;
     const int64_t down = 16 * at.N * OS;
+    auto column = [](int j) { return kPaired ? (j >> 1) * 32 + (j & 1) * 4 : j * 16; };
     if (full) {
 #pragma unroll
       for (int i = 0; i < T; i++) {
 #pragma unroll
         for (int j = 0; j < T; j += 2) {
           asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i][j + 1]));  // read out row by row
-          store8<OS>(out + j * 16 * OS, acc[i][j], acc[i][j + 1]);
+          if constexpr (kPaired) {
+            store8(out + column(j) * OS, acc[i][j], acc[i][j + 1]);
+          } else {
+            store4<OS>(out + column(j) * OS, acc[i][j], false);
+            store4<OS>(out + column(j + 1) * OS, acc[i][j + 1], false);
+          }
         }
         out += down;
         __builtin_amdgcn_sched_barrier(0);
@@ -675,8 +680,7 @@ __global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable t
 #pragma unroll
         for (int j = 0; j < T; j++) {
           asm volatile("" : "+a"(acc[i][j]));
-          const int c = (j >> 1) * 32 + (j & 1) * 4;
-          if (in && at.n0 + wn + (l >> 4) * 8 + c < at.N) store4<OS>(out + c * OS, acc[i][j], sh.add);
+          if (in && n + column(j) < at.N) store4<OS>(out + column(j) * OS, acc[i][j], sh.add);
         }
         out += down;
         __builtin_amdgcn_sched_barrier(0);
@@ -686,7 +690,7 @@ __global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable t
     at = next;
     // the next tile's step 0; its step 1 and part of a's step 2, and in a full
     // tile the results' stores, may be on their way
-    constexpr int kStores = T * T * OS / 4;
+    constexpr int kStores = kPaired ? T * T / 2 : T * T;
     if (full) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(21 + kStores < 63 ? 21 + kStores : 63) : "memory");
     else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     asm volatile("s_barrier" ::: "memory");
