@@ -186,6 +186,17 @@ __device__ __forceinline__ int xcd_tile(int b, int n) {
   return x * per + (x < rem ? x : rem) + (b >> 3);
 }
 
+// The same for tiles that do not take equally long (weight gradients, listed
+// from the longest on): the XCDs take turns at runs of kRun tiles, short enough
+// to share the long ones out, long enough to meet in an L2.  Weights 3016 x 336
+// of 8 experts of 40 to 17625 rows: 1024 us in contiguous runs, 203 us so; with
+// runs of 8 tiles equal experts lose a fifth (8 x 2000 rows: 43 -> 53 us).
+__device__ __forceinline__ int xcd_turns(int b, int n) {
+  constexpr int kRun = 16;
+  const int i = b >> 3, t = ((i / kRun) * 8 + (b & 7)) * kRun + i % kRun;
+  return b < n / (8 * kRun) * (8 * kRun) ? t : b;
+}
+
 // The tile that workgroup b of kCus takes in its round r, -1 for none.  Products and input
 // gradients, whose tiles take equally long: xcd_tile's contiguous runs.  Weight
 // gradients, whose tiles take as long as their expert has rows and are listed
@@ -278,7 +289,8 @@ __global__ __launch_bounds__(WM * WN * 64) void experts_ring_kernel(const Expert
   static_assert(LoadA::kLoads * NT == BM * 8 && LoadB::kLoads * NT == BN * 8, "whole loads");
   static_assert((NBUF - 2) * kLoads <= 63, "the wait count has 6 bits");
   __shared__ __align__(1024) char lds[NBUF * kBuf];
-  const Where at = place_of<OP, BM, BN>(tab, sh, xcd_tile(blockIdx.x, gridDim.x));
+  const int t = kACol ? xcd_turns(blockIdx.x, gridDim.x) : xcd_tile(blockIdx.x, gridDim.x);
+  const Where at = place_of<OP, BM, BN>(tab, sh, t);
   LoadA la;
   LoadB lb;
   la.init(at.a, (OP == ExpertOp::kProduct ? sh.H : sh.F) * ES, at.m0, at.M);
