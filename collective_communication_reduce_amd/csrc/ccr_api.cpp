@@ -2202,9 +2202,11 @@ ccr_status_t run_experts(ccr_ctx* ctx, ExpertOp op, const void* const* a, const 
     }
   }
   const ExpertTile tile = expert_tile(op, es, os, sh, work.data(), (int)work.size());
-  const int side = expert_tile_size(tile);
+  const ExpertTileSize side = expert_tile_size(tile);
   const int64_t N = op == ExpertOp::kProduct ? F : H;
-  auto tiles_of = [&](int64_t n) { return ceil_div(op == ExpertOp::kWgrad ? F : n, side) * ceil_div(N, side); };
+  auto tiles_of = [&](int64_t n) {
+    return ceil_div(op == ExpertOp::kWgrad ? F : n, side.rows) * ceil_div(N, side.cols);
+  };
   // one launch's grid, in work-items, is counted in 32 bits
   constexpr int64_t kMaxTiles = int64_t(UINT32_MAX) / 512;
   if (tiles_of(most) > kMaxTiles) return fail(CCR_ERR_UNSUPPORTED, "an expert's product is too large for one launch");

@@ -79,14 +79,15 @@ struct Loader {
   int k[kLoads];     // first k of the vector
 
   // p: the operand's first byte; x0: the tile's first row or column; extent:
-  // how many there are
-  __device__ __forceinline__ void init(const char* p, int64_t ld_bytes, int64_t x0, int64_t extent) {
+  // how many there are; thread: this thread's number among the NT
+  __device__ __forceinline__ void init(const char* p, int64_t ld_bytes, int64_t x0, int64_t extent,
+                                       int thread) {
     ld = ld_bytes;
     const int left = (int)(extent - x0 < X ? extent - x0 : X);
     base = COL ? p + x0 * ES : p + x0 * ld;
 #pragma unroll
     for (int i = 0; i < kLoads; i++) {
-      const int q = i * NT + threadIdx.x;
+      const int q = i * NT + thread;
       if constexpr (COL) {
         const int kr = q / kPerRow;
         const int c = (q % kPerRow) ^ col_swz<ES, X, PAIRED>(kr);
@@ -271,30 +272,35 @@ __device__ __forceinline__ void load_lds(uint32_t lds, const char* p) {
 }
 
 // ------------------------------------------------------- small and mid tiles
-// OP as in the table above.  Tile BM x BN of the output, WM x WN waves, a ring
-// of NBUF K-steps in LDS.  Per step one barrier: behind it the step's vectors
-// are in LDS and the step before is read by every wave, so its buffer takes
-// the loads of the step NBUF - 1 ahead.
-template <ExpertOp OP, int ES, int OS, int BM, int BN, int WM, int WN, int NBUF>
-__global__ __launch_bounds__(WM * WN * 64) void experts_ring_kernel(const ExpertTable tab,
-                                                                    const ExpertShape sh) {
+// OP as in the table above.  Tile BM x BN of the output; WK groups of WM x WN
+// waves, each of which takes every WK-th K-step over the whole tile; a ring of
+// NBUF rounds of WK K-steps in LDS.  Per round one barrier: behind it the
+// round's vectors are in LDS and the round before is read by every wave, so its
+// buffer takes the loads of the round NBUF - 1 ahead.
+template <ExpertOp OP, int ES, int OS, int BM, int BN, int WM, int WN, int WK, int NBUF>
+__global__ __launch_bounds__(WM * WN * WK * 64) void experts_ring_kernel(const ExpertTable tab,
+                                                                         const ExpertShape sh) {
   constexpr bool kACol = OP == ExpertOp::kWgrad;       // a: x, dout, dout
   constexpr bool kBCol = OP != ExpertOp::kProduct;     // b: W, W, x
-  constexpr int NT = WM * WN * 64;
+  constexpr int NT = WM * WN * 64;                     // threads of a group
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 blocks per wave
-  constexpr int kABytes = BM * KB, kBuf = (BM + BN) * KB;
+  constexpr int kABytes = BM * KB, kStepBytes = (BM + BN) * KB, kBuf = WK * kStepBytes;
   using LoadA = Loader<ES, BM, kACol, false, NT>;
   using LoadB = Loader<ES, BN, kBCol, false, NT>;
   constexpr int kLoads = LoadA::kLoads + LoadB::kLoads;
   static_assert(LoadA::kLoads * NT == BM * 8 && LoadB::kLoads * NT == BN * 8, "whole loads");
   static_assert((NBUF - 2) * kLoads <= 63, "the wait count has 6 bits");
+  static_assert(WK == 1 || WK * BM * BN * 4 <= NBUF * kBuf, "the groups' sums fit the ring");
   __shared__ __align__(1024) char lds[NBUF * kBuf];
   const int t = kACol ? xcd_turns(blockIdx.x, gridDim.x) : xcd_tile(blockIdx.x, gridDim.x);
   const Where at = place_of<OP, BM, BN>(tab, sh, t);
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wk = w / (WM * WN), wg = w % (WM * WN);
+  const int wm = (wg / WN) * (BM / WM), wn = (wg % WN) * (BN / WN);
   LoadA la;
   LoadB lb;
-  la.init(at.a, (OP == ExpertOp::kProduct ? sh.H : sh.F) * ES, at.m0, at.M);
-  lb.init(at.b, sh.H * ES, at.n0, at.N);
+  la.init(at.a, (OP == ExpertOp::kProduct ? sh.H : sh.F) * ES, at.m0, at.M, threadIdx.x % NT);
+  lb.init(at.b, sh.H * ES, at.n0, at.N, threadIdx.x % NT);
   constexpr int kStep = LoadA::kStep;
   // Step 0 holds the contraction's odd end (`rest` values, then zeros; no value
   // for a weight gradient without rows), so that every later step is whole.
@@ -303,20 +309,39 @@ __global__ __launch_bounds__(WM * WN * 64) void experts_ring_kernel(const Expert
   // way stays the same.
   const int whole = (int)((at.C - 1) / kStep), nk = whole + 1;
   const int rest = (int)(at.C - (int64_t)whole * kStep);
-  const char* pa = la.base + (kACol ? rest * la.ld : rest * ES);
-  const char* pb = lb.base + (kBCol ? rest * lb.ld : rest * ES);
   const int64_t da = la.stride(), db = lb.stride();
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = (w / WN) * (BM / WM), wn = (w % WN) * (BN / WN);
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(CCR_LDS char*)lds + w * 1024;
-  {
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(CCR_LDS char*)lds + wk * kStepBytes + wg * 1024;
+  const char *pa, *pb;  // step j, or the last whole one before it
+  int j = 0;
+  auto go_to = [&](int step) {
+    j = step < whole ? step : whole;
+    pa = la.base + (kACol ? rest * la.ld : rest * ES) + (j - 1) * da;
+    pb = lb.base + (kBCol ? rest * lb.ld : rest * ES) + (j - 1) * db;
+  };
+  auto issue = [&](uint32_t to) {
+#pragma unroll
+    for (int i = 0; i < LoadA::kLoads; i++) load_lds(to + i * NT * 16, (uint32_t)la.off[i], pa);
+#pragma unroll
+    for (int i = 0; i < LoadB::kLoads; i++)
+      load_lds(to + kABytes + i * NT * 16, (uint32_t)lb.off[i], pb);
+    const int next = j + WK < whole ? j + WK : whole;
+    pa += (next - j) * da;
+    pb += (next - j) * db;
+    j = next;
+  };
+  if (wk == 0 || wk >= nk) {  // the partial step, or zeros for a group without a step
+    const int until = wk == 0 ? rest : 0;
     const char* zero = reinterpret_cast<const char*>(&zero_vector);
 #pragma unroll
     for (int i = 0; i < LoadA::kLoads; i++)
-      load_lds(lds0 + i * NT * 16, la.k[i] < rest ? la.base + la.off[i] : zero);
+      load_lds(lds0 + i * NT * 16, la.k[i] < until ? la.base + la.off[i] : zero);
 #pragma unroll
     for (int i = 0; i < LoadB::kLoads; i++)
-      load_lds(lds0 + kABytes + i * NT * 16, lb.k[i] < rest ? lb.base + lb.off[i] : zero);
+      load_lds(lds0 + kABytes + i * NT * 16, lb.k[i] < until ? lb.base + lb.off[i] : zero);
+    go_to(wk + WK);
+  } else {
+    go_to(wk);
+    issue(lds0);
   }
   if (whole == 0) {
     pa = rest ? la.base : reinterpret_cast<const char*>(&zero_vector);
@@ -326,17 +351,6 @@ __global__ __launch_bounds__(WM * WN * 64) void experts_ring_kernel(const Expert
 #pragma unroll
     for (int i = 0; i < LoadB::kLoads; i++) lb.off[i] = 0;
   }
-  int j = 1;  // the step at pa, pb
-  auto issue = [&](uint32_t to) {
-#pragma unroll
-    for (int i = 0; i < LoadA::kLoads; i++) load_lds(to + i * NT * 16, (uint32_t)la.off[i], pa);
-#pragma unroll
-    for (int i = 0; i < LoadB::kLoads; i++)
-      load_lds(to + kABytes + i * NT * 16, (uint32_t)lb.off[i], pb);
-    pa += j < whole ? da : 0;
-    pb += j < whole ? db : 0;
-    j++;
-  };
 #pragma unroll
   for (int i = 1; i < NBUF - 1; i++) issue(lds0 + i * kBuf);
   f32x4 acc[TM][TN];
@@ -346,7 +360,7 @@ __global__ __launch_bounds__(WM * WN * 64) void experts_ring_kernel(const Expert
     for (int n = 0; n < TN; n++) acc[i][n] = f32x4{0, 0, 0, 0};
   // fp32 results are summed in chains of 64 products, and the chains' sums
   // apart: the error grows with the length of a chain of additions.  Over 4096
-  // values it is 2e-7 of the result, 1e-6 in one chain; the cost is 2%.
+  // values it is 3e-7 of the result, 1e-6 in one chain; the cost is 2%.
   constexpr int kChain = ES == 4 ? 8 : 32;  // K-steps
   f32x4 sum[OS == 4 ? TM : 1][OS == 4 ? TN : 1] = {};
   auto collect = [&]() {
@@ -358,23 +372,26 @@ __global__ __launch_bounds__(WM * WN * 64) void experts_ring_kernel(const Expert
         acc[i][n] = f32x4{0, 0, 0, 0};
       }
   };
-  int cur = 0, free = (NBUF - 1) * kBuf;  // byte offsets of this step's buffer and of the one read before
-  for (int s = 0; s < nk;) {
-    const int until = OS == 4 && s + kChain < nk ? s + kChain : nk;
+  int cur = 0, free = (NBUF - 1) * kBuf;  // byte offsets of this round's buffer and of the one read before
+  const int rounds = (nk + WK - 1) / WK;
+  for (int r = 0; r < rounds;) {
+    const int until = OS == 4 && r + kChain < rounds ? r + kChain : rounds;
 #pragma unroll 1
-    for (; s < until; s++) {
+    for (; r < until; r++) {
       asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NBUF - 2) * kLoads) : "memory");
+      const char* from = lds + cur + wk * kStepBytes;
       u32x4 a[2][TM], b[2][TN];
 #pragma unroll
       for (int h = 0; h < 2; h++) {
 #pragma unroll
-        for (int i = 0; i < TM; i++) a[h][i] = fragment<ES, BM, kACol, false>(lds + cur, wm, i, h);
+        for (int i = 0; i < TM; i++) a[h][i] = fragment<ES, BM, kACol, false>(from, wm, i, h);
 #pragma unroll
-        for (int n = 0; n < TN; n++) b[h][n] = fragment<ES, BN, kBCol, false>(lds + cur + kABytes, wn, n, h);
+        for (int n = 0; n < TN; n++) b[h][n] = fragment<ES, BN, kBCol, false>(from + kABytes, wn, n, h);
       }
       issue(lds0 + free);
       free = cur;
       cur = cur + kBuf == NBUF * kBuf ? 0 : cur + kBuf;
+      if (WK > 1 && r * WK + wk >= nk) continue;  // this group has no step in the last round
 #pragma unroll
       for (int h = 0; h < 2; h++)
 #pragma unroll
@@ -388,14 +405,34 @@ __global__ __launch_bounds__(WM * WN * 64) void experts_ring_kernel(const Expert
   // D holds b's rows (the output's columns) down its registers: lane l has
   // output row l % 16 and columns 4 (l / 16) + (0..3) of each 16 x 16 block.
   const int l = threadIdx.x & 63;
+  if constexpr (WK == 1) {
 #pragma unroll
-  for (int i = 0; i < TM; i++) {
-    const int64_t m = at.m0 + wm + i * 16 + (l & 15);
-    if (m >= at.M) continue;
+    for (int i = 0; i < TM; i++) {
+      const int64_t m = at.m0 + wm + i * 16 + (l & 15);
+      if (m >= at.M) continue;
 #pragma unroll
-    for (int n = 0; n < TN; n++) {
-      const int64_t c = at.n0 + wn + n * 16 + (l >> 4) * 4;
-      if (c < at.N) store4<OS>(at.c + (m * at.N + c) * OS, OS == 4 ? sum[i][n] : acc[i][n], sh.add);
+      for (int n = 0; n < TN; n++) {
+        const int64_t c = at.n0 + wn + n * 16 + (l >> 4) * 4;
+        if (c < at.N) store4<OS>(at.c + (m * at.N + c) * OS, OS == 4 ? sum[i][n] : acc[i][n], sh.add);
+      }
+    }
+  } else {
+    // the groups' sums, added in the groups' order
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    f32x4* part = reinterpret_cast<f32x4*>(lds);  // [WK][BM][BN / 4]
+#pragma unroll
+    for (int i = 0; i < TM; i++)
+#pragma unroll
+      for (int n = 0; n < TN; n++)
+        part[(wk * BM + wm + i * 16 + (l & 15)) * (BN / 4) + (wn + n * 16) / 4 + (l >> 4)] =
+            OS == 4 ? sum[i][n] : acc[i][n];
+    __syncthreads();
+    for (int q = threadIdx.x; q < BM * BN / 4; q += NT * WK) {
+      const int64_t m = at.m0 + q / (BN / 4), c = at.n0 + q % (BN / 4) * 4;
+      f32x4 v = part[q];
+#pragma unroll
+      for (int k = 1; k < WK; k++) v += part[k * BM * BN / 4 + q];
+      if (m < at.M && c < at.N) store4<OS>(at.c + (m * at.N + c) * OS, v, sh.add);
     }
   }
 }
@@ -524,8 +561,8 @@ __global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable t
   // values, then zeros; no value for a weight gradient without rows), so that
   // every later step is whole; step 1; the first of a's step 2.
   auto begin = [&](const Where& at) {
-    la.init(at.a, (OP == ExpertOp::kProduct ? sh.H : sh.F) * ES, at.m0, at.M);
-    lb.init(at.b, sh.H * ES, at.n0, at.N);
+    la.init(at.a, (OP == ExpertOp::kProduct ? sh.H : sh.F) * ES, at.m0, at.M, threadIdx.x);
+    lb.init(at.b, sh.H * ES, at.n0, at.N, threadIdx.x);
     whole = (int)((at.C - 1) / kStep);
     const int rest = (int)(at.C - (int64_t)whole * kStep);
     const char* zero = reinterpret_cast<const char*>(&zero_vector);
@@ -713,14 +750,17 @@ template <ExpertOp OP, int ES, int OS>
 hipError_t launch_as(const ExpertTable& tab, const ExpertShape& sh, ExpertTile tile, int tiles,
                      hipStream_t stream) {
   switch (tile) {
-    case ExpertTile::k32:  // 32 KiB of LDS: five workgroups to a compute unit
-      experts_ring_kernel<OP, ES, OS, 32, 32, 2, 2, 4><<<(unsigned)tiles, 256, 0, stream>>>(tab, sh);
+    case ExpertTile::k16:  // 64 KiB of LDS: two workgroups to a compute unit
+      experts_ring_kernel<OP, ES, OS, 16, 16, 1, 1, 4, 4><<<(unsigned)tiles, 256, 0, stream>>>(tab, sh);
+      break;
+    case ExpertTile::k32:  // 32 KiB: five
+      experts_ring_kernel<OP, ES, OS, 32, 32, 2, 2, 1, 4><<<(unsigned)tiles, 256, 0, stream>>>(tab, sh);
       break;
     case ExpertTile::k64:  // 48 KiB: three
-      experts_ring_kernel<OP, ES, OS, 64, 64, 2, 2, 3><<<(unsigned)tiles, 256, 0, stream>>>(tab, sh);
+      experts_ring_kernel<OP, ES, OS, 64, 64, 2, 2, 1, 3><<<(unsigned)tiles, 256, 0, stream>>>(tab, sh);
       break;
     case ExpertTile::k128:  // 128 KiB: one
-      experts_ring_kernel<OP, ES, OS, 128, 128, 2, 4, 4><<<(unsigned)tiles, 512, 0, stream>>>(tab, sh);
+      experts_ring_kernel<OP, ES, OS, 128, 128, 2, 4, 1, 4><<<(unsigned)tiles, 512, 0, stream>>>(tab, sh);
       break;
     case ExpertTile::k256:
       if constexpr (ES == 2)
@@ -735,53 +775,70 @@ hipError_t launch_as(const ExpertTable& tab, const ExpertShape& sh, ExpertTile t
 
 }  // namespace
 
-int expert_tile_size(ExpertTile tile) {
-  return tile == ExpertTile::k32 ? 32 : tile == ExpertTile::k64 ? 64 : tile == ExpertTile::k128 ? 128 : 256;
+ExpertTileSize expert_tile_size(ExpertTile tile) {
+  switch (tile) {
+    case ExpertTile::k16: return {16, 16};
+    case ExpertTile::k32: return {32, 32};
+    case ExpertTile::k64: return {64, 64};
+    case ExpertTile::k128: return {128, 128};
+    default: return {256, 256};
+  }
 }
 
 // The variant with the shortest estimated time.  A tile of s K-steps is taken
 // to cost c0 + c1 s + its output at an even share of 4.9 TB/s, and tiles to
 // run in rounds of one to a compute unit (of the smaller tiles, of which a unit
-// holds several, in fractions of a round).  c0 and c1 in us were fitted to all
-// three products of 24 shapes from 1 to 16000 rows; where the choice matters:
-//   bf16 product, us at tile          32     64    128    256
-//   1 row, 2048 x 1024               5.8    9.3   14.6   36.7
-//   8 x 16 rows, 512 x 512           3.4    4.4    6.0   13.9
-//   4 x 500 rows, 1024 x 1024       13.2    9.1   11.4   26.7
-//   8 x 200 rows, 2048 x 2048       41.3   30.5   21.7   44.2
-//   8 x 2000 rows, 1024 x 1024      95.3   59.4   50.6   35.7
-//   4 x 1500 rows, 2048 x 2048       131   77.7   62.4   50.4
-// fp32 products of 8 x 16 rows, 512 x 512: 5.5, 11.2, 32.3; weight gradients
-// (fp32 out) of 64 x 4 rows, 2048 x 1024: 268, 161, 181, 109.  Large fp32
-// products run at the rate of the matrix units from tile 64 on.
+// holds several, in fractions of a round).  A tile with a unit to itself takes
+// alone s instead of c1 s: in few tiles the groups of k16 share a long
+// contraction, in many its short rows cost it twice the loads of k32.  The
+// constants in us were fitted to all three products of 38 shapes from 1 to
+// 16000 rows; where the choice matters:
+//   us at tile                        16     32     64    128    256
+//   1 row, 2048 x 1024               3.8    6.2    9.3   14.6   36.7
+//   1 row, 8192 x 1024               6.7   17.4
+//   2 x 100 rows, 2856 x 120         4.4    7.8
+//   8 x 16 rows, 512 x 512           3.3    3.5    4.4    6.0   13.9
+//   6 x 120 rows, 512 x 512          8.2    4.2
+//   64 x 4 rows, 2048 x 1024        48.7   39.5
+//   4 x 500 rows, 1024 x 1024              13.2    9.1   11.4   26.7
+//   8 x 200 rows, 2048 x 2048              41.3   30.5   21.7   44.2
+//   8 x 2000 rows, 1024 x 1024             95.3   59.4   50.6   35.7
+//   4 x 1500 rows, 2048 x 2048              131   77.7   62.4   50.4
+// (products in bf16).  fp32 products of 8 x 16 rows, 512 x 512: 3.9, 6.0, 11.2,
+// 32.3; of 1 row, 8192 x 1024: 17.8, 55.1; weight gradients (fp32 out) of 64 x 4
+// rows, 2048 x 1024, from tile 32 on: 268, 161, 181, 109.  Large fp32 products
+// run at the rate of the matrix units from tile 64 on.
 ExpertTile expert_tile(ExpertOp op, int es, int os, const ExpertShape& sh, const int64_t* rows, int n) {
   struct Cost {
     ExpertTile tile;
-    double c0, c1;
+    double c0, c1, alone;
   };
-  const Cost costs[] = {{ExpertTile::k32, 0.25, es == 2 ? 0.09 : 0.15},
-                        {ExpertTile::k64, 0.4, es == 2 ? 0.2 : 0.52},
-                        {ExpertTile::k128, 2.0, es == 2 ? 0.5 : 2.0},
-                        {ExpertTile::k256, 1.0, 1.42}};
-  ExpertTile best = ExpertTile::k32;
+  const bool f32 = es == 4;
+  const Cost costs[] = {{ExpertTile::k16, 0.3, 0.09, f32 ? 0.058 : 0.03},
+                        {ExpertTile::k32, 0.25, f32 ? 0.15 : 0.09, f32 ? 0.2 : 0.11},
+                        {ExpertTile::k64, 0.4, f32 ? 0.52 : 0.2, f32 ? 0.52 : 0.2},
+                        {ExpertTile::k128, 2.0, f32 ? 2.0 : 0.5, f32 ? 2.0 : 0.5},
+                        {ExpertTile::k256, 1.0, 1.42, 1.42}};
+  ExpertTile best = ExpertTile::k16;
   double least = 0;
   for (const Cost& c : costs) {
     if (c.tile == ExpertTile::k256 && es == 4) continue;
-    const int x = expert_tile_size(c.tile), step = KB / es;
-    const double fixed = c.c0 + (double)x * x * os / 19000.0;
-    const int64_t across = ((op == ExpertOp::kProduct ? sh.F : sh.H) + x - 1) / x;
+    const ExpertTileSize x = expert_tile_size(c.tile);
+    const int step = KB / es;
+    const double fixed = c.c0 + (double)x.rows * x.cols * os / 19000.0;
+    const int64_t across = ((op == ExpertOp::kProduct ? sh.F : sh.H) + x.cols - 1) / x.cols;
     double tiles = 0, work = 0, longest = 0;
     for (int i = 0; i < n; i++) {
-      const int64_t down = ((op == ExpertOp::kWgrad ? sh.F : rows[i]) + x - 1) / x;
+      const int64_t down = ((op == ExpertOp::kWgrad ? sh.F : rows[i]) + x.rows - 1) / x.rows;
       const int64_t k = op == ExpertOp::kProduct ? sh.H : op == ExpertOp::kDgrad ? sh.F : rows[i];
-      const double t = fixed + c.c1 * (double)((k + step - 1) / step);
+      const double steps = (double)((k + step - 1) / step), alone = fixed + c.alone * steps;
       tiles += (double)(down * across);
-      work += t * (double)(down * across);
-      longest = t > longest ? t : longest;
+      work += (fixed + c.c1 * steps) * (double)(down * across);
+      longest = alone > longest ? alone : longest;
     }
     double est = work / kCus;
-    if (x >= 128 && op != ExpertOp::kWgrad) est = longest * ceil(tiles / kCus);
-    else if (x >= 128 && est > longest) est += longest / 4;  // the last round's unevenness
+    if (x.rows >= 128 && op != ExpertOp::kWgrad) est = longest * ceil(tiles / kCus);
+    else if (x.rows >= 128 && est > longest) est += longest / 4;  // the last round's unevenness
     if (est < longest) est = longest;
     if (least == 0 || est < least) {
       least = est;

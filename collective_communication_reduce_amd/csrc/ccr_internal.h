@@ -214,8 +214,11 @@ struct ExpertShape {
   bool add;  // wgrad: add to what c holds
 };
 // Kernel variants, by the side of their output tile.
-enum class ExpertTile : int { k32, k64, k128, k256 };
-int expert_tile_size(ExpertTile tile);
+enum class ExpertTile : int { k16, k32, k64, k128, k256 };
+struct ExpertTileSize {
+  int rows, cols;  // of the output
+};
+ExpertTileSize expert_tile_size(ExpertTile tile);
 // The variant for n experts of rows[i] rows.
 ExpertTile expert_tile(ExpertOp op, int es, int os, const ExpertShape& sh, const int64_t* rows, int n);
 // es, os: bytes per input and output value; tiles: in all, numbered group by group.

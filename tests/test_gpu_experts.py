@@ -182,6 +182,20 @@ def test_more_experts_than_one_launch_lists(ccr_mod, op):
     check(ccr_mod, op, "bf16", list(rng.integers(0, 20, 250)), 2, 40, 24)
 
 
+# one small output of a long sum, which the waves of a workgroup share by steps
+# of 32 (fp32) or 64 values: fewer steps than waves, steps that do not go round
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("long", [8, 32, 40, 64, 72, 128, 160, 192, 200, 256, 264, 328, 1288, 8200])
+def test_long_sums_of_few_outputs_bitwise(ccr_mod, op, dt, long):
+    if op == "wgrad":
+        check(ccr_mod, op, dt, [long, 0, long - 3], 1, 40, 24, seed=long)
+        check(ccr_mod, op, dt, [long], 1, 24, 40, seed=long, out_dt="f32", accumulate=True)
+    else:
+        H, F = (long, 40) if op == "product" else (40, long)
+        check(ccr_mod, op, dt, [1, 0, 19], 1, H, F, seed=long)
+
+
 @pytest.mark.parametrize("op,dt,rows,H,F", [
     ("product", "bf16", [700, 1300, 0, 2500], 1024, 768),
     ("dgrad", "bf16", [700, 1300, 0, 2500], 768, 1024),
