@@ -790,8 +790,11 @@ ExpertTileSize expert_tile_size(ExpertTile tile) {
 // run in rounds of one to a compute unit (of the smaller tiles, of which a unit
 // holds several, in fractions of a round).  A tile with a unit to itself takes
 // alone s instead of c1 s: in few tiles the groups of k16 share a long
-// contraction, in many its short rows cost it twice the loads of k32.  The
-// constants in us were fitted to all three products of 38 shapes from 1 to
+// contraction, in many its short rows cost it twice the loads of k32.  Rows
+// that are not whole lines of 128 bytes cost the tiles up to 64, whose reads
+// from L2 bound them, a third more, as each read touches two lines (4 x 3000
+// rows, 1000 x 1000 against 1024 x 1024: tile 64 57 and 42 us, tile 256 31.9 and
+// 30.0).  The constants in us were fitted to all three products of 38 shapes from 1 to
 // 16000 rows; where the choice matters:
 //   us at tile                        16     32     64    128    256
 //   1 row, 2048 x 1024               3.8    6.2    9.3   14.6   36.7
@@ -817,8 +820,9 @@ ExpertTile expert_tile(ExpertOp op, int es, int os, const ExpertShape& sh, const
   const Cost costs[] = {{ExpertTile::k16, 0.3, 0.09, f32 ? 0.058 : 0.03},
                         {ExpertTile::k32, 0.25, f32 ? 0.15 : 0.09, f32 ? 0.2 : 0.11},
                         {ExpertTile::k64, 0.4, f32 ? 0.52 : 0.2, f32 ? 0.52 : 0.2},
-                        {ExpertTile::k128, 2.0, f32 ? 2.0 : 0.5, f32 ? 2.0 : 0.5},
-                        {ExpertTile::k256, 1.0, 1.42, 1.42}};
+                        {ExpertTile::k128, 2.0, f32 ? 2.0 : 0.5, f32 ? 2.0 : 0.44},
+                        {ExpertTile::k256, 1.0, 1.42, 1.1}};
+  const bool odd_lines = sh.H * es % 128 || (op != ExpertOp::kProduct && sh.F * es % 128);
   ExpertTile best = ExpertTile::k16;
   double least = 0;
   for (const Cost& c : costs) {
@@ -826,19 +830,22 @@ ExpertTile expert_tile(ExpertOp op, int es, int os, const ExpertShape& sh, const
     const ExpertTileSize x = expert_tile_size(c.tile);
     const int step = KB / es;
     const double fixed = c.c0 + (double)x.rows * x.cols * os / 19000.0;
+    const double c1 = c.c1 * (odd_lines && x.rows <= 64 ? 1.35 : 1.0);
     const int64_t across = ((op == ExpertOp::kProduct ? sh.F : sh.H) + x.cols - 1) / x.cols;
-    double tiles = 0, work = 0, longest = 0;
+    double tiles = 0, work = 0, most = 0, longest = 0;
     for (int i = 0; i < n; i++) {
       const int64_t down = ((op == ExpertOp::kWgrad ? sh.F : rows[i]) + x.rows - 1) / x.rows;
       const int64_t k = op == ExpertOp::kProduct ? sh.H : op == ExpertOp::kDgrad ? sh.F : rows[i];
-      const double steps = (double)((k + step - 1) / step), alone = fixed + c.alone * steps;
+      const double steps = (double)((k + step - 1) / step);
+      const double t = fixed + c1 * steps, alone = fixed + c.alone * steps;
       tiles += (double)(down * across);
-      work += (fixed + c.c1 * steps) * (double)(down * across);
+      work += t * (double)(down * across);
+      most = t > most ? t : most;
       longest = alone > longest ? alone : longest;
     }
     double est = work / kCus;
-    if (x.rows >= 128 && op != ExpertOp::kWgrad) est = longest * ceil(tiles / kCus);
-    else if (x.rows >= 128 && est > longest) est += longest / 4;  // the last round's unevenness
+    if (x.rows >= 128 && op != ExpertOp::kWgrad) est = most * ceil(tiles / kCus);
+    else if (x.rows >= 128 && est > most) est += most / 4;  // the last round's unevenness
     if (est < longest) est = longest;
     if (least == 0 || est < least) {
       least = est;
