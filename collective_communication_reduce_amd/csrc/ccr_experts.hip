@@ -189,7 +189,7 @@ __device__ __forceinline__ int xcd_tile(int b, int n) {
 
 // The same for tiles that do not take equally long (weight gradients, listed
 // from the longest on): the XCDs take turns at runs of kRun tiles, short enough
-// to share the long ones out, long enough to meet in an L2.  Weights 3016 x 336
+// to share the long ones out, long enough to meet in an L2.  In tiles of 64, weights 3016 x 336
 // of 8 experts of 40 to 17625 rows: 1024 us in contiguous runs, 203 us so; with
 // runs of 8 tiles equal experts lose a fifth (8 x 2000 rows: 43 -> 53 us).
 __device__ __forceinline__ int xcd_turns(int b, int n) {
@@ -790,7 +790,8 @@ ExpertTileSize expert_tile_size(ExpertTile tile) {
 // run in rounds of one to a compute unit (of the smaller tiles, of which a unit
 // holds several, in fractions of a round).  A tile with a unit to itself takes
 // alone s instead of c1 s: in few tiles the groups of k16 share a long
-// contraction, in many its short rows cost it twice the loads of k32.  Rows
+// contraction, in many its short rows cost it twice the loads of k32 (and more
+// where they are rows of 16 columns: input and weight gradients).  Rows
 // that are not whole lines of 128 bytes cost the tiles up to 64, whose reads
 // from L2 bound them, a third more, as each read touches two lines (4 x 3000
 // rows, 1000 x 1000 against 1024 x 1024: tile 64 57 and 42 us, tile 256 31.9 and
@@ -799,6 +800,7 @@ ExpertTileSize expert_tile_size(ExpertTile tile) {
 //   us at tile                        16     32     64    128    256
 //   1 row, 2048 x 1024               3.8    6.2    9.3   14.6   36.7
 //   1 row, 8192 x 1024               6.7   17.4
+//   5 x 1 row, 2048 x 1024           5.1    6.3   10.1   14.7   37.1
 //   2 x 100 rows, 2856 x 120         4.4    7.8
 //   8 x 16 rows, 512 x 512           3.3    3.5    4.4    6.0   13.9
 //   6 x 120 rows, 512 x 512          8.2    4.2
@@ -817,7 +819,7 @@ ExpertTile expert_tile(ExpertOp op, int es, int os, const ExpertShape& sh, const
     double c0, c1, alone;
   };
   const bool f32 = es == 4;
-  const Cost costs[] = {{ExpertTile::k16, 0.3, 0.09, f32 ? 0.058 : 0.03},
+  const Cost costs[] = {{ExpertTile::k16, 0.3, op == ExpertOp::kProduct ? 0.07 : 0.09, f32 ? 0.058 : 0.03},
                         {ExpertTile::k32, 0.25, f32 ? 0.15 : 0.09, f32 ? 0.2 : 0.11},
                         {ExpertTile::k64, 0.4, f32 ? 0.52 : 0.2, f32 ? 0.52 : 0.2},
                         {ExpertTile::k128, 2.0, f32 ? 2.0 : 0.5, f32 ? 2.0 : 0.44},
