@@ -35,9 +35,10 @@ using dev::u32x4;
 __device__ const u32x4 zero_vector = {0, 0, 0, 0};
 
 // LDS image of an operand tile of X rows (the tile's m or n) by one K-step of
-// KB = 128 bytes per row (64 bf16 or 32 fp32), in 16-byte vectors.  Loads go straight from memory to LDS, which fixes each lane's LDS
-// place (its wave's base + 16 x lane), so the bank swizzle is applied to the
-// address a lane reads from.
+// KB = 128 bytes per row (64 bf16 or 32 fp32), in 16-byte vectors.  Loads go
+// straight from memory to LDS, which fixes each lane's LDS place (its wave's
+// base + 16 x lane), so the bank swizzle is applied to the address a lane reads
+// from.
 //
 // Row image (K contiguous in memory): X rows of 8 vectors; vector c of
 // row r sits at c ^ row_swz(r).  A 16-byte read serves 16 lanes at a time, of
@@ -189,18 +190,19 @@ __device__ __forceinline__ int xcd_tile(int b, int n) {
 
 // The same for tiles that do not take equally long (weight gradients, listed
 // from the longest on): the XCDs take turns at runs of kRun tiles, short enough
-// to share the long ones out, long enough to meet in an L2.  In tiles of 64, weights 3016 x 336
-// of 8 experts of 40 to 17625 rows: 1024 us in contiguous runs, 203 us so; with
-// runs of 8 tiles equal experts lose a fifth (8 x 2000 rows: 43 -> 53 us).
+// to share the long ones out, long enough to meet in an L2.  Tiles of 64,
+// weights 3016 x 336 of 8 experts of 40 to 17625 rows: 1024 us in contiguous
+// runs, 203 us so; with runs of 8 tiles equal experts lose a fifth (8 x 2000
+// rows: 43 -> 53 us).
 __device__ __forceinline__ int xcd_turns(int b, int n) {
   constexpr int kRun = 16;
   const int i = b >> 3, t = ((i / kRun) * 8 + (b & 7)) * kRun + i % kRun;
   return b < n / (8 * kRun) * (8 * kRun) ? t : b;
 }
 
-// The tile that workgroup b of kCus takes in its round r, -1 for none.  Products and input
-// gradients, whose tiles take equally long: xcd_tile's contiguous runs.  Weight
-// gradients, whose tiles take as long as their expert has rows and are listed
+// The tile that workgroup b of kCus takes in its round r, -1 for none.
+// Products and input gradients, whose tiles take equally long: xcd_tile's
+// contiguous runs.  Weight gradients, whose tiles take as long as their expert has rows and are listed
 // from the longest on: each round's tiles are dealt out in one piece, the later
 // rounds in reverse, so that who had a long tile gets a short one (a training
 // layer of 16 experts of 518 to 5999 rows: 323 us with contiguous runs, 274 us so).
@@ -276,7 +278,11 @@ __device__ __forceinline__ void load_lds(uint32_t lds, const char* p) {
 // waves, each of which takes every WK-th K-step over the whole tile; a ring of
 // NBUF rounds of WK K-steps in LDS.  Per round one barrier: behind it the
 // round's vectors are in LDS and the round before is read by every wave, so its
-// buffer takes the loads of the round NBUF - 1 ahead.
+// buffer takes the loads of the round NBUF - 1 ahead.  What bounds it: few rows,
+// HBM (the weights of 64 experts, 2048 x 1024 bf16, for 288 rows: 57.5 us, 4.7
+// TB/s) or, with few tiles, a tile's latency; tile 64, reads from L2 (21 TB/s
+// over the chip); fp32, the matrix units (8192 rows, 4096 x 4096: 1.94 ms, 142
+// TFLOP/s).
 template <ExpertOp OP, int ES, int OS, int BM, int BN, int WM, int WN, int WK, int NBUF>
 __global__ __launch_bounds__(WM * WN * WK * 64) void experts_ring_kernel(const ExpertTable tab,
                                                                          const ExpertShape sh) {
@@ -454,7 +460,10 @@ __global__ __launch_bounds__(WM * WN * WK * 64) void experts_ring_kernel(const E
 // With one wave to a SIMD nothing hides an instruction that stalls, so reads
 // and loads are placed one by one between the products.  Measured at 8192^3
 // against reads and loads in groups of three before every eight products:
-// 1283 -> 1433 TFLOP/s (dgrad).
+// 1283 -> 1433 TFLOP/s (dgrad).  What bounds it is power: a training layer's
+// product (196,608 rows of 64 experts, 2048 x 1024) takes 700 us, 1.18 PFLOP/s,
+// with the matrix units 67% busy at 1.6 GHz.
+
 // A fragment as fragment() gives it, read in parts.
 template <bool COL, bool PAIRED>
 struct Frag {

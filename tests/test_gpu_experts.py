@@ -134,6 +134,15 @@ def test_large_accumulation_bitwise(ccr_mod, out_dt):
 
 
 @pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [[2, 0, 1], [270, 0, 5]], ids=["few rows", "more than a tile"])
+@pytest.mark.parametrize("H,F", [(1 << 20, 8), (8, 1 << 20)])
+def test_longest_rows_bitwise(ccr_mod, op, dt, rows, H, F):
+    # 9 x 2^20 < 2^24: every sum is exact
+    check(ccr_mod, op, dt, rows, 1, H, F, seed=5)
+
+
+@pytest.mark.parametrize("op", OPS)
 def test_offsets_past_32_bits(ccr_mod, op):
     """Rows, weights and results that lie past 2^32 bytes from their buffer's
     first byte: expert 1's are compared, expert 0's are many."""
