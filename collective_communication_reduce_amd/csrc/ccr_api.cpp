@@ -2397,6 +2397,11 @@ ccr_status_t run_grads(ccr_ctx* ctx, bool clip, const void* const* grads, void* 
     tab.tile0[tab.n] = (int32_t)tab.ntiles;
     return (int)std::min<int64_t>(slots, std::max<int64_t>(1, tab.ntiles));
   };
+  if (launches.size() == 1 && total <= kGradSmallTiles) {
+    fill(launches[0]);
+    HIP_TRY(launch_grad_small(tab, clip, max_norm, norm, s));
+    return CCR_OK;
+  }
   int64_t before = 0;  // tiles of the launches so far
   for (size_t i = 0; i < launches.size(); i++) {
     const int grid = fill(launches[i]);

@@ -7,9 +7,9 @@
 // Both are streaming passes bound by HBM.  The tensors of a call are cut into
 // tiles and the tiles dealt round robin to at most kGradSlots workgroups, so a
 // call over hundreds of small tensors is still one launch per kGradTensors of
-// them.  Each workgroup leaves one fp64 partial in its own
-// slot of the caller's work array; the slots are added in a fixed order, so
-// the norm has the same bits on every run.  Squares are taken and added in
+// them.  Each workgroup leaves one fp64 partial in its own slot of the caller's
+// work array; the slots are added in a fixed order, so the norm has the same
+// bits on every run.  Squares are taken and added in
 // fp64: the square of any fp32 value is exact in it and neither overflows nor
 // underflows, and at HBM rate its cost does not show.
 
@@ -73,11 +73,12 @@ __device__ __forceinline__ double squares(u32x4 v, double acc) {
   return acc;
 }
 
+// thread: this thread's number among the kBlock that share the tile
 template <int ES, bool NT>
-__device__ __forceinline__ double tile_squares(const GradTensor& t, int64_t tile, double acc) {
+__device__ __forceinline__ double tile_squares(const GradTensor& t, int64_t tile, int thread, double acc) {
   const Span s = span_of<ES>(t);
   const u32x4* v = reinterpret_cast<const u32x4*>(s.src + (int64_t)s.head * ES);
-  const int64_t first = tile * kTileVecs + threadIdx.x;
+  const int64_t first = tile * kTileVecs + thread;
   u32x4 x[kVecs];
 #pragma unroll
   for (int u = 0; u < kVecs; u++) {
@@ -86,10 +87,8 @@ __device__ __forceinline__ double tile_squares(const GradTensor& t, int64_t tile
   }
 #pragma unroll
   for (int u = 0; u < kVecs; u++) acc = squares<ES>(x[u], acc);
-  if (tile == 0 && (int)threadIdx.x < s.head)
-    acc += square(element<ES>(s.src, threadIdx.x));
-  if (tile == 0 && (int)threadIdx.x < s.tail)
-    acc += square(element<ES>(s.src, s.count - s.tail + threadIdx.x));
+  if (tile == 0 && thread < s.head) acc += square(element<ES>(s.src, thread));
+  if (tile == 0 && thread < s.tail) acc += square(element<ES>(s.src, s.count - s.tail + thread));
   return acc;
 }
 
@@ -100,13 +99,14 @@ __device__ __forceinline__ double wave_sum(double x) {
 }
 
 // The sum over the workgroup, in every thread; `part` holds a double per wave.
+template <int WAVES = kBlock / 64>
 __device__ __forceinline__ double block_sum(double x, double* part) {
   x = wave_sum(x);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
   __syncthreads();
   double s = 0;
 #pragma unroll
-  for (int w = 0; w < kBlock / 64; w++) s += part[w];
+  for (int w = 0; w < WAVES; w++) s += part[w];
   return s;
 }
 
@@ -134,9 +134,11 @@ __global__ __launch_bounds__(kBlock) void grad_squares_kernel(const GradTable ta
     const GradTensor& t = tab.t[at];
     const int64_t in = tile - tab.tile0[at];
     if (tile < stream)
-      acc = t.es == 4 ? tile_squares<4, true>(t, in, acc) : tile_squares<2, true>(t, in, acc);
+      acc = t.es == 4 ? tile_squares<4, true>(t, in, threadIdx.x, acc)
+                      : tile_squares<2, true>(t, in, threadIdx.x, acc);
     else
-      acc = t.es == 4 ? tile_squares<4, false>(t, in, acc) : tile_squares<2, false>(t, in, acc);
+      acc = t.es == 4 ? tile_squares<4, false>(t, in, threadIdx.x, acc)
+                      : tile_squares<2, false>(t, in, threadIdx.x, acc);
   }
   const double s = block_sum(acc, part);
   if (threadIdx.x == 0) work[blockIdx.x] = add ? work[blockIdx.x] + s : s;
@@ -180,11 +182,11 @@ __device__ __forceinline__ void scale_element(const Span& s, int64_t i, float c)
 }
 
 template <int ES, bool NT>
-__device__ __forceinline__ void tile_scale(const GradTensor& t, int64_t tile, float c) {
+__device__ __forceinline__ void tile_scale(const GradTensor& t, int64_t tile, int thread, float c) {
   const Span s = span_of<ES>(t);
   const u32x4* v = reinterpret_cast<const u32x4*>(s.src + (int64_t)s.head * ES);
   char* const out = s.dst + (int64_t)s.head * ES;
-  const int64_t first = tile * kTileVecs + threadIdx.x;
+  const int64_t first = tile * kTileVecs + thread;
   u32x4 x[kVecs];
 #pragma unroll
   for (int u = 0; u < kVecs; u++) {
@@ -213,12 +215,18 @@ __device__ __forceinline__ void tile_scale(const GradTensor& t, int64_t tile, fl
       }
     }
   }
-  if (tile == 0 && (int)threadIdx.x < s.head) scale_element<ES>(s, threadIdx.x, c);
-  if (tile == 0 && (int)threadIdx.x < s.tail)
-    scale_element<ES>(s, s.count - s.tail + threadIdx.x, c);
+  if (tile == 0 && thread < s.head) scale_element<ES>(s, thread, c);
+  if (tile == 0 && thread < s.tail) scale_element<ES>(s, s.count - s.tail + thread, c);
 }
 
-// out = g * min(1, max_norm / (norm + 1e-6)) over the tiles, the last tile
+// min(1, max_norm / (norm + 1e-6)).  A NaN stays; an infinite max_norm only
+// measures, whatever the norm.
+__device__ __forceinline__ float factor_of(float norm, float max_norm) {
+  const float q = max_norm / (norm + 1e-6f);
+  return q > 1.0f || max_norm == __builtin_inff() ? 1.0f : q;
+}
+
+// out = g * factor over the tiles, the last tile
 // first: the pass before left the end of the gradients in the last-level
 // cache.  Every workgroup adds the slots itself (16 KiB from L2), which saves
 // a launch between the two passes.  In place, a factor of 1 writes nothing.
@@ -229,16 +237,49 @@ __global__ __launch_bounds__(kBlock) void grad_clip_kernel(const GradTable tab, 
   __shared__ double part[kBlock / 64];
   const float nv = (float)sqrt(total_of(work, slots, part));
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = nv;
-  const float q = max_norm / (nv + 1e-6f);
-  // a NaN stays; an infinite max_norm only measures, whatever the norm
-  const float c = q > 1.0f || max_norm == __builtin_inff() ? 1.0f : q;
+  const float c = factor_of(nv, max_norm);
   for (int64_t tile = tab.ntiles - 1 - blockIdx.x; tile >= 0; tile -= gridDim.x) {
     const int at = tensor_of(tab, tile);
     const GradTensor& t = tab.t[at];
     if (c == 1.0f && t.src == t.dst) continue;
     const int64_t in = tile - tab.tile0[at];
-    if (t.es == 4) tile_scale<4, NT>(t, in, c);
-    else tile_scale<2, NT>(t, in, c);
+    if (t.es == 4) tile_scale<4, NT>(t, in, threadIdx.x, c);
+    else tile_scale<2, NT>(t, in, threadIdx.x, c);
+  }
+}
+
+// A call of up to kGradSmallTiles tiles: one workgroup of kGroups times kBlock
+// threads, each kBlock of them taking every kGroups-th tile, makes the norm and
+// the clipping in one launch.  It is bound by latency, one round of tiles after
+// the other.  Against two launches, us back to back: 1 tile, norm 2.9 against
+// 4.3, clipping 3.2 against 5.7; 8 tiles 4.5 / 4.8 and 5.2 / 6.0; 10 tiles 4.7 /
+// 4.9 and 5.6 / 6.0; 12 tiles 5.5 / 4.9 and 6.5 / 6.0.
+constexpr int kGroups = 4;
+template <bool CLIP>
+__global__ __launch_bounds__(kBlock * kGroups) void grad_small_kernel(const GradTable tab, float max_norm,
+                                                                      float* norm) {
+  __shared__ double part[kGroups * kBlock / 64];
+  const int thread = threadIdx.x % kBlock;
+  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / kBlock);
+  double acc = 0;
+  for (int tile = group; tile < tab.ntiles; tile += kGroups) {
+    const int at = tensor_of(tab, tile);
+    const GradTensor& t = tab.t[at];
+    const int in = tile - tab.tile0[at];
+    acc = t.es == 4 ? tile_squares<4, false>(t, in, thread, acc) : tile_squares<2, false>(t, in, thread, acc);
+  }
+  const float nv = (float)sqrt(block_sum<kGroups * kBlock / 64>(acc, part));
+  if (threadIdx.x == 0) *norm = nv;
+  if constexpr (CLIP) {
+    const float c = factor_of(nv, max_norm);
+    for (int tile = group; tile < tab.ntiles; tile += kGroups) {
+      const int at = tensor_of(tab, tile);
+      const GradTensor& t = tab.t[at];
+      if (c == 1.0f && t.src == t.dst) continue;
+      const int in = tile - tab.tile0[at];
+      if (t.es == 4) tile_scale<4, false>(t, in, thread, c);
+      else tile_scale<2, false>(t, in, thread, c);
+    }
   }
 }
 
@@ -256,6 +297,13 @@ int64_t grad_tiles(const void* p, int64_t count, int es) {
 hipError_t launch_grad_squares(const GradTable& tab, int grid, int64_t stream_tiles, double* work,
                                bool add, hipStream_t stream) {
   grad_squares_kernel<<<(unsigned)grid, kBlock, 0, stream>>>(tab, stream_tiles, work, add ? 1 : 0);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_small(const GradTable& tab, bool clip, float max_norm, float* norm,
+                             hipStream_t stream) {
+  if (clip) grad_small_kernel<true><<<1, kBlock * kGroups, 0, stream>>>(tab, max_norm, norm);
+  else grad_small_kernel<false><<<1, kBlock * kGroups, 0, stream>>>(tab, max_norm, norm);
   return hipGetLastError();
 }
 

@@ -73,6 +73,12 @@ SIZES = {
 }
 
 
+# few tiles of 16 KiB, which one workgroup takes, and the first counts it does not
+for _tiles in (2, 5, 9, 10, 11, 12):
+    SIZES[f"{_tiles} tiles of one tensor"] = [(_tiles * 4096 - 3, "f32", 0)]
+    SIZES[f"{_tiles} tensors"] = [(700 + 3 * i, "bf16" if i % 2 else "f32", i % 4) for i in range(_tiles)]
+
+
 @pytest.mark.parametrize("sizes", SIZES.values(), ids=SIZES.keys())
 def test_norm(ccr_mod, sizes):
     import torch
