@@ -240,20 +240,37 @@ static_assert(sizeof(GateArgs) <= 3584, "fits the kernel argument segment");
 hipError_t launch_gate_sum(bool bwd, bool over_all, int es, const GateArgs& a, int R, int64_t T,
                            int E, int K, int64_t row_bytes, bool large, hipStream_t stream);
 
-// The gradient norm and clipping (ccr_grad.hip).  Up to kGradTensors tensors
-// go into one launch; tile0[i] = first tile of tensor i, tile0[n] = ntiles.
-constexpr int kGradTensors = 112;
+// The gradient norm and clipping (ccr_grad.hip).
 struct GradTensor {
   const char* src;
   char* dst;
   int64_t count;
   int32_t es;
 };
+// The tensors of one launch, as many as fit the kernel arguments: two words
+// each where every result goes to its source (a norm, clipping in place), else
+// three.  tile0[i] = first tile of tensor i.
+constexpr int kGradTensors = 200;
 struct GradTable {
-  int32_t n;
+  int32_t n, words;
   int64_t ntiles;
-  int32_t tile0[kGradTensors + 1];
-  GradTensor t[kGradTensors];
+  int32_t tile0[kGradTensors];
+  uint64_t word[2 * kGradTensors];  // src, 2 count + (1 for bf16), dst
+
+  static int capacity(bool apart) { return apart ? 2 * kGradTensors / 3 : kGradTensors; }
+  void clear(bool apart) {
+    n = 0;
+    words = apart ? 3 : 2;
+    ntiles = 0;
+  }
+  void add(const GradTensor& t, int64_t tiles) {
+    uint64_t* w = word + (int64_t)n * words;
+    w[0] = reinterpret_cast<uint64_t>(t.src);
+    w[1] = (uint64_t)t.count * 2 + (t.es == 2);
+    if (words == 3) w[2] = reinterpret_cast<uint64_t>(t.dst);
+    tile0[n++] = (int32_t)ntiles;
+    ntiles += tiles;
+  }
 };
 static_assert(sizeof(GradTable) <= 4056, "fits the kernel argument segment");
 // Slots of the work array, one per workgroup at most.
