@@ -74,23 +74,36 @@ __device__ __forceinline__ double squares(u32x4 v, double acc) {
   return acc;
 }
 
-// thread: this thread's number among the kBlock that share the tile
-template <int ES, bool NT>
-__device__ __forceinline__ double tile_squares(const GradTensor& t, int64_t tile, int thread, double acc) {
-  const Span s = span_of<ES>(t);
+// A tile's vectors: thread's of the kBlock threads that share it; past the
+// tensor's end zeros if FILL, else anything.
+template <int ES, bool NT, bool FILL>
+__device__ __forceinline__ void tile_load(const Span& s, int64_t tile, int thread, u32x4* x) {
   const u32x4* v = reinterpret_cast<const u32x4*>(s.src + (int64_t)s.head * ES);
   const int64_t first = tile * kTileVecs + thread;
-  u32x4 x[kVecs];
 #pragma unroll
   for (int u = 0; u < kVecs; u++) {
     const int64_t i = first + u * kBlock;
-    x[u] = i < s.nvec ? dev::load16<NT>(v + i) : u32x4{0, 0, 0, 0};
+    if constexpr (FILL) x[u] = i < s.nvec ? dev::load16<NT>(v + i) : u32x4{0, 0, 0, 0};
+    else if (i < s.nvec) x[u] = dev::load16<NT>(v + i);
   }
+}
+
+template <int ES>
+__device__ __forceinline__ double tile_sum(const Span& s, int64_t tile, int thread, const u32x4* x,
+                                           double acc) {
 #pragma unroll
   for (int u = 0; u < kVecs; u++) acc = squares<ES>(x[u], acc);
   if (tile == 0 && thread < s.head) acc += square(element<ES>(s.src, thread));
   if (tile == 0 && thread < s.tail) acc += square(element<ES>(s.src, s.count - s.tail + thread));
   return acc;
+}
+
+template <int ES, bool NT>
+__device__ __forceinline__ double tile_squares(const GradTensor& t, int64_t tile, double acc) {
+  const Span s = span_of<ES>(t);
+  u32x4 x[kVecs];
+  tile_load<ES, NT, true>(s, tile, threadIdx.x, x);
+  return tile_sum<ES>(s, tile, threadIdx.x, x, acc);
 }
 
 __device__ __forceinline__ double wave_sum(double x) {
@@ -152,11 +165,9 @@ __global__ __launch_bounds__(kBlock) void grad_squares_kernel(const GradTable ta
   for (int64_t tile = blockIdx.x; tile < tab.ntiles; tile += gridDim.x) {
     const Place p = place_of(tab, tile);
     if (tile < stream)
-      acc = p.t.es == 4 ? tile_squares<4, true>(p.t, p.tile, threadIdx.x, acc)
-                        : tile_squares<2, true>(p.t, p.tile, threadIdx.x, acc);
+      acc = p.t.es == 4 ? tile_squares<4, true>(p.t, p.tile, acc) : tile_squares<2, true>(p.t, p.tile, acc);
     else
-      acc = p.t.es == 4 ? tile_squares<4, false>(p.t, p.tile, threadIdx.x, acc)
-                        : tile_squares<2, false>(p.t, p.tile, threadIdx.x, acc);
+      acc = p.t.es == 4 ? tile_squares<4, false>(p.t, p.tile, acc) : tile_squares<2, false>(p.t, p.tile, acc);
   }
   const double s = block_sum(acc, part);
   if (threadIdx.x == 0) work[blockIdx.x] = add ? work[blockIdx.x] + s : s;
@@ -200,17 +211,10 @@ __device__ __forceinline__ void scale_element(const Span& s, int64_t i, float c)
 }
 
 template <int ES, bool NT>
-__device__ __forceinline__ void tile_scale(const GradTensor& t, int64_t tile, int thread, float c) {
-  const Span s = span_of<ES>(t);
-  const u32x4* v = reinterpret_cast<const u32x4*>(s.src + (int64_t)s.head * ES);
+__device__ __forceinline__ void tile_store(const Span& s, int64_t tile, int thread, const u32x4* x,
+                                           float c) {
   char* const out = s.dst + (int64_t)s.head * ES;
   const int64_t first = tile * kTileVecs + thread;
-  u32x4 x[kVecs];
-#pragma unroll
-  for (int u = 0; u < kVecs; u++) {
-    const int64_t i = first + u * kBlock;
-    if (i < s.nvec) x[u] = dev::load16<NT>(v + i);
-  }
   if ((reinterpret_cast<uintptr_t>(out) & 15) == 0) {
 #pragma unroll
     for (int u = 0; u < kVecs; u++) {
@@ -237,6 +241,14 @@ __device__ __forceinline__ void tile_scale(const GradTensor& t, int64_t tile, in
   if (tile == 0 && thread < s.tail) scale_element<ES>(s, s.count - s.tail + thread, c);
 }
 
+template <int ES, bool NT>
+__device__ __forceinline__ void tile_scale(const GradTensor& t, int64_t tile, float c) {
+  const Span s = span_of<ES>(t);
+  u32x4 x[kVecs];
+  tile_load<ES, NT, false>(s, tile, threadIdx.x, x);
+  tile_store<ES, NT>(s, tile, threadIdx.x, x, c);
+}
+
 // min(1, max_norm / (norm + 1e-6)).  A NaN stays; an infinite max_norm only
 // measures, whatever the norm.
 __device__ __forceinline__ float factor_of(float norm, float max_norm) {
@@ -261,39 +273,52 @@ __global__ __launch_bounds__(kBlock, 8) void grad_clip_kernel(const GradTable ta
   for (int64_t tile = tab.ntiles - 1 - blockIdx.x; tile >= 0; tile -= gridDim.x) {
     const Place p = place_of(tab, tile);
     if (c == 1.0f && p.t.src == p.t.dst) continue;
-    if (p.t.es == 4) tile_scale<4, NT>(p.t, p.tile, threadIdx.x, c);
-    else tile_scale<2, NT>(p.t, p.tile, threadIdx.x, c);
+    if (p.t.es == 4) tile_scale<4, NT>(p.t, p.tile, c);
+    else tile_scale<2, NT>(p.t, p.tile, c);
   }
 }
 
 // A call of up to kGradSmallTiles tiles: one workgroup of kGroups times kBlock
-// threads, each kBlock of them taking every kGroups-th tile, makes the norm and
-// the clipping in one launch.  It is bound by latency, one round of tiles after
-// the other.  Against two launches, us back to back: 1 tile, norm 2.9 against
-// 4.3, clipping 3.2 against 5.7; 8 tiles 4.5 / 4.8 and 5.2 / 6.0; 10 tiles 4.7 /
-// 4.9 and 5.6 / 6.0; 12 tiles 5.5 / 4.9 and 6.5 / 6.0.
-constexpr int kGroups = 4;
+// threads, each kBlock of them with up to kMine tiles in registers, makes the
+// norm and the clipping in one launch and one pass over the gradients.  It is
+// bound by latency: the launch, the loads, the stores.  Against two launches, us
+// back to back on warm buffers: 1 tile, norm 3.0 against 4.7, clipping 3.6
+// against 6.6; 8 tiles 4.7 / 5.3 and 6.2 / 7.4; 12 tiles 5.7 / 5.4 and 7.7 / 7.5;
+// 16 tiles 6.7 / 5.4 and 9.3 / 7.5.  On cold buffers, clipping 10 tiles: 6.7 / 10.6.
+constexpr int kGroups = 4, kMine = kGradSmallTiles / kGroups;
+static_assert(kMine * kGroups == kGradSmallTiles, "every tile has its threads");
 template <bool CLIP>
 __global__ __launch_bounds__(kBlock * kGroups) void grad_small_kernel(const GradTable tab, float max_norm,
                                                                       float* norm) {
   __shared__ double part[kGroups * kBlock / 64];
   const int thread = threadIdx.x % kBlock;
   const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / kBlock);
+  u32x4 x[kMine][kVecs];
+  Place p[kMine];
+#pragma unroll
+  for (int m = 0; m < kMine; m++) {
+    const int tile = m * kGroups + group;
+    if (tile >= tab.ntiles) continue;
+    p[m] = place_of(tab, tile);
+    if (p[m].t.es == 4) tile_load<4, false, true>(span_of<4>(p[m].t), p[m].tile, thread, x[m]);
+    else tile_load<2, false, true>(span_of<2>(p[m].t), p[m].tile, thread, x[m]);
+  }
   double acc = 0;
-  for (int tile = group; tile < tab.ntiles; tile += kGroups) {
-    const Place p = place_of(tab, tile);
-    acc = p.t.es == 4 ? tile_squares<4, false>(p.t, p.tile, thread, acc)
-                      : tile_squares<2, false>(p.t, p.tile, thread, acc);
+#pragma unroll
+  for (int m = 0; m < kMine; m++) {
+    if (m * kGroups + group >= tab.ntiles) continue;
+    acc = p[m].t.es == 4 ? tile_sum<4>(span_of<4>(p[m].t), p[m].tile, thread, x[m], acc)
+                         : tile_sum<2>(span_of<2>(p[m].t), p[m].tile, thread, x[m], acc);
   }
   const float nv = (float)sqrt(block_sum<kGroups * kBlock / 64>(acc, part));
   if (threadIdx.x == 0) *norm = nv;
   if constexpr (CLIP) {
     const float c = factor_of(nv, max_norm);
-    for (int tile = group; tile < tab.ntiles; tile += kGroups) {
-      const Place p = place_of(tab, tile);
-      if (c == 1.0f && p.t.src == p.t.dst) continue;
-      if (p.t.es == 4) tile_scale<4, false>(p.t, p.tile, thread, c);
-      else tile_scale<2, false>(p.t, p.tile, thread, c);
+#pragma unroll
+    for (int m = 0; m < kMine; m++) {
+      if (m * kGroups + group >= tab.ntiles || (c == 1.0f && p[m].t.src == p[m].t.dst)) continue;
+      if (p[m].t.es == 4) tile_store<4, false>(span_of<4>(p[m].t), p[m].tile, thread, x[m], c);
+      else tile_store<2, false>(span_of<2>(p[m].t), p[m].tile, thread, x[m], c);
     }
   }
 }

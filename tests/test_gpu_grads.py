@@ -77,7 +77,7 @@ SIZES = {
 for _n in (133, 134, 200, 201, 266, 267, 401):
     SIZES[f"{_n} tensors"] = [(5 + i % 40, "bf16" if i % 3 else "f32", i % 4) for i in range(_n)]
 # few tiles of 16 KiB, which one workgroup takes, and the first counts it does not
-for _tiles in (2, 5, 9, 10, 11, 12):
+for _tiles in (2, 5, 9, 10, 11, 12, 13):
     SIZES[f"{_tiles} tiles of one tensor"] = [(_tiles * 4096 - 3, "f32", 0)]
     SIZES[f"{_tiles} tensors"] = [(700 + 3 * i, "bf16" if i % 2 else "f32", i % 4) for i in range(_tiles)]
 
