@@ -462,7 +462,7 @@ __global__ __launch_bounds__(WM * WN * WK * 64) void experts_ring_kernel(const E
 // against reads and loads in groups of three before every eight products:
 // 1283 -> 1433 TFLOP/s (dgrad).  What bounds it is power: a training layer's
 // product (196,608 rows of 64 experts, 2048 x 1024) takes 700 us, 1.18 PFLOP/s,
-// with the matrix units 67% busy at 1.6 GHz.
+// with the matrix units 66% busy at 1.65 GHz.
 
 // A fragment as fragment() gives it, read in parts.
 template <bool COL, bool PAIRED>
