@@ -1,6 +1,9 @@
 """Host-side refusals of the experts' products, the gated sum and the gradient
 calls: what the binding and the C entries turn away before any device is
 touched.  No GPU is used."""
+import os
+import re
+import subprocess
 import types
 
 import numpy as np
@@ -8,6 +11,7 @@ import pytest
 import torch
 
 import collective_communication_reduce_amd as ccr
+from collective_communication_reduce_amd import build as ccr_build
 
 CTX = types.SimpleNamespace(device=0, handle=None)
 BF16 = torch.bfloat16
@@ -70,3 +74,21 @@ def test_work_constant_matches_the_header():
     root = os.path.dirname(os.path.dirname(os.path.abspath(ccr.__file__)))
     text = open(os.path.join(root, "include", "ccr.h")).read()
     assert int(re.search(r"#define CCR_GRAD_WORK (\d+)", text).group(1)) == ccr.CCR_GRAD_WORK
+
+
+def test_no_accumulator_is_copied_between_products(tmp_path):
+    # The large tiles' products are written in assembly, so the compiler does not
+    # wait for them: between a loop's first product and the wait before the results
+    # are read it must not move an accumulator.
+    asm = tmp_path / "experts.s"
+    subprocess.run([ccr_build.hipcc(), *ccr_build.FLAGS, "-S", "--offload-device-only",
+                    os.path.join(ccr_build.CSRC, "ccr_experts.hip"), "-o", str(asm)],
+                   check=True, capture_output=True)
+    text = asm.read_text()
+    kernels = re.findall(r"^(_ZN3ccr\S*experts_big_kernel\S*):(.*?)s_endpgm", text, re.S | re.M)
+    assert len(kernels) == 4  # product, input gradient, weight gradient to fp32 and to bf16
+    for name, body in kernels:
+        loop = body[body.index("v_mfma"):]
+        loop = loop[:loop.index("s_nop 15")]
+        assert loop.count("v_mfma") == 128, name
+        assert "v_accvgpr" not in loop and "scratch_" not in loop, name
