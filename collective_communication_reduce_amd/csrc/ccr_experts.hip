@@ -263,7 +263,10 @@ __device__ __forceinline__ Where place_of(const ExpertTable& tab, const ExpertSh
 
 // The loads are written in assembly (they have no result register, only LDS)
 // because the compiler would otherwise wait for all of them before any later
-// LDS read.
+// LDS read.  m0 holds the LDS place; a load must not follow its write directly,
+// which is why write, wait state and load are one block that nothing can be
+// moved into or out of.  (m0 is reserved and cannot be named as clobbered; the
+// compiler has no use of its own for it in these kernels.)
 __device__ __forceinline__ void load_lds(uint32_t lds, uint32_t off, const char* base) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                ::"s"(lds), "v"(off), "s"(base) : "memory");
@@ -538,16 +541,13 @@ __global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable t
   const char *pa, *pb;  // the step whose loads are next, of a and of b
   int64_t da, db;
   int ja, jb, whole;
-  // A slot's loads, one at a time: the LDS place in m0, then load i.
-  auto place = [&](int i, uint32_t to) {
-    asm volatile("s_add_u32 m0, %0, %1" ::"s"(to), "n"(i * NT * 16) : "scc");
+  // A slot's loads, one at a time: load i of the slot at `to`.
+  auto load_at = [&](int i, uint32_t to, const int* off, const char* p) {
+    asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3"
+                 ::"s"(to), "n"(i * NT * 16), "v"(off[i]), "s"(p) : "memory", "scc");
   };
-  auto load_a = [&](int i) {
-    asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(la.off[i]), "s"(pa) : "memory");
-  };
-  auto load_b = [&](int i) {
-    asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(lb.off[i]), "s"(pb) : "memory");
-  };
+  auto load_a = [&](int i, uint32_t to) { load_at(i, to, la.off, pa); };
+  auto load_b = [&](int i, uint32_t to) { load_at(i, to, lb.off, pb); };
   // Past the last step the loads bring the last whole step again (or, where
   // there is none, each operand's first vector) into slots that are not read
   // any more: the loop keeps no branch, and the count of loads on their way
@@ -562,11 +562,7 @@ __global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable t
   };
   auto load_whole = [&](auto& load, uint32_t to, int n) {
 #pragma unroll
-    for (int i = 0; i < n; i++) {
-      place(i, to);
-      asm volatile("s_nop 0");
-      load(i);
-    }
+    for (int i = 0; i < n; i++) load(i, to);
   };
   // A tile's first loads: step 0, which holds the contraction's odd end (`rest`
   // values, then zeros; no value for a weight gradient without rows), so that
@@ -664,10 +660,8 @@ __global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable t
             for (int u = n * kUnits / kReadSlots; u < (n + 1) * kUnits / kReadSlots; u++)
               read(u, 1, at_a, at_b);
           }
-          if (n / kLoadEvery < kLoads - kEarlyA) {  // the rest of a's step s + 2
-            if (n % kLoadEvery == 1) place(kEarlyA + n / kLoadEvery, to);
-            if (n % kLoadEvery == 2) load_a(kEarlyA + n / kLoadEvery);
-          }
+          if (n % kLoadEvery == 2 && n / kLoadEvery < kLoads - kEarlyA)
+            load_a(kEarlyA + n / kLoadEvery, to);  // the rest of a's step s + 2
           __builtin_amdgcn_sched_barrier(0);
         }
         next_a();
@@ -689,13 +683,8 @@ __global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable t
               read(u, 0, at_a, at_b);
           }
           const int i = n / kLoadEvery;
-          if (i < kLoads) {
-            if (n % kLoadEvery == 1) place(i, to_b);
-            if (n % kLoadEvery == 2) load_b(i);
-          } else if (i < kLoads + kEarlyA) {
-            if (n % kLoadEvery == 1) place(i - kLoads, to_a);
-            if (n % kLoadEvery == 2) load_a(i - kLoads);
-          }
+          if (n % kLoadEvery == 2 && i < kLoads) load_b(i, to_b);
+          else if (n % kLoadEvery == 2 && i < kLoads + kEarlyA) load_a(i - kLoads, to_a);
           __builtin_amdgcn_sched_barrier(0);
         }
         static_assert((kLoads + kEarlyA - 1) * kLoadEvery + 2 < T * T, "a phase holds its loads");

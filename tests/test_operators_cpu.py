@@ -92,3 +92,25 @@ def test_no_accumulator_is_copied_between_products(tmp_path):
         loop = loop[:loop.index("s_nop 15")]
         assert loop.count("v_mfma") == 128, name
         assert "v_accvgpr" not in loop and "scratch_" not in loop, name
+
+
+@pytest.fixture(scope="module")
+def experts_asm(tmp_path_factory):
+    asm = tmp_path_factory.mktemp("asm") / "experts.s"
+    subprocess.run([ccr_build.hipcc(), *ccr_build.FLAGS, "-S", "--offload-device-only",
+                    os.path.join(ccr_build.CSRC, "ccr_experts.hip"), "-o", str(asm)],
+                   check=True, capture_output=True)
+    return asm.read_text()
+
+
+def test_no_load_to_lds_follows_the_write_of_m0_directly(experts_asm):
+    # m0 holds the LDS place of a load that goes straight there; the load needs a
+    # wait state between the write and itself, or it may take the place before.
+    lines = [x.split(";")[0].strip() for x in experts_asm.splitlines()]
+    lines = [x for x in lines if x and not x.startswith(".") and not x.endswith(":")]
+    loads = [i for i, x in enumerate(lines) if x.startswith("global_load_lds")]
+    assert len(loads) > 64
+    bare = [lines[i - 1:i + 1] for i in loads if re.match(r"s_\w+ m0\b", lines[i - 1])]
+    assert not bare, f"{len(bare)} of {len(loads)}, first {bare[0]}"
+    # nothing but these loads writes m0
+    assert sum(bool(re.match(r"\w+ m0\b", x)) for x in lines) == len(loads)
