@@ -490,9 +490,10 @@ struct Frag {
 // because all 256 of them are accumulators here, which the compiler's own
 // allocation mixes with the fragments and moves about in the loop.  No two
 // products in a row touch the same D, so no wait states are due between them;
-// drain() provides those before D is read.  (The compiler does not know of them:
+// drain() provides those before D is read.  The compiler does not know of them:
 // were it to copy an accumulator inside the loop, the copy would miss the last
-// sums.  It has no cause to while every D is read in place after drain().)
+// sums.  It has no cause to while every D is read in place after drain(); the
+// build reads the assembly of these kernels and refuses one that does.
 __device__ __forceinline__ void mma_acc(u32x4 a, u32x4 b, f32x4& d) {
   asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(d) : "v"(a), "v"(b));
 }

@@ -114,3 +114,33 @@ def test_no_load_to_lds_follows_the_write_of_m0_directly(experts_asm):
     assert not bare, f"{len(bare)} of {len(loads)}, first {bare[0]}"
     # nothing but these loads writes m0
     assert sum(bool(re.match(r"\w+ m0\b", x)) for x in lines) == len(loads)
+
+
+def test_the_build_refuses_moved_accumulators_and_bare_loads(experts_asm):
+    ccr_build.check_experts(experts_asm)
+    at = experts_asm.index("v_mfma", experts_asm.index("experts_big_kernel"))
+    end = experts_asm.index("\n", at) + 1
+    for planted in ("\tv_accvgpr_read_b32 v0, a0\n", "\tscratch_store_dword off, v0, s0\n"):
+        with pytest.raises(RuntimeError, match="moved"):
+            ccr_build.check_experts(experts_asm[:end] + planted + experts_asm[end:])
+    with pytest.raises(RuntimeError, match="m0"):
+        ccr_build.check_experts(experts_asm[:end] + "\ts_mov_b32 m0, s0\n" + experts_asm[end:])
+    load = re.search(r"\ts_add_u32 m0, .*\n(\ts_nop 0\n)\tglobal_load_lds", experts_asm)
+    with pytest.raises(RuntimeError, match="m0"):
+        ccr_build.check_experts(experts_asm[:load.start(1)] + experts_asm[load.end(1):])
+    with pytest.raises(RuntimeError, match="kernels"):
+        ccr_build.check_experts("")
+
+
+def test_the_build_checks_what_it_links(monkeypatch, tmp_path):
+    done = []
+    monkeypatch.setattr(ccr_build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(ccr_build, "build_marshal", lambda: "")
+    monkeypatch.setattr(ccr_build.subprocess, "run", lambda cmd, **k: done.append(cmd) or types.SimpleNamespace(
+        returncode=0, stdout="", stderr=""))
+    (tmp_path / f"ccr_experts-hip-amdgcn-amd-amdhsa-{ccr_build.ARCH}.s").write_text("s_endpgm")
+    with pytest.raises(RuntimeError, match="large tiles"):
+        ccr_build.build()
+    assert not any("-shared" in cmd for cmd in done)  # nothing was linked
+    # the checked file is the one that the object is assembled from
+    assert any("-save-temps=obj" in cmd and cmd[-1] == str(tmp_path / "ccr_experts.o") for cmd in done)
