@@ -516,25 +516,27 @@ def _ctx_stream(ctx: Context, stream):
     return _stream(torch.cuda.current_stream(ctx.device) if stream is None else stream)
 
 
-def _refuse(ctx: Context, t, i, dtype, shape, what: str):
+def _refuse(ctx: Context, t, i, dtype, shape, what: str, room: bool):
     """Say why tensor i of `what` is not what the call takes."""
     if t.dtype is not dtype:
         raise TypeError(f"{what}[{i}] is {t.dtype}, not {dtype}")
+    have, want = tuple(t.shape), tuple(shape)
+    if have[1:] != want[1:] or len(have) != len(want) or (have[0] < want[0] if room else have[0] != want[0]):
+        raise ValueError(f"{what}[{i}] has shape {have}, needs {want}{' or more rows' if room else ''}")
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what}[{i}] must be a contiguous device tensor")
-    if t.get_device() != ctx.device:
-        raise ValueError(f"{what}[{i}] is on {t.device}, the context on device {ctx.device}")
-    raise ValueError(f"{what}[{i}] has shape {tuple(t.shape)}, needs {tuple(shape)}")
+    raise ValueError(f"{what}[{i}] is on {t.device}, the context on device {ctx.device}")
 
 
-def _buffers(ctx: Context, tensors, dtype, shapes, what: str) -> bytes:
+def _buffers(ctx: Context, tensors, dtype, shapes, what: str, room: bool = False) -> bytes:
     """Pointer array of contiguous tensors of `dtype` on the context's device,
-    one per entry of `shapes` (each of at least as many rows)."""
+    one per entry of `shapes`.  `room`: each may have more rows, which the call
+    leaves alone."""
     if len(tensors) != len(shapes):
         raise ValueError(f"{what}: {len(tensors)} buffers for {len(shapes)} ranks")
-    p = _ccr_torch.pointers(tensors, dtype, ctx.device, shapes)
+    p = _ccr_torch.pointers(tensors, dtype, ctx.device, shapes, room)
     if type(p) is int:
-        _refuse(ctx, tensors[p], p, dtype, shapes[p], what)
+        _refuse(ctx, tensors[p], p, dtype, shapes[p], what, room)
     return p
 
 
@@ -551,16 +553,17 @@ def _expert_counts(ecnt, R: int):
 
 def ccr_moe_experts(ctx: Context, exp: Sequence, w: Sequence, ecnt, out: Sequence, stream=None):
     """out[d] row i = w_e @ exp[d] row i, e the expert of the row: exp[d]
-    [rows, H] as the dispatch leaves it, w[d] [E/R, F, H], ecnt [R, E]."""
+    [rows, H] as the dispatch leaves it, w[d] [E/R, F, H], ecnt [R, E].  Buffers
+    of rows may have more than ecnt counts: those are left alone."""
     R = len(w)
     ecnt, counts, E, rows = _expert_counts(ecnt, R)
     _, F, H = w[0].shape
     dt = w[0].dtype
     code = _dtype_code(w[0])
     _check(_lib.ccr_moe_experts(
-        ctx.handle, _buffers(ctx, exp, dt, [(n, H) for n in rows], "exp"),
+        ctx.handle, _buffers(ctx, exp, dt, [(n, H) for n in rows], "exp", True),
         _buffers(ctx, w, dt, [(E // R, F, H)] * R, "w"), counts, R, E, H, F, code,
-        _buffers(ctx, out, dt, [(n, F) for n in rows], "out"), _ctx_stream(ctx, stream)))
+        _buffers(ctx, out, dt, [(n, F) for n in rows], "out", True), _ctx_stream(ctx, stream)))
 
 
 def ccr_moe_experts_dgrad(ctx: Context, dout: Sequence, w: Sequence, ecnt, dexp: Sequence, stream=None):
@@ -572,9 +575,9 @@ def ccr_moe_experts_dgrad(ctx: Context, dout: Sequence, w: Sequence, ecnt, dexp:
     dt = w[0].dtype
     code = _dtype_code(w[0])
     _check(_lib.ccr_moe_experts_dgrad(
-        ctx.handle, _buffers(ctx, dout, dt, [(n, F) for n in rows], "dout"),
+        ctx.handle, _buffers(ctx, dout, dt, [(n, F) for n in rows], "dout", True),
         _buffers(ctx, w, dt, [(E // R, F, H)] * R, "w"), counts, R, E, H, F, code,
-        _buffers(ctx, dexp, dt, [(n, H) for n in rows], "dexp"), _ctx_stream(ctx, stream)))
+        _buffers(ctx, dexp, dt, [(n, H) for n in rows], "dexp", True), _ctx_stream(ctx, stream)))
 
 
 def ccr_moe_experts_wgrad(ctx: Context, exp: Sequence, dout: Sequence, ecnt, dw: Sequence,
@@ -587,8 +590,8 @@ def ccr_moe_experts_wgrad(ctx: Context, exp: Sequence, dout: Sequence, ecnt, dw:
     dt = exp[0].dtype
     code, dw_code = _dtype_code(exp[0]), _dtype_code(dw[0])
     _check(_lib.ccr_moe_experts_wgrad(
-        ctx.handle, _buffers(ctx, exp, dt, [(n, H) for n in rows], "exp"),
-        _buffers(ctx, dout, dt, [(n, F) for n in rows], "dout"), counts, R, E, H, F, code,
+        ctx.handle, _buffers(ctx, exp, dt, [(n, H) for n in rows], "exp", True),
+        _buffers(ctx, dout, dt, [(n, F) for n in rows], "dout", True), counts, R, E, H, F, code,
         dw_code, int(bool(accumulate)), _buffers(ctx, dw, dw[0].dtype, [(E // R, F, H)] * R, "dw"),
         _ctx_stream(ctx, stream)))
 
@@ -612,7 +615,8 @@ def _gate_args(ctx, rows, logits, topk, norm):
 def ccr_moe_gate_sum(ctx: Context, rows: Sequence, logits: Sequence, topk: Sequence, y: Sequence,
                      norm: str = "chosen", stream=None):
     """y[r][t] = sum_k w_k rows[r][t, k], w the softmax of logits[r][t] at
-    topk[r][t], over the chosen experts or over "all"."""
+    topk[r][t], over the chosen experts or over "all".  Every rank has the same
+    number of tokens."""
     R, T, E, K, H, code, p, l, k = _gate_args(ctx, rows, logits, topk, norm)
     _check(_lib.ccr_moe_gate_sum(ctx.handle, p, l, k, R, T, E, K, H, code, _GATE_NORM[norm],
                                  _buffers(ctx, y, rows[0].dtype, [(T, H)] * R, "y"),
@@ -645,8 +649,8 @@ def _grad_list(tensors, what: str):
 
 def _grad_scratch(ctx, work, norm):
     import torch
-    _buffers(ctx, [work], torch.float64, [(CCR_GRAD_WORK,)], "work")
-    _buffers(ctx, [norm], torch.float32, [(1,)], "norm")
+    _buffers(ctx, [work], torch.float64, [(CCR_GRAD_WORK,)], "work", True)
+    _buffers(ctx, [norm], torch.float32, [(1,)], "norm", True)
 
 
 def ccr_grad_norm(ctx: Context, grads: Sequence, work, norm, stream=None):

@@ -4,10 +4,10 @@
 // method call of 50 to 60 ns, which for the gradients of a training step
 // (hundreds of tensors, five properties each) takes longer than the kernels.
 //
-//   pointers(tensors, dtype, device, shapes) -> bytes of data pointers, or the
-//       index of the first tensor that is not a contiguous tensor of `dtype`
-//       on GPU `device` with its entry of `shapes` as its shape (the first
-//       dimension may be larger)
+//   pointers(tensors, dtype, device, shapes, room) -> bytes of data pointers, or
+//       the index of the first tensor that is not a contiguous tensor of `dtype`
+//       on GPU `device` with its entry of `shapes` as its shape (if `room`, the
+//       first dimension may be larger)
 //   grad_list(tensors) -> (data pointers, element counts, dtype codes) as bytes
 //       (uint64, int64, int32), or the index of the first tensor that is not a
 //       contiguous GPU tensor of float32 (code 0) or bfloat16 (code 1)
@@ -45,25 +45,26 @@ PyObject* as_bytes(const std::vector<T>& v) {
                                    static_cast<Py_ssize_t>(v.size() * sizeof(T)));
 }
 
-// Whether t has `shape`, its first dimension at least as large.
-bool has_shape(const at::Tensor& t, PyObject* shape) {
+// Whether t has `shape`; with `room`, its first dimension at least as large.
+bool has_shape(const at::Tensor& t, PyObject* shape, bool room) {
   if (!PyTuple_Check(shape) || PyTuple_GET_SIZE(shape) != t.dim()) return false;
   for (int64_t d = 0; d < t.dim(); d++) {
     const long long n = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, d));
-    if (n < 0 || (d == 0 ? t.size(0) < n : t.size(d) != n)) return false;
+    if (n < 0 || (d == 0 && room ? t.size(0) < n : t.size(d) != n)) return false;
   }
   return true;
 }
 
 PyObject* pointers(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
-  if (nargs != 4 || !THPDtype_Check(args[1])) {
-    PyErr_SetString(PyExc_TypeError, "pointers(tensors, dtype, device, shapes)");
+  if (nargs != 5 || !THPDtype_Check(args[1])) {
+    PyErr_SetString(PyExc_TypeError, "pointers(tensors, dtype, device, shapes, room)");
     return nullptr;
   }
   Items tensors(args[0], "a list of tensors"), shapes(args[3], "a list of shapes");
   if (!tensors.ok() || !shapes.ok()) return nullptr;
   const long device = PyLong_AsLong(args[2]);
   if (device == -1 && PyErr_Occurred()) return nullptr;
+  const bool room = args[4] == Py_True;
   const at::ScalarType dtype = reinterpret_cast<THPDtype*>(args[1])->scalar_type;
   const Py_ssize_t n = tensors.size();
   if (shapes.size() != n) {
@@ -75,7 +76,7 @@ PyObject* pointers(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     if (!THPVariable_Check(tensors[i])) return PyLong_FromSsize_t(i);
     const at::Tensor& t = THPVariable_Unpack(tensors[i]);
     if (t.scalar_type() != dtype || !t.is_cuda() || t.get_device() != device || !t.is_contiguous() ||
-        !has_shape(t, shapes[i])) {
+        !has_shape(t, shapes[i], room)) {
       if (PyErr_Occurred()) return nullptr;
       return PyLong_FromSsize_t(i);
     }

@@ -96,3 +96,49 @@ def test_training_step(ccr_mod, R, T, E, K, H, F, norm):
     gsum = torch.sqrt((4 * W.grad[:E // R] ** 2).sum() + (L.grad ** 2).sum())
     near(total, gsum.reshape(1), R * T + K + H + F)
     near(clipped[0], 2 * W.grad[:E // R] * min(1.0, 0.5 / (float(gsum) + 1e-6)), R * T + K + H + F)
+
+
+def test_tokens_and_experts_that_a_call_would_not_compute_are_refused(ccr_mod):
+    """A rank with more (or fewer) tokens than the first, in any buffer, and more
+    weights than the ranks' experts: refused, and nothing written."""
+    import torch
+    dev = dict(device="cuda")
+    T, K, H, E = 3, 2, 8, 4
+
+    def gate(n):
+        return [torch.ones(n, K, H, **dev), torch.ones(n, E, **dev), torch.zeros(n, K, dtype=torch.int32, **dev),
+                torch.ones(n, H, **dev), torch.full((n, K, H), 7.0, **dev), torch.full((n, E), 7.0, **dev),
+                torch.full((n, H), 7.0, **dev)]
+
+    first = gate(T)
+    with ccr_mod.Context(0) as c:
+        for n in (T - 1, T + 1):
+            for i in range(7):  # the second rank's i-th buffer, or all of them
+                second = gate(T)
+                second[i] = gate(n)[i]
+                for other in (second, gate(n)):
+                    rows, logits, topk, dy, dr, dl, y = ([a, b] for a, b in zip(first, other))
+                    if i in (0, 1, 2, 6) or other is not second:
+                        with pytest.raises(ValueError, match="shape"):
+                            ccr_mod.ccr_moe_gate_sum(c, rows, logits, topk, y)
+                    if i != 6 or other is not second:
+                        with pytest.raises(ValueError, match="shape"):
+                            ccr_mod.ccr_moe_gate_sum_bwd(c, dy, rows, logits, topk, dr, dl)
+                    torch.cuda.synchronize()
+                    assert all(bool((t == 7.0).all()) for t in (*dr, *dl, *y))
+        x, y = torch.ones(5, H, **dev), torch.full((5, 16), 7.0, **dev)
+        ecnt = [[1, 2, 0, 0]]
+        for experts in (3, 5):
+            w = torch.full((experts, 16, H), 7.0, **dev)
+            with pytest.raises(ValueError, match="shape"):
+                ccr_mod.ccr_moe_experts(c, [x], [w], ecnt, [y])
+            with pytest.raises(ValueError, match="shape"):
+                ccr_mod.ccr_moe_experts_dgrad(c, [y], [w], ecnt, [x])
+            with pytest.raises(ValueError, match="shape"):
+                ccr_mod.ccr_moe_experts_wgrad(c, [x], [y], ecnt, [w])
+            torch.cuda.synchronize()
+            assert bool((w == 7.0).all()) and bool((y == 7.0).all()) and bool((x == 1.0).all())
+        w = torch.ones(4, 16, H, **dev)
+        ccr_mod.ccr_moe_experts(c, [x], [w], ecnt, [y])  # rows behind the last are left alone
+        torch.cuda.synchronize()
+    assert bool((y[:3] == H).all()) and bool((y[3:] == 7.0).all())

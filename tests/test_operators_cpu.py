@@ -144,3 +144,12 @@ def test_the_build_checks_what_it_links(monkeypatch, tmp_path):
     assert not any("-shared" in cmd for cmd in done)  # nothing was linked
     # the checked file is the one that the object is assembled from
     assert any("-save-temps=obj" in cmd and cmd[-1] == str(tmp_path / "ccr_experts.o") for cmd in done)
+
+
+def test_rows_beyond_the_counted_ones_are_taken_where_they_are_left_alone():
+    x = torch.ones(5, 2)
+    for shape, room, word in [((4, 2), True, "device tensor"), ((5, 2), True, "device tensor"),
+                              ((6, 2), True, "shape"), ((4, 2), False, "shape"), ((5, 2), False, "device tensor"),
+                              ((5, 1), True, "shape"), ((5,), True, "shape"), ((5, 2, 1), True, "shape")]:
+        with pytest.raises(ValueError, match=word):
+            ccr._buffers(CTX, [x], torch.float32, [shape], "x", room)
