@@ -4,7 +4,7 @@ A thin ctypes layer over the C ABI in ``include/ccr.h``: every function here
 only marshals arguments (torch tensors -> device pointers, sizes, dtype
 codes, the current HIP stream) and calls the C entry point of the same name.
 (Lists of tensors that can be long are read by a small compiled module,
-``_ccr_torch``, built with the library.)
+``_ccr_torch``, built with the library and loaded by the first such call.)
 All of the work runs in the library's HIP kernels and SDMA copies; there is
 no Python or CPU fallback, and importing this package fails loudly if the
 library has not been built (``python collective_communication_reduce_amd/build.py``).
@@ -14,6 +14,7 @@ PyTorch only provides device memory (tensors) and streams.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 from dataclasses import dataclass
 from typing import Optional, Sequence
@@ -22,7 +23,6 @@ import numpy as np
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libccr.so")
-MARSHAL_PATH = os.path.join(_HERE, "_ccr_torch.so")
 
 CCR_OK, CCR_ERR_INVALID_ARG, CCR_ERR_UNSUPPORTED, CCR_ERR_HIP, CCR_ERR_OOM, CCR_ERR_TIMEOUT = range(6)
 CCR_F32, CCR_BF16 = 0, 1
@@ -135,9 +135,6 @@ def _load():
         raise ImportError(
             f"{LIB_PATH} is missing: build it with "
             "`python collective_communication_reduce_amd/build.py` (hipcc, gfx950)")
-    if not os.path.exists(MARSHAL_PATH):
-        raise ImportError(f"{MARSHAL_PATH} is missing: build it with "
-                          "`python collective_communication_reduce_amd/build.py`")
     lib = ctypes.CDLL(LIB_PATH)
     if len(_hip_runtimes()) > 1:
         raise ImportError(f"two HIP runtimes are loaded ({sorted(_hip_runtimes())}); import "
@@ -150,7 +147,21 @@ def _load():
 
 
 _lib = _load()
-from . import _ccr_torch  # noqa: E402  (needs torch loaded, which _load does)
+_marshal_module = None
+
+
+def _marshal():
+    """The compiled module that reads tensor lists, loaded by the first call that
+    takes one: the other calls do without it."""
+    global _marshal_module
+    if _marshal_module is None:
+        try:
+            _marshal_module = importlib.import_module("._ccr_torch", __name__)
+        except ImportError as e:
+            raise ImportError(f"{__name__}._ccr_torch, which reads this call's tensors, cannot be loaded "
+                              f"({e}): build it for this Python and torch with "
+                              "`python collective_communication_reduce_amd/build.py`") from e
+    return _marshal_module
 
 
 def _raw_stream_getter():
@@ -534,7 +545,7 @@ def _buffers(ctx: Context, tensors, dtype, shapes, what: str, room: bool = False
     leaves alone."""
     if len(tensors) != len(shapes):
         raise ValueError(f"{what}: {len(tensors)} buffers for {len(shapes)} ranks")
-    p = _ccr_torch.pointers(tensors, dtype, ctx.device, shapes, room)
+    p = _marshal().pointers(tensors, dtype, ctx.device, shapes, room)
     if type(p) is int:
         _refuse(ctx, tensors[p], p, dtype, shapes[p], what, room)
     return p
@@ -542,10 +553,10 @@ def _buffers(ctx: Context, tensors, dtype, shapes, what: str, room: bool = False
 
 def _expert_counts(ecnt, R: int):
     """([R x E] int64 counts, their address, E, rows of each rank's experts)."""
-    r = _ccr_torch.expert_rows(ecnt, R)
+    r = _marshal().expert_rows(ecnt, R)
     if r is None:
         ecnt = np.ascontiguousarray(ecnt, dtype=np.int64)
-        r = _ccr_torch.expert_rows(ecnt, R)
+        r = _marshal().expert_rows(ecnt, R)
         if r is None:
             raise ValueError(f"ecnt has shape {ecnt.shape}, needs [R = {R}, E] with R | E")
     return (ecnt, *r)
@@ -639,7 +650,7 @@ def ccr_moe_gate_sum_bwd(ctx: Context, dy: Sequence, rows: Sequence, logits: Seq
 def _grad_list(tensors, what: str):
     """(pointers, element counts, dtype codes) of contiguous float32 and
     bfloat16 tensors, as arrays."""
-    r = _ccr_torch.grad_list(tensors)
+    r = _marshal().grad_list(tensors)
     if type(r) is int:
         t = tensors[r]
         _dtype_code(t)

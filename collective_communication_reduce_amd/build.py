@@ -1,5 +1,6 @@
 """Build libccr.so (the C-ABI library) in place with hipcc for gfx950, and
-_ccr_torch.so (the Python binding's marshalling of tensor lists) with g++.
+_ccr_torch (the Python binding's marshalling of tensor lists) with g++ for the
+interpreter and the torch that run this.
 
     python collective_communication_reduce_amd/build.py
 
@@ -8,7 +9,6 @@ tree; nothing is installed.
 """
 from __future__ import annotations
 
-import importlib.util
 import os
 import re
 import shutil
@@ -22,7 +22,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libccr.so")
-MARSHAL = os.path.join(PKG, "_ccr_torch.so")
+MARSHAL = os.path.join(PKG, "_ccr_torch" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["ccr_api.cpp", "ccr_dma.cpp", "ccr_schedule.cpp", "ccr_kernels.hip", "ccr_ring.hip",
            "ccr_moe_kernels.hip", "ccr_experts.hip", "ccr_gate.hip", "ccr_grad.hip", "ccr_scratch.hip"]
 # Per-source additions: the ring-hop kernels take their leading scalar
@@ -78,13 +78,15 @@ def check_experts(asm: str) -> None:
 
 
 def build_marshal() -> str:
-    """Compile _ccr_torch.so, the binding's marshalling of tensor lists: host
-    code against torch's C++ headers (found without importing torch)."""
-    root = importlib.util.find_spec("torch").submodule_search_locations[0]
+    """Compile _ccr_torch, the binding's marshalling of tensor lists: host code
+    against torch's C++ headers, with torch's own C++ ABI."""
+    import torch
+    root = os.path.dirname(torch.__file__)
     inc = [os.path.join(root, "include"),
            os.path.join(root, "include", "torch", "csrc", "api", "include")]
     tmp = MARSHAL + ".tmp"
-    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", "-D_GLIBCXX_USE_CXX11_ABI=1",
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            *[a for i in inc for a in ("-isystem", i)], "-I" + sysconfig.get_paths()["include"],
            os.path.join(CSRC, "ccr_torch.cpp"), "-o", tmp, "-L" + os.path.join(root, "lib"),
            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
@@ -117,7 +119,6 @@ def build(verbose: bool = False) -> str:
     with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
         marshal = ex.submit(build_marshal)
         objs = list(ex.map(compile_one, SOURCES))
-        marshal.result()
     tmp = LIB + ".tmp"
     # libhsa-runtime64 (SDMA engine copies): resolved at load time to the HSA
     # runtime already in the process (torch's), like libamdhip64.  The roctx
@@ -128,6 +129,7 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link of libccr.so failed:\n{r.stdout}{r.stderr}")
     os.replace(tmp, LIB)
+    marshal.result()  # the library stands without it
     return LIB
 
 

@@ -4,6 +4,8 @@ touched.  No GPU is used."""
 import os
 import re
 import subprocess
+import sys
+import sysconfig
 import types
 
 import numpy as np
@@ -153,3 +155,42 @@ def test_rows_beyond_the_counted_ones_are_taken_where_they_are_left_alone():
                               ((5, 1), True, "shape"), ((5,), True, "shape"), ((5, 2, 1), True, "shape")]:
         with pytest.raises(ValueError, match=word):
             ccr._buffers(CTX, [x], torch.float32, [shape], "x", room)
+
+
+def test_the_collectives_do_without_the_marshalling_module(tmp_path):
+    """Without the compiled module the package loads and its other calls work; the
+    calls that need it say what is missing."""
+    pkg = tmp_path / "collective_communication_reduce_amd"
+    pkg.mkdir()
+    home = os.path.dirname(os.path.abspath(ccr.__file__))
+    for name in ("__init__.py", "libccr.so"):
+        os.symlink(os.path.join(home, name), pkg / name)
+    code = """
+import sys, types
+import torch
+import collective_communication_reduce_amd as ccr
+assert ccr.__file__.startswith(sys.argv[1]), ccr.__file__
+print(ccr.ccr_version(), ccr.ccr_config_default().slices, "_ccr_torch" in "".join(sys.modules))
+try:
+    ccr.ccr_grad_norm(types.SimpleNamespace(device=0, handle=None), [], None, None)
+except ImportError as e:
+    print("refused:", e)
+"""
+    env = dict(os.environ, PYTHONPATH=str(tmp_path))
+    r = subprocess.run([sys.executable, "-c", code, str(tmp_path)], capture_output=True, text=True, env=env,
+                       cwd=tmp_path)
+    assert r.returncode == 0, r.stderr
+    first, second = r.stdout.splitlines()
+    assert first == f"{ccr.ccr_version()} {ccr.ccr_config_default().slices} False"
+    assert second.startswith("refused:") and "_ccr_torch" in second and "build.py" in second
+
+
+@pytest.mark.parametrize("abi", [False, True])
+def test_the_marshalling_module_is_built_for_this_torch_and_python(monkeypatch, tmp_path, abi):
+    done = []
+    monkeypatch.setattr(ccr_build, "MARSHAL", str(tmp_path / os.path.basename(ccr_build.MARSHAL)))
+    monkeypatch.setattr(torch, "compiled_with_cxx11_abi", lambda: abi)
+    monkeypatch.setattr(ccr_build.subprocess, "run", lambda cmd, **k: done.append(cmd) or
+                        open(cmd[cmd.index("-o") + 1], "w").close() or types.SimpleNamespace(returncode=0))
+    assert ccr_build.build_marshal().endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    assert f"-D_GLIBCXX_USE_CXX11_ABI={int(abi)}" in done[0]
