@@ -2154,7 +2154,7 @@ ccr_status_t run_experts(ccr_ctx* ctx, ExpertOp op, const void* const* a, const 
   if (!a || !b || !c) return fail(CCR_ERR_INVALID_ARG, "a buffer list is NULL");
   const int eloc = E / R;
   std::vector<int64_t> rows((size_t)E, 0), rank_rows((size_t)R, 0);
-  int64_t total = 0, most = 0;
+  int64_t total = 0;
   for (int e = 0; e < E; e++) {
     for (int r = 0; r < R; r++) {
       const int64_t n = h_ecnt[(size_t)r * E + e];
@@ -2164,7 +2164,6 @@ ccr_status_t run_experts(ccr_ctx* ctx, ExpertOp op, const void* const* a, const 
     }
     rank_rows[(size_t)(e / eloc)] += rows[(size_t)e];
     total += rows[(size_t)e];
-    most = std::max(most, rows[(size_t)e]);
   }
   if (total > INT32_MAX) return fail(CCR_ERR_UNSUPPORTED, "more than 2^31 - 1 rows");
   const int64_t wsize = F * H;  // one expert's weight, in values
@@ -2204,12 +2203,11 @@ ccr_status_t run_experts(ccr_ctx* ctx, ExpertOp op, const void* const* a, const 
   const ExpertTile tile = expert_tile(op, es, os, sh, work.data(), (int)work.size());
   const ExpertTileSize side = expert_tile_size(tile);
   const int64_t N = op == ExpertOp::kProduct ? F : H;
-  auto tiles_of = [&](int64_t n) {
-    return ceil_div(op == ExpertOp::kWgrad ? F : n, side.rows) * ceil_div(N, side.cols);
-  };
-  // one launch's grid, in work-items, is counted in 32 bits
+  const int64_t across = ceil_div(N, side.cols);
+  // one launch's grid, in work-items, is counted in 32 bits; what an expert has
+  // beyond that goes into another
   constexpr int64_t kMaxTiles = int64_t(UINT32_MAX) / 512;
-  if (tiles_of(most) > kMaxTiles) return fail(CCR_ERR_UNSUPPORTED, "an expert's product is too large for one launch");
+  const int64_t most_rows = kMaxTiles / across * side.rows;  // of c in one group
   ExpertTable tab;
   tab.n = 0;
   int64_t tiles = 0;
@@ -2226,23 +2224,28 @@ ccr_status_t run_experts(ccr_ctx* ctx, ExpertOp op, const void* const* a, const 
   for (const int e : listed) {
     const int d = e / eloc, l = e % eloc;
     const int64_t n = rows[(size_t)e], row = first[(size_t)e];
-    const int64_t more = tiles_of(n);
-    if (tab.n == kExpertGroups || tiles + more > kMaxTiles) CCR_TRY(flush());
-    ExpertGroup& g = tab.g[tab.n];
+    const int64_t m_all = op == ExpertOp::kWgrad ? F : n;
     const char *pa = static_cast<const char*>(a[d]), *pb = static_cast<const char*>(b[d]);
     char* pc = static_cast<char*>(c[d]);
-    g.rows = (int32_t)n;
-    if (op == ExpertOp::kWgrad) {
-      g.a = pa + row * F * es;
-      g.b = pb + row * H * es;
-      g.c = pc + l * wsize * os;
-    } else {
-      g.a = pa + row * (op == ExpertOp::kProduct ? H : F) * es;
-      g.b = pb + l * wsize * es;
-      g.c = pc + row * N * es;
+    for (int64_t m0 = 0; m0 < m_all; m0 += most_rows) {
+      const int64_t m = std::min(most_rows, m_all - m0);
+      const int64_t more = ceil_div(m, side.rows) * across;
+      if (tab.n == kExpertGroups || tiles + more > kMaxTiles) CCR_TRY(flush());
+      ExpertGroup& g = tab.g[tab.n];
+      g.m = (int32_t)m;
+      g.rows = (int32_t)n;
+      if (op == ExpertOp::kWgrad) {
+        g.a = pa + (row * F + m0) * es;
+        g.b = pb + row * H * es;
+        g.c = pc + (l * wsize + m0 * H) * os;
+      } else {
+        g.a = pa + (row + m0) * (op == ExpertOp::kProduct ? H : F) * es;
+        g.b = pb + l * wsize * es;
+        g.c = pc + (row + m0) * N * es;
+      }
+      tab.tile0[tab.n++] = (int32_t)tiles;
+      tiles += more;
     }
-    tab.tile0[tab.n++] = (int32_t)tiles;
-    tiles += more;
   }
   return tab.n > 0 ? flush() : CCR_OK;
 }

@@ -251,7 +251,7 @@ __device__ __forceinline__ Where place_of(const ExpertTable& tab, const ExpertSh
   at.a = g.a;
   at.b = g.b;
   at.c = g.c;
-  at.M = OP == ExpertOp::kWgrad ? sh.F : g.rows;
+  at.M = g.m;
   at.N = OP == ExpertOp::kProduct ? sh.F : sh.H;
   at.C = OP == ExpertOp::kProduct ? sh.H : OP == ExpertOp::kDgrad ? sh.F : g.rows;
   int tm, tn;

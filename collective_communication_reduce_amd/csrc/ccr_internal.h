@@ -192,13 +192,15 @@ hipError_t launch_moe_plan(const int32_t* topk, int64_t T, int E, int K, int elo
 
 // The experts' products (ccr_experts.hip).  A group is one expert's work of a
 // launch: its first operand a (x, dout, dout), second operand b (W, W, x) and
-// output c (out, dexp, dw), and its rows.
+// output c (out, dexp, dw), its rows of c, and the values each of them sums over
+// for a weight gradient (the expert's rows).  An expert too large for a launch
+// is cut into groups by rows of c.
 enum class ExpertOp : int { kProduct = 0, kDgrad = 1, kWgrad = 2 };
 struct ExpertGroup {
   const char* a;
   const char* b;
   char* c;
-  int32_t rows;
+  int32_t m, rows;
 };
 // Up to kExpertGroups experts go into one launch, passed by value as kernel
 // arguments (4 KiB at most); tile0[i] = first tile of group i.

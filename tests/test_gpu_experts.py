@@ -417,3 +417,47 @@ def test_refusals(ccr_mod):
             ccr_mod.ccr_moe_experts(c, [x], [w], ecnt[0], [y])
         with pytest.raises(ccr_mod.CcrError):  # bf16 gradients of fp32 rows
             ccr_mod.ccr_moe_experts_wgrad(c, [x.float()], [y.float()], ecnt, [w.clone()])
+
+
+@pytest.mark.parametrize("op", ["product", "dgrad"])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_more_rows_than_one_launch_covers(ccr_mod, op, dt):
+    """2^29 narrow rows of one expert, past the 2^23 - 1 tiles of one launch for
+    any tile of up to 64 rows: every result, bit for bit."""
+    import torch
+    n, w = (1 << 29) + 77, 16 // (4 if dt == "f32" else 2)
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GiB")
+    say(f"experts {op} {dt} {n} rows of {w}")
+    x = torch.empty(n, w, dtype=tdtype(dt), device="cuda").random_(0, 4)
+    weight = torch.empty(1, w, w, dtype=tdtype(dt), device="cuda").random_(0, 4)
+    out = torch.full((n, w), 7.0, dtype=tdtype(dt), device="cuda")  # 9 w at most, exact
+    with ccr_mod.Context(0) as c:
+        call(ccr_mod, c, op, [x], [weight], [[n]], [out])
+        torch.cuda.synchronize()
+    m = weight[0].t() if op == "product" else weight[0]
+    step = 1 << 26
+    for at in range(0, n, step):
+        part = x[at:at + step]
+        want = torch.zeros_like(part)
+        for k in range(w):
+            want += part[:, k:k + 1] * m[k]
+        assert torch.equal(out[at:at + step], want), f"rows from {at}"
+
+
+def test_more_weights_than_one_launch_covers(ccr_mod):
+    """An fp32 weight gradient of 2^18 x 131,136 from one row: more tiles of 64 x 64
+    than one launch covers."""
+    import torch
+    F, H = 1 << 18, 131136
+    if torch.cuda.mem_get_info()[0] < 160 << 30:
+        pytest.skip("needs 160 GiB")
+    say(f"experts wgrad f32 {F} x {H}")
+    x = torch.empty(1, H, device="cuda").random_(1, 4)
+    dout = torch.empty(1, F, device="cuda").random_(1, 4)
+    dw = torch.empty(1, F, H, device="cuda")
+    with ccr_mod.Context(0) as c:
+        ccr_mod.ccr_moe_experts_wgrad(c, [x], [dout], [[1]], [dw])
+        torch.cuda.synchronize()
+    for at in range(0, F, 1 << 14):
+        assert torch.equal(dw[0, at:at + (1 << 14)], dout[0, at:at + (1 << 14), None] * x), f"rows from {at}"
