@@ -461,3 +461,51 @@ def test_more_weights_than_one_launch_covers(ccr_mod):
         torch.cuda.synchronize()
     for at in range(0, F, 1 << 14):
         assert torch.equal(dw[0, at:at + (1 << 14)], dout[0, at:at + (1 << 14), None] * x), f"rows from {at}"
+
+
+@pytest.mark.parametrize("op,dt,rows,H,F,chain", [
+    ("product", "f32", 1, 65536, 64, 256), ("product", "f32", 300, 65536, 64, 256),
+    ("product", "f32", 700, 65536, 512, 256), ("dgrad", "f32", 1, 64, 65536, 256),
+    ("dgrad", "f32", 300, 64, 65536, 256), ("dgrad", "f32", 700, 512, 65536, 256),
+    ("wgrad", "f32", 65536, 64, 64, 256), ("wgrad", "f32", 65536, 520, 512, 256),
+    ("wgrad", "f32", 65536, 2048, 1024, 256), ("wgrad", "bf16", 131072, 64, 64, 2048),
+    ("wgrad", "bf16", 262144, 1032, 1024, 2048), ("wgrad", "bf16", 262144, 4096, 4096, 8192),
+    ("wgrad", "bf16", 262144 + 8191, 4104, 4096, 8192)])
+def test_error_of_long_sums(ccr_mod, op, dt, rows, H, F, chain):
+    """Positive values, whose partial sums grow evenly: an addition at k of n is
+    off by at most k / n of half a unit of the result, evenly spread, so the
+    RMS error of n additions is below sqrt(n) / 3 half units.  A chain of
+    `chain` products has at most as many additions; m chains of equal size, joined one
+    after the other, come to sqrt(chain / m) / 3 + sqrt(m) / 3.  The sum in one chain of
+    matrix instructions is 4 to 8 times as far off."""
+    import torch
+    say(f"error of long sums {op} {dt} rows={rows} H={H} F={F}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(rows)
+    rnd = lambda *s: (torch.rand(s, generator=g, device="cuda") + 0.5).to(tdtype(dt))
+    n = {"product": H, "dgrad": F, "wgrad": rows}[op]
+    a = rnd(rows, H if op == "product" else F)
+    b = rnd(rows, H) if op == "wgrad" else rnd(1, F, H)
+    shape = {"product": (rows, F), "dgrad": (rows, H), "wgrad": (1, F, H)}[op]
+    out = torch.empty(shape, dtype=torch.float32, device="cuda")
+    with ccr_mod.Context(0) as c:
+        call(ccr_mod, c, op, [a], [b], [[rows]], [out])
+        torch.cuda.synchronize()
+    if op == "wgrad":  # some rows of the weight, over the tile
+        some = torch.arange(0, F, max(1, F // 64), device="cuda")
+        want, got = a[:, some].double().t() @ b.double(), out[0][some]
+    else:
+        want = a.double() @ (b[0].double().t() if op == "product" else b[0].double())
+        got = out
+    m = n / chain
+    rms = float(((got.double() - want) / want).pow(2).mean().sqrt())
+    bound = 2.0 ** -24 * ((chain / m) ** 0.5 + m ** 0.5) / 3
+    say(f"  RMS {rms:.3g}, bound {bound:.3g}")
+    assert rms <= bound
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_weight_gradients_of_several_chains_bitwise(ccr_mod, accumulate):
+    # 256 x 256 tiles, inside and at the edge, of one to four chains of 8192 rows
+    check(ccr_mod, "wgrad", "bf16", [8191, 8192, 8193, 20000, 0, 16384, 16385, 30000], 2, 2056, 2040, out_dt="f32",
+          accumulate=accumulate)
