@@ -509,3 +509,55 @@ def test_weight_gradients_of_several_chains_bitwise(ccr_mod, accumulate):
     # 256 x 256 tiles, inside and at the edge, of one to four chains of 8192 rows
     check(ccr_mod, "wgrad", "bf16", [8191, 8192, 8193, 20000, 0, 16384, 16385, 30000], 2, 2056, 2040, out_dt="f32",
           accumulate=accumulate)
+
+
+@pytest.mark.parametrize("side", ["first", "second"])
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,H,F", [([1], 2048, 1024), ([3, 0, 1, 2], 1028, 520), ([16] * 8, 512, 512),
+                                      ([33, 130, 0, 64], 264, 200), ([500] * 4, 1024, 1024),
+                                      ([900, 1, 1200], 2048, 1032), ([4095, 4090], 1032, 2048)])
+def test_every_bit_of_the_operands_counts(ccr_mod, op, dt, rows, H, F, side):
+    """One operand selects: one power of two in the sum of each result, the rest
+    zeros.  Every result is then a value of the other operand, all of its bits."""
+    import torch
+    if dt == "bf16":
+        H, F = (H + 7) // 8 * 8, (F + 7) // 8 * 8
+    say(f"bits {op} {dt} rows={rows} H={H} F={F} the {side} operand selects")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(H + F)
+    E = len(rows)
+    a, b, want = [], [], []
+    for n in rows:
+        shape_a, shape_b = (n, H if op == "product" else F), (n, H) if op == "wgrad" else (F, H)
+        x, y = (torch.randn(s, generator=g, device="cuda").to(tdtype(dt)) for s in (shape_a, shape_b))
+        # x as [outputs, summed], y as [summed, outputs]
+        X, Y = (x.t() if op == "wgrad" else x), (y.t() if op == "product" else y)
+        M, C, N = X.shape[0], X.shape[1], Y.shape[1]
+        if C == 0:
+            want.append(torch.zeros(M, N, dtype=tdtype(dt), device="cuda"))
+        else:
+            k = M if side == "first" else N
+            pick = torch.randint(0, C, (k,), generator=g, device="cuda")
+            power = 2.0 ** torch.randint(-2, 3, (k,), generator=g, device="cuda").to(tdtype(dt))
+            at = torch.arange(k, device="cuda")
+            if side == "first":
+                X.zero_()
+                X[at, pick] = power
+                want.append(power[:, None] * Y[pick])
+            else:
+                Y.zero_()
+                Y[pick, at] = power
+                want.append(X[:, pick] * power)
+        a.append(x)
+        b.append(y)
+    a = torch.cat(a).contiguous()
+    if op == "wgrad":
+        b, want = torch.cat(b).contiguous(), torch.stack(want).contiguous()
+    else:
+        b, want = torch.stack(b).contiguous(), torch.cat(want).contiguous()
+    out = Guarded(want.shape, tdtype(dt))
+    with ccr_mod.Context(0) as c:
+        call(ccr_mod, c, op, [inside_nan(a)], [inside_nan(b)], [rows], [out.t])
+        torch.cuda.synchronize()
+    assert out.intact() and torch.equal(out.t, want)
