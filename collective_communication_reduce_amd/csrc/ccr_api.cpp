@@ -2401,7 +2401,7 @@ ccr_status_t run_grads(ccr_ctx* ctx, bool clip, const void* const* grads, void* 
       tab.add(list[i], grad_tiles(list[i].src, list[i].count, list[i].es));
     return (int)std::min<int64_t>(slots, std::max<int64_t>(1, tab.ntiles));
   };
-  if (launches.size() == 1 && total <= kGradSmallTiles) {
+  if (launches.size() == 1 && total <= grad_small_tiles(clip)) {
     fill(launches[0]);
     HIP_TRY(launch_grad_small(tab, clip, max_norm, norm, s));
     return CCR_OK;

@@ -278,25 +278,30 @@ __global__ __launch_bounds__(kBlock, 8) void grad_clip_kernel(const GradTable ta
   }
 }
 
-// A call of up to kGradSmallTiles tiles: one workgroup of kGroups times kBlock
+// A call of up to grad_small_tiles tiles: one workgroup of kGroups times kBlock
 // threads, each kBlock of them with up to kMine tiles in registers, makes the
 // norm and the clipping in one launch and one pass over the gradients.  It is
-// bound by latency: the launch, the loads, the stores.  Against two launches, us
-// back to back on warm buffers: 1 tile, norm 3.0 against 4.7, clipping 3.6
-// against 6.6; 8 tiles 4.7 / 5.3 and 6.2 / 7.4; 12 tiles 5.7 / 5.4 and 7.7 / 7.5;
-// 16 tiles 6.7 / 5.4 and 9.3 / 7.5.  On cold buffers, clipping 10 tiles: 6.7 / 10.6.
-constexpr int kGroups = 4, kMine = kGradSmallTiles / kGroups;
-static_assert(kMine * kGroups == kGradSmallTiles, "every tile has its threads");
+// bound by latency: the launch, the loads, the stores.  The norm alone saves a
+// launch, clipping a read of cold gradients too, so it pays up to more tiles.  us
+// in one launch / in two, replayed from a graph, of whole tiles of fp32:
+//   tiles              1         4         6         8        10        11        12
+//   norm, warm     2.2/3.7   2.8/4.1   3.2/4.2   3.8/4.2   4.2/4.2   4.4/4.2   4.8/4.2
+//   norm, cold     2.9/4.2   3.4/4.5   4.0/4.6   5.7/4.6   6.6/4.6   6.9/4.6   7.5/4.6
+//   clip, warm     2.9/5.4   3.9/6.1   4.5/6.2   5.6/6.3   6.1/6.3   6.3/6.4   7.1/6.4
+//   clip, cold     3.6/6.6   5.3/8.8   6.5/9.3   7.5/9.5   8.3/9.5   8.8/9.5   9.6/9.5
+constexpr int kGroups = 4;
+template <bool CLIP>
+constexpr int kMine = (grad_small_tiles(CLIP) + kGroups - 1) / kGroups;
 template <bool CLIP>
 __global__ __launch_bounds__(kBlock * kGroups) void grad_small_kernel(const GradTable tab, float max_norm,
                                                                       float* norm) {
   __shared__ double part[kGroups * kBlock / 64];
   const int thread = threadIdx.x % kBlock;
   const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / kBlock);
-  u32x4 x[kMine][kVecs];
-  Place p[kMine];
+  u32x4 x[kMine<CLIP>][kVecs];
+  Place p[kMine<CLIP>];
 #pragma unroll
-  for (int m = 0; m < kMine; m++) {
+  for (int m = 0; m < kMine<CLIP>; m++) {
     const int tile = m * kGroups + group;
     if (tile >= tab.ntiles) continue;
     p[m] = place_of(tab, tile);
@@ -305,7 +310,7 @@ __global__ __launch_bounds__(kBlock * kGroups) void grad_small_kernel(const Grad
   }
   double acc = 0;
 #pragma unroll
-  for (int m = 0; m < kMine; m++) {
+  for (int m = 0; m < kMine<CLIP>; m++) {
     if (m * kGroups + group >= tab.ntiles) continue;
     acc = p[m].t.es == 4 ? tile_sum<4>(span_of<4>(p[m].t), p[m].tile, thread, x[m], acc)
                          : tile_sum<2>(span_of<2>(p[m].t), p[m].tile, thread, x[m], acc);
@@ -315,7 +320,7 @@ __global__ __launch_bounds__(kBlock * kGroups) void grad_small_kernel(const Grad
   if constexpr (CLIP) {
     const float c = factor_of(nv, max_norm);
 #pragma unroll
-    for (int m = 0; m < kMine; m++) {
+    for (int m = 0; m < kMine<CLIP>; m++) {
       if (m * kGroups + group >= tab.ntiles || (c == 1.0f && p[m].t.src == p[m].t.dst)) continue;
       if (p[m].t.es == 4) tile_store<4, false>(span_of<4>(p[m].t), p[m].tile, thread, x[m], c);
       else tile_store<2, false>(span_of<2>(p[m].t), p[m].tile, thread, x[m], c);

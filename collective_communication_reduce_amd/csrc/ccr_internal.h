@@ -285,8 +285,8 @@ int64_t grad_tile_bytes();
 hipError_t launch_grad_squares(const GradTable& tab, int grid, int64_t stream_tiles, double* work,
                                bool add, hipStream_t stream);
 hipError_t launch_grad_norm(const double* work, int slots, float* norm, hipStream_t stream);
-// All of a call of up to kGradSmallTiles tiles.
-constexpr int kGradSmallTiles = 12;
+// All of a call of few tiles.
+constexpr int grad_small_tiles(bool clip) { return clip ? 11 : 6; }
 hipError_t launch_grad_small(const GradTable& tab, bool clip, float max_norm, float* norm,
                              hipStream_t stream);
 // norm may be NULL (a later launch of the same call).

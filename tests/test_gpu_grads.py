@@ -287,3 +287,24 @@ def test_two_graphs_and_two_streams_with_their_own_work(ccr_mod):
                 ccr_mod.ccr_grad_clip(c, g, 1.0, w, n, out=o)
                 torch.cuda.synchronize()
                 assert all(torch.equal(a, b) for a, b in zip(got, o)), f"replay {step}"
+
+
+@pytest.mark.parametrize("tiles", range(1, 14))
+@pytest.mark.parametrize("where", ["in place", "apart"])
+def test_one_launch_or_two(ccr_mod, tiles, where):
+    """Norm and clipping of as many tiles of 16 KiB as one launch takes, and of one
+    more, of one tensor, of one per tile, and of both types off a boundary."""
+    import torch
+    for sizes in ([(tiles * 4096, "f32", 0)], [(4096, "f32", 0)] * tiles, [(8192, "bf16", 0)] * tiles,
+                  [(4096 - i % 3, "f32", i % 4) for i in range(tiles)],
+                  [(8192 + i % 8, "bf16", (8 - i) % 8) for i in range(tiles)]):
+        grads = grads_of(sizes, seed=tiles)
+        w, n = Guarded((ccr_mod.CCR_GRAD_WORK,), torch.float64), Guarded((1,), torch.float32)
+        with ccr_mod.Context(0) as c:
+            ccr_mod.ccr_grad_norm(c, grads, w.t, n.t)
+            torch.cuda.synchronize()
+        assert close_norm(float(n.t), norm64(grads))
+        n.t.fill_(float("nan"))
+        outs = [Guarded((k,), tdtype(dt), offset_elements=off) for k, dt, off in sizes]
+        check_clip(ccr_mod, grads, 0.5, w.t, n.t, out=None if where == "in place" else [o.t for o in outs])
+        assert w.intact() and n.intact() and all(o.intact() for o in outs)
