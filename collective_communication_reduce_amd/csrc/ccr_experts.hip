@@ -467,9 +467,13 @@ __global__ __launch_bounds__(WM * WN * WK * 64) void experts_ring_kernel(const E
 // With one wave to a SIMD nothing hides an instruction that stalls, so reads
 // and loads are placed one by one between the products.  Measured at 8192^3
 // against reads and loads in groups of three before every eight products:
-// 1283 -> 1433 TFLOP/s (dgrad).  What bounds it is power: a training layer's
-// product (196,608 rows of 64 experts, 2048 x 1024) takes 700 us, 1.18 PFLOP/s,
-// with the matrix units 66% busy at 1.65 GHz.
+// 1283 -> 1433 TFLOP/s (dgrad).  A training layer's product (196,608 rows of 64
+// experts, 2048 x 1024) takes 705 to 728 us, 1.13 to 1.17 PFLOP/s, and is bound by
+// power: the matrix units are 64% busy at 1.65 GHz, and where gaps are filled the
+// clock falls.  The gradients of 49,152 rows of 16 experts (2048 x 1408: 271 and
+// 275 us, 1.04 and 1.03 PFLOP/s) run at 2.06 GHz with the matrix units 50% busy:
+// the start and the stores of a tile, the last round's empty units and, in the input
+// gradient, LDS conflicts (33% of the LDS cycles) count there.
 
 // A fragment as fragment() gives it, read in parts.
 template <bool COL, bool PAIRED>
@@ -537,7 +541,7 @@ __global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable t
   static_assert(BM == BN, "both operands fill a slot");
   using LoadA = Loader<ES, BM, kACol, false, NT>;
   // Paired fragments of b give 16-byte stores of bf16 (dgrad of 8 x 4096 rows,
-  // 2048 x 1024: 119 us, unpaired 130), though in a column image their reads meet
+  // 2048 x 1024: 122 us, unpaired 130), though in a column image their reads meet
   // on half of the banks.  fp32 results are stored by 16 bytes either way.
   constexpr bool kPaired = OS == 2;
   using LoadB = Loader<ES, BN, kBCol, kPaired, NT>;
@@ -794,7 +798,8 @@ __global__ __launch_bounds__(256, 1) void experts_big_kernel(const ExpertTable t
     if (!again) return;
     at = next;
     // the next tile's step 0; its step 1 and part of a's step 2, and in a full
-    // tile the results' stores, may be on their way
+    // tile the results' stores, may be on their way here.  (What place() loads of
+    // the table at the loop's start is waited for behind all of them.)
     constexpr int kStores = kPaired ? T * T / 2 : T * T;
     if (full) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(21 + kStores < 63 ? 21 + kStores : 63) : "memory");
     else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
