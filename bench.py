@@ -16,6 +16,8 @@ Printed: one JSON line with
   gemm        slowdown of a concurrent 8192^3 bf16 GEMM while all-reduces run
               on a second stream, with kernel copies vs SDMA copies
   cpu_baseline the CPU oracle on the same workload (1 thread)
+The whole record (every run of the slowdown sweeps, percentiles) goes to
+stderr before it, as "bench: record {...}".
 """
 from __future__ import annotations
 
@@ -347,6 +349,19 @@ def compact_verdict(o):
             "pareto": v["pareto"],
             "sdma_lower_at_full_cus": v["target_sdma_lower_at_full_cus"],
             "sdma_lower_at_some_matched_time": v["sdma_lower_at_some_matched_time"]}
+
+
+# What the printed line leaves to the record: single runs, percentiles, notes.
+RECORD_ONLY = {"runs", "verdict", "size_sweep_r8_bf16", "p10_ms", "p90_ms", "n", "note"}
+
+
+def short_line(record):
+    """The record of a run without RECORD_ONLY (and the dicts that leaves
+    empty): a line short enough to be read whole from the end of an output."""
+    if not isinstance(record, dict):
+        return record
+    kept = {k: short_line(v) for k, v in record.items() if k not in RECORD_ONLY}
+    return {k: v for k, v in kept.items() if v != {} or record[k] == {}}
 
 
 def reduce_hops_by_position(iv, bytes_per_launch, calls):
@@ -1306,7 +1321,8 @@ def main():
                                                                   ("pp_staging", pp))
                               if v is not None}
     ctx.close()
-    print(json.dumps(line), flush=True)
+    log("bench: record " + json.dumps(line))
+    print(json.dumps(short_line(line)), flush=True)
 
 
 if __name__ == "__main__":

@@ -182,3 +182,22 @@ def test_reduce_hops_by_position():
     assert out["later_hops"]["mean_launch_us"] == pytest.approx(24.0)
     assert out["first_hop"]["bound"] == "hbm" and out["later_hops"]["bound"] == "hbm+mall"
     assert bench.reduce_hops_by_position(iv, 1, 4) is None
+
+
+def test_the_printed_line_stays_short():
+    # a record as a run makes it: 15 pairs in each of a dozen runs, three sweeps
+    runs = [{"label": f"sdma/B256/E{i}", "pairs_pct": [0.123] * 15, "n": 15, "makespan": {"p10_ms": 1.0}} for i in range(14)]
+    sweep = {"gemm": "8192x8192x8192 bf16 x20", "gemm_alone_ms": 17.7, "runs": runs, "verdict": {"pareto": runs}}
+    head = {"metric": bench.METRIC, "value": 335.6, "unit": "GB/s", "n_gpus": 1, "steps": 20, "warmup": 5,
+            "ms_per_step": 0.27, "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "bf16",
+            "data": "synthetic", "config": {"workload": "w", "ranks": 8}}
+    record = {**head, "gemm_slowdown": sweep, "gemm_slowdown_all_gather_only": sweep, "pp_staging_gemm_slowdown": sweep,
+              "gemm_slowdown_pct": {"kernel": 0.9}, "cpu_baseline": {"value": 0.15, "cores": 1, "sample": "all"},
+              "other_workloads": {"w": {"ms": 0.02, "p10_ms": 0.02, "p90_ms": 0.03, "cold": {"p10_ms": 0.1, "n": 20}},
+                                  "size_sweep_r8_bf16": [{"mib_per_rank": 2}] * 7}, "sdma_copies": None}
+    line = bench.short_line(record)
+    assert {k: line[k] for k in head} == head
+    assert line["gemm_slowdown"] == {"gemm": "8192x8192x8192 bf16 x20", "gemm_alone_ms": 17.7}
+    assert line["gemm_slowdown_pct"] == {"kernel": 0.9} and line["cpu_baseline"] == record["cpu_baseline"]
+    assert line["other_workloads"] == {"w": {"ms": 0.02}} and line["sdma_copies"] is None
+    assert len(json_dumps(record)) > 8000 > 2000 > len(json_dumps(line))
