@@ -28,7 +28,9 @@ CCR_OK, CCR_ERR_INVALID_ARG, CCR_ERR_UNSUPPORTED, CCR_ERR_HIP, CCR_ERR_OOM, CCR_
 CCR_F32, CCR_BF16 = 0, 1
 CCR_COPY_KERNEL, CCR_COPY_SDMA = 0, 1
 CCR_BF16_ACC_PER_HOP, CCR_BF16_ACC_FP32_PARTIALS = 0, 1
-CCR_GATE_CHOSEN, CCR_GATE_ALL = 0, 1
+CCR_GATE_CHOSEN, CCR_GATE_ALL, CCR_GATE_GIVEN = 0, 1, 2
+CCR_SCORE_SOFTMAX, CCR_SCORE_SIGMOID = 0, 1
+CCR_MAX_EXPERTS = 1024  # of a router or a gated sum
 CCR_GRAD_WORK = 2048  # float64 elements of a gradient call's work tensor
 _STATUS = {1: "invalid argument", 2: "unsupported", 3: "HIP error", 4: "out of memory", 5: "timeout"}
 
@@ -62,6 +64,11 @@ STAGE_ENTRY_DTYPE = np.dtype([("stage", np.int32), ("kind", np.int32), ("src", n
                               ("dst", np.int32), ("bytes", np.int64)])
 STAGE_TIME_DTYPE = np.dtype([("load", np.int64), ("bw", np.int64)])
 STAGE_KINDS = ("rdma", "forward", "native")
+
+class ccr_route_t(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("kept_groups", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
+
 
 # Every exported entry point and its argument types.
 _vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
@@ -97,6 +104,17 @@ _SIGNATURES = {
     "ccr_moe_gate_sum": [_vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _i64, _i32, _i32, _vp, _vp],
     "ccr_moe_gate_sum_bwd": [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _i64, _i32, _i32, _vp,
                              _vp, _vp],
+    "ccr_moe_experts_q8": [_vp, _vp, _vp, _vp, _i32, _i32, _i64, _i64, _vp, _vp],
+    "ccr_q8_row_bytes": [_i64],
+    "ccr_quantize_rows": [_vp, _vp, _vp, _i32, _i64, _i32, _vp, _vp],
+    "ccr_dequantize_rows": [_vp, _vp, _vp, _i32, _i64, _i32, _vp, _vp],
+    "ccr_rms_norm_work": [_i32, _i64, _i64],
+    "ccr_rms_norm": [_vp, _vp, _vp, _vp, _i32, _i64, _i64, _i32, _i32, ctypes.c_float, _vp, _vp, _vp, _vp, _vp],
+    "ccr_rms_norm_bwd": [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp],
+    "ccr_moe_route_work": [_i32, _i64, _i32],
+    "ccr_moe_route": [_vp, _vp, _vp, _i32, _i64, _i32, _i32, ctypes.POINTER(ccr_route_t), _vp, _vp, _vp, _vp, _vp,
+                      _vp],
+    "ccr_moe_route_bwd": [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _i32, _i32, ctypes.c_float, _vp, _vp],
     "ccr_grad_norm": [_vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp],
     "ccr_grad_clip": [_vp, _vp, _vp, _vp, _vp, _i32, ctypes.c_float, _vp, _vp, _vp],
     "ccr_last_error": [],
@@ -114,6 +132,9 @@ _SIGNATURES = {
     "ccr_graph_cache_stats": [_vp, ctypes.POINTER(_i64), ctypes.POINTER(_i64)],
     "ccr_ctx_streams": [_vp, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)],
 }
+
+
+_SIZES = ("ccr_q8_row_bytes", "ccr_rms_norm_work", "ccr_moe_route_work")
 
 
 def _hip_runtimes():
@@ -142,7 +163,8 @@ def _load():
     for name, args in _SIGNATURES.items():
         fn = getattr(lib, name)
         fn.argtypes = args
-        fn.restype = ctypes.c_char_p if name in ("ccr_last_error", "ccr_version") else ctypes.c_int
+        fn.restype = (ctypes.c_char_p if name in ("ccr_last_error", "ccr_version") else
+                      ctypes.c_int64 if name in _SIZES else ctypes.c_int)
     return lib
 
 
@@ -607,7 +629,7 @@ def ccr_moe_experts_wgrad(ctx: Context, exp: Sequence, dout: Sequence, ecnt, dw:
         _ctx_stream(ctx, stream)))
 
 
-_GATE_NORM = {"chosen": CCR_GATE_CHOSEN, "all": CCR_GATE_ALL}
+_GATE_NORM = {"chosen": CCR_GATE_CHOSEN, "all": CCR_GATE_ALL, "given": CCR_GATE_GIVEN}
 
 
 def _gate_args(ctx, rows, logits, topk, norm):
@@ -616,17 +638,19 @@ def _gate_args(ctx, rows, logits, topk, norm):
         raise ValueError(f"norm {norm!r} is not one of {sorted(_GATE_NORM)}")
     R = len(rows)
     T, K, H = rows[0].shape
-    E = logits[0].shape[1]
+    given = norm == "given"
+    E = CCR_MAX_EXPERTS if given else logits[0].shape[1]
     code = _dtype_code(rows[0])
     return (R, T, E, K, H, code, _buffers(ctx, rows, rows[0].dtype, [(T, K, H)] * R, "rows"),
-            _buffers(ctx, logits, torch.float32, [(T, E)] * R, "logits"),
+            _buffers(ctx, logits, torch.float32, [(T, K if given else E)] * R, "logits"),
             _buffers(ctx, topk, torch.int32, [(T, K)] * R, "topk"))
 
 
 def ccr_moe_gate_sum(ctx: Context, rows: Sequence, logits: Sequence, topk: Sequence, y: Sequence,
                      norm: str = "chosen", stream=None):
     """y[r][t] = sum_k w_k rows[r][t, k], w the softmax of logits[r][t] at
-    topk[r][t], over the chosen experts or over "all".  Every rank has the same
+    topk[r][t], over the chosen experts or over "all"; "given": w_k = logits[r][t,
+    k], [T, K] weights as ccr_moe_route writes them.  Every rank has the same
     number of tokens."""
     R, T, E, K, H, code, p, l, k = _gate_args(ctx, rows, logits, topk, norm)
     _check(_lib.ccr_moe_gate_sum(ctx.handle, p, l, k, R, T, E, K, H, code, _GATE_NORM[norm],
@@ -636,15 +660,174 @@ def ccr_moe_gate_sum(ctx: Context, rows: Sequence, logits: Sequence, topk: Seque
 
 def ccr_moe_gate_sum_bwd(ctx: Context, dy: Sequence, rows: Sequence, logits: Sequence, topk: Sequence,
                          drows: Sequence, dlogits: Sequence, norm: str = "chosen", stream=None):
-    """Gradients of ccr_moe_gate_sum: drows[r] [T, K, H] and dlogits[r] [T, E]."""
+    """Gradients of ccr_moe_gate_sum: drows[r] [T, K, H] and dlogits[r] [T, E]
+    ("given": [T, K], of the weights)."""
     import torch
     R, T, E, K, H, code, p, l, k = _gate_args(ctx, rows, logits, topk, norm)
     dt = rows[0].dtype
     _check(_lib.ccr_moe_gate_sum_bwd(ctx.handle, _buffers(ctx, dy, dt, [(T, H)] * R, "dy"), p, l, k, R, T,
                                      E, K, H, code, _GATE_NORM[norm],
                                      _buffers(ctx, drows, dt, [(T, K, H)] * R, "drows"),
-                                     _buffers(ctx, dlogits, torch.float32, [(T, E)] * R, "dlogits"),
+                                     _buffers(ctx, dlogits, torch.float32,
+                                              [(T, K if norm == "given" else E)] * R, "dlogits"),
                                      _ctx_stream(ctx, stream)))
+
+
+def ccr_q8_row_bytes(H: int) -> int:
+    """Bytes of an 8-bit row of H values (host only; 0 for an H out of range)."""
+    return int(_lib.ccr_q8_row_bytes(H))
+
+
+def _q8_lists(ctx, rows, q, what):
+    """(row pointers, 8-bit row pointers, counts, H, dtype code) of lists of
+    [..., H] tensors and of uint8 ones of the same rows."""
+    import torch
+    H = rows[0].shape[-1]
+    code, nbytes = _dtype_code(rows[0]), ccr_q8_row_bytes(H)
+    return (_buffers(ctx, rows, rows[0].dtype, [(*t.shape[:-1], H) for t in rows], what),
+            _buffers(ctx, q, torch.uint8, [(*t.shape[:-1], nbytes) for t in rows], "q"),
+            (ctypes.c_int64 * len(rows))(*[t.shape[:-1].numel() for t in rows]), H, code)
+
+
+def ccr_quantize_rows(ctx: Context, x: Sequence, q: Sequence, stream=None):
+    """q[r] = x[r] [..., H] as 8-bit rows (uint8 [..., ccr_q8_row_bytes(H)])."""
+    p, pq, counts, H, code = _q8_lists(ctx, x, q, "x")
+    _check(_lib.ccr_quantize_rows(ctx.handle, p, counts, len(x), H, code, pq, _ctx_stream(ctx, stream)))
+
+
+def ccr_dequantize_rows(ctx: Context, q: Sequence, y: Sequence, stream=None):
+    """y[r] [..., H] = what the 8-bit rows q[r] stand for."""
+    p, pq, counts, H, code = _q8_lists(ctx, y, q, "y")
+    _check(_lib.ccr_dequantize_rows(ctx.handle, pq, counts, len(y), H, code, p, _ctx_stream(ctx, stream)))
+
+
+def ccr_moe_experts_q8(ctx: Context, exp: Sequence, w: Sequence, ecnt, H: int, out: Sequence, stream=None):
+    """ccr_moe_experts on 8-bit rows of H values: exp[d] [rows, B], w[d] [E/R, F,
+    B], B = ccr_q8_row_bytes(H), both uint8; out[d] [rows, F] bfloat16."""
+    import torch
+    R = len(w)
+    ecnt, counts, E, rows = _expert_counts(ecnt, R)
+    F, B = w[0].shape[1], ccr_q8_row_bytes(H)
+    _check(_lib.ccr_moe_experts_q8(
+        ctx.handle, _buffers(ctx, exp, torch.uint8, [(n, B) for n in rows], "exp", True),
+        _buffers(ctx, w, torch.uint8, [(E // R, F, B)] * R, "w"), counts, R, E, H, F,
+        _buffers(ctx, out, torch.bfloat16, [(n, F) for n in rows], "out", True), _ctx_stream(ctx, stream)))
+
+
+def ccr_rms_norm_work(R: int, T: int, H: int) -> int:
+    """float32 elements of ccr_rms_norm_bwd's work tensor."""
+    return int(_lib.ccr_rms_norm_work(R, T, H))
+
+
+def ccr_rms_norm(ctx: Context, x: Sequence, w: Sequence, y=None, q=None, residual=None, h=None, rstd=None,
+                 eps: float = 1e-6, stream=None):
+    """h[r] = x[r] + residual[r] (x[r] itself without them), and its norm times
+    w[r], to y[r] (x's dtype), q[r] (8-bit rows) or both.  x, residual, h, y: [T,
+    H]; w: [H], float32 or x's dtype; rstd: float32 [T], for the gradients.  h[r]
+    may be x[r] or residual[r]."""
+    import torch
+    R = len(x)
+    T, H = x[0].shape
+    dt = x[0].dtype
+    rows = [(T, H)] * R
+
+    def some(tensors, dtype, shapes, what):
+        return None if tensors is None else _buffers(ctx, tensors, dtype, shapes, what)
+
+    _check(_lib.ccr_rms_norm(
+        ctx.handle, _buffers(ctx, x, dt, rows, "x"), some(residual, dt, rows, "residual"),
+        _buffers(ctx, w, w[0].dtype, [(H,)] * R, "w"), R, T, H, _dtype_code(x[0]), _dtype_code(w[0]), eps,
+        some(h, dt, rows, "h"), some(y, dt, rows, "y"),
+        some(q, torch.uint8, [(T, ccr_q8_row_bytes(H))] * R, "q"), some(rstd, torch.float32, [(T,)] * R, "rstd"),
+        _ctx_stream(ctx, stream)))
+
+
+def ccr_rms_norm_bwd(ctx: Context, dy: Sequence, h: Sequence, w: Sequence, rstd: Sequence, dx: Sequence,
+                     dw: Sequence, work, dh=None, accumulate: bool = False, stream=None):
+    """Gradients of ccr_rms_norm: dx[r] [T, H] (with dh[r], the gradient of h[r]
+    from elsewhere, added; dx[r] may be that tensor) and dw[r] float32 [H], written
+    or added to.  work: float32 [ccr_rms_norm_work(R, T, H)], this call's alone
+    while it runs."""
+    import torch
+    R = len(dy)
+    T, H = dy[0].shape
+    dt = dy[0].dtype
+    rows = [(T, H)] * R
+    _check(_lib.ccr_rms_norm_bwd(
+        ctx.handle, _buffers(ctx, dy, dt, rows, "dy"), _buffers(ctx, h, dt, rows, "h"),
+        _buffers(ctx, w, w[0].dtype, [(H,)] * R, "w"), _buffers(ctx, rstd, torch.float32, [(T,)] * R, "rstd"),
+        None if dh is None else _buffers(ctx, dh, dt, rows, "dh"), R, T, H, _dtype_code(dy[0]), _dtype_code(w[0]),
+        int(bool(accumulate)), _buffers(ctx, dx, dt, rows, "dx"),
+        _buffers(ctx, dw, torch.float32, [(H,)] * R, "dw"), _work(ctx, work, ccr_rms_norm_work(R, T, H)),
+        _ctx_stream(ctx, stream)))
+
+
+def _work(ctx, work, n):
+    """The address of a float32 work tensor of at least n elements."""
+    import torch
+    if n > 0:
+        if work is None:
+            raise ValueError(f"work is None, needs a float32 tensor of {n} elements")
+        _buffers(ctx, [work], torch.float32, [(n,)], "work", True)
+    return work.data_ptr() if work is not None else None
+
+
+_SCORE = {"softmax": CCR_SCORE_SOFTMAX, "sigmoid": CCR_SCORE_SIGMOID}
+
+
+def ccr_moe_route_work(R: int, T: int, E: int) -> int:
+    """float32 elements of ccr_moe_route's work tensor."""
+    return int(_lib.ccr_moe_route_work(R, T, E))
+
+
+def ccr_moe_route(ctx: Context, logits: Sequence, topk: Sequence, weights: Sequence, bias=None,
+                  score: str = "softmax", groups: int = 1, kept: int = 1, group_top: int = 1, renorm: bool = True,
+                  scale: float = 1.0, counts=None, score_sums=None, work=None, stream=None):
+    """topk[r] int32 [T, K] and weights[r] float32 [T, K]: the experts that the
+    tokens of logits[r] float32 [T, E] go to, and their weights.  bias: float32 [E]
+    per rank, added to the scores for the choice; groups of experts, of which the
+    `kept` best stay.  counts[r] int64 [E] and score_sums[r] float32 [E] take what
+    each expert gets; they need work, float32 [ccr_moe_route_work(R, T, E)], this
+    call's alone while it runs."""
+    import torch
+    if score not in _SCORE:
+        raise ValueError(f"score {score!r} is not one of {sorted(_SCORE)}")
+    R = len(logits)
+    T, E = logits[0].shape
+    K = topk[0].shape[1]
+    stats = counts is not None or score_sums is not None
+
+    def some(tensors, dtype, what):
+        return None if tensors is None else _buffers(ctx, tensors, dtype, [(E,)] * R, what)
+
+    _check(_lib.ccr_moe_route(
+        ctx.handle, _buffers(ctx, logits, torch.float32, [(T, E)] * R, "logits"), some(bias, torch.float32, "bias"),
+        R, T, E, K, ccr_route_t(_SCORE[score], groups, kept, group_top, int(bool(renorm)), scale),
+        _buffers(ctx, topk, torch.int32, [(T, K)] * R, "topk"),
+        _buffers(ctx, weights, torch.float32, [(T, K)] * R, "weights"), some(counts, torch.int64, "counts"),
+        some(score_sums, torch.float32, "score_sums"),
+        _work(ctx, work, ccr_moe_route_work(R, T, E)) if stats else None, _ctx_stream(ctx, stream)))
+
+
+def ccr_moe_route_bwd(ctx: Context, logits: Sequence, topk: Sequence, dweights: Sequence, dlogits: Sequence,
+                      dscore_sums=None, score: str = "softmax", renorm: bool = True, scale: float = 1.0,
+                      stream=None):
+    """dlogits[r] [T, E]: the gradient of the logits of ccr_moe_route from
+    dweights[r] [T, K] and dscore_sums[r] [E], with its score, renorm and scale."""
+    import torch
+    if score not in _SCORE:
+        raise ValueError(f"score {score!r} is not one of {sorted(_SCORE)}")
+    R = len(logits)
+    T, E = logits[0].shape
+    K = topk[0].shape[1]
+    f32 = torch.float32
+    _check(_lib.ccr_moe_route_bwd(
+        ctx.handle, _buffers(ctx, logits, f32, [(T, E)] * R, "logits"),
+        _buffers(ctx, topk, torch.int32, [(T, K)] * R, "topk"),
+        _buffers(ctx, dweights, f32, [(T, K)] * R, "dweights"),
+        None if dscore_sums is None else _buffers(ctx, dscore_sums, f32, [(E,)] * R, "dscore_sums"), R, T, E, K,
+        _SCORE[score], int(bool(renorm)), scale, _buffers(ctx, dlogits, f32, [(T, E)] * R, "dlogits"),
+        _ctx_stream(ctx, stream)))
 
 
 def _grad_list(tensors, what: str):

@@ -24,7 +24,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libccr.so")
 MARSHAL = os.path.join(PKG, "_ccr_torch" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["ccr_api.cpp", "ccr_dma.cpp", "ccr_schedule.cpp", "ccr_kernels.hip", "ccr_ring.hip",
-           "ccr_moe_kernels.hip", "ccr_experts.hip", "ccr_gate.hip", "ccr_grad.hip", "ccr_scratch.hip"]
+           "ccr_moe_kernels.hip", "ccr_experts.hip", "ccr_experts8.hip", "ccr_gate.hip", "ccr_grad.hip",
+           "ccr_norm.hip", "ccr_route.hip", "ccr_scratch.hip"]
 # Per-source additions: the ring-hop kernels take their leading scalar
 # arguments preloaded into registers (gfx950 kernel-argument preloading), so
 # a workgroup's first scalar memory access is the load of its base addresses.

@@ -20,6 +20,7 @@
 #include <rocprofiler-sdk-roctx/roctx.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <chrono>
 #include <cmath>
 #include <cstdarg>
@@ -2137,17 +2138,20 @@ constexpr int kMaxExperts = 65536;
 ccr_status_t run_experts(ccr_ctx* ctx, ExpertOp op, const void* const* a, const char* a_name,
                          const void* const* b, const char* b_name, void* const* c, const char* c_name,
                          const int64_t* h_ecnt, int R, int E, int64_t H, int64_t F, int dtype,
-                         int out_dtype, bool add, hipStream_t s) {
+                         int out_dtype, bool add, bool q8, hipStream_t s) {
   OnDevice on;
   CCR_TRY(on.enter(ctx));
   if (R < 1 || R > kMaxRanks || E < 1 || E > kMaxExperts || E % R != 0)
     return fail(CCR_ERR_INVALID_ARG, "need 1 <= R <= %d, 1 <= E <= %d, R | E", kMaxRanks, kMaxExperts);
-  const int es = dtype_size(dtype), os = dtype_size(out_dtype);
+  const int es = q8 ? 1 : dtype_size(dtype), os = dtype_size(out_dtype);
   if (!es) return fail(CCR_ERR_INVALID_ARG, "dtype %d is not CCR_F32 or CCR_BF16", dtype);
   if (!os || (es == 4 && os != 4))
     return fail(CCR_ERR_INVALID_ARG, "dw_dtype %d: CCR_F32, or CCR_BF16 when dtype is", out_dtype);
+  if (q8 && (H < 1 || H > kMaxExpertDim || F < 1 || F > kMaxExpertDim || F * os % 16 != 0))
+    return fail(CCR_ERR_INVALID_ARG, "H = %lld, F = %lld: each in [1, %lld], rows of out a multiple of 16 bytes",
+                (long long)H, (long long)F, (long long)kMaxExpertDim);
   for (int64_t d : {H, F})
-    if (d < 1 || d > kMaxExpertDim || d * es % 16 != 0)
+    if (!q8 && (d < 1 || d > kMaxExpertDim || d * es % 16 != 0))
       return fail(CCR_ERR_INVALID_ARG, "H = %lld, F = %lld: each in [1, %lld], rows a multiple of 16 bytes",
                   (long long)H, (long long)F, (long long)kMaxExpertDim);
   if (!h_ecnt) return fail(CCR_ERR_INVALID_ARG, "h_ecnt is NULL");
@@ -2166,7 +2170,8 @@ ccr_status_t run_experts(ccr_ctx* ctx, ExpertOp op, const void* const* a, const 
     total += rows[(size_t)e];
   }
   if (total > INT32_MAX) return fail(CCR_ERR_UNSUPPORTED, "more than 2^31 - 1 rows");
-  const int64_t wsize = F * H;  // one expert's weight, in values
+  const int64_t h_bytes = q8 ? q8_row_bytes(H) : H * es;  // of a row of H values
+  const int64_t wsize = F * H;  // one expert's weight gradient, in values
   std::vector<Touched> t;
   KnownRanges known;
   for (int d = 0; d < R; d++) {
@@ -2177,9 +2182,9 @@ ccr_status_t run_experts(ccr_ctx* ctx, ExpertOp op, const void* const* a, const 
       bb = n * H * es;
       cb = add && n == 0 ? 0 : eloc * wsize * os;
     } else {
-      ab = n * (op == ExpertOp::kProduct ? H : F) * es;
-      bb = n == 0 ? 0 : eloc * wsize * es;
-      cb = n * (op == ExpertOp::kProduct ? F : H) * es;
+      ab = n * (op == ExpertOp::kProduct ? h_bytes : F * es);
+      bb = n == 0 ? 0 : eloc * F * h_bytes;
+      cb = n * (op == ExpertOp::kProduct ? F : H) * os;
     }
     CCR_TRY(check_dev_range(ctx, a[d], ab, 16, a_name, d, &known));
     CCR_TRY(check_dev_range(ctx, b[d], bb, 16, b_name, d, &known));
@@ -2212,7 +2217,8 @@ ccr_status_t run_experts(ccr_ctx* ctx, ExpertOp op, const void* const* a, const 
   tab.n = 0;
   int64_t tiles = 0;
   auto flush = [&]() -> ccr_status_t {
-    HIP_TRY(launch_experts(op, es, os, tab, sh, tile, (int)tiles, s));
+    if (q8) HIP_TRY(launch_experts8(tab, sh, tile, (int)tiles, s));
+    else HIP_TRY(launch_experts(op, es, os, tab, sh, tile, (int)tiles, s));
     tab.n = 0;
     tiles = 0;
     return CCR_OK;
@@ -2239,9 +2245,9 @@ ccr_status_t run_experts(ccr_ctx* ctx, ExpertOp op, const void* const* a, const 
         g.b = pb + row * H * es;
         g.c = pc + (l * wsize + m0 * H) * os;
       } else {
-        g.a = pa + (row + m0) * (op == ExpertOp::kProduct ? H : F) * es;
-        g.b = pb + l * wsize * es;
-        g.c = pc + (row + m0) * N * es;
+        g.a = pa + (row + m0) * (op == ExpertOp::kProduct ? h_bytes : F * es);
+        g.b = pb + l * F * h_bytes;
+        g.c = pc + (row + m0) * N * os;
       }
       tab.tile0[tab.n++] = (int32_t)tiles;
       tiles += more;
@@ -2261,15 +2267,17 @@ ccr_status_t run_gate(ccr_ctx* ctx, bool bwd, const void* const* dy, const void*
                 kMaxRanks);
   const int es = dtype_size(dtype);
   if (!es) return fail(CCR_ERR_INVALID_ARG, "dtype %d is not CCR_F32 or CCR_BF16", dtype);
-  if (norm != CCR_GATE_CHOSEN && norm != CCR_GATE_ALL)
-    return fail(CCR_ERR_INVALID_ARG, "norm %d is not CCR_GATE_CHOSEN (0) or CCR_GATE_ALL (1)", norm);
+  if (norm != CCR_GATE_CHOSEN && norm != CCR_GATE_ALL && norm != CCR_GATE_GIVEN)
+    return fail(CCR_ERR_INVALID_ARG,
+                "norm %d is not CCR_GATE_CHOSEN (0), CCR_GATE_ALL (1) or CCR_GATE_GIVEN (2)", norm);
   if (H < 1 || H > kMaxExpertDim || H * es % 16 != 0)
     return fail(CCR_ERR_INVALID_ARG, "H = %lld: in [1, %lld], a row a multiple of 16 bytes", (long long)H,
                 (long long)kMaxExpertDim);
   if (!rows || !logits || !topk || (bwd ? !dy || !drows || !dlogits : !y))
     return fail(CCR_ERR_INVALID_ARG, "a buffer list is NULL");
   if (T == 0) return CCR_OK;
-  const int64_t rb = T * K * H * es, yb = T * H * es, lb = T * E * 4, kb = T * K * 4;
+  const int64_t rb = T * K * H * es, yb = T * H * es, kb = T * K * 4;
+  const int64_t lb = norm == CCR_GATE_GIVEN ? kb : T * E * 4;
   std::vector<Touched> t;
   KnownRanges known;
   GateArgs args{};
@@ -2299,7 +2307,10 @@ ccr_status_t run_gate(ccr_ctx* ctx, bool bwd, const void* const* dy, const void*
   }
   CCR_TRY(check_touched(t));
   if (T > kMaxGridWorkgroups / R) return fail(CCR_ERR_UNSUPPORTED, "R x T is too large for one launch");
-  HIP_TRY(launch_gate_sum(bwd, norm == CCR_GATE_ALL, es, args, R, T, E, K, H * es,
+  const GateNorm by = norm == CCR_GATE_ALL     ? GateNorm::kAll
+                      : norm == CCR_GATE_GIVEN ? GateNorm::kGiven
+                                               : GateNorm::kChosen;
+  HIP_TRY(launch_gate_sum(bwd, by, es, args, R, T, E, K, H * es,
                           R * (rb + yb) > kMallBytes, s));
   return CCR_OK;
 }
@@ -2423,6 +2434,223 @@ ccr_status_t run_grads(ccr_ctx* ctx, bool clip, const void* const* grads, void* 
   return CCR_OK;
 }
 
+// The R device lists of a call's arguments: each checked, and held against the
+// others for overlaps.
+struct CallBuffers {
+  ccr_ctx* ctx;
+  KnownRanges known;
+  std::vector<Touched> touched;
+  ccr_status_t add(const void* p, int64_t nbytes, bool written, const char* what, int r, int align = 16) {
+    CCR_TRY(check_dev_range(ctx, p, nbytes, align, what, r, &known));
+    touch(&touched, p, nbytes, written, what, r);
+    return CCR_OK;
+  }
+  ccr_status_t disjoint() const { return check_touched(touched); }
+};
+
+// What the norm and its gradients, and 8-bit rows, ask of R, T, H and the type.
+ccr_status_t check_rows_shape(int R, int64_t T, int64_t H, int dtype) {
+  if (R < 1 || R > kMaxRanks || T < 0 || T > INT32_MAX)
+    return fail(CCR_ERR_INVALID_ARG, "need 1 <= R <= %d, 0 <= T < 2^31", kMaxRanks);
+  const int es = dtype_size(dtype);
+  if (!es) return fail(CCR_ERR_INVALID_ARG, "dtype %d is not CCR_F32 or CCR_BF16", dtype);
+  if (H < 1 || H > kMaxExpertDim || H * es % 16 != 0)
+    return fail(CCR_ERR_INVALID_ARG, "H = %lld: in [1, %lld], a row a multiple of 16 bytes", (long long)H,
+                (long long)kMaxExpertDim);
+  if (T > kMaxGridWorkgroups / R) return fail(CCR_ERR_UNSUPPORTED, "R x T is too large for one launch");
+  return CCR_OK;
+}
+
+ccr_status_t run_norm(ccr_ctx* ctx, const void* const* x, const void* const* residual, const void* const* w, int R,
+                      int64_t T, int64_t H, int dtype, int w_dtype, float eps, void* const* h, void* const* y,
+                      void* const* q, float* const* rstd, hipStream_t s) {
+  OnDevice on;
+  CCR_TRY(on.enter(ctx));
+  CCR_TRY(check_rows_shape(R, T, H, dtype));
+  const int es = dtype_size(dtype), wes = dtype_size(w_dtype);
+  if (!wes) return fail(CCR_ERR_INVALID_ARG, "w_dtype %d is not CCR_F32 or CCR_BF16", w_dtype);
+  if (!(eps >= 0.0f) || eps > FLT_MAX) return fail(CCR_ERR_INVALID_ARG, "eps %g is not finite and >= 0", eps);
+  if (!x || !w) return fail(CCR_ERR_INVALID_ARG, "x or w is NULL");
+  if (!residual != !h) return fail(CCR_ERR_INVALID_ARG, "residual and h come together");
+  if (!y && !q) return fail(CCR_ERR_INVALID_ARG, "y and q are NULL");
+  if (T == 0) return CCR_OK;
+  const int64_t rb = T * H * es;
+  CallBuffers b{ctx, {}, {}};
+  NormArgs args{};
+  for (int r = 0; r < R; r++) {
+    // h may take the place of x or of the residual: each value is read before it is written
+    const bool on_x = h && h[r] == x[r], on_res = h && h[r] == residual[r];
+    if (!on_x) CCR_TRY(b.add(x[r], rb, false, "x", r));
+    CCR_TRY(b.add(w[r], H * wes, false, "w", r));
+    args.x[r] = static_cast<const char*>(x[r]);
+    args.w[r] = static_cast<const char*>(w[r]);
+    if (h) {
+      if (!on_res) CCR_TRY(b.add(residual[r], rb, false, "residual", r));
+      CCR_TRY(b.add(h[r], rb, true, "h", r));
+      args.res[r] = static_cast<const char*>(residual[r]);
+      args.h[r] = static_cast<char*>(h[r]);
+    }
+    if (y) {
+      CCR_TRY(b.add(y[r], rb, true, "y", r));
+      args.y[r] = static_cast<char*>(y[r]);
+    }
+    if (q) {
+      CCR_TRY(b.add(q[r], T * q8_row_bytes(H), true, "q", r));
+      args.q[r] = static_cast<char*>(q[r]);
+    }
+    if (rstd) {
+      CCR_TRY(b.add(rstd[r], T * 4, true, "rstd", r, 4));
+      args.rstd[r] = rstd[r];
+    }
+  }
+  CCR_TRY(b.disjoint());
+  HIP_TRY(launch_norm(args, NormShape{R, T, H, es, wes, h != nullptr, eps, false}, s));
+  return CCR_OK;
+}
+
+ccr_status_t run_norm_bwd(ccr_ctx* ctx, const void* const* dy, const void* const* h, const void* const* w,
+                          const float* const* rstd, const void* const* dh, int R, int64_t T, int64_t H, int dtype,
+                          int w_dtype, int accumulate, void* const* dx, float* const* dw, float* work,
+                          hipStream_t s) {
+  OnDevice on;
+  CCR_TRY(on.enter(ctx));
+  CCR_TRY(check_rows_shape(R, T, H, dtype));
+  const int es = dtype_size(dtype), wes = dtype_size(w_dtype);
+  if (!wes) return fail(CCR_ERR_INVALID_ARG, "w_dtype %d is not CCR_F32 or CCR_BF16", w_dtype);
+  if (accumulate != 0 && accumulate != 1) return fail(CCR_ERR_INVALID_ARG, "accumulate %d is not 0 or 1", accumulate);
+  if (!dy || !h || !w || !rstd || !dx || !dw) return fail(CCR_ERR_INVALID_ARG, "a buffer list is NULL");
+  if (T == 0 && accumulate) return CCR_OK;
+  const int64_t rb = T * H * es;
+  CallBuffers b{ctx, {}, {}};
+  NormBwdArgs args{};
+  CCR_TRY(b.add(work, ccr_rms_norm_work(R, T, H) * 4, true, "work", 0));
+  for (int r = 0; r < R; r++) {
+    const bool on_dh = dh && dx[r] == dh[r];  // each value is read before it is written
+    CCR_TRY(b.add(dy[r], rb, false, "dy", r));
+    CCR_TRY(b.add(h[r], rb, false, "h", r));
+    CCR_TRY(b.add(w[r], T ? H * wes : 0, false, "w", r));
+    CCR_TRY(b.add(rstd[r], T * 4, false, "rstd", r, 4));
+    if (dh && !on_dh) CCR_TRY(b.add(dh[r], rb, false, "dh", r));
+    CCR_TRY(b.add(dx[r], rb, true, "dx", r));
+    CCR_TRY(b.add(dw[r], H * 4, true, "dw", r, 4));
+    args.dy[r] = static_cast<const char*>(dy[r]);
+    args.h[r] = static_cast<const char*>(h[r]);
+    args.w[r] = static_cast<const char*>(w[r]);
+    args.dh[r] = dh ? static_cast<const char*>(dh[r]) : nullptr;
+    args.rstd[r] = rstd[r];
+    args.dx[r] = static_cast<char*>(dx[r]);
+    args.dw[r] = dw[r];
+  }
+  CCR_TRY(b.disjoint());
+  HIP_TRY(launch_norm_bwd(args, NormShape{R, T, H, es, wes, dh != nullptr, 0.0f, accumulate == 1}, work, s));
+  return CCR_OK;
+}
+
+// To 8-bit rows, or from them.
+ccr_status_t run_q8(ccr_ctx* ctx, bool to_q8, const void* const* rows, const void* const* q, const int64_t* counts,
+                    int R, int64_t H, int dtype, hipStream_t s) {
+  OnDevice on;
+  CCR_TRY(on.enter(ctx));
+  CCR_TRY(check_rows_shape(R, 0, H, dtype));
+  const int es = dtype_size(dtype);
+  if (!rows || !q || !counts) return fail(CCR_ERR_INVALID_ARG, "a list is NULL");
+  CallBuffers b{ctx, {}, {}};
+  Q8Args args{};
+  for (int r = 0; r < R; r++) {
+    if (counts[r] < 0) return fail(CCR_ERR_INVALID_ARG, "counts[%d] < 0", r);
+    if (counts[r] > INT32_MAX) return fail(CCR_ERR_UNSUPPORTED, "counts[%d] exceeds 2^31 - 1", r);
+    CCR_TRY(b.add(rows[r], counts[r] * H * es, !to_q8, to_q8 ? "x" : "y", r));
+    CCR_TRY(b.add(q[r], counts[r] * q8_row_bytes(H), to_q8, "q", r));
+    args.rows[r] = static_cast<const char*>(rows[r]);
+    args.q[r] = const_cast<char*>(static_cast<const char*>(q[r]));
+    args.first[r + 1] = args.first[r] + counts[r];
+  }
+  CCR_TRY(b.disjoint());
+  if (q8_grid(to_q8, es, args.first[R], H) > kMaxGridWorkgroups)
+    return fail(CCR_ERR_UNSUPPORTED, "too many rows for one launch");
+  HIP_TRY(launch_q8(to_q8, es, args, R, H, s));
+  return CCR_OK;
+}
+
+ccr_status_t check_route_shape(int R, int64_t T, int E, int K, int score, int renorm, float scale) {
+  if (R < 1 || R > kMaxRanks || T < 0 || T > INT32_MAX || E < 1 || E > 1024 || K < 1 || K > 16 || K > E)
+    return fail(CCR_ERR_INVALID_ARG, "need 1 <= R <= %d, 0 <= T < 2^31, 1 <= E <= 1024, 1 <= K <= min(E, 16)",
+                kMaxRanks);
+  if (score != CCR_SCORE_SOFTMAX && score != CCR_SCORE_SIGMOID)
+    return fail(CCR_ERR_INVALID_ARG, "score %d is not CCR_SCORE_SOFTMAX (0) or CCR_SCORE_SIGMOID (1)", score);
+  if (renorm != 0 && renorm != 1) return fail(CCR_ERR_INVALID_ARG, "renorm %d is not 0 or 1", renorm);
+  if (!std::isfinite(scale)) return fail(CCR_ERR_INVALID_ARG, "scale %g is not finite", scale);
+  if (T > kMaxGridWorkgroups / R) return fail(CCR_ERR_UNSUPPORTED, "R x T is too large for one launch");
+  return CCR_OK;
+}
+
+ccr_status_t run_route(ccr_ctx* ctx, const float* const* logits, const float* const* bias, int R, int64_t T, int E,
+                       int K, const ccr_route_t* how, int32_t* const* topk, float* const* weights,
+                       int64_t* const* counts, float* const* sums, float* work, hipStream_t s) {
+  OnDevice on;
+  CCR_TRY(on.enter(ctx));
+  if (!how) return fail(CCR_ERR_INVALID_ARG, "how is NULL");
+  CCR_TRY(check_route_shape(R, T, E, K, how->score, how->renorm, how->scale));
+  if (how->groups < 1 || how->groups > kRouteGroups || E % how->groups != 0 || how->kept_groups < 1 ||
+      how->kept_groups > how->groups || (how->group_top != 1 && how->group_top != 2))
+    return fail(CCR_ERR_INVALID_ARG, "need groups in [1, %d] dividing E, 1 <= kept_groups <= groups, group_top 1 or 2",
+                kRouteGroups);
+  if (K > E / how->groups * how->kept_groups)
+    return fail(CCR_ERR_INVALID_ARG, "K = %d of the %d experts of kept groups", K, E / how->groups * how->kept_groups);
+  if (!logits || !topk || !weights) return fail(CCR_ERR_INVALID_ARG, "logits, topk or weights is NULL");
+  CallBuffers b{ctx, {}, {}};
+  RouteArgs args{};
+  if (counts || sums) CCR_TRY(b.add(work, ccr_moe_route_work(R, T, E) * 4, true, "work", 0));
+  for (int r = 0; r < R; r++) {
+    CCR_TRY(b.add(logits[r], T * E * 4, false, "logits", r, 4));
+    if (bias) CCR_TRY(b.add(bias[r], T ? E * 4 : 0, false, "bias", r, 4));
+    CCR_TRY(b.add(topk[r], T * K * 4, true, "topk", r, 4));
+    CCR_TRY(b.add(weights[r], T * K * 4, true, "weights", r, 4));
+    if (counts) CCR_TRY(b.add(counts[r], E * 8, true, "counts", r, 8));
+    if (sums) CCR_TRY(b.add(sums[r], E * 4, true, "score_sums", r, 4));
+    args.logits[r] = logits[r];
+    args.bias[r] = bias ? bias[r] : nullptr;
+    args.topk[r] = topk[r];
+    args.weights[r] = weights[r];
+    args.counts[r] = counts ? counts[r] : nullptr;
+    args.sums[r] = sums ? sums[r] : nullptr;
+  }
+  CCR_TRY(b.disjoint());
+  HIP_TRY(launch_route(args,
+                       RouteShape{R, T, E, K, how->groups, how->kept_groups, how->group_top,
+                                  how->score == CCR_SCORE_SIGMOID, how->renorm == 1, how->scale},
+                       work, s));
+  return CCR_OK;
+}
+
+ccr_status_t run_route_bwd(ccr_ctx* ctx, const float* const* logits, const int32_t* const* topk,
+                           const float* const* dweights, const float* const* dsums, int R, int64_t T, int E, int K,
+                           int score, int renorm, float scale, float* const* dlogits, hipStream_t s) {
+  OnDevice on;
+  CCR_TRY(on.enter(ctx));
+  CCR_TRY(check_route_shape(R, T, E, K, score, renorm, scale));
+  if (!logits || !topk || !dweights || !dlogits) return fail(CCR_ERR_INVALID_ARG, "a buffer list is NULL");
+  if (T == 0) return CCR_OK;
+  CallBuffers b{ctx, {}, {}};
+  RouteBwdArgs args{};
+  for (int r = 0; r < R; r++) {
+    CCR_TRY(b.add(logits[r], T * E * 4, false, "logits", r, 4));
+    CCR_TRY(b.add(topk[r], T * K * 4, false, "topk", r, 4));
+    CCR_TRY(b.add(dweights[r], T * K * 4, false, "dweights", r, 4));
+    if (dsums) CCR_TRY(b.add(dsums[r], E * 4, false, "dscore_sums", r, 4));
+    CCR_TRY(b.add(dlogits[r], T * E * 4, true, "dlogits", r, 4));
+    args.logits[r] = logits[r];
+    args.topk[r] = topk[r];
+    args.dweights[r] = dweights[r];
+    args.dsums[r] = dsums ? dsums[r] : nullptr;
+    args.dlogits[r] = dlogits[r];
+  }
+  CCR_TRY(b.disjoint());
+  HIP_TRY(launch_route_bwd(args,
+                           RouteShape{R, T, E, K, 1, 1, 1, score == CCR_SCORE_SIGMOID, renorm == 1, scale}, s));
+  return CCR_OK;
+}
+
 }  // namespace
 
 ccr_status_t ccr_moe_experts(ccr_ctx_t ctx, const void* const* exp, const void* const* w,
@@ -2431,7 +2659,7 @@ ccr_status_t ccr_moe_experts(ccr_ctx_t ctx, const void* const* exp, const void* 
   CCR_MARK("ccr_moe_experts");
   return no_throw([&] {
     return run_experts(ctx, ExpertOp::kProduct, exp, "exp", w, "w", out, "out", h_ecnt, R, E, H, F, dtype,
-                       dtype, false, static_cast<hipStream_t>(stream));
+                       dtype, false, false, static_cast<hipStream_t>(stream));
   });
 }
 
@@ -2441,7 +2669,7 @@ ccr_status_t ccr_moe_experts_dgrad(ccr_ctx_t ctx, const void* const* dout, const
   CCR_MARK("ccr_moe_experts_dgrad");
   return no_throw([&] {
     return run_experts(ctx, ExpertOp::kDgrad, dout, "dout", w, "w", dexp, "dexp", h_ecnt, R, E, H, F, dtype,
-                       dtype, false, static_cast<hipStream_t>(stream));
+                       dtype, false, false, static_cast<hipStream_t>(stream));
   });
 }
 
@@ -2453,7 +2681,7 @@ ccr_status_t ccr_moe_experts_wgrad(ccr_ctx_t ctx, const void* const* exp, const 
     if (accumulate != 0 && accumulate != 1)
       return fail(CCR_ERR_INVALID_ARG, "accumulate %d is not 0 or 1", accumulate);
     return run_experts(ctx, ExpertOp::kWgrad, dout, "dout", exp, "exp", dw, "dw", h_ecnt, R, E, H, F, dtype,
-                       dw_dtype, accumulate == 1, static_cast<hipStream_t>(stream));
+                       dw_dtype, accumulate == 1, false, static_cast<hipStream_t>(stream));
   });
 }
 
@@ -2475,6 +2703,84 @@ ccr_status_t ccr_moe_gate_sum_bwd(ccr_ctx_t ctx, const void* const* dy, const vo
   return no_throw([&] {
     return run_gate(ctx, true, dy, rows, logits, topk, nullptr, drows, dlogits, R, T, E, K, H, dtype, norm,
                     static_cast<hipStream_t>(stream));
+  });
+}
+
+int64_t ccr_q8_row_bytes(int64_t H) { return H < 1 || H > kMaxExpertDim ? 0 : q8_row_bytes(H); }
+
+int64_t ccr_rms_norm_work(int R, int64_t T, int64_t H) {
+  return R < 1 || R > kMaxRanks || T < 1 || H < 1 || H > kMaxExpertDim ? 0 : R * norm_slots(R, T) * H;
+}
+
+int64_t ccr_moe_route_work(int R, int64_t T, int E) {
+  return R < 1 || R > kMaxRanks || T < 1 || E < 1 || E > 1024 ? 0 : (int64_t)R * route_slots(R, T) * 2 * E;
+}
+
+ccr_status_t ccr_rms_norm(ccr_ctx_t ctx, const void* const* x, const void* const* residual, const void* const* w,
+                          int R, int64_t T, int64_t H, int dtype, int w_dtype, float eps, void* const* h,
+                          void* const* y, void* const* q, float* const* rstd, void* stream) {
+  CCR_MARK("ccr_rms_norm");
+  return no_throw([&] {
+    return run_norm(ctx, x, residual, w, R, T, H, dtype, w_dtype, eps, h, y, q, rstd,
+                    static_cast<hipStream_t>(stream));
+  });
+}
+
+ccr_status_t ccr_rms_norm_bwd(ccr_ctx_t ctx, const void* const* dy, const void* const* h, const void* const* w,
+                              const float* const* rstd, const void* const* dh, int R, int64_t T, int64_t H, int dtype,
+                              int w_dtype, int accumulate, void* const* dx, float* const* dw, float* work,
+                              void* stream) {
+  CCR_MARK("ccr_rms_norm_bwd");
+  return no_throw([&] {
+    return run_norm_bwd(ctx, dy, h, w, rstd, dh, R, T, H, dtype, w_dtype, accumulate, dx, dw, work,
+                        static_cast<hipStream_t>(stream));
+  });
+}
+
+ccr_status_t ccr_quantize_rows(ccr_ctx_t ctx, const void* const* x, const int64_t* counts, int R, int64_t H,
+                               int dtype, void* const* q, void* stream) {
+  CCR_MARK("ccr_quantize_rows");
+  return no_throw([&] {
+    return run_q8(ctx, true, x, const_cast<const void* const*>(q), counts, R, H, dtype,
+                  static_cast<hipStream_t>(stream));
+  });
+}
+
+ccr_status_t ccr_dequantize_rows(ccr_ctx_t ctx, const void* const* q, const int64_t* counts, int R, int64_t H,
+                                 int dtype, void* const* y, void* stream) {
+  CCR_MARK("ccr_dequantize_rows");
+  return no_throw([&] {
+    return run_q8(ctx, false, const_cast<const void* const*>(y), q, counts, R, H, dtype,
+                  static_cast<hipStream_t>(stream));
+  });
+}
+
+ccr_status_t ccr_moe_route(ccr_ctx_t ctx, const float* const* logits, const float* const* bias, int R, int64_t T,
+                           int E, int K, const ccr_route_t* how, int32_t* const* topk, float* const* weights,
+                           int64_t* const* counts, float* const* score_sums, float* work, void* stream) {
+  CCR_MARK("ccr_moe_route");
+  return no_throw([&] {
+    return run_route(ctx, logits, bias, R, T, E, K, how, topk, weights, counts, score_sums, work,
+                     static_cast<hipStream_t>(stream));
+  });
+}
+
+ccr_status_t ccr_moe_route_bwd(ccr_ctx_t ctx, const float* const* logits, const int32_t* const* topk,
+                               const float* const* dweights, const float* const* dscore_sums, int R, int64_t T, int E,
+                               int K, int score, int renorm, float scale, float* const* dlogits, void* stream) {
+  CCR_MARK("ccr_moe_route_bwd");
+  return no_throw([&] {
+    return run_route_bwd(ctx, logits, topk, dweights, dscore_sums, R, T, E, K, score, renorm, scale, dlogits,
+                         static_cast<hipStream_t>(stream));
+  });
+}
+
+ccr_status_t ccr_moe_experts_q8(ccr_ctx_t ctx, const void* const* exp, const void* const* w, const int64_t* h_ecnt,
+                                int R, int E, int64_t H, int64_t F, void* const* out, void* stream) {
+  CCR_MARK("ccr_moe_experts_q8");
+  return no_throw([&] {
+    return run_experts(ctx, ExpertOp::kProduct, exp, "exp", w, "w", out, "out", h_ecnt, R, E, H, F, CCR_BF16,
+                       CCR_BF16, false, true, static_cast<hipStream_t>(stream));
   });
 }
 

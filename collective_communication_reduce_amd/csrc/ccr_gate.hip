@@ -11,6 +11,8 @@
 //   dl[e_k]  += w_k (g_k - s)         (S = the choices)
 //   dl[e]     = sum_{k: e_k = e} w_k g_k - p_e s   (S = all experts)
 //
+// or, with weights given instead of logits, w_k as it is and dw_k = g_k.
+//
 // An absent choice (its expert id outside [0, E), or its logit -inf) has
 // weight 0 and its row is not read.  Everything is one pass over the rows,
 // bound by HBM: 16-byte loads, all K rows of a column in flight together,
@@ -82,16 +84,20 @@ struct Choice {
   float m, s;  // maximum and sum of the softmax, in every lane
 };
 
-template <bool ALL>
+template <GateNorm NORM>
 __device__ __forceinline__ Choice choices(const float* logits, const int32_t* topk, int E, int K) {
   const int lane = threadIdx.x & 63;
   Choice c;
   c.e = lane < K ? topk[lane] : -1;
   if (c.e >= E) c.e = -1;
+  if constexpr (NORM == GateNorm::kGiven) {  // logits: the choices' weights
+    c.w = c.e >= 0 ? logits[lane] : 0.0f;
+    return c;
+  }
   const float l = c.e >= 0 ? logits[c.e] : kNegInf;
   if (l == kNegInf) c.e = -1;
   float sum = 0;
-  if constexpr (ALL) {
+  if constexpr (NORM == GateNorm::kAll) {
     float m = kNegInf;
     for (int e = lane; e < E; e += 64) m = fmaxf(m, logits[e]);
     c.m = wave_max(m);
@@ -110,7 +116,7 @@ __device__ __forceinline__ Choice choices(const float* logits, const int32_t* to
 // One token per TPT threads (a wave, or the whole workgroup); KM >= K rows
 // are held at once.  NTL, NTS: the rows are loaded, the results stored
 // non-temporally.
-template <int ES, int TPT, int KM, bool ALL, bool NTL, bool NTS>
+template <int ES, int TPT, int KM, GateNorm NORM, bool NTL, bool NTS>
 __global__ __launch_bounds__(kBlock) void gate_sum_kernel(const GateArgs a, int64_t T, int E, int K,
                                                           int64_t vpr, int64_t blocks_per_rank) {
   constexpr int kTok = kBlock / TPT;
@@ -118,7 +124,7 @@ __global__ __launch_bounds__(kBlock) void gate_sum_kernel(const GateArgs a, int6
   const int r = (int)(blockIdx.x / blocks_per_rank);
   const int64_t t = (blockIdx.x % blocks_per_rank) * kTok + (TPT == kBlock ? 0 : threadIdx.x / TPT);
   if (t >= T) return;
-  const Choice c = choices<ALL>(a.logits[r] + t * E, a.topk[r] + t * K, E, K);
+  const Choice c = choices<NORM>(a.logits[r] + t * (NORM == GateNorm::kGiven ? K : E), a.topk[r] + t * K, E, K);
   const u32x4* rows = reinterpret_cast<const u32x4*>(a.rows[r]) + t * K * vpr;
   u32x4* y = reinterpret_cast<u32x4*>(a.y[r]) + t * vpr;
   float w[KM];
@@ -146,7 +152,7 @@ __global__ __launch_bounds__(kBlock) void gate_sum_kernel(const GateArgs a, int6
   }
 }
 
-template <int ES, int TPT, int KM, bool ALL, bool NTS>
+template <int ES, int TPT, int KM, GateNorm NORM, bool NTS>
 __global__ __launch_bounds__(kBlock) void gate_sum_bwd_kernel(const GateArgs a, int64_t T, int E,
                                                               int K, int64_t vpr,
                                                               int64_t blocks_per_rank) {
@@ -157,8 +163,9 @@ __global__ __launch_bounds__(kBlock) void gate_sum_bwd_kernel(const GateArgs a, 
   const int r = (int)(blockIdx.x / blocks_per_rank);
   const int64_t t = (blockIdx.x % blocks_per_rank) * kTok + (TPT == kBlock ? 0 : threadIdx.x / TPT);
   if (t >= T) return;  // uniform over the threads of a token
-  const float* logits = a.logits[r] + t * E;
-  const Choice c = choices<ALL>(logits, a.topk[r] + t * K, E, K);
+  constexpr bool kGiven = NORM == GateNorm::kGiven, kAll = NORM == GateNorm::kAll;
+  const float* logits = a.logits[r] + t * (kGiven ? K : E);
+  const Choice c = choices<NORM>(logits, a.topk[r] + t * K, E, K);
   const u32x4* rows = reinterpret_cast<const u32x4*>(a.rows[r]) + t * K * vpr;
   const u32x4* dy = reinterpret_cast<const u32x4*>(a.dy[r]) + t * vpr;
   u32x4* drows = reinterpret_cast<u32x4*>(a.drows[r]) + t * K * vpr;
@@ -206,6 +213,13 @@ __global__ __launch_bounds__(kBlock) void gate_sum_bwd_kernel(const GateArgs a, 
       for (int x = 0; x < kBlock / 64; x++) g[k] += part[x][k];
     }
   }
+  if constexpr (kGiven) {
+    float* dw = a.dlogits[r] + t * K;
+#pragma unroll
+    for (int k = 0; k < KM; k++)
+      if (k < K && (int)threadIdx.x % TPT == k) dw[k] = ex[k] >= 0 ? g[k] : 0.0f;
+    return;
+  }
   float s = 0.0f;
 #pragma unroll
   for (int k = 0; k < KM; k++)
@@ -215,8 +229,8 @@ __global__ __launch_bounds__(kBlock) void gate_sum_bwd_kernel(const GateArgs a, 
     float d = 0.0f;
 #pragma unroll
     for (int k = 0; k < KM; k++)
-      if (ex[k] == e) d += ALL ? w[k] * g[k] : w[k] * (g[k] - s);
-    if constexpr (ALL) {
+      if (ex[k] == e) d += kAll ? w[k] * g[k] : w[k] * (g[k] - s);
+    if constexpr (kAll) {
       const float l = logits[e];
       if (c.s != 0.0f && l != kNegInf) d -= term(l, c.m) / c.s * s;
     }
@@ -238,7 +252,7 @@ struct Caching {
   bool nt_load, nt_store;
 };
 
-template <int ES, int TPT, int KM, bool ALL>
+template <int ES, int TPT, int KM, GateNorm NORM>
 hipError_t launch_gate_as(bool bwd, const GateArgs& a, int R, int64_t T, int E, int K, int64_t vpr,
                           Caching c, hipStream_t stream) {
   constexpr int kTok = kBlock / TPT;
@@ -246,48 +260,54 @@ hipError_t launch_gate_as(bool bwd, const GateArgs& a, int R, int64_t T, int E, 
   if (per_rank * R > kMaxGridWorkgroups) return hipErrorInvalidValue;
   const unsigned grid = (unsigned)(per_rank * R);
   if (bwd && c.nt_store)
-    gate_sum_bwd_kernel<ES, TPT, KM, ALL, true><<<grid, kBlock, 0, stream>>>(a, T, E, K, vpr, per_rank);
+    gate_sum_bwd_kernel<ES, TPT, KM, NORM, true><<<grid, kBlock, 0, stream>>>(a, T, E, K, vpr, per_rank);
   else if (bwd)
-    gate_sum_bwd_kernel<ES, TPT, KM, ALL, false><<<grid, kBlock, 0, stream>>>(a, T, E, K, vpr, per_rank);
+    gate_sum_bwd_kernel<ES, TPT, KM, NORM, false><<<grid, kBlock, 0, stream>>>(a, T, E, K, vpr, per_rank);
   else if (c.nt_load)
-    gate_sum_kernel<ES, TPT, KM, ALL, true, true><<<grid, kBlock, 0, stream>>>(a, T, E, K, vpr, per_rank);
+    gate_sum_kernel<ES, TPT, KM, NORM, true, true><<<grid, kBlock, 0, stream>>>(a, T, E, K, vpr, per_rank);
   else if (c.nt_store)
-    gate_sum_kernel<ES, TPT, KM, ALL, false, true><<<grid, kBlock, 0, stream>>>(a, T, E, K, vpr, per_rank);
+    gate_sum_kernel<ES, TPT, KM, NORM, false, true><<<grid, kBlock, 0, stream>>>(a, T, E, K, vpr, per_rank);
   else
-    gate_sum_kernel<ES, TPT, KM, ALL, false, false><<<grid, kBlock, 0, stream>>>(a, T, E, K, vpr, per_rank);
+    gate_sum_kernel<ES, TPT, KM, NORM, false, false><<<grid, kBlock, 0, stream>>>(a, T, E, K, vpr, per_rank);
   return hipGetLastError();
 }
 
-template <int ES, int TPT, bool ALL>
+template <int ES, int TPT, GateNorm NORM>
 hipError_t launch_gate_k(bool bwd, const GateArgs& a, int R, int64_t T, int E, int K, int64_t vpr,
                          Caching c, hipStream_t stream) {
-  if (K <= 2) return launch_gate_as<ES, TPT, 2, ALL>(bwd, a, R, T, E, K, vpr, c, stream);
-  if (K <= 4) return launch_gate_as<ES, TPT, 4, ALL>(bwd, a, R, T, E, K, vpr, c, stream);
-  if (K <= 8) return launch_gate_as<ES, TPT, 8, ALL>(bwd, a, R, T, E, K, vpr, c, stream);
-  return launch_gate_as<ES, TPT, 16, ALL>(bwd, a, R, T, E, K, vpr, c, stream);
+  if (K <= 2) return launch_gate_as<ES, TPT, 2, NORM>(bwd, a, R, T, E, K, vpr, c, stream);
+  if (K <= 4) return launch_gate_as<ES, TPT, 4, NORM>(bwd, a, R, T, E, K, vpr, c, stream);
+  if (K <= 8) return launch_gate_as<ES, TPT, 8, NORM>(bwd, a, R, T, E, K, vpr, c, stream);
+  return launch_gate_as<ES, TPT, 16, NORM>(bwd, a, R, T, E, K, vpr, c, stream);
 }
 
 // A row of up to 64 vectors takes one wave, a longer one the workgroup.
-template <int ES, bool ALL>
+template <int ES, GateNorm NORM>
 hipError_t launch_gate_t(bool bwd, const GateArgs& a, int R, int64_t T, int E, int K, int64_t vpr,
                          Caching c, hipStream_t stream) {
-  return vpr <= 64 ? launch_gate_k<ES, 64, ALL>(bwd, a, R, T, E, K, vpr, c, stream)
-                   : launch_gate_k<ES, kBlock, ALL>(bwd, a, R, T, E, K, vpr, c, stream);
+  return vpr <= 64 ? launch_gate_k<ES, 64, NORM>(bwd, a, R, T, E, K, vpr, c, stream)
+                   : launch_gate_k<ES, kBlock, NORM>(bwd, a, R, T, E, K, vpr, c, stream);
 }
 
 }  // namespace
 
-hipError_t launch_gate_sum(bool bwd, bool over_all, int es, const GateArgs& a, int R, int64_t T,
+hipError_t launch_gate_sum(bool bwd, GateNorm norm, int es, const GateArgs& a, int R, int64_t T,
                            int E, int K, int64_t row_bytes, bool large, hipStream_t stream) {
   if (R <= 0 || T <= 0) return hipSuccess;
   const int64_t vpr = row_bytes >> 4, result = R * T * row_bytes * (bwd ? K : 1);
   const bool nt_store = large || result > (int64_t(2) << 20);
   const Caching c{large && !bwd, nt_store};
-  if (es == 4)
-    return over_all ? launch_gate_t<4, true>(bwd, a, R, T, E, K, vpr, c, stream)
-                    : launch_gate_t<4, false>(bwd, a, R, T, E, K, vpr, c, stream);
-  return over_all ? launch_gate_t<2, true>(bwd, a, R, T, E, K, vpr, c, stream)
-                  : launch_gate_t<2, false>(bwd, a, R, T, E, K, vpr, c, stream);
+  switch (norm) {
+    case GateNorm::kAll:
+      return es == 4 ? launch_gate_t<4, GateNorm::kAll>(bwd, a, R, T, E, K, vpr, c, stream)
+                     : launch_gate_t<2, GateNorm::kAll>(bwd, a, R, T, E, K, vpr, c, stream);
+    case GateNorm::kGiven:
+      return es == 4 ? launch_gate_t<4, GateNorm::kGiven>(bwd, a, R, T, E, K, vpr, c, stream)
+                     : launch_gate_t<2, GateNorm::kGiven>(bwd, a, R, T, E, K, vpr, c, stream);
+    default:
+      return es == 4 ? launch_gate_t<4, GateNorm::kChosen>(bwd, a, R, T, E, K, vpr, c, stream)
+                     : launch_gate_t<2, GateNorm::kChosen>(bwd, a, R, T, E, K, vpr, c, stream);
+  }
 }
 
 }  // namespace ccr

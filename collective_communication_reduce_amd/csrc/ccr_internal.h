@@ -227,6 +227,10 @@ ExpertTile expert_tile(ExpertOp op, int es, int os, const ExpertShape& sh, const
 hipError_t launch_experts(ExpertOp op, int es, int os, const ExpertTable& tab, const ExpertShape& sh,
                           ExpertTile tile, int tiles, hipStream_t stream);
 
+// The product on 8-bit rows to bf16 (ccr_experts8.hip).
+hipError_t launch_experts8(const ExpertTable& tab, const ExpertShape& sh, ExpertTile tile, int tiles,
+                           hipStream_t stream);
+
 // The gated sum and its gradients (ccr_gate.hip).  Per rank, device pointers.
 struct GateArgs {
   const char* rows[kRingHopMaxRanks];
@@ -238,9 +242,105 @@ struct GateArgs {
   float* dlogits[kRingHopMaxRanks];
 };
 static_assert(sizeof(GateArgs) <= 3584, "fits the kernel argument segment");
+// What weighs the rows: the softmax of the chosen logits, of all, or weights
+// given in the place of the logits ([T x K], and their gradients likewise).
+enum class GateNorm : int { kChosen = 0, kAll = 1, kGiven = 2 };
 // large: rows and results exceed the last-level cache.
-hipError_t launch_gate_sum(bool bwd, bool over_all, int es, const GateArgs& a, int R, int64_t T,
+hipError_t launch_gate_sum(bool bwd, GateNorm norm, int es, const GateArgs& a, int R, int64_t T,
                            int E, int K, int64_t row_bytes, bool large, hipStream_t stream);
+
+// Rows of 8 bits (ccr_rows.h states the format): bytes of values, and of a row.
+constexpr int64_t q8_values(int64_t H) { return (H + 127) / 128 * 128; }
+constexpr int64_t q8_row_bytes(int64_t H) {
+  return q8_values(H) + (q8_values(H) / 32 + 127) / 128 * 128;
+}
+// R lists of rows, of rows[r] with first[r+1] - first[r] rows each.
+struct Q8Args {
+  const char* rows[kRingHopMaxRanks];
+  char* q[kRingHopMaxRanks];
+  int64_t first[kRingHopMaxRanks + 1];
+};
+// Pieces of a row that one wave makes (64 vectors of the row) or one thread
+// expands (16 values), and the workgroups for `rows` rows.
+constexpr int64_t q8_chunks(bool to_q8, int es, int64_t H) {
+  return to_q8 ? (q8_values(H) * es / 16 + 63) / 64 : (H + 15) / 16;
+}
+constexpr int64_t q8_grid(bool to_q8, int es, int64_t rows, int64_t H) {
+  const int64_t per = to_q8 ? kBlock / 64 : kBlock;
+  return (rows * q8_chunks(to_q8, es, H) + per - 1) / per;
+}
+// To 8 bits, or back (rows is written then).
+hipError_t launch_q8(bool to_q8, int es, const Q8Args& a, int R, int64_t H, hipStream_t stream);
+
+// The root-mean-square norm and its gradients (ccr_norm.hip).  Per rank, device
+// pointers; y, q and rstd may be NULL.
+struct NormArgs {
+  const char* x[kRingHopMaxRanks];
+  const char* res[kRingHopMaxRanks];
+  const char* w[kRingHopMaxRanks];
+  char* h[kRingHopMaxRanks];
+  char* y[kRingHopMaxRanks];
+  char* q[kRingHopMaxRanks];
+  float* rstd[kRingHopMaxRanks];
+};
+struct NormBwdArgs {
+  const char* dy[kRingHopMaxRanks];
+  const char* h[kRingHopMaxRanks];
+  const char* w[kRingHopMaxRanks];
+  const char* dh[kRingHopMaxRanks];
+  const float* rstd[kRingHopMaxRanks];
+  char* dx[kRingHopMaxRanks];
+  float* dw[kRingHopMaxRanks];
+};
+static_assert(sizeof(NormArgs) <= 3584 && sizeof(NormBwdArgs) <= 3584, "fits the kernel argument segment");
+struct NormShape {
+  int R;
+  int64_t T, H;
+  int es, wes;      // bytes of a value of the rows and of the weight
+  bool add;         // a residual, or the gradient of h
+  float eps;        // norm
+  bool accumulate;  // gradients: add to what dw holds
+};
+hipError_t launch_norm(const NormArgs& a, const NormShape& n, hipStream_t stream);
+// Workgroups of a rank that sum dw, each with a slot of H values of the work array.
+constexpr int norm_slots(int R, int64_t T) {
+  const int most = 1024 / R;
+  return T < most ? (int)T : most;
+}
+hipError_t launch_norm_bwd(const NormBwdArgs& a, const NormShape& n, float* work, hipStream_t stream);
+
+// The router (ccr_route.hip).  Per rank, device pointers; bias, counts and sums
+// may be NULL.
+struct RouteArgs {
+  const float* logits[kRingHopMaxRanks];
+  const float* bias[kRingHopMaxRanks];
+  int32_t* topk[kRingHopMaxRanks];
+  float* weights[kRingHopMaxRanks];
+  int64_t* counts[kRingHopMaxRanks];
+  float* sums[kRingHopMaxRanks];
+};
+struct RouteBwdArgs {
+  const float* logits[kRingHopMaxRanks];
+  const int32_t* topk[kRingHopMaxRanks];
+  const float* dweights[kRingHopMaxRanks];
+  const float* dsums[kRingHopMaxRanks];  // may be NULL
+  float* dlogits[kRingHopMaxRanks];
+};
+struct RouteShape {
+  int R;
+  int64_t T;
+  int E, K, groups, kept, group_top;
+  bool sigmoid, renorm;
+  float scale;
+};
+constexpr int kRouteGroups = 64;  // at most
+// Workgroups of a rank that count, each with a slot of 2 E words of the work array.
+constexpr int route_slots(int R, int64_t T) {
+  const int64_t most = 1024 / R, of = (T + 15) / 16;
+  return (int)(of < most ? of : most);
+}
+hipError_t launch_route(const RouteArgs& a, const RouteShape& n, float* work, hipStream_t stream);
+hipError_t launch_route_bwd(const RouteBwdArgs& a, const RouteShape& n, hipStream_t stream);
 
 // The gradient norm and clipping (ccr_grad.hip).
 struct GradTensor {

@@ -1,0 +1,478 @@
+// Device kernels of the root-mean-square norm with the residual's addition, its
+// gradients, and 8-bit rows, written for gfx950 (CDNA4: wave64, 256 CUs in 8 XCDs,
+// HBM3E).
+//
+//   h = round(x + residual)             (x itself without a residual)
+//   r = 1 / sqrt(mean(h^2) + eps)
+//   y = h r w                           rounded once, to the rows' type or 8 bits
+//
+//   g = w dy,  hh = h r
+//   dx = r (g - hh mean(g hh)) + dh     rounded once
+//   dw = sum over rows of dy hh         fp32
+//
+// Every value is read once and written once: bound by HBM.  Squares are taken
+// and added in fp64 (no finite row overflows), everything else in fp32.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ccr_device.h"
+#include "ccr_internal.h"
+#include "ccr_rows.h"
+
+namespace ccr {
+namespace {
+
+using namespace dev;
+
+// The P weights of vector i.
+template <int P, int WES>
+__device__ __forceinline__ void load_weight(const char* w, int64_t i, float* f) {
+  if constexpr (P * WES == 16) {
+    unpack<WES>(reinterpret_cast<const u32x4*>(w)[i], f);
+  } else if constexpr (P * WES == 32) {  // bf16 rows, fp32 weights
+    unpack<4>(reinterpret_cast<const u32x4*>(w)[2 * i], f);
+    unpack<4>(reinterpret_cast<const u32x4*>(w)[2 * i + 1], f + 4);
+  } else {  // fp32 rows, bf16 weights
+    const u32x2 v = reinterpret_cast<const u32x2*>(w)[i];
+    f[0] = bf16_lo(v[0]);
+    f[1] = bf16_hi(v[0]);
+    f[2] = bf16_lo(v[1]);
+    f[3] = bf16_hi(v[1]);
+  }
+}
+
+// One lane's part of an 8-bit row: the P values of vector i (all lanes of a
+// block take part, those past the row's end with zeros).
+template <int P>
+__device__ __forceinline__ void store_q8(char* q, int64_t i, int64_t values, const float* f) {
+  uint32_t bytes[P / 4];
+  int scale;
+  q8_pack<P>(f, bytes, &scale);
+  if (i * P >= values) return;
+  if constexpr (P == 8) *reinterpret_cast<u32x2*>(q + i * 8) = u32x2{bytes[0], bytes[1]};
+  else *reinterpret_cast<uint32_t*>(q + i * 4) = bytes[0];
+  if (i % (32 / P) == 0) q[values + i / (32 / P)] = (char)scale;
+}
+
+// The zeros behind an 8-bit row's scales.
+template <int TPR>
+__device__ __forceinline__ void pad_q8(char* q, int64_t values, int64_t row_bytes, int thread) {
+  const int64_t from = values + values / 32;
+  for (int64_t i = from + thread * 4; i < row_bytes; i += TPR * 4) *reinterpret_cast<uint32_t*>(q + i) = 0;
+}
+
+// A row per TPR threads (a wave, or the workgroup), NV vectors of it in each
+// thread's registers; NV = 0: a row of any length, read twice.
+template <int ES, int WES, int TPR, int NV, bool ADD>
+__global__ __launch_bounds__(kBlock) void norm_kernel(const NormArgs a, int64_t T, int64_t vpr, int64_t values,
+                                                      int64_t q_bytes, float H, float eps,
+                                                      int64_t blocks_per_rank) {
+  constexpr int P = kPer<ES>, kRows = kBlock / TPR;
+  __shared__ double part[kBlock / 64];
+  const int rank = (int)(blockIdx.x / blocks_per_rank);
+  const int tid = TPR == kBlock ? threadIdx.x : threadIdx.x % TPR;
+  const int64_t t = (blockIdx.x % blocks_per_rank) * kRows + (TPR == kBlock ? 0 : threadIdx.x / TPR);
+  if (t >= T) return;  // uniform over the threads of a row
+  const u32x4* x = reinterpret_cast<const u32x4*>(a.x[rank]) + t * vpr;
+  const u32x4* res = ADD ? reinterpret_cast<const u32x4*>(a.res[rank]) + t * vpr : nullptr;
+  u32x4* h = ADD ? reinterpret_cast<u32x4*>(a.h[rank]) + t * vpr : nullptr;
+  u32x4* y = a.y[rank] ? reinterpret_cast<u32x4*>(a.y[rank]) + t * vpr : nullptr;
+  char* q = a.q[rank] ? a.q[rank] + t * q_bytes : nullptr;
+  const char* w = a.w[rank];
+  double sum = 0;
+  auto joined = [&](int64_t i) {  // vector i of h
+    u32x4 v = x[i];
+    if constexpr (ADD) {
+      if constexpr (ES == 4) v = add_f32x4(v, res[i]);
+      else v = add_bf16x8(v, res[i]);
+    }
+    return v;
+  };
+  auto squares = [&](u32x4 v) {
+    float f[P];
+    unpack<ES>(v, f);
+#pragma unroll
+    for (int j = 0; j < P; j++) sum = __builtin_fma((double)f[j], (double)f[j], sum);
+  };
+  auto finish = [&]() {
+    if constexpr (TPR == kBlock) sum = block_sum(sum, part);
+    else sum = wave_sum(sum);
+    // in fp64, where the mean of any finite values has a root
+    return (float)(1.0 / sqrt(sum / (double)H + (double)eps));
+  };
+  auto emit = [&](int64_t i, u32x4 v, float r) {  // of every vector up to the 8-bit row's end
+    float f[P], g[P];
+    if (i < vpr) {
+      unpack<ES>(v, f);
+      load_weight<P, WES>(w, i, g);
+    }
+#pragma unroll
+    for (int j = 0; j < P; j++) f[j] = i < vpr ? f[j] * r * g[j] : 0.0f;
+    if (y && i < vpr) y[i] = pack<ES>(f);
+    if (q) store_q8<P>(q, i, values, f);
+  };
+  float r;
+  const int64_t end = q ? values / P : vpr;
+  if constexpr (NV > 0) {
+    u32x4 v[NV];
+#pragma unroll
+    for (int n = 0; n < NV; n++) {
+      const int64_t i = tid + n * TPR;
+      v[n] = i < vpr ? joined(i) : u32x4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int n = 0; n < NV; n++) {
+      const int64_t i = tid + n * TPR;
+      if (ADD && i < vpr) h[i] = v[n];
+      squares(v[n]);
+    }
+    r = finish();
+#pragma unroll
+    for (int n = 0; n < NV; n++)
+      if (n * TPR < end) emit(tid + n * TPR, v[n], r);
+  } else {
+    for (int64_t i = tid; i < vpr; i += TPR) {
+      const u32x4 v = joined(i);
+      if (ADD) h[i] = v;
+      squares(v);
+    }
+    r = finish();
+    const u32x4* from = ADD ? h : x;
+    for (int64_t n = 0; n < end; n += TPR) {
+      const int64_t i = n + tid;
+      emit(i, i < vpr ? from[i] : u32x4{0, 0, 0, 0}, r);
+    }
+  }
+  if (q) pad_q8<TPR>(q, values, q_bytes, tid);
+  if (a.rstd[rank] && tid == 0) a.rstd[rank][t] = r;
+}
+
+// ---------------------------------------------------------------- backward
+// Every workgroup takes every slots-th row (or, of short rows, every slots-th
+// four) of its rank, so that it can add up dw in its registers; what it has
+// goes to its slot of the work array, and norm_dw_kernel adds the slots.
+template <int ES, int WES, int TPR, int NV, bool ADD>
+__global__ __launch_bounds__(kBlock) void norm_bwd_kernel(const NormBwdArgs a, int64_t T, int64_t vpr, float H,
+                                                          int slots, float* work) {
+  constexpr int P = kPer<ES>, kRows = kBlock / TPR;
+  __shared__ float part[2][kBlock / 64];
+  __shared__ float wave_dw[TPR == kBlock ? 1 : kRows][TPR == kBlock ? 1 : TPR * NV * P];
+  const int rank = blockIdx.x / slots, slot = blockIdx.x % slots;
+  const int tid = TPR == kBlock ? threadIdx.x : threadIdx.x % TPR;
+  const int sub = TPR == kBlock ? 0 : threadIdx.x / TPR;
+  const u32x4* dy = reinterpret_cast<const u32x4*>(a.dy[rank]);
+  const u32x4* h = reinterpret_cast<const u32x4*>(a.h[rank]);
+  const u32x4* dh = reinterpret_cast<const u32x4*>(a.dh[rank]);
+  u32x4* dx = reinterpret_cast<u32x4*>(a.dx[rank]);
+  const float* rstd = a.rstd[rank];
+  float w[NV][P], dw[NV][P];
+#pragma unroll
+  for (int n = 0; n < NV; n++) {
+    const int64_t i = tid + n * TPR;
+#pragma unroll
+    for (int j = 0; j < P; j++) w[n][j] = dw[n][j] = 0.0f;
+    if (i < vpr) load_weight<P, WES>(a.w[rank], i, w[n]);
+  }
+  int turn = 0;
+  for (int64_t t = (int64_t)slot * kRows + sub; t < T; t += (int64_t)slots * kRows) {
+    u32x4 vd[NV], vh[NV], ve[NV];
+#pragma unroll
+    for (int n = 0; n < NV; n++) {
+      const int64_t i = tid + n * TPR;
+      if (i < vpr) {
+        vd[n] = dy[t * vpr + i];
+        vh[n] = h[t * vpr + i];
+        if (ADD) ve[n] = dh[t * vpr + i];
+      } else {
+        vd[n] = vh[n] = ve[n] = u32x4{0, 0, 0, 0};
+      }
+    }
+    const float r = rstd[t];
+    float s = 0;
+#pragma unroll
+    for (int n = 0; n < NV; n++) {
+      float d[P], f[P];
+      unpack<ES>(vd[n], d);
+      unpack<ES>(vh[n], f);
+#pragma unroll
+      for (int j = 0; j < P; j++) {
+        const float hh = f[j] * r;
+        s = __builtin_fmaf(w[n][j] * d[j], hh, s);
+        dw[n][j] = __builtin_fmaf(d[j], hh, dw[n][j]);
+      }
+    }
+    // two arrays in turn: a wave may be a row ahead of one that still reads
+    if constexpr (TPR == kBlock) s = block_sum(s, part[turn]);
+    else s = wave_sum(s);
+    turn ^= 1;
+    s /= H;
+#pragma unroll
+    for (int n = 0; n < NV; n++) {
+      const int64_t i = tid + n * TPR;
+      float d[P], f[P], e[P], o[P];
+      unpack<ES>(vd[n], d);
+      unpack<ES>(vh[n], f);
+      if (ADD) unpack<ES>(ve[n], e);
+#pragma unroll
+      for (int j = 0; j < P; j++) {
+        o[j] = r * (w[n][j] * d[j] - f[j] * r * s);
+        if (ADD) o[j] += e[j];
+      }
+      if (i < vpr) dx[t * vpr + i] = pack<ES>(o);
+    }
+  }
+  float* out = work + (int64_t)blockIdx.x * vpr * P;
+  if constexpr (TPR == kBlock) {
+#pragma unroll
+    for (int n = 0; n < NV; n++) {
+      const int64_t i = tid + n * TPR;
+      if (i >= vpr) continue;
+#pragma unroll
+      for (int j = 0; j < P; j += 4)
+        *reinterpret_cast<f32x4*>(out + i * P + j) = f32x4{dw[n][j], dw[n][j + 1], dw[n][j + 2], dw[n][j + 3]};
+    }
+  } else {
+#pragma unroll
+    for (int n = 0; n < NV; n++)
+#pragma unroll
+      for (int j = 0; j < P; j++) wave_dw[sub][(tid + n * TPR) * P + j] = dw[n][j];
+    __syncthreads();
+    for (int64_t c = threadIdx.x; c < vpr * P; c += kBlock) {
+      float v = 0;
+#pragma unroll
+      for (int k = 0; k < kRows; k++) v += wave_dw[k][c];
+      out[c] = v;
+    }
+  }
+}
+
+// Rows of any length: dx in two passes over a row, a workgroup to each.
+template <int ES, int WES, bool ADD>
+__global__ __launch_bounds__(kBlock) void norm_bwd_long_kernel(const NormBwdArgs a, int64_t T, int64_t vpr,
+                                                               float H) {
+  constexpr int P = kPer<ES>;
+  __shared__ float part[kBlock / 64];
+  const int rank = (int)(blockIdx.x / T);
+  const int64_t t = blockIdx.x % T;
+  const u32x4* dy = reinterpret_cast<const u32x4*>(a.dy[rank]) + t * vpr;
+  const u32x4* h = reinterpret_cast<const u32x4*>(a.h[rank]) + t * vpr;
+  const u32x4* dh = ADD ? reinterpret_cast<const u32x4*>(a.dh[rank]) + t * vpr : nullptr;
+  u32x4* dx = reinterpret_cast<u32x4*>(a.dx[rank]) + t * vpr;
+  const float r = a.rstd[rank][t];
+  float s = 0;
+  for (int64_t i = threadIdx.x; i < vpr; i += kBlock) {
+    float d[P], f[P], w[P];
+    unpack<ES>(dy[i], d);
+    unpack<ES>(h[i], f);
+    load_weight<P, WES>(a.w[rank], i, w);
+#pragma unroll
+    for (int j = 0; j < P; j++) s = __builtin_fmaf(w[j] * d[j], f[j] * r, s);
+  }
+  s = block_sum(s, part) / H;
+  for (int64_t i = threadIdx.x; i < vpr; i += kBlock) {
+    float d[P], f[P], w[P], e[P];
+    unpack<ES>(dy[i], d);
+    unpack<ES>(h[i], f);
+    load_weight<P, WES>(a.w[rank], i, w);
+    if (ADD) unpack<ES>(dh[i], e);
+    float o[P];
+#pragma unroll
+    for (int j = 0; j < P; j++) {
+      o[j] = r * (w[j] * d[j] - f[j] * r * s);
+      if (ADD) o[j] += e[j];
+    }
+    dx[i] = pack<ES>(o);
+  }
+}
+
+// ... and their dw: a workgroup takes kBlock vectors of every slots-th row.
+template <int ES>
+__global__ __launch_bounds__(kBlock) void norm_dw_long_kernel(const NormBwdArgs a, int64_t T, int64_t vpr,
+                                                              int slots, float* work) {
+  constexpr int P = kPer<ES>;
+  const int rank = blockIdx.x / slots, slot = blockIdx.x % slots;
+  const int64_t i = (int64_t)blockIdx.y * kBlock + threadIdx.x;
+  if (i >= vpr) return;
+  const u32x4* dy = reinterpret_cast<const u32x4*>(a.dy[rank]);
+  const u32x4* h = reinterpret_cast<const u32x4*>(a.h[rank]);
+  float dw[P] = {};
+  for (int64_t t = slot; t < T; t += slots) {
+    const float r = a.rstd[rank][t];
+    float d[P], f[P];
+    unpack<ES>(dy[t * vpr + i], d);
+    unpack<ES>(h[t * vpr + i], f);
+#pragma unroll
+    for (int j = 0; j < P; j++) dw[j] = __builtin_fmaf(d[j], f[j] * r, dw[j]);
+  }
+  float* out = work + ((int64_t)blockIdx.x * vpr + i) * P;
+#pragma unroll
+  for (int j = 0; j < P; j++) out[j] = dw[j];
+}
+
+// dw (+)= the slots' sums, in the slots' order: a workgroup takes 64 columns, a
+// wave of it every fourth slot.
+__global__ __launch_bounds__(kBlock) void norm_dw_kernel(const NormBwdArgs a, const float* work, int slots,
+                                                         int64_t H, bool add) {
+  __shared__ float part[kBlock / 64][64];
+  const int rank = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  const float* from = work + (int64_t)rank * slots * H;
+  float s = 0;
+  if (c < H)
+    for (int k = wave; k < slots; k += kBlock / 64) s += from[k * H + c];
+  part[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < H) {
+    float v = add ? a.dw[rank][c] : 0.0f;
+    float sum = 0;
+#pragma unroll
+    for (int k = 0; k < kBlock / 64; k++) sum += part[k][lane];
+    a.dw[rank][c] = v + sum;
+  }
+}
+
+// -------------------------------------------------------------- 8-bit rows
+// A wave takes 64 vectors of the padded row, whatever the row's length.
+template <int ES>
+__global__ __launch_bounds__(kBlock) void quantize_kernel(const Q8Args a, int R, int64_t vpr, int64_t values,
+                                                          int64_t q_bytes, int64_t chunks) {
+  constexpr int P = kPer<ES>;
+  const int64_t unit = (int64_t)blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6);
+  int rank = 0;
+  while (rank < R && unit >= a.first[rank + 1] * chunks) rank++;
+  if (rank == R) return;
+  const int64_t k = unit - a.first[rank] * chunks, t = k / chunks;
+  const int64_t i = (k % chunks) * 64 + (threadIdx.x & 63);
+  const u32x4* x = reinterpret_cast<const u32x4*>(a.rows[rank]) + t * vpr;
+  char* q = a.q[rank] + t * q_bytes;
+  float f[P] = {};
+  if (i < vpr) unpack<ES>(x[i], f);
+  store_q8<P>(q, i, values, f);
+  if (k % chunks == chunks - 1) pad_q8<64>(q, values, q_bytes, threadIdx.x & 63);
+}
+
+// A thread expands 16 bytes.
+template <int ES>
+__global__ __launch_bounds__(kBlock) void dequantize_kernel(const Q8Args a, int R, int64_t H, int64_t values,
+                                                            int64_t q_bytes, int64_t chunks) {
+  const int64_t unit = (int64_t)blockIdx.x * kBlock + threadIdx.x;
+  int rank = 0;
+  while (rank < R && unit >= a.first[rank + 1] * chunks) rank++;
+  if (rank == R) return;
+  const int64_t k = unit - a.first[rank] * chunks, t = k / chunks, i = k % chunks;
+  const char* q = a.q[rank] + t * q_bytes;
+  const u32x4 v = *reinterpret_cast<const u32x4*>(q + i * 16);
+  const float s = q8_factor((uint8_t)q[values + i / 2]);
+  char* y = const_cast<char*>(a.rows[rank]) + (t * H + i * 16) * ES;
+  float f[16];
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)v[j], false);
+    const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)v[j], true);
+    f[4 * j] = lo[0] * s;
+    f[4 * j + 1] = lo[1] * s;
+    f[4 * j + 2] = hi[0] * s;
+    f[4 * j + 3] = hi[1] * s;
+  }
+  constexpr int P = kPer<ES>;
+#pragma unroll
+  for (int j = 0; j < 16 / P; j++)  // rows are whole vectors
+    if (i * 16 + j * P < H) reinterpret_cast<u32x4*>(y)[j] = pack<ES>(f + j * P);
+}
+
+template <int ES, int WES, int TPR, int NV>
+hipError_t launch_norm_as(const NormArgs& a, const NormShape& n, hipStream_t stream) {
+  constexpr int kRows = kBlock / TPR;
+  const int64_t vpr = n.H * ES >> 4, per_rank = (n.T + kRows - 1) / kRows;
+  if (per_rank * n.R > kMaxGridWorkgroups) return hipErrorInvalidValue;
+  const unsigned grid = (unsigned)(per_rank * n.R);
+  const int64_t values = q8_values(n.H), row = q8_row_bytes(n.H);
+  if (n.add)
+    norm_kernel<ES, WES, TPR, NV, true><<<grid, kBlock, 0, stream>>>(a, n.T, vpr, values, row, (float)n.H, n.eps, per_rank);
+  else
+    norm_kernel<ES, WES, TPR, NV, false><<<grid, kBlock, 0, stream>>>(a, n.T, vpr, values, row, (float)n.H, n.eps, per_rank);
+  return hipGetLastError();
+}
+
+// Vectors that a row's registers have to hold: up to the end of the 8-bit row
+// where there is one.
+template <int ES, int WES>
+hipError_t launch_norm_w(const NormArgs& a, const NormShape& n, hipStream_t stream) {
+  const int64_t v = q8_values(n.H) * ES >> 4;
+  if (v <= 64) return launch_norm_as<ES, WES, 64, 1>(a, n, stream);
+  if (v <= kBlock) return launch_norm_as<ES, WES, kBlock, 1>(a, n, stream);
+  if (v <= 2 * kBlock) return launch_norm_as<ES, WES, kBlock, 2>(a, n, stream);
+  if (v <= 4 * kBlock) return launch_norm_as<ES, WES, kBlock, 4>(a, n, stream);
+  if (v <= 8 * kBlock) return launch_norm_as<ES, WES, kBlock, 8>(a, n, stream);
+  return launch_norm_as<ES, WES, kBlock, 0>(a, n, stream);
+}
+
+template <int ES, int WES, int TPR, int NV>
+hipError_t launch_norm_bwd_as(const NormBwdArgs& a, const NormShape& n, float* work, hipStream_t stream) {
+  const int64_t vpr = n.H * ES >> 4;
+  const int slots = norm_slots(n.R, n.T);
+  const unsigned grid = (unsigned)(slots * n.R);
+  if constexpr (NV > 0) {
+    if (n.add)
+      norm_bwd_kernel<ES, WES, TPR, NV, true><<<grid, kBlock, 0, stream>>>(a, n.T, vpr, (float)n.H, slots, work);
+    else
+      norm_bwd_kernel<ES, WES, TPR, NV, false><<<grid, kBlock, 0, stream>>>(a, n.T, vpr, (float)n.H, slots, work);
+  } else {
+    if (n.T * n.R > kMaxGridWorkgroups) return hipErrorInvalidValue;
+    if (n.add)
+      norm_bwd_long_kernel<ES, WES, true><<<(unsigned)(n.T * n.R), kBlock, 0, stream>>>(a, n.T, vpr, (float)n.H);
+    else
+      norm_bwd_long_kernel<ES, WES, false><<<(unsigned)(n.T * n.R), kBlock, 0, stream>>>(a, n.T, vpr, (float)n.H);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    norm_dw_long_kernel<ES><<<dim3(grid, (unsigned)((vpr + kBlock - 1) / kBlock)), kBlock, 0, stream>>>(
+        a, n.T, vpr, slots, work);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  norm_dw_kernel<<<dim3((unsigned)((n.H + 63) / 64), n.R), kBlock, 0, stream>>>(a, work, slots, n.H, n.accumulate);
+  return hipGetLastError();
+}
+
+template <int ES, int WES>
+hipError_t launch_norm_bwd_w(const NormBwdArgs& a, const NormShape& n, float* work, hipStream_t stream) {
+  const int64_t v = n.H * ES >> 4;
+  if (v <= 64) return launch_norm_bwd_as<ES, WES, 64, 1>(a, n, work, stream);
+  if (v <= kBlock) return launch_norm_bwd_as<ES, WES, kBlock, 1>(a, n, work, stream);
+  if (v <= 2 * kBlock) return launch_norm_bwd_as<ES, WES, kBlock, 2>(a, n, work, stream);
+  if (v <= 4 * kBlock) return launch_norm_bwd_as<ES, WES, kBlock, 4>(a, n, work, stream);
+  return launch_norm_bwd_as<ES, WES, kBlock, 0>(a, n, work, stream);
+}
+
+}  // namespace
+
+hipError_t launch_norm(const NormArgs& a, const NormShape& n, hipStream_t stream) {
+  if (n.es == 4) return n.wes == 4 ? launch_norm_w<4, 4>(a, n, stream) : launch_norm_w<4, 2>(a, n, stream);
+  return n.wes == 4 ? launch_norm_w<2, 4>(a, n, stream) : launch_norm_w<2, 2>(a, n, stream);
+}
+
+hipError_t launch_norm_bwd(const NormBwdArgs& a, const NormShape& n, float* work, hipStream_t stream) {
+  if (n.T == 0) {  // no slot: dw is 0
+    norm_dw_kernel<<<dim3((unsigned)((n.H + 63) / 64), n.R), kBlock, 0, stream>>>(a, work, 0, n.H, n.accumulate);
+    return hipGetLastError();
+  }
+  if (n.es == 4)
+    return n.wes == 4 ? launch_norm_bwd_w<4, 4>(a, n, work, stream) : launch_norm_bwd_w<4, 2>(a, n, work, stream);
+  return n.wes == 4 ? launch_norm_bwd_w<2, 4>(a, n, work, stream) : launch_norm_bwd_w<2, 2>(a, n, work, stream);
+}
+
+hipError_t launch_q8(bool to_q8, int es, const Q8Args& a, int R, int64_t H, hipStream_t stream) {
+  const int64_t rows = a.first[R], grid64 = q8_grid(to_q8, es, rows, H);
+  if (rows == 0) return hipSuccess;
+  if (grid64 > kMaxGridWorkgroups) return hipErrorInvalidValue;
+  const unsigned grid = (unsigned)grid64;
+  const int64_t vpr = H * es >> 4, values = q8_values(H), row = q8_row_bytes(H), chunks = q8_chunks(to_q8, es, H);
+  if (to_q8 && es == 4) quantize_kernel<4><<<grid, kBlock, 0, stream>>>(a, R, vpr, values, row, chunks);
+  else if (to_q8) quantize_kernel<2><<<grid, kBlock, 0, stream>>>(a, R, vpr, values, row, chunks);
+  else if (es == 4) dequantize_kernel<4><<<grid, kBlock, 0, stream>>>(a, R, H, values, row, chunks);
+  else dequantize_kernel<2><<<grid, kBlock, 0, stream>>>(a, R, H, values, row, chunks);
+  return hipGetLastError();
+}
+
+}  // namespace ccr

@@ -53,7 +53,8 @@
  *     and per-hop bf16, with or without slices or overlap; ccr_alltoall,
  *     ccr_alltoall_rows, ccr_moe_dispatch and ccr_moe_combine with kernel
  *     copies; ccr_permute_rows; ccr_moe_topk; the experts' products, the
- *     gated sum, ccr_grad_norm and ccr_grad_clip).  A replay reuses the device
+ *     gated sum, ccr_grad_norm and ccr_grad_clip; the norm, the router and
+ *     the 8-bit rows).  A replay reuses the device
  *     pointers given at capture time.  Calls that would depend on context
  *     scratch that may be reallocated, on host memory copied at launch, or
  *     on the DMA proxy (SDMA copies, fp32 partials, ccr_sendrecv,
@@ -62,8 +63,8 @@
  *     so does every call of a context with a CU budget, because a replay
  *     runs the captured kernels on the replaying stream's hardware queue,
  *     without the budget's CU mask.
- *   - The experts' products, the gated sum and the gradient calls are
- *     compute, not communication: like ccr_moe_topk they run on the caller's
+ *   - The experts' products, the gated sum, the gradient calls, the norm,
+ *     the router and the 8-bit rows are compute, not communication: like ccr_moe_topk they run on the caller's
  *     stream, whatever the context's CU budget, and keep no device state in
  *     the context.
  */
@@ -546,11 +547,16 @@ ccr_status_t ccr_moe_experts_wgrad(ccr_ctx_t ctx, const void *const *exp, const 
  *   written): the gradient through the softmax of g_k = <dy[r][t],
  *   rows[r][t, k]>.  An expert chosen twice by a token collects both parts.
  *
+ * CCR_GATE_GIVEN: logits[r] holds the weights themselves, fp32 [T x K], as
+ *   ccr_moe_route writes them; w_k = logits[r][t, k], and ccr_moe_gate_sum_bwd
+ *   writes their gradients g_k to dlogits[r] (fp32 [T x K], 0 for an absent
+ *   choice).  E only bounds the ids of topk.
+ *
  * Weights and sums are fp32; each result is rounded once.  dtype: of rows, y,
  * dy and drows.  1 <= E <= 1024, 1 <= K <= min(E, 16), H 1 .. 2^20 with rows a
  * multiple of 16 bytes, R x T < 2^24.  Written buffers must not overlap any other buffer.
  * ---------------------------------------------------------------------- */
-typedef enum { CCR_GATE_CHOSEN = 0, CCR_GATE_ALL = 1 } ccr_gate_norm_t;
+typedef enum { CCR_GATE_CHOSEN = 0, CCR_GATE_ALL = 1, CCR_GATE_GIVEN = 2 } ccr_gate_norm_t;
 ccr_status_t ccr_moe_gate_sum(ccr_ctx_t ctx, const void *const *rows, const float *const *logits,
                               const int32_t *const *topk, int R, int64_t T, int E, int K, int64_t H,
                               int dtype, int norm, void *const *y, void *stream);
@@ -558,6 +564,145 @@ ccr_status_t ccr_moe_gate_sum_bwd(ccr_ctx_t ctx, const void *const *dy, const vo
                                   const float *const *logits, const int32_t *const *topk, int R,
                                   int64_t T, int E, int K, int64_t H, int dtype, int norm,
                                   void *const *drows, float *const *dlogits, void *stream);
+
+/* ----------------------------------------------------------------------
+ * Rows of 8 bits, the form in which rows can cross the exchange at half their
+ * bytes (HOCCL §2.1: dispatch moves every token K times; the pages say nothing
+ * of 8 bits, so the format is that of the device's matrix instructions).  A row
+ * of H values is ccr_q8_row_bytes(H) bytes, a whole number of 128-byte lines:
+ *   H values of e4m3 (1 sign, 4 exponent, 3 mantissa bits; largest 448, no
+ *     infinity), then zeros up to V, the next multiple of 128;
+ *   V / 32 scale bytes, one for each 32 values: b stands for 2^(b - 127);
+ *   zeros to the end of the line.
+ * b is the smallest byte whose scale times 448 reaches the block's largest
+ * magnitude (0 for zeros), so nothing saturates, and each value is rounded once
+ * to the nearest multiple (ties to even).  A block with an infinity or a NaN gets
+ * b = 255 and stands for NaN.  Rows are plain bytes to the exchange: row_bytes =
+ * ccr_q8_row_bytes(H) in ccr_moe_dispatch, ccr_moe_dispatch_fused,
+ * ccr_alltoall_rows and ccr_permute_rows.
+ *
+ * ccr_q8_row_bytes: host only; 0 for H outside [1, 2^20].
+ * ccr_quantize_rows: q[r] row i = x[r] row i in 8 bits, for i < counts[r] (host
+ *   int64 [R], read during the call).
+ * ccr_dequantize_rows: y[r] row i = what q[r] row i stands for, rounded once to
+ *   dtype (exact but for values below 2^-126, and in bf16 below 2^-133 / 2).
+ * H: 1 .. 2^20 with rows of x and y a multiple of 16 bytes.  Written buffers
+ * must not overlap any other buffer.
+ * ---------------------------------------------------------------------- */
+int64_t ccr_q8_row_bytes(int64_t H);
+ccr_status_t ccr_quantize_rows(ccr_ctx_t ctx, const void *const *x, const int64_t *counts, int R,
+                               int64_t H, int dtype, void *const *q, void *stream);
+ccr_status_t ccr_dequantize_rows(ccr_ctx_t ctx, const void *const *q, const int64_t *counts, int R,
+                                 int64_t H, int dtype, void *const *y, void *stream);
+
+/* The experts' product on 8-bit rows and 8-bit weights: ccr_moe_experts with
+ * exp[d] rows, and w[d] [E/R x F] rows, of ccr_q8_row_bytes(H) bytes each, and
+ * out[d] rows of F bf16 values.  Every result is the sum of the products of what
+ * the rows stand for, kept in fp32 between matrix instructions and rounded
+ * once; inside an instruction the products of 16 neighbouring values are
+ * aligned to the largest of them and lose what lies 13 bits below it.  H: 1 ..
+ * 2^20; F: 1 .. 2^20, a multiple of 8.  Everything else as for ccr_moe_experts;
+ * the gradients of a layer that dispatched 8-bit rows are those of the rows that
+ * ccr_dequantize_rows gives. */
+ccr_status_t ccr_moe_experts_q8(ccr_ctx_t ctx, const void *const *exp, const void *const *w,
+                                const int64_t *h_ecnt, int R, int E, int64_t H, int64_t F,
+                                void *const *out, void *stream);
+
+/* ----------------------------------------------------------------------
+ * The root-mean-square norm in front of an expert-parallel layer (or behind a
+ * tensor-parallel all-reduce), with the residual's addition, and its gradients.
+ * Per rank r, rows of H values, T of them, and a weight w[r] [H] (the ranks may
+ * share one buffer).
+ *
+ * ccr_rms_norm: h[r][t] = x[r][t] + residual[r][t], rounded to dtype, or x[r][t]
+ *   where residual and h are NULL (they come together); rstd[r][t] = 1 /
+ *   sqrt(mean of the squares of h[r][t] + eps) (fp32 [T]; rstd may be NULL);
+ *   y[r][t] = h[r][t] rstd w[r], to y (dtype), to q (8-bit rows), or to both;
+ *   one of them may be NULL.  h[r] may be the buffer x[r] or residual[r].
+ * ccr_rms_norm_bwd: from dy[r] and the forward's h[r] (x[r] without a residual),
+ *   w[r] and rstd[r]: with hh = h rstd and g = dy w,
+ *     dx[r][t]       = rstd (g - hh mean(g hh)) + dh[r][t]
+ *     dw[r] (fp32 [H]) (+)= sum over t of dy hh
+ *   dh[r] is the gradient of h[r] from elsewhere (the residual stream; NULL:
+ *   none), and dx[r], which may be that buffer, the gradient of x and of the
+ *   residual alike.  accumulate = 1 adds to what dw holds.  The ranks' dw are
+ *   sums over their own rows: ccr_allreduce joins them.
+ *
+ * Squares are summed in fp64 (no finite row overflows), all else in fp32, each
+ * result is rounded once, and dw has the same bits on every run.  work: device
+ * fp32 [ccr_rms_norm_work(R, T, H)] (host only), the call's alone until it
+ * completes, contents of no meaning before and after: two calls that may run at
+ * the same time, captured graphs included, need one each.  H: 1 .. 2^20 with
+ * rows a multiple of 16 bytes; R x T < 2^24; w_dtype: of w, either; eps >= 0;
+ * rstd and dw need their elements' alignment only.  Written buffers must not
+ * overlap any other buffer, but for the two named above.  T = 0 writes dw
+ * alone.
+ * ---------------------------------------------------------------------- */
+int64_t ccr_rms_norm_work(int R, int64_t T, int64_t H);
+ccr_status_t ccr_rms_norm(ccr_ctx_t ctx, const void *const *x, const void *const *residual,
+                          const void *const *w, int R, int64_t T, int64_t H, int dtype, int w_dtype,
+                          float eps, void *const *h, void *const *y, void *const *q,
+                          float *const *rstd, void *stream);
+ccr_status_t ccr_rms_norm_bwd(ccr_ctx_t ctx, const void *const *dy, const void *const *h,
+                              const void *const *w, const float *const *rstd, const void *const *dh,
+                              int R, int64_t T, int64_t H, int dtype, int w_dtype, int accumulate,
+                              void *const *dx, float *const *dw, float *work, void *stream);
+
+/* ----------------------------------------------------------------------
+ * The router in front of the exchange (HOCCL §2.1: tokens are dispatched to the
+ * experts a gate chooses; the pages leave the gate open), and its gradient.  Per
+ * rank r, logits[r] (fp32 [T x E]) of its tokens; per token:
+ *   s      = softmax of the logits, or 1 / (1 + exp(-l)) of each (how->score);
+ *   key    = s + bias[r] (fp32 [E]; the ranks may share one buffer), and where
+ *            bias is NULL the logit, with which s grows;
+ *   groups of E / groups neighbouring experts (how->groups > 1): a group's value
+ *            is the largest of its keys (group_top = 1) or the sum of its two
+ *            largest (2; of scores where bias is NULL), and only the experts of
+ *            the kept_groups best ones stay, equal ones by number;
+ *   topk[r][t]    = the K experts of largest key, by decreasing key, equal ones
+ *            by number (int32 [T x K], as ccr_moe_plan takes it);
+ *   weights[r][t] = their s (not the key), divided by their sum if renorm, times
+ *            scale (fp32 [T x K], as ccr_moe_gate_sum takes them with
+ *            CCR_GATE_GIVEN).
+ * Keys are compared as if computed in 64 bits.  An expert whose logit is
+ * -infinity has s = 0 and is never chosen, and adds nothing to its group; where
+ * fewer than K can be chosen the last entries are -1 with weight 0.  A NaN key is
+ * above all others and shows in the weights.  A sum of 0 gives weights 0.
+ *   counts[r] (device int64 [E]; counts may be NULL): the tokens that chose e;
+ *   score_sums[r] (device fp32 [E]; may be NULL): the sum over the tokens of s_e,
+ *            from which a loss for balance is made.
+ * ccr_moe_route_bwd: dlogits[r] (fp32 [T x E], every entry written) from
+ *   dweights[r] (fp32 [T x K]) at the choices topk[r] and dscore_sums[r] (fp32
+ *   [E]; dscore_sums may be NULL).  Choices themselves have no gradient, nor has
+ *   the bias.  An id outside [0, E) or of a logit of -infinity is absent: its
+ *   dweights are not used.
+ *
+ * work: device fp32 [ccr_moe_route_work(R, T, E)] (host only), needed for counts
+ * and score_sums (else it may be NULL), the call's alone until it completes:
+ * two calls that may run at the same time need one each.  1 <= E <= 1024, 1 <= K
+ * <= min(E, 16) and at most the experts of the kept groups, 1 <= groups <= 64
+ * dividing E, R x T < 2^24, scale finite.  Buffers but work need their elements'
+ * alignment only; written ones must not overlap any other.  T = 0 writes counts
+ * and score_sums alone.
+ * ---------------------------------------------------------------------- */
+typedef enum { CCR_SCORE_SOFTMAX = 0, CCR_SCORE_SIGMOID = 1 } ccr_score_t;
+typedef struct {
+    int32_t score;       /* ccr_score_t */
+    int32_t groups;      /* 1: none */
+    int32_t kept_groups;
+    int32_t group_top;   /* 1 or 2 */
+    int32_t renorm;      /* 0 or 1 */
+    float scale;
+} ccr_route_t;
+int64_t ccr_moe_route_work(int R, int64_t T, int E);
+ccr_status_t ccr_moe_route(ccr_ctx_t ctx, const float *const *logits, const float *const *bias, int R,
+                           int64_t T, int E, int K, const ccr_route_t *how, int32_t *const *topk,
+                           float *const *weights, int64_t *const *counts, float *const *score_sums,
+                           float *work, void *stream);
+ccr_status_t ccr_moe_route_bwd(ccr_ctx_t ctx, const float *const *logits, const int32_t *const *topk,
+                               const float *const *dweights, const float *const *dscore_sums, int R,
+                               int64_t T, int E, int K, int score, int renorm, float scale,
+                               float *const *dlogits, void *stream);
 
 /* ----------------------------------------------------------------------
  * The global norm of gradients and clipping, after the bucket's all-reduce
