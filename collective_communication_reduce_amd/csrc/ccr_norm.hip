@@ -174,27 +174,45 @@ __global__ __launch_bounds__(kBlock) void norm_bwd_kernel(const NormBwdArgs a, i
     for (int j = 0; j < P; j++) w[n][j] = dw[n][j] = 0.0f;
     if (i < vpr) load_weight<P, WES>(a.w[rank], i, w[n]);
   }
-  int turn = 0;
-  for (int64_t t = (int64_t)slot * kRows + sub; t < T; t += (int64_t)slots * kRows) {
-    u32x4 vd[NV], vh[NV], ve[NV];
+  // A row is loaded while the one before is summed: short rows leave the
+  // registers for it.
+  constexpr bool kAhead = NV <= 2;
+  struct Row {
+    u32x4 d[NV], h[NV], e[NV];
+    float r;
+  };
+  auto load = [&](int64_t t, Row& x) {
 #pragma unroll
     for (int n = 0; n < NV; n++) {
       const int64_t i = tid + n * TPR;
-      if (i < vpr) {
-        vd[n] = dy[t * vpr + i];
-        vh[n] = h[t * vpr + i];
-        if (ADD) ve[n] = dh[t * vpr + i];
-      } else {
-        vd[n] = vh[n] = ve[n] = u32x4{0, 0, 0, 0};
+      x.d[n] = x.h[n] = x.e[n] = u32x4{0, 0, 0, 0};
+      if (t < T && i < vpr) {
+        x.d[n] = dy[t * vpr + i];
+        x.h[n] = h[t * vpr + i];
+        if (ADD) x.e[n] = dh[t * vpr + i];
       }
     }
-    const float r = rstd[t];
+    x.r = t < T ? rstd[t] : 0.0f;
+  };
+  int turn = 0;
+  const int64_t step = (int64_t)slots * kRows;
+  int64_t t = (int64_t)slot * kRows + sub;
+  Row x, next;
+  if (kAhead) load(t, next);
+  for (; t < T; t += step) {
+    if (kAhead) {
+      x = next;
+      load(t + step, next);
+    } else {
+      load(t, x);
+    }
+    const float r = x.r;
     float s = 0;
 #pragma unroll
     for (int n = 0; n < NV; n++) {
       float d[P], f[P];
-      unpack<ES>(vd[n], d);
-      unpack<ES>(vh[n], f);
+      unpack<ES>(x.d[n], d);
+      unpack<ES>(x.h[n], f);
 #pragma unroll
       for (int j = 0; j < P; j++) {
         const float hh = f[j] * r;
@@ -211,9 +229,9 @@ __global__ __launch_bounds__(kBlock) void norm_bwd_kernel(const NormBwdArgs a, i
     for (int n = 0; n < NV; n++) {
       const int64_t i = tid + n * TPR;
       float d[P], f[P], e[P], o[P];
-      unpack<ES>(vd[n], d);
-      unpack<ES>(vh[n], f);
-      if (ADD) unpack<ES>(ve[n], e);
+      unpack<ES>(x.d[n], d);
+      unpack<ES>(x.h[n], f);
+      if (ADD) unpack<ES>(x.e[n], e);
 #pragma unroll
       for (int j = 0; j < P; j++) {
         o[j] = r * (w[n][j] * d[j] - f[j] * r * s);
@@ -310,25 +328,33 @@ __global__ __launch_bounds__(kBlock) void norm_dw_long_kernel(const NormBwdArgs 
   for (int j = 0; j < P; j++) out[j] = dw[j];
 }
 
-// dw (+)= the slots' sums, in the slots' order: a workgroup takes 64 columns, a
-// wave of it every fourth slot.
-__global__ __launch_bounds__(kBlock) void norm_dw_kernel(const NormBwdArgs a, const float* work, int slots,
-                                                         int64_t H, bool add) {
-  __shared__ float part[kBlock / 64][64];
-  const int rank = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
-  const float* from = work + (int64_t)rank * slots * H;
-  float s = 0;
+// dw (+)= the slots' sums, in a fixed order: a workgroup takes 64 columns, 16
+// threads (four columns each) to a slot.
+constexpr int kDwBlock = 1024;
+__global__ __launch_bounds__(kDwBlock) void norm_dw_kernel(const NormBwdArgs a, const float* work, int slots,
+                                                           int64_t H, bool add) {
+  constexpr int kWaves = kDwBlock / 64;
+  __shared__ f32x4 part[kWaves][16];
+  const int rank = blockIdx.y, col = threadIdx.x & 15, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + col * 4;
+  const float* from = work + (int64_t)rank * slots * H + c;
+  f32x4 s = {0, 0, 0, 0};
   if (c < H)
-    for (int k = wave; k < slots; k += kBlock / 64) s += from[k * H + c];
-  part[wave][lane] = s;
-  __syncthreads();
-  if (wave == 0 && c < H) {
-    float v = add ? a.dw[rank][c] : 0.0f;
-    float sum = 0;
+#pragma unroll 4
+    for (int k = threadIdx.x >> 4; k < slots; k += kDwBlock / 16) s += *reinterpret_cast<const f32x4*>(from + k * H);
 #pragma unroll
-    for (int k = 0; k < kBlock / 64; k++) sum += part[k][lane];
-    a.dw[rank][c] = v + sum;
+  for (int off = 16; off <= 32; off <<= 1)
+#pragma unroll
+    for (int j = 0; j < 4; j++) s[j] += __shfl_xor(s[j], off);
+  if ((threadIdx.x & 63) < 16) part[wave][col] = s;
+  __syncthreads();
+  if (threadIdx.x < 16 && c < H) {
+    s = part[0][col];
+#pragma unroll
+    for (int k = 1; k < kWaves; k++) s += part[k][col];
+    float* dw = a.dw[rank] + c;  // of a float's alignment
+#pragma unroll
+    for (int j = 0; j < 4; j++) dw[j] = add ? dw[j] + s[j] : s[j];
   }
 }
 
@@ -431,7 +457,7 @@ hipError_t launch_norm_bwd_as(const NormBwdArgs& a, const NormShape& n, float* w
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  norm_dw_kernel<<<dim3((unsigned)((n.H + 63) / 64), n.R), kBlock, 0, stream>>>(a, work, slots, n.H, n.accumulate);
+  norm_dw_kernel<<<dim3((unsigned)((n.H + 63) / 64), n.R), kDwBlock, 0, stream>>>(a, work, slots, n.H, n.accumulate);
   return hipGetLastError();
 }
 
@@ -454,7 +480,7 @@ hipError_t launch_norm(const NormArgs& a, const NormShape& n, hipStream_t stream
 
 hipError_t launch_norm_bwd(const NormBwdArgs& a, const NormShape& n, float* work, hipStream_t stream) {
   if (n.T == 0) {  // no slot: dw is 0
-    norm_dw_kernel<<<dim3((unsigned)((n.H + 63) / 64), n.R), kBlock, 0, stream>>>(a, work, 0, n.H, n.accumulate);
+    norm_dw_kernel<<<dim3((unsigned)((n.H + 63) / 64), n.R), kDwBlock, 0, stream>>>(a, work, 0, n.H, n.accumulate);
     return hipGetLastError();
   }
   if (n.es == 4)

@@ -28,21 +28,41 @@ namespace {
 
 constexpr float kNegInf = -__builtin_inff();
 
-// Over the LPT neighbouring lanes that share a token (16: a row of the wave's
-// lanes, by its own exchanges; 64: the wave).
-template <int LPT, typename T, typename F>
+// Over the LPT neighbouring lanes that share a token, every lane's own result.
+// Within a row of 16 lanes the exchanges are operands of the operation (quads,
+// then halves and the row mirrored: after each step the lanes below it agree, so
+// a mirror image is as good as any other lane of the other half).  As LDS
+// permutes the router of 256 experts took twice as long.
+template <int CTRL, typename T>
+__device__ __forceinline__ T across(T x) {
+  return __builtin_bit_cast(T, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+template <int N, typename T, typename F>
 __device__ __forceinline__ T reduce(T x, F&& f) {
+  if constexpr (sizeof(T) == 4) {
+    if constexpr (N > 1) x = f(x, across<0xb1>(x));
+    if constexpr (N > 2) x = f(x, across<0x4e>(x));
+    if constexpr (N > 4) x = f(x, across<0x141>(x));
+    if constexpr (N > 8) x = f(x, across<0x140>(x));
+    if constexpr (N > 16) x = f(x, __shfl_xor(x, 16));
+    if constexpr (N > 32) x = f(x, __shfl_xor(x, 32));
+  } else {
 #pragma unroll
-  for (int off = 1; off < LPT; off <<= 1) x = f(x, __shfl_xor(x, off));
+    for (int off = 1; off < N; off <<= 1) x = f(x, __shfl_xor(x, off));
+  }
   return x;
 }
-template <int LPT, typename T>
+template <int N, typename T>
 __device__ __forceinline__ T sum_of(T x) {
-  return reduce<LPT>(x, [](T a, T b) { return a + b; });
+  return reduce<N>(x, [](T a, T b) { return a + b; });
 }
-template <int LPT, typename T>
+template <int N, typename T>
 __device__ __forceinline__ T max_of(T x) {
-  return reduce<LPT>(x, [](T a, T b) { return a > b ? a : b; });
+  return reduce<N>(x, [](T a, T b) { return a > b ? a : b; });
+}
+template <int N, typename T>
+__device__ __forceinline__ T min_of(T x) {
+  return reduce<N>(x, [](T a, T b) { return a < b ? a : b; });
 }
 
 // Keys in the order of their values: larger numbers for larger values, NaN
@@ -106,72 +126,76 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Where a wave's tokens keep keys and group values while groups are chosen.
-template <int LPT, int J>
-struct GroupRoom {
-  static constexpr int kTok = 64 / LPT;
-  double key[kTok][LPT * J];
-  double value[kTok][kRouteGroups];
-  uint8_t keep[kTok][kRouteGroups];
+constexpr uint32_t kNone = 0xffffffffu;  // no choice
+
+// Where the experts of a token lie: group g's on the lanes g q .. g q + q - 1, J
+// neighbours to a lane (without groups, one group on all lanes).  A lane's place
+// is where it would be if every lane held J.
+struct Layout {
+  int eg, q;  // experts of a group, lanes of a group (a power of two)
 };
 
-struct Chosen {
-  int32_t id;
-  float s;
-};
-
-// One round of choosing for the wave's tokens; T: the arithmetic of the keys.
-// Lane k of a token ends with its k-th choice (id -1: none left).  Returns
-// whether any decision of the lane's token was nearer than `tol` (T = float).
-template <int LPT, int J, bool GROUPS, typename T>
-__device__ __forceinline__ bool choose(const float* l, const float* s32, const float* bias, bool with_bias,
-                                       const RouteShape& n, GroupRoom<LPT, J>* room, Chosen (*out)[16],
-                                       bool* taken) {
-  using U = decltype(ordered(T(0)));
-  constexpr bool kExact = sizeof(T) == 8;
-  const int sub = threadIdx.x % LPT, tok = (threadIdx.x & 63) / LPT;
-  const uint64_t mine = (LPT == 64 ? ~0ull : ((1ull << (LPT & 63)) - 1)) << (tok * LPT);
-  T s[J];
-  const bool need = with_bias || (GROUPS && n.group_top == 2);
-  if constexpr (kExact) {
-    if (need) scores<LPT, J, T>(l, n.sigmoid, s);
+// J values from p, the first n of them (the others: none).  Rows of logits need
+// not be aligned to more than a value.
+template <int J>
+__device__ __forceinline__ void load_some(const float* p, int n, float none, float* v) {
+  struct Four {
+    float f[4];
+  };
+  if (n >= J) {
+#pragma unroll
+    for (int j = 0; j < J; j += 4) {
+      Four x;
+      __builtin_memcpy(&x, p + j, 16);
+#pragma unroll
+      for (int i = 0; i < 4; i++) v[j + i] = x.f[i];
+    }
   } else {
 #pragma unroll
-    for (int j = 0; j < J; j++) s[j] = s32[j];
+    for (int j = 0; j < J; j++) v[j] = j < n ? p[j] : none;
   }
-  T v[J];
+}
+
+// ------------------------------------------------------------ 64 bits, exactly
+// One token's choice by a whole wave, keys in fp64.
+template <int E>
+struct ExactRoom {
+  double key[E];
+  double value[kRouteGroups];
+  uint8_t keep[kRouteGroups];
+};
+
+template <int J, bool GROUPS>
+__device__ __forceinline__ void choose_exactly(const float* logits, const float* bias, const RouteShape& n,
+                                            ExactRoom<GROUPS ? 64 * J : 1>* room, const Layout at, int J32,
+                                            uint32_t* out) {
+  const int lane = threadIdx.x & 63;
+  const bool real = GROUPS && n.group_top == 2;  // values, not only their order, count
+  float l[J];
+  double s[J], v[J];
 #pragma unroll
-  for (int j = 0; j < J; j++) v[j] = with_bias ? s[j] + (T)bias[j] : (T)l[j];
-  // fp32 scores are off by up to 2^-21 (sigmoid) or 2^-20 (softmax) of the
-  // largest one, the sum with the bias by 2^-24 of itself
-  float top = 1.0f;
-  if (!kExact && !n.sigmoid) {
-    top = 0;
+  for (int j = 0; j < J; j++) l[j] = lane * J + j < n.E ? logits[lane * J + j] : kNegInf;
+  if (bias || real) scores<64, J, double>(l, n.sigmoid, s);
+  uint64_t key[J];
 #pragma unroll
-    for (int j = 0; j < J; j++) top = fmaxf(top, s32[j]);
-    top = max_of<LPT>(top);
+  for (int j = 0; j < J; j++) {
+    v[j] = bias && lane * J + j < n.E ? s[j] + (double)bias[lane * J + j] : (double)l[j];
+    key[j] = l[j] == kNegInf ? 0 : ordered(v[j]);
   }
-  const float err = n.sigmoid ? 0x1p-21f : 0x1p-20f * top;
-  bool near = false;
-  U key[J];
-#pragma unroll
-  for (int j = 0; j < J; j++) key[j] = l[j] == kNegInf ? U(0) : ordered(v[j]);
   if constexpr (GROUPS) {
     // a group's value: of one key that key, of two their sum (of scores, where
     // the keys are logits); a group's masked experts add nothing
-    const bool real = n.group_top == 2 && !with_bias;
 #pragma unroll
-    for (int j = 0; j < J; j++) {
-      const int e = sub * J + j;
-      if (e < n.E) room->key[tok][e] = l[j] == kNegInf ? (double)kNegInf : (double)(real ? s[j] : v[j]);
-    }
+    for (int j = 0; j < J; j++)
+      if (lane * J + j < n.E)
+        room->key[lane * J + j] = l[j] == kNegInf ? (double)kNegInf : real && !bias ? s[j] : v[j];
     wave_sync();
-    const int eg = n.E / n.groups;
-    for (int g = sub; g < n.groups; g += LPT) {
+    if (lane < n.groups) {
+      const int eg = n.E / n.groups;
       double a = kNegInf, b = kNegInf;
       bool nan = false;
       for (int i = 0; i < eg; i++) {
-        const double x = room->key[tok][g * eg + i];
+        const double x = room->key[lane * eg + i];
         nan |= x != x;
         if (x > a) {
           b = a;
@@ -180,152 +204,211 @@ __device__ __forceinline__ bool choose(const float* l, const float* s32, const f
           b = x;
         }
       }
-      double y = a;
-      if (n.group_top == 2 && b != (double)kNegInf) y = kExact ? a + b : (double)((float)a + (float)b);
-      room->value[tok][g] = nan ? __builtin_nan("") : y;
+      room->value[lane] = nan ? __builtin_nan("") : n.group_top == 2 && b != (double)kNegInf ? a + b : a;
     }
     wave_sync();
-    double low = __builtin_inf(), high = kNegInf;  // the worst kept value, the best other one
-    for (int g = sub; g < n.groups; g += LPT) {
-      const double y = room->value[tok][g];
-      const uint64_t o = ordered(y);
+    if (lane < n.groups) {
+      const uint64_t o = ordered(room->value[lane]);
       int rank = 0;
       for (int i = 0; i < n.groups; i++) {
-        const uint64_t p = ordered(room->value[tok][i]);
-        rank += p > o || (p == o && i < g);
+        const uint64_t p = ordered(room->value[i]);
+        rank += p > o || (p == o && i < lane);
       }
-      const bool keep = rank < n.kept;
-      room->keep[tok][g] = keep;
-      if (keep && y < low) low = y;
-      if (!keep && y > high) high = y;
+      room->keep[lane] = rank < n.kept;
     }
     wave_sync();
-    if (!kExact && need && n.kept < n.groups) {
-      low = reduce<LPT>(low, [](double a, double b) { return a < b ? a : b; });
-      high = max_of<LPT>(high);
-      near |= !(low - high > 4 * (double)err + 0x1p-21 * (fabs(low) + fabs(high)));
-    }
 #pragma unroll
-    for (int j = 0; j < J; j++) {
-      const int e = sub * J + j;
-      if (e < n.E && !room->keep[tok][e / eg]) key[j] = 0;
-    }
+    for (int j = 0; j < J; j++)
+      if (lane * J + j < n.E && !room->keep[(lane * J + j) / (n.E / n.groups)]) key[j] = 0;
   }
-#pragma unroll
-  for (int j = 0; j < J; j++) taken[j] = false;
-  U before = 0;
-  const bool check = !kExact && with_bias;
-  const int rounds = n.K + (check ? 1 : 0);  // one more for the key that just missed
-  for (int k = 0; k < rounds; k++) {
-    U m = 0;
+  for (int k = 0; k < n.K; k++) {
+    uint64_t m = 0;
 #pragma unroll
     for (int j = 0; j < J; j++) m = key[j] > m ? key[j] : m;
-    const U best = max_of<LPT>(m);
-    if (check && k > 0 && best != 0) {
-      const float a = value_of((uint32_t)before), b = value_of((uint32_t)best);
-      near |= !(a - b > 2 * err + 0x1p-23f * (fabsf(a) + fabsf(b)));
-    }
-    before = best;
-    if (k == n.K) break;
-    const uint64_t who = __ballot(m == best && best != 0) & mine;
-    if (who == 0) {
-      if (sub == 0) out[tok][k] = Chosen{-1, 0.0f};
-    } else if (__ffsll((unsigned long long)who) - 1 == (int)(threadIdx.x & 63)) {
+    const uint64_t best = max_of<64>(m);
+    const uint64_t who = __ballot(m == best);
+    if (best == 0) {
+      if (lane == 0) out[k] = kNone;
+    } else if (__ffsll((unsigned long long)who) - 1 == lane) {
       bool open = true;
 #pragma unroll
       for (int j = 0; j < J; j++)
         if (open && key[j] == best) {
           open = false;
           key[j] = 0;
-          taken[j] = true;
-          out[tok][k] = Chosen{sub * J + j, s32[j]};
+          const int e = lane * J + j, g = e / at.eg, i = e - g * at.eg;
+          out[k] = (uint32_t)((g * at.q + i / J32) * J32 + i % J32) << 16 | (uint32_t)e;
         }
     }
+  }
+  wave_sync();
+}
+
+// ------------------------------------------------------------------ 32 bits
+// The wave's tokens' choices; l, s, bias: those of this lane's J experts, of
+// which e0 is the first.  Choice k of a token goes to out[tok][k], place and
+// expert.  Returns whether a decision of this lane's token was too near to make.
+template <int LPT, int J, bool GROUPS>
+__device__ __forceinline__ bool choose(const float* l, const float* s, const float* bias, bool with_bias, int e0,
+                                       const RouteShape& n, int q, uint32_t (*out)[16]) {
+  const int sub = threadIdx.x % LPT, tok = (threadIdx.x & 63) / LPT;
+  uint32_t key[J];
+#pragma unroll
+  for (int j = 0; j < J; j++) key[j] = l[j] == kNegInf ? 0 : ordered(with_bias ? s[j] + bias[j] : l[j]);
+  // fp32 scores are off by up to 2^-21 (sigmoid) or 2^-20 (softmax) of the
+  // largest one, the sum with the bias by 2^-24 of itself
+  float err = 0x1p-21f;
+  if (!n.sigmoid && (with_bias || (GROUPS && n.group_top == 2))) {
+    float top = 0;
+#pragma unroll
+    for (int j = 0; j < J; j++) top = fmaxf(top, s[j]);
+    err = 0x1p-20f * max_of<LPT>(top);
+  }
+  bool near = false;
+  if constexpr (GROUPS) {
+    // the two largest keys (scores, where the keys are logits) of the group
+    const bool of_scores = n.group_top == 2 && !with_bias;
+    uint32_t a = 0, b = 0;
+    auto merge = [&](uint32_t c, uint32_t d) {  // c >= d
+      b = max(min(a, c), max(b, d));
+      a = max(a, c);
+    };
+#pragma unroll
+    for (int j = 0; j < J; j++) merge(of_scores && key[j] ? ordered(s[j]) : key[j], 0);
+    if (q > 1) merge(across<0xb1>(a), across<0xb1>(b));
+    if (q > 2) merge(across<0x4e>(a), across<0x4e>(b));
+    if (q > 4) merge(across<0x141>(a), across<0x141>(b));
+    if (q > 8) merge(across<0x140>(a), across<0x140>(b));
+    if constexpr (LPT == 64) {
+      if (q > 16) merge(__shfl_xor(a, 16), __shfl_xor(b, 16));
+    }
+    if (n.group_top == 2 && b != 0) a = ordered(value_of(a) + value_of(b));
+    const int g = sub / q;
+    if (g >= n.groups) a = 0;
+    int rank = 0;
+    const int first = threadIdx.x & 63 & ~(LPT - 1);
+    for (int i = 0; i < n.groups; i++) {
+      const uint32_t o = __shfl(a, first + i * q);
+      rank += o > a || (o == a && i < g);
+    }
+    const bool keep = rank < n.kept && g < n.groups;
+    if (with_bias || n.group_top == 2) {
+      const uint32_t low = min_of<LPT>(keep ? a : ~0u), high = max_of<LPT>(keep ? 0u : a);
+      const float x = value_of(low), y = value_of(high);
+      near |= high != 0 && !(x - y > 4 * err + 0x1p-21f * (fabsf(x) + fabsf(y)));
+    }
+    if (!keep) {
+#pragma unroll
+      for (int j = 0; j < J; j++) key[j] = 0;
+    }
+  }
+  uint32_t before = 0;
+  const int rounds = n.K + (with_bias ? 1 : 0);  // one more for the key that just missed
+  for (int k = 0; k < rounds; k++) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < J; j++) m = max(m, key[j]);
+    const uint32_t best = max_of<LPT>(m);
+    if (with_bias && k > 0 && best != 0) {
+      const float x = value_of(before), y = value_of(best);
+      near |= !(x - y > 2 * err + 0x1p-23f * (fabsf(x) + fabsf(y)));
+    }
+    before = best;
+    if (k == n.K) break;
+    const int winner = min_of<LPT>(m == best ? sub : LPT);  // the lowest lane that has it
+    bool open = winner == sub && best != 0;
+    int at = 0;
+#pragma unroll
+    for (int j = 0; j < J; j++) {
+      const bool hit = open && key[j] == best;
+      key[j] = hit ? 0 : key[j];
+      at = hit ? j : at;
+      open = open && !hit;
+    }
+    if (winner == sub) out[tok][k] = best == 0 ? kNone : (uint32_t)(sub * J + at) << 16 | (uint32_t)(e0 + at);
   }
   wave_sync();
   return near;
 }
 
-// A token per LPT lanes, J neighbouring experts to a lane; a workgroup takes
-// every slots-th step of its rank's tokens.  STATS: it counts its tokens'
-// choices and sums their scores, in its slot of the work array or, alone, in
-// the results.
+// A token per LPT lanes, J experts to a lane; a workgroup takes every slots-th
+// step of its rank's tokens.  STATS: it counts its tokens' choices and sums their
+// scores, in its slot of the work array or, alone, in the results.
 template <int LPT, int J, bool GROUPS, bool STATS>
-__global__ __launch_bounds__(kBlock) void route_kernel(const RouteArgs a, const RouteShape n, int slots,
-                                                       float* work) {
-  constexpr int kTok = 64 / LPT, kWaves = kBlock / 64;
-  __shared__ Chosen chosen[kWaves][kTok][16];
-  __shared__ GroupRoom<GROUPS ? LPT : 64, GROUPS ? J : 1> rooms[GROUPS ? kWaves : 1];
-  __shared__ float sum_part[STATS ? kWaves * kTok : 1][STATS ? LPT * J : 1];
-  __shared__ int count_part[STATS ? kWaves * kTok : 1][STATS ? LPT * J : 1];
+__global__ __launch_bounds__(kBlock) void route_kernel(const RouteArgs a, const RouteShape n, const Layout at,
+                                                       bool exact, int slots, float* work) {
+  constexpr int kTok = 64 / LPT, kWaves = kBlock / 64, kPlaces = LPT * J;
+  constexpr int kExactJ = (kPlaces + 63) / 64;
+  __shared__ uint32_t chosen[kWaves][kTok][16];
+  __shared__ __align__(16) float score[kWaves][kTok][kPlaces];
+  __shared__ ExactRoom<GROUPS ? 64 * kExactJ : 1> rooms[GROUPS ? kWaves : 1];
+  __shared__ int count[STATS ? kPlaces : 1];
   const int rank = blockIdx.x / slots, slot = blockIdx.x % slots;
   const int wave = threadIdx.x >> 6, sub = threadIdx.x % LPT, tok = (threadIdx.x & 63) / LPT;
   const float* logits = a.logits[rank];
   const bool with_bias = a.bias[rank] != nullptr;
+  const int g = sub / at.q, i0 = sub % at.q * J, e0 = g * at.eg + i0;
+  const int mine = g * at.eg < n.E ? max(0, min(J, at.eg - i0)) : 0;
   float bias[J], sums[J];
-  int counts[J];
+  if (with_bias) load_some<J>(a.bias[rank] + (mine > 0 ? e0 : 0), mine, 0.0f, bias);
+  if constexpr (STATS) {
 #pragma unroll
-  for (int j = 0; j < J; j++) {
-    const int e = sub * J + j;
-    bias[j] = with_bias && e < n.E ? a.bias[rank][e] : 0.0f;
-    sums[j] = 0;
-    counts[j] = 0;
+    for (int j = 0; j < J; j++) sums[j] = 0;
+    for (int e = threadIdx.x; e < kPlaces; e += kBlock) count[e] = 0;
+    __syncthreads();
   }
   for (int64_t t0 = ((int64_t)slot * kWaves + wave) * kTok; t0 < n.T; t0 += (int64_t)slots * kWaves * kTok) {
     const int64_t t = t0 + tok;
     const bool live = t < n.T;
     float l[J], s[J];
-#pragma unroll
-    for (int j = 0; j < J; j++) {
-      const int e = sub * J + j;
-      l[j] = live && e < n.E ? logits[t * n.E + e] : kNegInf;
-    }
+    load_some<J>(logits + (live && mine > 0 ? t * n.E + e0 : 0), live ? mine : 0, kNegInf, l);
     scores<LPT, J, float>(l, n.sigmoid, s);
-    bool taken[J];
-    auto* room = reinterpret_cast<GroupRoom<LPT, J>*>(&rooms[GROUPS ? wave : 0]);
-    const bool near = choose<LPT, J, GROUPS, float>(l, s, bias, with_bias, n, room, chosen[wave], taken);
-    if (__ballot(near && live))
-      choose<LPT, J, GROUPS, double>(l, s, bias, with_bias, n, room, chosen[wave], taken);
-    Chosen c = sub < n.K ? chosen[wave][tok][sub & 15] : Chosen{-1, 0.0f};
-    const float total = sum_of<LPT>(c.s);
-    float w = c.s;
-    if (n.renorm) w = total == 0.0f ? 0.0f : w / total;
-    if (live && sub < n.K) {
-      a.topk[rank][t * n.K + sub] = c.id;
-      a.weights[rank][t * n.K + sub] = w * n.scale;
-    }
-    wave_sync();
+#pragma unroll
+    for (int j = 0; j < J; j += 4)
+      *reinterpret_cast<dev::f32x4*>(&score[wave][tok][sub * J + j]) = dev::f32x4{s[j], s[j + 1], s[j + 2], s[j + 3]};
     if constexpr (STATS) {
 #pragma unroll
-      for (int j = 0; j < J; j++)
-        if (live && sub * J + j < n.E) {
-          sums[j] += l[j] == kNegInf ? 0.0f : s[j];
-          counts[j] += taken[j];
-        }
+      for (int j = 0; j < J; j++) sums[j] += l[j] == kNegInf ? 0.0f : s[j];
     }
+    bool near = exact;
+    if (!exact) near = choose<LPT, J, GROUPS>(l, s, bias, with_bias, e0, n, at.q, chosen[wave]);
+    for (uint64_t todo = __ballot(near && live && sub == 0); todo; todo &= todo - 1) {
+      const int k = (__ffsll((unsigned long long)todo) - 1) / LPT;
+      choose_exactly<kExactJ, GROUPS>(logits + (t0 + k) * n.E, a.bias[rank], n, &rooms[GROUPS ? wave : 0], at, J,
+                                      chosen[wave][k]);
+    }
+    wave_sync();
+    const uint32_t c = live && sub < n.K ? chosen[wave][tok][sub & 15] : kNone;
+    float w = c != kNone ? score[wave][tok][c >> 16] : 0.0f;
+    if (n.renorm) {
+      const float total = sum_of<LPT>(w);
+      w = total == 0.0f ? 0.0f : w / total;
+    }
+    if (live && sub < n.K) {
+      a.topk[rank][t * n.K + sub] = c != kNone ? (int)(c & 0xffff) : -1;
+      a.weights[rank][t * n.K + sub] = w * n.scale;
+    }
+    if constexpr (STATS) {
+      if (c != kNone) atomicAdd(&count[c >> 16], 1);  // whole numbers: the order does not show
+    }
+    wave_sync();
   }
   if constexpr (STATS) {
 #pragma unroll
-    for (int j = 0; j < J; j++) {
-      sum_part[wave * kTok + tok][sub * J + j] = sums[j];
-      count_part[wave * kTok + tok][sub * J + j] = counts[j];
-    }
+    for (int j = 0; j < J; j++) score[wave][tok][sub * J + j] = sums[j];
     __syncthreads();
     for (int e = threadIdx.x; e < n.E; e += kBlock) {
+      const int eg = e / at.eg, i = e - eg * at.eg, p = (eg * at.q + i / J) * J + i % J;
       float s = 0;
-      int c = 0;
 #pragma unroll
-      for (int k = 0; k < kWaves * kTok; k++) {
-        s += sum_part[k][e];
-        c += count_part[k][e];
-      }
+      for (int k = 0; k < kWaves * kTok; k++) s += score[k / kTok][k % kTok][p];
       if (slots == 1) {
         if (a.sums[rank]) a.sums[rank][e] = s;
-        if (a.counts[rank]) a.counts[rank][e] = c;
+        if (a.counts[rank]) a.counts[rank][e] = count[p];
       } else {
         float* out = work + (int64_t)blockIdx.x * 2 * n.E;
         out[e] = s;
-        reinterpret_cast<int*>(out)[n.E + e] = c;
+        reinterpret_cast<int*>(out)[n.E + e] = count[p];
       }
     }
   }
@@ -369,18 +452,19 @@ template <int LPT, int J>
 __global__ __launch_bounds__(kBlock) void route_bwd_kernel(const RouteBwdArgs a, const RouteShape n,
                                                            int64_t blocks_per_rank) {
   constexpr int kTok = 64 / LPT, kWaves = kBlock / 64;
-  __shared__ Chosen back[kWaves][kTok][16];
+  struct Part {
+    int id;
+    float u;
+  };
+  __shared__ Part back[kWaves][kTok][16];
   const int rank = (int)(blockIdx.x / blocks_per_rank);
   const int wave = threadIdx.x >> 6, sub = threadIdx.x % LPT, tok = (threadIdx.x & 63) / LPT;
   const int64_t t = ((int64_t)(blockIdx.x % blocks_per_rank) * kWaves + wave) * kTok + tok;
   const bool live = t < n.T;
   const float* logits = a.logits[rank] + (live ? t : 0) * n.E;
+  const int e0 = sub * J, mine = max(0, min(J, n.E - e0));
   float l[J], s[J], ds[J];
-#pragma unroll
-  for (int j = 0; j < J; j++) {
-    const int e = sub * J + j;
-    l[j] = live && e < n.E ? logits[e] : kNegInf;
-  }
+  load_some<J>(logits + (mine > 0 ? e0 : 0), live ? mine : 0, kNegInf, l);
   float m = 0, inv = 0;
   if (!n.sigmoid) {
     m = kNegInf;
@@ -415,18 +499,14 @@ __global__ __launch_bounds__(kBlock) void route_bwd_kernel(const RouteBwdArgs a,
     const float total = sum_of<LPT>(c), dot = sum_of<LPT>(u * c);
     u = id < 0 || total == 0.0f ? 0.0f : (u - dot / total) / total;
   }
-  if (sub < 16) back[wave][tok][sub] = Chosen{id, u};
+  if (sub < 16) back[wave][tok][sub] = Part{id, u};
   wave_sync();
   const float* dsums = a.dsums[rank];
-#pragma unroll
-  for (int j = 0; j < J; j++) {
-    const int e = sub * J + j;
-    ds[j] = dsums && e < n.E ? dsums[e] : 0.0f;
-  }
+  load_some<J>(dsums ? dsums + (mine > 0 ? e0 : 0) : nullptr, dsums ? mine : 0, 0.0f, ds);
   for (int k = 0; k < n.K; k++) {
-    const Chosen b = back[wave][tok][k];
+    const Part b = back[wave][tok][k];
 #pragma unroll
-    for (int j = 0; j < J; j++) ds[j] += b.id == sub * J + j ? b.s : 0.0f;
+    for (int j = 0; j < J; j++) ds[j] += b.id == e0 + j ? b.u : 0.0f;
   }
   float dot = 0;
   if (!n.sigmoid) {
@@ -434,17 +514,25 @@ __global__ __launch_bounds__(kBlock) void route_bwd_kernel(const RouteBwdArgs a,
     for (int j = 0; j < J; j++) dot = __builtin_fmaf(s[j], ds[j], dot);
     dot = sum_of<LPT>(dot);
   }
+  float d[J];
 #pragma unroll
   for (int j = 0; j < J; j++) {
-    const int e = sub * J + j;
-    float d;
     if (n.sigmoid) {
       const Sigmoid<float> x = sigmoid(l[j]);
-      d = x.s * x.rest * ds[j];
+      d[j] = x.s * x.rest * ds[j];
     } else {
-      d = s[j] * (ds[j] - dot);
+      d[j] = s[j] * (ds[j] - dot);
     }
-    if (live && e < n.E) a.dlogits[rank][t * n.E + e] = l[j] == kNegInf ? 0.0f : d;
+    if (l[j] == kNegInf) d[j] = 0.0f;
+  }
+  float* out = a.dlogits[rank] + t * n.E + e0;
+  if (live && mine == J) {
+#pragma unroll
+    for (int j = 0; j < J; j += 4) __builtin_memcpy(out + j, d + j, 16);
+  } else if (live) {
+#pragma unroll
+    for (int j = 0; j < J; j++)
+      if (j < mine) out[j] = d[j];
   }
 }
 
@@ -454,14 +542,15 @@ hipError_t launch_stats(const RouteArgs& a, const RouteShape& n, const float* wo
 }
 
 template <int LPT, int J>
-hipError_t launch_route_as(const RouteArgs& a, const RouteShape& n, bool stats, float* work, hipStream_t stream) {
+hipError_t launch_route_as(const RouteArgs& a, const RouteShape& n, const Layout& at, bool exact, bool stats,
+                           float* work, hipStream_t stream) {
   const int slots = route_slots(n.R, n.T);
   const unsigned grid = (unsigned)(slots * n.R);
   const bool groups = n.kept < n.groups;
-  if (groups && stats) route_kernel<LPT, J, true, true><<<grid, kBlock, 0, stream>>>(a, n, slots, work);
-  else if (groups) route_kernel<LPT, J, true, false><<<grid, kBlock, 0, stream>>>(a, n, slots, work);
-  else if (stats) route_kernel<LPT, J, false, true><<<grid, kBlock, 0, stream>>>(a, n, slots, work);
-  else route_kernel<LPT, J, false, false><<<grid, kBlock, 0, stream>>>(a, n, slots, work);
+  if (groups && stats) route_kernel<LPT, J, true, true><<<grid, kBlock, 0, stream>>>(a, n, at, exact, slots, work);
+  else if (groups) route_kernel<LPT, J, true, false><<<grid, kBlock, 0, stream>>>(a, n, at, exact, slots, work);
+  else if (stats) route_kernel<LPT, J, false, true><<<grid, kBlock, 0, stream>>>(a, n, at, exact, slots, work);
+  else route_kernel<LPT, J, false, false><<<grid, kBlock, 0, stream>>>(a, n, at, exact, slots, work);
   hipError_t e = hipGetLastError();
   return e != hipSuccess || !stats || slots == 1 ? e : launch_stats(a, n, work, slots, stream);
 }
@@ -475,15 +564,27 @@ hipError_t launch_route_bwd_as(const RouteBwdArgs& a, const RouteShape& n, hipSt
   return hipGetLastError();
 }
 
+// Lanes of a group where `lanes` share a token and hold J experts each; 0 where
+// the groups do not fit.
+int lanes_of(int lanes, int J, int groups, int eg) {
+  int q = 1;
+  while (2 * q * groups <= lanes) q *= 2;
+  return groups <= lanes && q * J >= eg ? q : 0;
+}
+
 }  // namespace
 
 hipError_t launch_route(const RouteArgs& a, const RouteShape& n, float* work, hipStream_t stream) {
   bool stats = false;
   for (int r = 0; r < n.R; r++) stats |= a.counts[r] || a.sums[r];
   if (n.T <= 0) return stats ? launch_stats(a, n, work, 0, stream) : hipSuccess;  // no slot: zeros
-  if (n.E <= 64) return launch_route_as<16, 4>(a, n, stats, work, stream);
-  if (n.E <= 256) return launch_route_as<16, 16>(a, n, stats, work, stream);
-  return launch_route_as<64, 16>(a, n, stats, work, stream);
+  const int groups = n.kept < n.groups ? n.groups : 1, eg = n.E / groups;
+  if (const int q = lanes_of(16, 4, groups, eg)) return launch_route_as<16, 4>(a, n, Layout{eg, q}, false, stats, work, stream);
+  if (const int q = lanes_of(16, 16, groups, eg)) return launch_route_as<16, 16>(a, n, Layout{eg, q}, false, stats, work, stream);
+  if (const int q = lanes_of(64, 4, groups, eg)) return launch_route_as<64, 4>(a, n, Layout{eg, q}, false, stats, work, stream);
+  if (const int q = lanes_of(64, 16, groups, eg)) return launch_route_as<64, 16>(a, n, Layout{eg, q}, false, stats, work, stream);
+  // groups that do not fit the lanes: every token by the whole wave, in 64 bits
+  return launch_route_as<64, 16>(a, n, Layout{n.E, 64}, true, stats, work, stream);
 }
 
 hipError_t launch_route_bwd(const RouteBwdArgs& a, const RouteShape& n, hipStream_t stream) {
