@@ -30,8 +30,8 @@ SOURCES = ["ccr_api.cpp", "ccr_dma.cpp", "ccr_schedule.cpp", "ccr_kernels.hip", 
 # arguments preloaded into registers (gfx950 kernel-argument preloading), so
 # a workgroup's first scalar memory access is the load of its base addresses.
 SOURCE_FLAGS = {"ccr_ring.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=16"],
-                # assembled from a file that stays behind, which check_experts reads
-                "ccr_experts.hip": ["-save-temps=obj"]}
+                # assembled from files that stay behind, which the checks below read
+                "ccr_experts.hip": ["-save-temps=obj"], "ccr_experts8.hip": ["-save-temps=obj"]}
 ARCH = "gfx950"
 
 # -packed-fp32-ops keeps the compiler from emitting packed fp32 arithmetic;
@@ -52,30 +52,51 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found; the HIP library cannot be built")
 
 
+def check_loop(source: str, name: str, body: str, products: int) -> None:
+    """Refuse a kernel of large tiles whose loop does not hold `products` matrix
+    instructions that all leave their accumulators in place: the instructions are
+    written in assembly, so the compiler does not wait for their results, and
+    between a loop's first product and the wait before the results are read it must
+    not move an accumulator."""
+    loop = body[body.find("v_mfma"):]
+    loop = loop[:loop.find("s_nop 15")]
+    if loop.count("v_mfma") != products or "v_accvgpr" in loop or "scratch_" in loop:
+        raise RuntimeError(f"{source}: an accumulator of {name} is moved between its products")
+
+
+def check_lds_loads(source: str, asm: str) -> None:
+    """Refuse an assembly with a load straight to LDS directly behind the write of
+    its LDS place (m0), or with anything else that writes m0."""
+    lines = [x.split(";")[0].strip() for x in asm.splitlines()]
+    lines = [x for x in lines if x and not x.startswith(".") and not x.endswith(":")]
+    loads = [i for i, x in enumerate(lines) if re.match(r"global_load_lds|buffer_load.* lds$", x)]
+    if any(re.match(r"\w+ m0\b", lines[i - 1]) for i in loads):
+        raise RuntimeError(f"{source}: a load to LDS directly behind the write of m0")
+    if sum(bool(re.match(r"\w+ m0\b", x)) for x in lines) != len(loads):
+        raise RuntimeError(f"{source}: m0 is written apart from the loads to LDS")
+
+
 def check_experts(asm: str) -> None:
     """Refuse an assembly of ccr_experts.hip whose hand-written instructions do
-    not stand as they have to.
-
-    The large tiles' matrix instructions are written in assembly, so the compiler
-    does not wait for their results: between a loop's first product and the wait
-    before the results are read it must not move an accumulator.  A load straight
-    to LDS must not follow the write of its LDS place (m0) directly, and nothing
-    else may write m0."""
+    not stand as they have to."""
     kernels = re.findall(r"^(_ZN3ccr\S*experts_big_kernel\S*):(.*?)s_endpgm", asm, re.S | re.M)
     if len(kernels) != 4:  # product, input gradient, weight gradient to fp32 and to bf16
         raise RuntimeError(f"ccr_experts.hip: {len(kernels)} kernels of large tiles, not 4")
     for name, body in kernels:
-        loop = body[body.find("v_mfma"):]
-        loop = loop[:loop.find("s_nop 15")]
-        if loop.count("v_mfma") != 128 or "v_accvgpr" in loop or "scratch_" in loop:
-            raise RuntimeError(f"ccr_experts.hip: an accumulator of {name} is moved between its products")
-    lines = [x.split(";")[0].strip() for x in asm.splitlines()]
-    lines = [x for x in lines if x and not x.startswith(".") and not x.endswith(":")]
-    loads = [i for i, x in enumerate(lines) if x.startswith("global_load_lds")]
-    if any(re.match(r"\w+ m0\b", lines[i - 1]) for i in loads):
-        raise RuntimeError("ccr_experts.hip: a load to LDS directly behind the write of m0")
-    if sum(bool(re.match(r"\w+ m0\b", x)) for x in lines) != len(loads):
-        raise RuntimeError("ccr_experts.hip: m0 is written apart from the loads to LDS")
+        check_loop("ccr_experts.hip", name, body, 128)
+    check_lds_loads("ccr_experts.hip", asm)
+
+
+def check_experts8(asm: str) -> None:
+    """The same for ccr_experts8.hip."""
+    kernels = re.findall(r"^(_ZN3ccr\S*experts8_big_kernel\S*):(.*?)s_endpgm", asm, re.S | re.M)
+    if len(kernels) != 1:
+        raise RuntimeError(f"ccr_experts8.hip: {len(kernels)} kernels of large tiles, not 1")
+    check_loop("ccr_experts8.hip", *kernels[0], 64)
+    check_lds_loads("ccr_experts8.hip", asm)
+
+
+CHECKS = {"ccr_experts.hip": check_experts, "ccr_experts8.hip": check_experts8}
 
 
 def build_marshal() -> str:
@@ -110,9 +131,9 @@ def build(verbose: bool = False) -> str:
         err = "\n".join(l for l in (r.stdout + r.stderr).splitlines() if noise not in l)
         if r.returncode != 0:
             raise RuntimeError(f"hipcc failed on {src}:\n{err}")
-        if src == "ccr_experts.hip":
-            with open(os.path.join(BUILD, f"ccr_experts-hip-amdgcn-amd-amdhsa-{ARCH}.s")) as f:
-                check_experts(f.read())
+        if src in CHECKS:
+            with open(os.path.join(BUILD, f"{os.path.splitext(src)[0]}-hip-amdgcn-amd-amdhsa-{ARCH}.s")) as f:
+                CHECKS[src](f.read())
         if verbose and err.strip():
             print(err, file=sys.stderr)
         return obj

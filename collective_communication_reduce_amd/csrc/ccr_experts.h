@@ -113,7 +113,7 @@ __device__ __forceinline__ s16x4 fragment_half(const char* lds, int x0, int i, i
 // product needs.
 template <int ES, int X, bool COL, bool PAIRED>
 __device__ __forceinline__ u32x4 fragment(const char* lds, int x0, int i, int h) {
-  static_assert(ES == 2 || !PAIRED, "fp32 results are 16 bytes by fours");
+  static_assert(ES != 4 || !PAIRED, "fp32 results are 16 bytes by fours");
   const int l = threadIdx.x & 63, j = l & 15, g = l >> 4;
   if constexpr (!COL) {
     const int r = PAIRED ? x0 + (i >> 1) * 32 + (j >> 2) * 8 + (i & 1) * 4 + (j & 3) : x0 + i * 16 + j;

@@ -651,7 +651,7 @@ ExpertTile expert_tile(ExpertOp op, int es, int os, const ExpertShape& sh, const
   ExpertTile best = ExpertTile::k16;
   double least = 0;
   for (const Cost& c : costs) {
-    if (c.tile == ExpertTile::k256 && es != 2) continue;
+    if (c.tile == ExpertTile::k256 && es == 4) continue;
     const ExpertTileSize x = expert_tile_size(c.tile);
     const int step = KB / es;
     const double fixed = c.c0 + (double)x.rows * x.cols * os / 19000.0;

@@ -16,6 +16,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "ccr_device.h"
 #include "ccr_experts.h"
 #include "ccr_internal.h"
@@ -171,6 +173,288 @@ __global__ __launch_bounds__(WM * WN * WK * 64) void experts8_ring_kernel(const 
   }
 }
 
+// ------------------------------------------------------------- large tiles
+// 256 x 256 tiles: four waves, one to a SIMD, each with a 128 x 128 part of the
+// tile in its accumulators: per K-step 64 matrix instructions on 16 fragments and
+// their scales.
+//
+// The workgroup's tiles are one sequence of steps: a persistent workgroup takes
+// every gridDim.x-th tile, and the loads of its next tile's first steps go out
+// during the last steps of this one, so that a tile's start waits for nothing.
+//
+// LDS holds two steps of lines (four slots of 32 KiB: a and b of an even and of an
+// odd step) and four of scales.  A step has two phases of 32 products: the first
+// multiplies the first four fragments of a with all of b, the second the last
+// four.  Each phase reads the fragments that the next one needs, into the
+// registers that it sets free: the first a's last four of this step, the second
+// b's (each behind its last product) and a's first four of the next step.  So a
+// line is loaded a step and a half before it is read, into the place of the one
+// that has just been read: behind a barrier a little into the first phase, b, the
+// first half of a and the scales of the step after next; behind one between the
+// phases, the second half of a.
+//
+// With one wave to a SIMD nothing hides an instruction that stalls, so reads and
+// loads are placed one by one between the products.
+//
+// The products are written in assembly, as all 256 accumulation registers are
+// accumulators here.  No two products in a row touch the same one, so no wait
+// states are due between them; drain() provides those before they are read.  The
+// build reads the assembly and refuses one that moves an accumulator in the loop.
+// (s_nop: two wait states between the shift that makes a scale and its product.)
+__device__ __forceinline__ void mma8_acc(i32x8 a, i32x8 b, f32x4& d, int sa, int sb) {
+  asm("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
+      : "+a"(d) : "v"(a), "v"(b), "v"(sa), "v"(sb));
+}
+__device__ __forceinline__ void drain8(f32x4* d) {
+  asm volatile("s_nop 15\n\ts_nop 15"
+               : "+a"(d[0]), "+a"(d[1]), "+a"(d[2]), "+a"(d[3]), "+a"(d[4]), "+a"(d[5]), "+a"(d[6]),
+                 "+a"(d[7]));
+}
+
+// Row of the tile that lane l's row of the i-th fragment from x0 on is.
+template <bool PAIRED>
+__device__ __forceinline__ int fragment_row(int x0, int i) {
+  const int j = threadIdx.x & 15;
+  return PAIRED ? x0 + (i >> 1) * 32 + (j >> 2) * 8 + (i & 1) * 4 + (j & 3) : x0 + i * 16 + j;
+}
+
+// A fragment and the scales of its rows' step, read in three parts.  A lane's own
+// scale is a byte of its row's four.
+struct Frag8 {
+  u32x4 half[2];
+  uint32_t scales;
+  template <bool PAIRED>
+  __device__ __forceinline__ void read(const char* lines, const char* sc, int x0, int i, int part) {
+    if (part < 2) half[part] = fragment<1, 256, false, PAIRED>(lines, x0, i, part);
+    else scales = *reinterpret_cast<const uint32_t*>(sc + fragment_row<PAIRED>(x0, i) * 4);
+  }
+  __device__ __forceinline__ i32x8 v() const { return __builtin_bit_cast(i32x8, half); }
+  __device__ __forceinline__ int scale() const { return (int)(scales >> ((threadIdx.x & 48) >> 1)); }
+};
+
+// Memory as the bounded buffer that loads to LDS take: a lane whose offset lies
+// past `bytes` reads nothing.
+__device__ __forceinline__ u32x4 bounded(const char* p, int64_t bytes) {
+  const uint64_t q = reinterpret_cast<uint64_t>(p);
+  return u32x4{(uint32_t)q, (uint32_t)(q >> 32), (uint32_t)bytes, 0x00020000u};
+}
+
+__global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable tab, const ExpertShape sh,
+                                                              int64_t row_bytes, int tiles) {
+  constexpr int BM = 256, BN = 256, NT = 256, T = 8, kSlot = 256 * KB, kScales = 2048;
+  constexpr bool kPaired = true;  // b: 16-byte stores of the results
+  __shared__ __align__(1024) char lds[4 * kSlot + 4 * kScales];  // a, a, b, b; the scales of a, of b
+  char* const scales = lds + 4 * kSlot;
+  const int l = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = (w >> 1) * 128, wn = (w & 1) * 128;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(CCR_LDS char*)lds;
+  const int nk = (int)((sh.H + KB - 1) / KB);
+  // First tiles of the groups, in the lanes: read once, since to wait for a later
+  // read would be to wait for all loads and stores before it.
+  static_assert(kExpertGroups <= 128, "two to a lane");
+  const int first0 = l < tab.n ? tab.tile0[l] : INT32_MAX;
+  const int first1 = l + 64 < tab.n ? tab.tile0[l + 64 < kExpertGroups ? l + 64 : 0] : INT32_MAX;
+  auto place = [&](int t) {
+    const int gi = __popcll(__ballot(first0 <= t)) + __popcll(__ballot(first1 <= t)) - 1;
+    const ExpertGroup& g = tab.g[gi];
+    Where x;
+    x.a = g.a;
+    x.b = g.b;
+    x.c = g.c;
+    x.M = g.m;
+    x.N = sh.F;
+    int tm, tn;
+    tile_at(t - tab.tile0[gi], (int)((x.M + BM - 1) / BM), (int)((x.N + BN - 1) / BN), &tm, &tn);
+    x.m0 = (int64_t)tm * BM;
+    x.n0 = (int64_t)tn * BN;
+    return x;
+  };
+
+  // What is loaded next: a step of tile `aimed`, whose rows are bounded buffers: a
+  // lane's offsets are the same in every tile, and what the last tile has no rows
+  // for is not read.  (LDS then holds old values there, whose products are not
+  // stored.)
+  int off_a[8], off_b[8], off_s;
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const int q = i * NT + threadIdx.x, r = q >> 3;
+    off_a[i] = (int)(r * row_bytes) + (((q & 7) ^ row_swz<false>(r)) << 4);
+    off_b[i] = (int)(r * row_bytes) + (((q & 7) ^ row_swz<kPaired>(r)) << 4);
+  }
+  off_s = (int)(threadIdx.x * row_bytes);
+  const char *pa, *pb;
+  int64_t bytes_a, bytes_b;  // from the first row's line to the last one's end
+  int aimed_step;
+  auto aim = [&](const Where& x) {
+    const int64_t ra = x.M - x.m0, rb = x.N - x.n0;
+    pa = x.a + x.m0 * row_bytes;
+    pb = x.b + x.n0 * row_bytes;
+    bytes_a = ((ra < BM ? ra : BM) - 1) * row_bytes + KB;
+    bytes_b = ((rb < BN ? rb : BN) - 1) * row_bytes + KB;
+    aimed_step = 0;
+  };
+  // Load k of a step's 18: b's, the first half of a's (of each wave's 128 rows),
+  // the scales; then the second half of a's.
+  constexpr int kFirst = 14, kAll = 18;
+  auto load_at = [&](int i, uint32_t to, const int* off, u32x4 from) {
+    asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds"
+                 ::"s"(to), "n"(i * NT * 16), "v"(off[i]), "s"(from) : "memory", "scc");
+  };
+  auto load_scales = [&](uint32_t to, const char* p, int64_t bytes) {
+    const u32x4 from = bounded(p + (int64_t)(nk - aimed_step) * KB + 4 * aimed_step, bytes - KB + 4);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 ::"s"(to), "v"(off_s), "s"(from) : "memory");
+  };
+  auto load = [&](int k, int step) {
+    const uint32_t slot = lds0 + (step & 1) * kSlot + w * 1024, sc = lds0 + 4 * kSlot + (step & 3) * kScales + w * 256;
+    if (k < 8) load_at(k, slot + 2 * kSlot, off_b, bounded(pb, bytes_b));
+    else if (k < 12) load_at((k & 1) + (k & 2) * 2, slot, off_a, bounded(pa, bytes_a));
+    else if (k == 12) load_scales(sc, pa, bytes_a);
+    else if (k == 13) load_scales(sc + 1024, pb, bytes_b);
+    else load_at(((k - 14) & 1) + ((k - 14) & 2) * 2 + 2, slot, off_a, bounded(pa, bytes_a));
+  };
+  // To the next step, and from a tile's last one to the next tile's first.  Past
+  // the last tile the loads bring its last step again, into places that are not
+  // read any more: the count of loads on their way stays the same.
+  int aimed = 0;  // round
+  auto advance = [&]() {
+    if (aimed_step + 1 < nk) {
+      aimed_step++;
+      pa += KB;
+      pb += KB;
+    } else {
+      const int t = tile_of<false>(blockIdx.x, aimed + 1, tiles);
+      if (t >= 0) {
+        aimed++;
+        aim(place(t));
+      }
+    }
+  };
+
+  Frag8 a[T], b[T];
+  f32x4 acc[T][T];
+  constexpr int kStores = T * T / 2;
+  static_assert(kAll + kStores <= 63, "the wait count has 6 bits");
+
+  aim(place(tile_of<false>(blockIdx.x, 0, tiles)));  // a grid has no more workgroups than tiles
+#pragma unroll
+  for (int g = 0; g < 2; g++) {
+#pragma unroll
+    for (int k = 0; k < kAll; k++) load(k, g);
+    advance();
+  }
+  asm volatile("s_waitcnt vmcnt(18)\n\ts_barrier" ::: "memory");  // step 0
+#pragma unroll
+  for (int p = 0; p < 3; p++) {
+#pragma unroll
+    for (int i = 0; i < T; i++) b[i].read<kPaired>(lds + 2 * kSlot, scales + 1024, wn, i, p);
+#pragma unroll
+    for (int i = 0; i < 4; i++) a[i].read<false>(lds, scales, wm, i, p);
+  }
+  // A full tile's results are on their way during the next tile's first step and
+  // are counted with its loads.
+  bool stored = false;
+  int g = 0, t = tile_of<false>(blockIdx.x, 0, tiles);
+#pragma unroll 1
+  for (int round = 1; t >= 0; round++) {
+#pragma unroll
+    for (int i = 0; i < T; i++)
+#pragma unroll
+      for (int j = 0; j < T; j++) {
+        acc[i][j] = f32x4{0, 0, 0, 0};
+        asm volatile("" : "+a"(acc[i][j]));
+      }
+#pragma unroll 1
+    for (int s = 0; s < nk; s++, g++) {
+      const char* lines = lds + (g & 1) * kSlot;
+      const char* sc = scales + (g & 3) * kScales;
+      auto wait = [&]() {
+        if (stored) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kAll + kStores) : "memory");
+        else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kAll) : "memory");
+      };
+      // ---- first phase: a's first four fragments
+      constexpr int kBarrier = 6;  // products in front of the barrier
+#pragma unroll
+      for (int n = 0; n < 32; n++) {
+        mma8_acc(b[n / 4].v(), a[n % 4].v(), acc[n % 4][n / 4], b[n / 4].scale(), a[n % 4].scale());
+        // the last fragment of b, whose registers the phase before used to its end
+        // (in the very first step read again)
+        if (n < 3) b[7].read<kPaired>(lines + 2 * kSlot, sc + 1024, wn, 7, n);
+        // b and the first half of a are read by every wave; the second half is there
+        if (n == kBarrier) wait();
+        if (n > kBarrier && n <= kBarrier + 12) {
+          const int u = n - kBarrier - 1;
+          a[4 + u / 3].read<false>(lines, sc, wm, 4 + u / 3, u % 3);
+        }
+        if (n > kBarrier) {
+          constexpr int kRoom = 31 - kBarrier;
+          const int from = (n - kBarrier - 1) * kFirst / kRoom, to = (n - kBarrier) * kFirst / kRoom;
+#pragma unroll
+          for (int k = from; k < to; k++) load(k, g);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // the second half of a is read by every wave; the next step is there but for
+      // its second half of a
+      wait();
+      stored = false;  // the step behind waits for them
+      const char* lines1 = lds + ((g + 1) & 1) * kSlot;
+      const char* sc1 = scales + ((g + 1) & 3) * kScales;
+      // ---- second phase: a's last four (after the very last step this reads what
+      // the places hold; unused)
+#pragma unroll
+      for (int n = 0; n < 32; n++) {
+        mma8_acc(b[n / 4].v(), a[4 + n % 4].v(), acc[4 + n % 4][n / 4], b[n / 4].scale(), a[4 + n % 4].scale());
+        if (n < 12) a[n / 3].read<false>(lines1, sc1, wm, n / 3, n % 3);
+        if (n >= 4 && n % 4 < 3) b[n / 4 - 1].read<kPaired>(lines1 + 2 * kSlot, sc1 + 1024, wn, n / 4 - 1, n % 4);
+        if (n % 6 == 2 && n / 6 < kAll - kFirst) load(kFirst + n / 6, g);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      advance();
+    }
+    drain8(acc[T - 1]);
+
+    // D holds b's rows (the output's columns) down its registers: lane l has
+    // output row l % 16 of each block and of a pair of blocks columns 8 (l / 16) +
+    // (0..7).
+    const Where at = place(t);
+    const bool full = at.m0 + BM <= at.M && at.n0 + BN <= at.N;
+    const int64_t n = at.n0 + wn + (l >> 4) * 8;
+    char* out = at.c + ((at.m0 + wm + (l & 15)) * at.N + n) * 2;
+    const int64_t down = 16 * at.N * 2;
+    auto store = [&](int i, int j) {
+      asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i][j + 1]));  // read out row by row
+      const bf16x4 lo = __builtin_convertvector(acc[i][j], bf16x4), hi = __builtin_convertvector(acc[i][j + 1], bf16x4);
+      *reinterpret_cast<bf16x8*>(out + j * 32) = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    if (full) {
+#pragma unroll
+      for (int i = 0; i < T; i++) {
+#pragma unroll
+        for (int j = 0; j < T; j += 2) store(i, j);
+        out += down;
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < T; i++) {
+        const bool in = at.m0 + wm + i * 16 + (l & 15) < at.M;
+#pragma unroll
+        for (int j = 0; j < T; j += 2)
+          if (in && n + j * 16 < at.N) store(i, j);  // rows are whole vectors
+        out += down;
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // how many stores these were differs by wave: none is counted below
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    stored = full;
+    t = tile_of<false>(blockIdx.x, round, tiles);
+  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+}
+
 }  // namespace
 
 hipError_t launch_experts8(const ExpertTable& tab, const ExpertShape& sh, ExpertTile tile, int tiles,
@@ -186,6 +470,9 @@ hipError_t launch_experts8(const ExpertTable& tab, const ExpertShape& sh, Expert
       break;
     case ExpertTile::k64:
       experts8_ring_kernel<64, 64, 2, 2, 1, 3><<<(unsigned)tiles, 256, 0, stream>>>(tab, sh, row);
+      break;
+    case ExpertTile::k256:
+      experts8_big_kernel<<<(unsigned)(tiles < kCus ? tiles : kCus), 256, 0, stream>>>(tab, sh, row, tiles);
       break;
     default:
       experts8_ring_kernel<128, 128, 2, 4, 1, 4><<<(unsigned)tiles, 512, 0, stream>>>(tab, sh, row);
