@@ -183,7 +183,7 @@ __global__ __launch_bounds__(WM * WN * WK * 64) void experts8_ring_kernel(const 
 // during the last steps of this one, so that a tile's start waits for nothing.
 //
 // LDS holds two steps of lines (four slots of 32 KiB: a and b of an even and of an
-// odd step) and four of scales.  A step has two phases of 32 products: the first
+// odd step) and the scales of three groups of four steps.  A step has two phases of 32 products: the first
 // multiplies the first four fragments of a with all of b, the second the last
 // four.  Each phase reads the fragments that the next one needs, into the
 // registers that it sets free: the first a's last four of this step, the second
@@ -226,7 +226,7 @@ struct Frag8 {
   template <bool PAIRED>
   __device__ __forceinline__ void read(const char* lines, const char* sc, int x0, int i, int part) {
     if (part < 2) half[part] = fragment<1, 256, false, PAIRED>(lines, x0, i, part);
-    else scales = *reinterpret_cast<const uint32_t*>(sc + fragment_row<PAIRED>(x0, i) * 4);
+    else scales = *reinterpret_cast<const uint32_t*>(sc + fragment_row<PAIRED>(x0, i) * 16);
   }
   __device__ __forceinline__ i32x8 v() const { return __builtin_bit_cast(i32x8, half); }
   __device__ __forceinline__ int scale() const { return (int)(scales >> ((threadIdx.x & 48) >> 1)); }
@@ -241,9 +241,10 @@ __device__ __forceinline__ u32x4 bounded(const char* p, int64_t bytes) {
 
 __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable tab, const ExpertShape sh,
                                                               int64_t row_bytes, int tiles) {
-  constexpr int BM = 256, BN = 256, NT = 256, T = 8, kSlot = 256 * KB, kScales = 2048;
+  constexpr int BM = 256, BN = 256, NT = 256, T = 8, kSlot = 256 * KB;
+  constexpr int kGroup = 4, kScales = (BM + BN) * 4 * kGroup;  // steps whose scales are loaded together, their bytes
   constexpr bool kPaired = true;  // b: 16-byte stores of the results
-  __shared__ __align__(1024) char lds[4 * kSlot + 4 * kScales];  // a, a, b, b; the scales of a, of b
+  __shared__ __align__(1024) char lds[4 * kSlot + 3 * kScales + 1024];  // a, a, b, b; three groups' scales of a and b
   char* const scales = lds + 4 * kSlot;
   const int l = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -285,7 +286,7 @@ __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable 
   off_s = (int)(threadIdx.x * row_bytes);
   const char *pa, *pb;
   int64_t bytes_a, bytes_b;  // from the first row's line to the last one's end
-  int aimed_step;
+  int aimed_step, aimed_group = 2;  // the group's place, of the three
   auto aim = [&](const Where& x) {
     const int64_t ra = x.M - x.m0, rb = x.N - x.n0;
     pa = x.a + x.m0 * row_bytes;
@@ -293,6 +294,7 @@ __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable 
     bytes_a = ((ra < BM ? ra : BM) - 1) * row_bytes + KB;
     bytes_b = ((rb < BN ? rb : BN) - 1) * row_bytes + KB;
     aimed_step = 0;
+    aimed_group = aimed_group == 2 ? 0 : aimed_group + 1;
   };
   // Load k of a step's 18: b's, the first half of a's (of each wave's 128 rows),
   // the scales; then the second half of a's.
@@ -301,17 +303,21 @@ __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable 
     asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds"
                  ::"s"(to), "n"(i * NT * 16), "v"(off[i]), "s"(from) : "memory", "scc");
   };
-  auto load_scales = [&](uint32_t to, const char* p, int64_t bytes) {
-    const u32x4 from = bounded(p + (int64_t)(nk - aimed_step) * KB + 4 * aimed_step, bytes - KB + 4);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+  // In a group's first step its scales, 16 bytes of each row (a step's four alone
+  // would bring their line from the L2 in every step); else nothing.
+  auto load_scales = [&](int of_b, const char* p, int64_t bytes) {
+    const bool first = aimed_step % kGroup == 0;
+    const uint32_t to = lds0 + 4 * kSlot + (first ? aimed_group * kScales + of_b * (kScales / 2) + w * 1024 : 3 * kScales);
+    const u32x4 from = bounded(p + (int64_t)(nk - aimed_step) * KB + 4 * aimed_step, first ? bytes - KB + 16 : 0);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  ::"s"(to), "v"(off_s), "s"(from) : "memory");
   };
   auto load = [&](int k, int step) {
-    const uint32_t slot = lds0 + (step & 1) * kSlot + w * 1024, sc = lds0 + 4 * kSlot + (step & 3) * kScales + w * 256;
+    const uint32_t slot = lds0 + (step & 1) * kSlot + w * 1024;
     if (k < 8) load_at(k, slot + 2 * kSlot, off_b, bounded(pb, bytes_b));
     else if (k < 12) load_at((k & 1) + (k & 2) * 2, slot, off_a, bounded(pa, bytes_a));
-    else if (k == 12) load_scales(sc, pa, bytes_a);
-    else if (k == 13) load_scales(sc + 1024, pb, bytes_b);
+    else if (k == 12) load_scales(0, pa, bytes_a);
+    else if (k == 13) load_scales(1, pb, bytes_b);
     else load_at(((k - 14) & 1) + ((k - 14) & 2) * 2 + 2, slot, off_a, bounded(pa, bytes_a));
   };
   // To the next step, and from a tile's last one to the next tile's first.  Past
@@ -321,6 +327,7 @@ __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable 
   auto advance = [&]() {
     if (aimed_step + 1 < nk) {
       aimed_step++;
+      if (aimed_step % kGroup == 0) aimed_group = aimed_group == 2 ? 0 : aimed_group + 1;
       pa += KB;
       pb += KB;
     } else {
@@ -348,14 +355,14 @@ __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable 
 #pragma unroll
   for (int p = 0; p < 3; p++) {
 #pragma unroll
-    for (int i = 0; i < T; i++) b[i].read<kPaired>(lds + 2 * kSlot, scales + 1024, wn, i, p);
+    for (int i = 0; i < T; i++) b[i].read<kPaired>(lds + 2 * kSlot, scales + kScales / 2, wn, i, p);
 #pragma unroll
     for (int i = 0; i < 4; i++) a[i].read<false>(lds, scales, wm, i, p);
   }
   // A full tile's results are on their way during the next tile's first step and
   // are counted with its loads.
   bool stored = false;
-  int g = 0, t = tile_of<false>(blockIdx.x, 0, tiles);
+  int g = 0, group = 0, t = tile_of<false>(blockIdx.x, 0, tiles);
 #pragma unroll 1
   for (int round = 1; t >= 0; round++) {
 #pragma unroll
@@ -368,7 +375,9 @@ __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable 
 #pragma unroll 1
     for (int s = 0; s < nk; s++, g++) {
       const char* lines = lds + (g & 1) * kSlot;
-      const char* sc = scales + (g & 3) * kScales;
+      const char* sc = scales + group * kScales + s % kGroup * 4;
+      const int in1 = s + 1 < nk ? (s + 1) % kGroup : 0;  // of the next step, in its group
+      const int group1 = in1 != 0 ? group : group == 2 ? 0 : group + 1;
       auto wait = [&]() {
         if (stored) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kAll + kStores) : "memory");
         else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kAll) : "memory");
@@ -380,7 +389,7 @@ __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable 
         mma8_acc(b[n / 4].v(), a[n % 4].v(), acc[n % 4][n / 4], b[n / 4].scale(), a[n % 4].scale());
         // the last fragment of b, whose registers the phase before used to its end
         // (in the very first step read again)
-        if (n < 3) b[7].read<kPaired>(lines + 2 * kSlot, sc + 1024, wn, 7, n);
+        if (n < 3) b[7].read<kPaired>(lines + 2 * kSlot, sc + kScales / 2, wn, 7, n);
         // b and the first half of a are read by every wave; the second half is there
         if (n == kBarrier) wait();
         if (n > kBarrier && n <= kBarrier + 12) {
@@ -400,18 +409,19 @@ __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable 
       wait();
       stored = false;  // the step behind waits for them
       const char* lines1 = lds + ((g + 1) & 1) * kSlot;
-      const char* sc1 = scales + ((g + 1) & 3) * kScales;
+      const char* sc1 = scales + group1 * kScales + in1 * 4;
       // ---- second phase: a's last four (after the very last step this reads what
       // the places hold; unused)
 #pragma unroll
       for (int n = 0; n < 32; n++) {
         mma8_acc(b[n / 4].v(), a[4 + n % 4].v(), acc[4 + n % 4][n / 4], b[n / 4].scale(), a[4 + n % 4].scale());
         if (n < 12) a[n / 3].read<false>(lines1, sc1, wm, n / 3, n % 3);
-        if (n >= 4 && n % 4 < 3) b[n / 4 - 1].read<kPaired>(lines1 + 2 * kSlot, sc1 + 1024, wn, n / 4 - 1, n % 4);
+        if (n >= 4 && n % 4 < 3) b[n / 4 - 1].read<kPaired>(lines1 + 2 * kSlot, sc1 + kScales / 2, wn, n / 4 - 1, n % 4);
         if (n % 6 == 2 && n / 6 < kAll - kFirst) load(kFirst + n / 6, g);
         __builtin_amdgcn_sched_barrier(0);
       }
       advance();
+      group = group1;
     }
     drain8(acc[T - 1]);
 
