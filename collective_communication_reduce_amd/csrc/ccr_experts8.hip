@@ -25,6 +25,7 @@
 namespace ccr {
 namespace {
 
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 // As load_lds(), 4 bytes per lane.
@@ -175,7 +176,7 @@ __global__ __launch_bounds__(WM * WN * WK * 64) void experts8_ring_kernel(const 
 
 // ------------------------------------------------------------- large tiles
 // 256 x 256 tiles: four waves, one to a SIMD, each with a 128 x 128 part of the
-// tile in its accumulators: per K-step 64 matrix instructions on 16 fragments and
+// tile in its accumulators: per K-step 32 matrix instructions on 8 fragments and
 // their scales.
 //
 // The workgroup's tiles are one sequence of steps: a persistent workgroup takes
@@ -183,11 +184,11 @@ __global__ __launch_bounds__(WM * WN * WK * 64) void experts8_ring_kernel(const 
 // during the last steps of this one, so that a tile's start waits for nothing.
 //
 // LDS holds two steps of lines (four slots of 32 KiB: a and b of an even and of an
-// odd step) and the scales of three groups of four steps.  A step has two phases of 32 products: the first
-// multiplies the first four fragments of a with all of b, the second the last
-// four.  Each phase reads the fragments that the next one needs, into the
-// registers that it sets free: the first a's last four of this step, the second
-// b's (each behind its last product) and a's first four of the next step.  So a
+// odd step) and the scales of three groups of four steps.  A step has two phases of 16 products: the first
+// multiplies the first two fragments of a with all of b, the second the last
+// two.  Each phase reads the fragments that the next one needs, into the
+// registers that it sets free: the first a's last two of this step, the second
+// b's (each half behind its last product) and a's first two of the next step.  So a
 // line is loaded a step and a half before it is read, into the place of the one
 // that has just been read: behind a barrier a little into the first phase, b, the
 // first half of a and the scales of the step after next; behind one between the
@@ -196,40 +197,58 @@ __global__ __launch_bounds__(WM * WN * WK * 64) void experts8_ring_kernel(const 
 // With one wave to a SIMD nothing hides an instruction that stalls, so reads and
 // loads are placed one by one between the products.
 //
-// The products are written in assembly, as all 256 accumulation registers are
-// accumulators here.  No two products in a row touch the same one, so no wait
-// states are due between them; drain() provides those before they are read.  The
-// build reads the assembly and refuses one that moves an accumulator in the loop.
-// (s_nop: two wait states between the shift that makes a scale and its product.)
-__device__ __forceinline__ void mma8_acc(i32x8 a, i32x8 b, f32x4& d, int sa, int sb) {
-  asm("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
-      : "+a"(d) : "v"(a), "v"(b), "v"(sa), "v"(sb));
+// The products are 32 x 32 x 64: half as many instructions as 16 x 16 x 128 for
+// the same work, with twice the room between two of them for all others.  They
+// are written in assembly, as all 256 accumulation registers are accumulators
+// here.  No two in a row touch the same one, so no wait states are due between
+// them; drain8() provides those before they are read.  The build reads the
+// assembly and refuses one that moves an accumulator in the loop.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// D += a b^T over half a step, H of two.  (s_nop: two wait states between the
+// shift that makes a scale and its product.)
+template <int H>
+__device__ __forceinline__ void mma8_acc(i32x8 a, i32x8 b, f32x16& d, int sa, int sb) {
+  if constexpr (H == 0)
+    asm("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
+        : "+a"(d) : "v"(a), "v"(b), "v"(sa), "v"(sb));
+  else
+    asm("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[1,1,0]"
+        : "+a"(d) : "v"(a), "v"(b), "v"(sa), "v"(sb));
 }
-__device__ __forceinline__ void drain8(f32x4* d) {
-  asm volatile("s_nop 15\n\ts_nop 15"
-               : "+a"(d[0]), "+a"(d[1]), "+a"(d[2]), "+a"(d[3]), "+a"(d[4]), "+a"(d[5]), "+a"(d[6]),
-                 "+a"(d[7]));
+__device__ __forceinline__ void drain8(f32x16* d) {
+  asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15" : "+a"(d[0]), "+a"(d[1]), "+a"(d[2]), "+a"(d[3]));
 }
 
-// Row of the tile that lane l's row of the i-th fragment from x0 on is.
+// Row of the tile that lane l's row of the i-th fragment of 32 from x0 on is.
+// PAIRED: fragments 2 p and 2 p + 1 share 64 rows in turns of four, so that the
+// results that a lane holds of both are runs of eight.
 template <bool PAIRED>
 __device__ __forceinline__ int fragment_row(int x0, int i) {
-  const int j = threadIdx.x & 15;
-  return PAIRED ? x0 + (i >> 1) * 32 + (j >> 2) * 8 + (i & 1) * 4 + (j & 3) : x0 + i * 16 + j;
+  const int j = threadIdx.x & 31;
+  return PAIRED ? x0 + (i >> 1) * 64 + (j >> 2) * 8 + (i & 1) * 4 + (j & 3) : x0 + i * 32 + j;
 }
 
-// A fragment and the scales of its rows' step, read in three parts.  A lane's own
-// scale is a byte of its row's four.
+// 32 rows of a step, in two halves of 64 values: lane l holds row l % 32 and, with
+// g = l / 32, of half h the vectors 4 h + g and 4 h + 2 + g of its line, as the
+// matrix instruction takes them.  It gives the scale of values 64 h + 32 g +
+// (0..31): byte 2 h + g of its row's four, which the instruction picks as byte 2 h
+// of what scale() is.
 struct Frag8 {
-  u32x4 half[2];
+  u32x4 part[4];
   uint32_t scales;
   template <bool PAIRED>
-  __device__ __forceinline__ void read(const char* lines, const char* sc, int x0, int i, int part) {
-    if (part < 2) half[part] = fragment<1, 256, false, PAIRED>(lines, x0, i, part);
-    else scales = *reinterpret_cast<const uint32_t*>(sc + fragment_row<PAIRED>(x0, i) * 16);
+  __device__ __forceinline__ void read(const char* lines, const char* sc, int x0, int i, int n) {
+    const int r = fragment_row<PAIRED>(x0, i), g = (threadIdx.x & 63) >> 5;
+    if (n < 4) part[n] = *reinterpret_cast<const u32x4*>(lines + r * KB + (((2 * n + g) ^ row_swz<PAIRED>(r)) << 4));
+    else scales = *reinterpret_cast<const uint32_t*>(sc + r * 16);
   }
-  __device__ __forceinline__ i32x8 v() const { return __builtin_bit_cast(i32x8, half); }
-  __device__ __forceinline__ int scale() const { return (int)(scales >> ((threadIdx.x & 48) >> 1)); }
+  template <int H>
+  __device__ __forceinline__ i32x8 v() const {
+    return __builtin_shufflevector(__builtin_bit_cast(i32x4, part[2 * H]), __builtin_bit_cast(i32x4, part[2 * H + 1]), 0,
+                                   1, 2, 3, 4, 5, 6, 7);
+  }
+  __device__ __forceinline__ int scale() const { return (int)(scales >> ((threadIdx.x & 32) >> 2)); }
 };
 
 // Memory as the bounded buffer that loads to LDS take: a lane whose offset lies
@@ -241,7 +260,7 @@ __device__ __forceinline__ u32x4 bounded(const char* p, int64_t bytes) {
 
 __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable tab, const ExpertShape sh,
                                                               int64_t row_bytes, int tiles) {
-  constexpr int BM = 256, BN = 256, NT = 256, T = 8, kSlot = 256 * KB;
+  constexpr int BM = 256, BN = 256, NT = 256, T = 4, kSlot = 256 * KB;
   constexpr int kGroup = 4, kScales = (BM + BN) * 4 * kGroup;  // steps whose scales are loaded together, their bytes
   constexpr bool kPaired = true;  // b: 16-byte stores of the results
   __shared__ __align__(1024) char lds[4 * kSlot + 3 * kScales + 1024];  // a, a, b, b; three groups' scales of a and b
@@ -296,7 +315,7 @@ __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable 
     aimed_step = 0;
     aimed_group = aimed_group == 2 ? 0 : aimed_group + 1;
   };
-  // Load k of a step's 18: b's, the first half of a's (of each wave's 128 rows),
+  // Load k of a step's 18: the first half of a's (of each wave's 128 rows), b's,
   // the scales; then the second half of a's.
   constexpr int kFirst = 14, kAll = 18;
   auto load_at = [&](int i, uint32_t to, const int* off, u32x4 from) {
@@ -314,8 +333,8 @@ __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable 
   };
   auto load = [&](int k, int step) {
     const uint32_t slot = lds0 + (step & 1) * kSlot + w * 1024;
-    if (k < 8) load_at(k, slot + 2 * kSlot, off_b, bounded(pb, bytes_b));
-    else if (k < 12) load_at((k & 1) + (k & 2) * 2, slot, off_a, bounded(pa, bytes_a));
+    if (k < 4) load_at((k & 1) + (k & 2) * 2, slot, off_a, bounded(pa, bytes_a));
+    else if (k < 12) load_at(k - 4, slot + 2 * kSlot, off_b, bounded(pb, bytes_b));
     else if (k == 12) load_scales(0, pa, bytes_a);
     else if (k == 13) load_scales(1, pb, bytes_b);
     else load_at(((k - 14) & 1) + ((k - 14) & 2) * 2 + 2, slot, off_a, bounded(pa, bytes_a));
@@ -340,8 +359,8 @@ __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable 
   };
 
   Frag8 a[T], b[T];
-  f32x4 acc[T][T];
-  constexpr int kStores = T * T / 2;
+  f32x16 acc[T][T];
+  constexpr int kStores = 32;
   static_assert(kAll + kStores <= 63, "the wait count has 6 bits");
 
   aim(place(tile_of<false>(blockIdx.x, 0, tiles)));  // a grid has no more workgroups than tiles
@@ -353,11 +372,11 @@ __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable 
   }
   asm volatile("s_waitcnt vmcnt(18)\n\ts_barrier" ::: "memory");  // step 0
 #pragma unroll
-  for (int p = 0; p < 3; p++) {
+  for (int p = 0; p < 5; p++) {
 #pragma unroll
     for (int i = 0; i < T; i++) b[i].read<kPaired>(lds + 2 * kSlot, scales + kScales / 2, wn, i, p);
 #pragma unroll
-    for (int i = 0; i < 4; i++) a[i].read<false>(lds, scales, wm, i, p);
+    for (int i = 0; i < T / 2; i++) a[i].read<false>(lds, scales, wm, i, p);
   }
   // A full tile's results are on their way during the next tile's first step and
   // are counted with its loads.
@@ -369,7 +388,7 @@ __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable 
     for (int i = 0; i < T; i++)
 #pragma unroll
       for (int j = 0; j < T; j++) {
-        acc[i][j] = f32x4{0, 0, 0, 0};
+        acc[i][j] = f32x16{};
         asm volatile("" : "+a"(acc[i][j]));
       }
 #pragma unroll 1
@@ -382,22 +401,27 @@ __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable 
         if (stored) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kAll + kStores) : "memory");
         else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kAll) : "memory");
       };
-      // ---- first phase: a's first four fragments
-      constexpr int kBarrier = 6;  // products in front of the barrier
+      // ---- first phase: a's first two fragments
+      constexpr int kBarrier = 3;  // products in front of the barrier
+      auto product = [&](int n, int half_of_a) {
+        const int i = half_of_a * 2 + n % 2, j = n % 8 / 2;
+        if (n < 8) mma8_acc<0>(b[j].v<0>(), a[i].v<0>(), acc[i][j], b[j].scale(), a[i].scale());
+        else mma8_acc<1>(b[j].v<1>(), a[i].v<1>(), acc[i][j], b[j].scale(), a[i].scale());
+      };
 #pragma unroll
-      for (int n = 0; n < 32; n++) {
-        mma8_acc(b[n / 4].v(), a[n % 4].v(), acc[n % 4][n / 4], b[n / 4].scale(), a[n % 4].scale());
-        // the last fragment of b, whose registers the phase before used to its end
-        // (in the very first step read again)
-        if (n < 3) b[7].read<kPaired>(lines + 2 * kSlot, sc + kScales / 2, wn, 7, n);
+      for (int n = 0; n < 16; n++) {
+        product(n, 0);
+        // the last half fragment of b, whose registers the phase before used to its
+        // end (in the very first step read again)
+        if (n < 3) b[3].read<kPaired>(lines + 2 * kSlot, sc + kScales / 2, wn, 3, 2 + n);
         // b and the first half of a are read by every wave; the second half is there
         if (n == kBarrier) wait();
-        if (n > kBarrier && n <= kBarrier + 12) {
+        if (n > kBarrier && n <= kBarrier + 10) {
           const int u = n - kBarrier - 1;
-          a[4 + u / 3].read<false>(lines, sc, wm, 4 + u / 3, u % 3);
+          a[2 + u / 5].read<false>(lines, sc, wm, 2 + u / 5, u % 5);
         }
         if (n > kBarrier) {
-          constexpr int kRoom = 31 - kBarrier;
+          constexpr int kRoom = 15 - kBarrier;
           const int from = (n - kBarrier - 1) * kFirst / kRoom, to = (n - kBarrier) * kFirst / kRoom;
 #pragma unroll
           for (int k = from; k < to; k++) load(k, g);
@@ -410,14 +434,19 @@ __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable 
       stored = false;  // the step behind waits for them
       const char* lines1 = lds + ((g + 1) & 1) * kSlot;
       const char* sc1 = scales + group1 * kScales + in1 * 4;
-      // ---- second phase: a's last four (after the very last step this reads what
+      // ---- second phase: a's last two (after the very last step this reads what
       // the places hold; unused)
 #pragma unroll
-      for (int n = 0; n < 32; n++) {
-        mma8_acc(b[n / 4].v(), a[4 + n % 4].v(), acc[4 + n % 4][n / 4], b[n / 4].scale(), a[4 + n % 4].scale());
-        if (n < 12) a[n / 3].read<false>(lines1, sc1, wm, n / 3, n % 3);
-        if (n >= 4 && n % 4 < 3) b[n / 4 - 1].read<kPaired>(lines1 + 2 * kSlot, sc1 + kScales / 2, wn, n / 4 - 1, n % 4);
-        if (n % 6 == 2 && n / 6 < kAll - kFirst) load(kFirst + n / 6, g);
+      for (int n = 0; n < 16; n++) {
+        product(n, 1);
+        if (n < 10) a[n / 5].read<false>(lines1, sc1, wm, n / 5, n % 5);
+        // b's first halves from product 2 on, its second halves and scales from 10
+        if (n >= 2) {
+          const int j = n < 10 ? n / 2 - 1 : n / 2 - 5, h = n < 10 ? 0 : 1;
+          b[j].read<kPaired>(lines1 + 2 * kSlot, sc1 + kScales / 2, wn, j, 2 * h + n % 2);
+          if (h == 1 && n % 2 == 1) b[j].read<kPaired>(lines1 + 2 * kSlot, sc1 + kScales / 2, wn, j, 4);
+        }
+        if (n % 3 == 2 && n / 3 < kAll - kFirst) load(kFirst + n / 3, g);
         __builtin_amdgcn_sched_barrier(0);
       }
       advance();
@@ -426,39 +455,38 @@ __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable 
     drain8(acc[T - 1]);
 
     // D holds b's rows (the output's columns) down its registers: lane l has
-    // output row l % 16 of each block and of a pair of blocks columns 8 (l / 16) +
-    // (0..7).
+    // output row l % 32 of each block and of a pair of blocks columns 16 q + 8 (l /
+    // 32) + (0..7), q < 4.
     const Where at = place(t);
     const bool full = at.m0 + BM <= at.M && at.n0 + BN <= at.N;
-    const int64_t n = at.n0 + wn + (l >> 4) * 8;
-    char* out = at.c + ((at.m0 + wm + (l & 15)) * at.N + n) * 2;
-    const int64_t down = 16 * at.N * 2;
-    auto store = [&](int i, int j) {
-      asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i][j + 1]));  // read out row by row
-      const bf16x4 lo = __builtin_convertvector(acc[i][j], bf16x4), hi = __builtin_convertvector(acc[i][j + 1], bf16x4);
-      *reinterpret_cast<bf16x8*>(out + j * 32) = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    const int64_t n = at.n0 + wn + (l >> 5) * 8;
+    char* out = at.c + ((at.m0 + wm + (l & 31)) * at.N + n) * 2;
+    const int64_t down = 32 * at.N * 2;
+    auto store = [&](int i, int p, int q) {
+      f32x4 lo, hi;
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        lo[e] = acc[i][2 * p][4 * q + e];
+        hi[e] = acc[i][2 * p + 1][4 * q + e];
+      }
+      const bf16x4 x = __builtin_convertvector(lo, bf16x4), y = __builtin_convertvector(hi, bf16x4);
+      *reinterpret_cast<bf16x8*>(out + p * 128 + q * 32) = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
     };
-    if (full) {
 #pragma unroll
-      for (int i = 0; i < T; i++) {
+    for (int i = 0; i < T; i++) {
+      const bool in = full || at.m0 + wm + i * 32 + (l & 31) < at.M;
 #pragma unroll
-        for (int j = 0; j < T; j += 2) store(i, j);
-        out += down;
+      for (int p = 0; p < T / 2; p++) {
+        asm volatile("" : "+a"(acc[i][2 * p]), "+a"(acc[i][2 * p + 1]));  // read out row by row
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+          if (full || (in && n + p * 64 + q * 16 < at.N)) store(i, p, q);  // rows are whole vectors
         __builtin_amdgcn_sched_barrier(0);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < T; i++) {
-        const bool in = at.m0 + wm + i * 16 + (l & 15) < at.M;
-#pragma unroll
-        for (int j = 0; j < T; j += 2)
-          if (in && n + j * 16 < at.N) store(i, j);  // rows are whole vectors
-        out += down;
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      // how many stores these were differs by wave: none is counted below
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      out += down;
     }
+    // how many stores an incomplete tile's were differs by wave: none is counted
+    if (!full) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     stored = full;
     t = tile_of<false>(blockIdx.x, round, tiles);
   }
