@@ -184,18 +184,21 @@ __global__ __launch_bounds__(WM * WN * WK * 64) void experts8_ring_kernel(const 
 // during the last steps of this one, so that a tile's start waits for nothing.
 //
 // LDS holds two steps of lines (four slots of 32 KiB: a and b of an even and of an
-// odd step) and the scales of three groups of four steps.  A step has two phases of 16 products: the first
-// multiplies the first two fragments of a with all of b, the second the last
-// two.  Each phase reads the fragments that the next one needs, into the
-// registers that it sets free: the first a's last two of this step, the second
-// b's (each half behind its last product) and a's first two of the next step.  So a
-// line is loaded a step and a half before it is read, into the place of the one
-// that has just been read: behind a barrier a little into the first phase, b, the
-// first half of a and the scales of the step after next; behind one between the
-// phases, the second half of a.
+// odd step) and the scales of three groups of four steps.  A step has two phases of
+// 16 products: the first multiplies the first two fragments of a with all of b, the
+// second the last two.  Each phase reads the fragments that the next one needs,
+// into the registers that it sets free: the first a's last two of this step, the
+// second b's (each half behind its last product) and a's first two of the next
+// step.  So a line is loaded a step and a half before it is read, into the place of
+// the one that has just been read: behind a barrier a little into the first phase,
+// b, the first half of a and the scales of the step after next; behind one a little
+// into the second, the second half of a.
 //
 // With one wave to a SIMD nothing hides an instruction that stalls, so reads and
-// loads are placed one by one between the products.
+// loads are placed one by one between the products, no branch of the loop is taken
+// but its own, and a tile's first step is code of its own, whose products start the
+// sums: no pass over the accumulators sets them to zero (434 us before, 417 with
+// all of it; 196,608 rows of 2048 in 16 groups, each times 1024 rows).
 //
 // The products are 32 x 32 x 64: half as many instructions as 16 x 16 x 128 for
 // the same work, with twice the room between two of them for all others.  They
@@ -205,11 +208,14 @@ __global__ __launch_bounds__(WM * WN * WK * 64) void experts8_ring_kernel(const 
 // assembly and refuses one that moves an accumulator in the loop.
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// D += a b^T over half a step, H of two.  (s_nop: two wait states between the
-// shift that makes a scale and its product.)
-template <int H>
+// D += a b^T over half a step, H of two; FIRST: D = a b^T.  (s_nop: two wait states
+// between the shift that makes a scale and its product.)
+template <int H, bool FIRST>
 __device__ __forceinline__ void mma8_acc(i32x8 a, i32x8 b, f32x16& d, int sa, int sb) {
-  if constexpr (H == 0)
+  if constexpr (H == 0 && FIRST)
+    asm("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, 0, %3, %4 op_sel_hi:[0,0,0]"
+        : "=a"(d) : "v"(a), "v"(b), "v"(sa), "v"(sb));
+  else if constexpr (H == 0)
     asm("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
         : "+a"(d) : "v"(a), "v"(b), "v"(sa), "v"(sb));
   else
@@ -344,18 +350,19 @@ __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable 
   // read any more: the count of loads on their way stays the same.
   int aimed = 0;  // round
   auto advance = [&]() {
-    if (aimed_step + 1 < nk) {
-      aimed_step++;
-      if (aimed_step % kGroup == 0) aimed_group = aimed_group == 2 ? 0 : aimed_group + 1;
-      pa += KB;
-      pb += KB;
-    } else {
+    if (__builtin_expect(aimed_step + 1 == nk, 0)) {
       const int t = tile_of<false>(blockIdx.x, aimed + 1, tiles);
       if (t >= 0) {
         aimed++;
         aim(place(t));
       }
+      return;
     }
+    aimed_step++;
+    const int next_group = aimed_group == 2 ? 0 : aimed_group + 1;
+    aimed_group = aimed_step % kGroup == 0 ? next_group : aimed_group;
+    pa += KB;
+    pb += KB;
   };
 
   Frag8 a[T], b[T];
@@ -378,80 +385,82 @@ __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable 
 #pragma unroll
     for (int i = 0; i < T / 2; i++) a[i].read<false>(lds, scales, wm, i, p);
   }
-  // A full tile's results are on their way during the next tile's first step and
-  // are counted with its loads.
-  bool stored = false;
-  int g = 0, group = 0, t = tile_of<false>(blockIdx.x, 0, tiles);
-#pragma unroll 1
-  for (int round = 1; t >= 0; round++) {
+  // Step g of all, the s-th of its tile.
+  int g = 0, group = 0;
+  auto step = [&](auto first, int s, bool after) {
+    constexpr bool kFirstStep = decltype(first)::value;
+    const char* lines = lds + (g & 1) * kSlot;
+    const char* lines1 = lds + ((g + 1) & 1) * kSlot;
+    const char* sc = scales + group * kScales + s % kGroup * 4;
+    const int in1 = s + 1 < nk ? (s + 1) % kGroup : 0;  // of the next step, in its group
+    group = in1 != 0 ? group : group == 2 ? 0 : group + 1;
+    const char* sc1 = scales + group * kScales + in1 * 4;
+    // after: the full tile before left its results on their way, which the first
+    // step counts with the loads; the step behind waits for them
+    auto wait = [&]() {
+      if (kFirstStep && after)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kAll + kStores) : "memory");
+      else
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kAll) : "memory");
+    };
+    auto product = [&](int n, int half_of_a) {
+      const int i = half_of_a * 2 + n % 2, j = n % 8 / 2;
+      if (n < 8) mma8_acc<0, kFirstStep>(b[j].v<0>(), a[i].v<0>(), acc[i][j], b[j].scale(), a[i].scale());
+      else mma8_acc<1, kFirstStep>(b[j].v<1>(), a[i].v<1>(), acc[i][j], b[j].scale(), a[i].scale());
+    };
+    // Products of a phase in front of its barrier, which waits for the reads of the
+    // phase before: at the start of the phase they are still on their way.
+    constexpr int kBarrier = 4, kRoom = 15 - kBarrier;
+    // `count` things over the products behind the barrier: those of product n
+    auto spread = [&](int n, int count, auto&& f) {
+      if (n <= kBarrier) return;
 #pragma unroll
-    for (int i = 0; i < T; i++)
+      for (int k = (n - kBarrier - 1) * count / kRoom; k < (n - kBarrier) * count / kRoom; k++) f(k);
+    };
+    // ---- first phase: a's first two fragments
 #pragma unroll
-      for (int j = 0; j < T; j++) {
-        acc[i][j] = f32x16{};
-        asm volatile("" : "+a"(acc[i][j]));
-      }
-#pragma unroll 1
-    for (int s = 0; s < nk; s++, g++) {
-      const char* lines = lds + (g & 1) * kSlot;
-      const char* sc = scales + group * kScales + s % kGroup * 4;
-      const int in1 = s + 1 < nk ? (s + 1) % kGroup : 0;  // of the next step, in its group
-      const int group1 = in1 != 0 ? group : group == 2 ? 0 : group + 1;
-      auto wait = [&]() {
-        if (stored) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kAll + kStores) : "memory");
-        else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kAll) : "memory");
-      };
-      // ---- first phase: a's first two fragments
-      constexpr int kBarrier = 3;  // products in front of the barrier
-      auto product = [&](int n, int half_of_a) {
-        const int i = half_of_a * 2 + n % 2, j = n % 8 / 2;
-        if (n < 8) mma8_acc<0>(b[j].v<0>(), a[i].v<0>(), acc[i][j], b[j].scale(), a[i].scale());
-        else mma8_acc<1>(b[j].v<1>(), a[i].v<1>(), acc[i][j], b[j].scale(), a[i].scale());
-      };
+    for (int n = 0; n < 16; n++) {
+      product(n, 0);
+      // the last half fragment of b, whose registers the phase before used to its
+      // end (in the very first step read again)
+      if (n < 3) b[3].read<kPaired>(lines + 2 * kSlot, sc + kScales / 2, wn, 3, 2 + n);
+      // b and the first half of a are read by every wave; the second half is there
+      if (n == kBarrier) wait();
+      spread(n, 10, [&](int u) { a[2 + u % 2].read<false>(lines, sc, wm, 2 + u % 2, u < 2 ? 4 : u / 2 - 1); });
+      spread(n, kFirst, [&](int k) { load(k, g); });
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // ---- second phase: a's last two (after the very last step this reads what the
+    // places hold; unused)
 #pragma unroll
-      for (int n = 0; n < 16; n++) {
-        product(n, 0);
-        // the last half fragment of b, whose registers the phase before used to its
-        // end (in the very first step read again)
-        if (n < 3) b[3].read<kPaired>(lines + 2 * kSlot, sc + kScales / 2, wn, 3, 2 + n);
-        // b and the first half of a are read by every wave; the second half is there
-        if (n == kBarrier) wait();
-        if (n > kBarrier && n <= kBarrier + 10) {
-          const int u = n - kBarrier - 1;
-          a[2 + u / 5].read<false>(lines, sc, wm, 2 + u / 5, u % 5);
-        }
-        if (n > kBarrier) {
-          constexpr int kRoom = 15 - kBarrier;
-          const int from = (n - kBarrier - 1) * kFirst / kRoom, to = (n - kBarrier) * kFirst / kRoom;
-#pragma unroll
-          for (int k = from; k < to; k++) load(k, g);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
+    for (int n = 0; n < 16; n++) {
+      product(n, 1);
       // the second half of a is read by every wave; the next step is there but for
       // its second half of a
-      wait();
-      stored = false;  // the step behind waits for them
-      const char* lines1 = lds + ((g + 1) & 1) * kSlot;
-      const char* sc1 = scales + group1 * kScales + in1 * 4;
-      // ---- second phase: a's last two (after the very last step this reads what
-      // the places hold; unused)
-#pragma unroll
-      for (int n = 0; n < 16; n++) {
-        product(n, 1);
-        if (n < 10) a[n / 5].read<false>(lines1, sc1, wm, n / 5, n % 5);
-        // b's first halves from product 2 on, its second halves and scales from 10
-        if (n >= 2) {
-          const int j = n < 10 ? n / 2 - 1 : n / 2 - 5, h = n < 10 ? 0 : 1;
-          b[j].read<kPaired>(lines1 + 2 * kSlot, sc1 + kScales / 2, wn, j, 2 * h + n % 2);
-          if (h == 1 && n % 2 == 1) b[j].read<kPaired>(lines1 + 2 * kSlot, sc1 + kScales / 2, wn, j, 4);
-        }
-        if (n % 3 == 2 && n / 3 < kAll - kFirst) load(kFirst + n / 3, g);
-        __builtin_amdgcn_sched_barrier(0);
+      if (n == kBarrier) wait();
+      spread(n, 10, [&](int u) { a[u % 2].read<false>(lines1, sc1, wm, u % 2, u < 2 ? 4 : u / 2 - 1); });
+      // b's parts, each behind its last product: 0 and 1 of fragment j, 2 and 3 and
+      // the scales
+      if (n > kBarrier && n < 13)
+        b[(n - 5) / 2].read<kPaired>(lines1 + 2 * kSlot, sc1 + kScales / 2, wn, (n - 5) / 2, (n - 5) % 2);
+      if (n >= 10) {
+        const int j = n / 2 - 5;
+        b[j].read<kPaired>(lines1 + 2 * kSlot, sc1 + kScales / 2, wn, j, 2 + n % 2);
+        if (n % 2 == 1) b[j].read<kPaired>(lines1 + 2 * kSlot, sc1 + kScales / 2, wn, j, 4);
       }
-      advance();
-      group = group1;
+      spread(n, kAll - kFirst, [&](int k) { load(kFirst + k, g); });
+      __builtin_amdgcn_sched_barrier(0);
     }
+    advance();
+    g++;
+  };
+  bool stored = false;
+  int t = tile_of<false>(blockIdx.x, 0, tiles);
+#pragma unroll 1
+  for (int round = 1; t >= 0; round++) {
+    step(std::true_type{}, 0, stored);
+#pragma unroll 1
+    for (int s = 1; s < nk; s++) step(std::false_type{}, s, false);
     drain8(acc[T - 1]);
 
     // D holds b's rows (the output's columns) down its registers: lane l has
