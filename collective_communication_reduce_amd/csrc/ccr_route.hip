@@ -26,6 +26,8 @@
 namespace ccr {
 namespace {
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
 constexpr float kNegInf = -__builtin_inff();
 
 // Over the LPT neighbouring lanes that share a token, every lane's own result.
@@ -37,19 +39,38 @@ template <int CTRL, typename T>
 __device__ __forceinline__ T across(T x) {
   return __builtin_bit_cast(T, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
 }
+// The same for 64 bits, and the rows of 16 and halves of 32 lanes against each other.
+template <int CTRL, typename T>
+__device__ __forceinline__ T other(T x) {
+  if constexpr (sizeof(T) == 4) {
+    return across<CTRL>(x);
+  } else {
+    const u32x2 v = __builtin_bit_cast(u32x2, x);
+    return __builtin_bit_cast(T, u32x2{across<CTRL>(v[0]), across<CTRL>(v[1])});
+  }
+}
+template <typename T, typename F, typename S>
+__device__ __forceinline__ T swapped(T x, F&& f, S&& swap) {
+  if constexpr (sizeof(T) == 4) {
+    const auto r = swap(__builtin_bit_cast(uint32_t, x));
+    return f(__builtin_bit_cast(T, (uint32_t)r[0]), __builtin_bit_cast(T, (uint32_t)r[1]));
+  } else {
+    const u32x2 v = __builtin_bit_cast(u32x2, x);
+    const auto lo = swap(v[0]), hi = swap(v[1]);
+    return f(__builtin_bit_cast(T, u32x2{(uint32_t)lo[0], (uint32_t)hi[0]}),
+             __builtin_bit_cast(T, u32x2{(uint32_t)lo[1], (uint32_t)hi[1]}));
+  }
+}
 template <int N, typename T, typename F>
 __device__ __forceinline__ T reduce(T x, F&& f) {
-  if constexpr (sizeof(T) == 4) {
-    if constexpr (N > 1) x = f(x, across<0xb1>(x));
-    if constexpr (N > 2) x = f(x, across<0x4e>(x));
-    if constexpr (N > 4) x = f(x, across<0x141>(x));
-    if constexpr (N > 8) x = f(x, across<0x140>(x));
-    if constexpr (N > 16) x = f(x, __shfl_xor(x, 16));
-    if constexpr (N > 32) x = f(x, __shfl_xor(x, 32));
-  } else {
-#pragma unroll
-    for (int off = 1; off < N; off <<= 1) x = f(x, __shfl_xor(x, off));
-  }
+  if constexpr (N > 1) x = f(x, other<0xb1>(x));
+  if constexpr (N > 2) x = f(x, other<0x4e>(x));
+  if constexpr (N > 4) x = f(x, other<0x141>(x));
+  if constexpr (N > 8) x = f(x, other<0x140>(x));
+  if constexpr (N > 16)
+    x = swapped(x, f, [](uint32_t v) { return __builtin_amdgcn_permlane16_swap(v, v, false, false); });
+  if constexpr (N > 32)
+    x = swapped(x, f, [](uint32_t v) { return __builtin_amdgcn_permlane32_swap(v, v, false, false); });
   return x;
 }
 template <int N, typename T>
@@ -66,10 +87,10 @@ __device__ __forceinline__ T min_of(T x) {
 }
 
 // Keys in the order of their values: larger numbers for larger values, NaN
-// largest; never 0.
+// largest; never 0 (nor, of 32 bits, the largest number).
 __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.0f);  // -0 is 0
-  return x != x ? 0xffffffffu : b & 0x80000000u ? ~b : b | 0x80000000u;
+  return x != x ? 0xfffffffeu : b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ uint64_t ordered(double x) {
   const uint64_t b = __builtin_bit_cast(uint64_t, x + 0.0);
@@ -79,21 +100,32 @@ __device__ __forceinline__ float value_of(uint32_t k) {
   return __builtin_bit_cast(float, k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
+// exp(x), x <= 0: 2^n 2^f with n + f = x log2(e), whose last bits the second
+// product adds; off by two units of its 24 bits at most.
+__device__ __forceinline__ float exponential(float x) {
+  constexpr double kLog2e = 1.4426950408889634;
+  constexpr float kHigh = (float)kLog2e, kLow = (float)(kLog2e - (double)kHigh);
+  const float y = x < -200.0f ? -200.0f : x;  // 0 from -104 on; NaN stays
+  const float n = __builtin_rintf(y * kHigh);
+  const float f = __builtin_fmaf(y, kLow, __builtin_fmaf(y, kHigh, -n));
+  return ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
+}
+__device__ __forceinline__ double exponential(double x) { return exp(x); }
+
 // 1 / (1 + exp(-l)) without overflow, and its complement.
 template <typename T>
 struct Sigmoid {
   T s, rest;
 };
 __device__ __forceinline__ Sigmoid<float> sigmoid(float l) {
-  const float t = expf(-fabsf(l)), q = 1.0f / (1.0f + t);
+  const float t = exponential(-fabsf(l)), d = 1.0f + t, r = __builtin_amdgcn_rcpf(d);
+  const float q = __builtin_fmaf(r, __builtin_fmaf(-d, r, 1.0f), r);  // 1 / d
   return l >= 0 ? Sigmoid<float>{q, t * q} : Sigmoid<float>{t * q, q};
 }
 __device__ __forceinline__ Sigmoid<double> sigmoid(double l) {
   const double t = exp(-fabs(l)), q = 1.0 / (1.0 + t);
   return l >= 0 ? Sigmoid<double>{q, t * q} : Sigmoid<double>{t * q, q};
 }
-__device__ __forceinline__ float exponential(float x) { return expf(x); }
-__device__ __forceinline__ double exponential(double x) { return exp(x); }
 
 // The scores of a lane's J experts; l: the logits, -inf where there is none.
 template <int LPT, int J, typename T>
@@ -132,7 +164,7 @@ constexpr uint32_t kNone = 0xffffffffu;  // no choice
 // neighbours to a lane (without groups, one group on all lanes).  A lane's place
 // is where it would be if every lane held J.
 struct Layout {
-  int eg, q;  // experts of a group, lanes of a group (a power of two)
+  int eg, log_q;  // experts of a group, log2 of its lanes
 };
 
 // J values from p, the first n of them (the others: none).  Rows of logits need
@@ -169,7 +201,11 @@ template <int J, bool GROUPS>
 __device__ __forceinline__ void choose_exactly(const float* logits, const float* bias, const RouteShape& n,
                                             ExactRoom<GROUPS ? 64 * J : 1>* room, const Layout at, int J32,
                                             uint32_t* out) {
-  const int lane = threadIdx.x & 63;
+  int lane = threadIdx.x & 63;
+  int eg = at.eg, size = n.groups;
+  // seldom used: nothing of this is worth a register of the caller's loop
+  asm volatile("" : "+v"(lane), "+s"(eg), "+s"(size));
+  size = n.E / size;
   const bool real = GROUPS && n.group_top == 2;  // values, not only their order, count
   float l[J];
   double s[J], v[J];
@@ -191,11 +227,10 @@ __device__ __forceinline__ void choose_exactly(const float* logits, const float*
         room->key[lane * J + j] = l[j] == kNegInf ? (double)kNegInf : real && !bias ? s[j] : v[j];
     wave_sync();
     if (lane < n.groups) {
-      const int eg = n.E / n.groups;
       double a = kNegInf, b = kNegInf;
       bool nan = false;
-      for (int i = 0; i < eg; i++) {
-        const double x = room->key[lane * eg + i];
+      for (int i = 0; i < size; i++) {
+        const double x = room->key[lane * size + i];
         nan |= x != x;
         if (x > a) {
           b = a;
@@ -219,7 +254,7 @@ __device__ __forceinline__ void choose_exactly(const float* logits, const float*
     wave_sync();
 #pragma unroll
     for (int j = 0; j < J; j++)
-      if (lane * J + j < n.E && !room->keep[(lane * J + j) / (n.E / n.groups)]) key[j] = 0;
+      if (lane * J + j < n.E && !room->keep[(lane * J + j) / size]) key[j] = 0;
   }
   for (int k = 0; k < n.K; k++) {
     uint64_t m = 0;
@@ -236,8 +271,8 @@ __device__ __forceinline__ void choose_exactly(const float* logits, const float*
         if (open && key[j] == best) {
           open = false;
           key[j] = 0;
-          const int e = lane * J + j, g = e / at.eg, i = e - g * at.eg;
-          out[k] = (uint32_t)((g * at.q + i / J32) * J32 + i % J32) << 16 | (uint32_t)e;
+          const int e = lane * J + j, g = e / eg, i = e - g * eg;
+          out[k] = (uint32_t)(((g << at.log_q) + i / J32) * J32 + i % J32) << 16 | (uint32_t)e;
         }
     }
   }
@@ -245,36 +280,96 @@ __device__ __forceinline__ void choose_exactly(const float* logits, const float*
 }
 
 // ------------------------------------------------------------------ 32 bits
-// The wave's tokens' choices; l, s, bias: those of this lane's J experts, of
-// which e0 is the first.  Choice k of a token goes to out[tok][k], place and
-// expert.  Returns whether a decision of this lane's token was too near to make.
+// A network that sorts N numbers, N a power of two: sorts halves and merges them,
+// the merge splitting even and odd places (Batcher).
+template <int N>
+struct Network {
+  int n = 0, a[64] = {}, b[64] = {};
+  constexpr Network() {
+    for (int p = 1; p < N; p *= 2)
+      for (int k = p; k >= 1; k /= 2)
+        for (int j = k % p; j + k < N; j += 2 * k)
+          for (int i = 0; i < k && i + j + k < N; i++)
+            if ((i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+              a[n] = i + j;
+              b[n] = i + j + k;
+              n++;
+            }
+  }
+};
+
+// What a wave's lanes tell each other of their tokens.
+template <int LPT, int J>
+struct Room {
+  static constexpr int kTok = 64 / LPT;
+  uint32_t chosen[kTok][16];                       // choice k: its place and expert
+  u32x2 pick[kTok][16];                       // choice k: its lane and how often the lane had its key before; its key
+  __align__(16) uint32_t group[kTok][LPT];         // groups' values
+  __align__(16) uint32_t of_place[kTok][LPT * J];  // keys, then scores
+  // The word of a place: a lane's vectors in another order from lane to lane, or
+  // those of every fourth lane would lie in the same banks.
+  static __device__ __forceinline__ int at(int lane, int j) {
+    return J < 16 ? lane * J + j : lane * J + (((j >> 2) ^ (lane >> 2 & 3)) << 2 | (j & 3));
+  }
+  template <typename T>
+  __device__ __forceinline__ void put(int tok, int lane, const T* v) {
+#pragma unroll
+    for (int j = 0; j < J; j += 4) {
+      const T four[4] = {v[j], v[j + 1], v[j + 2], v[j + 3]};
+      *reinterpret_cast<dev::u32x4*>(&of_place[tok][at(lane, j)]) = __builtin_bit_cast(dev::u32x4, four);
+    }
+  }
+};
+
+// The wave's tokens' choices; l, s, bias: those of this lane's J experts.  Returns
+// whether a decision of this lane's token was too near to make.
+//
+// Each lane sorts its keys (they alone: 2 instructions to a comparison), and a
+// round takes the largest of the lanes' first ones.  Which expert a choice is, the
+// K lanes of the choices find at the end, all at once, among the winners' keys.
+// (Searching and striking out in every round took twice the instructions.)
 template <int LPT, int J, bool GROUPS>
-__device__ __forceinline__ bool choose(const float* l, const float* s, const float* bias, bool with_bias, int e0,
-                                       const RouteShape& n, int q, uint32_t (*out)[16]) {
-  const int sub = threadIdx.x % LPT, tok = (threadIdx.x & 63) / LPT;
+__device__ __forceinline__ bool choose(const float* l, const float* s, const float* bias, bool with_bias,
+                                       const RouteShape& n, const Layout at, int lane, Room<LPT, J>* room) {
+  const int sub = lane % LPT, tok = lane / LPT;
+  const bool of_scores = GROUPS && n.group_top == 2 && !with_bias;  // groups' values
   uint32_t key[J];
 #pragma unroll
   for (int j = 0; j < J; j++) key[j] = l[j] == kNegInf ? 0 : ordered(with_bias ? s[j] + bias[j] : l[j]);
+  room->put(tok, sub, key);
   // fp32 scores are off by up to 2^-21 (sigmoid) or 2^-20 (softmax) of the
   // largest one, the sum with the bias by 2^-24 of itself
   float err = 0x1p-21f;
-  if (!n.sigmoid && (with_bias || (GROUPS && n.group_top == 2))) {
+  if (!n.sigmoid && (with_bias || of_scores)) {
     float top = 0;
 #pragma unroll
     for (int j = 0; j < J; j++) top = fmaxf(top, s[j]);
     err = 0x1p-20f * max_of<LPT>(top);
   }
-  bool near = false;
+  bool near = false, keep = true;
+  uint32_t a = 0, b = 0;
+  auto merge = [&](uint32_t c, uint32_t d) {  // c >= d
+    b = max(min(a, c), max(b, d));
+    a = max(a, c);
+  };
+  if (of_scores) {
+#pragma unroll
+    for (int j = 0; j < J; j++) merge(key[j] ? ordered(s[j]) : 0, 0);
+  }
+  constexpr Network<J> net;
+#pragma unroll
+  for (int c = 0; c < net.n; c++) {
+    const uint32_t x = key[net.a[c]], y = key[net.b[c]];
+    key[net.a[c]] = max(x, y);
+    key[net.b[c]] = min(x, y);
+  }
   if constexpr (GROUPS) {
     // the two largest keys (scores, where the keys are logits) of the group
-    const bool of_scores = n.group_top == 2 && !with_bias;
-    uint32_t a = 0, b = 0;
-    auto merge = [&](uint32_t c, uint32_t d) {  // c >= d
-      b = max(min(a, c), max(b, d));
-      a = max(a, c);
-    };
-#pragma unroll
-    for (int j = 0; j < J; j++) merge(of_scores && key[j] ? ordered(s[j]) : key[j], 0);
+    if (!of_scores) {
+      a = key[0];
+      b = key[1];
+    }
+    const int q = 1 << at.log_q, g = sub >> at.log_q;
     if (q > 1) merge(across<0xb1>(a), across<0xb1>(b));
     if (q > 2) merge(across<0x4e>(a), across<0x4e>(b));
     if (q > 4) merge(across<0x141>(a), across<0x141>(b));
@@ -283,51 +378,65 @@ __device__ __forceinline__ bool choose(const float* l, const float* s, const flo
       if (q > 16) merge(__shfl_xor(a, 16), __shfl_xor(b, 16));
     }
     if (n.group_top == 2 && b != 0) a = ordered(value_of(a) + value_of(b));
-    const int g = sub / q;
-    if (g >= n.groups) a = 0;
+    if ((sub & (q - 1)) == 0) room->group[tok][g] = g < n.groups ? a : 0;
+    wave_sync();
+    // how many groups are before this one: a larger value, or as large and left
     int rank = 0;
-    const int first = threadIdx.x & 63 & ~(LPT - 1);
-    for (int i = 0; i < n.groups; i++) {
-      const uint32_t o = __shfl(a, first + i * q);
-      rank += o > a || (o == a && i < g);
+    for (int i = 0; i < n.groups; i += 4) {
+      const dev::u32x4 o = *reinterpret_cast<const dev::u32x4*>(&room->group[tok][i]);
+#pragma unroll
+      for (int k = 0; k < 4; k++) rank += i + k < n.groups && o[k] >= a + (i + k < g ? 0 : 1);
     }
-    const bool keep = rank < n.kept && g < n.groups;
+    keep = rank < n.kept && g < n.groups;
     if (with_bias || n.group_top == 2) {
-      const uint32_t low = min_of<LPT>(keep ? a : ~0u), high = max_of<LPT>(keep ? 0u : a);
+      const uint32_t low = min_of<LPT>(keep ? a : ~0u), high = max_of<LPT>(keep || g >= n.groups ? 0u : a);
       const float x = value_of(low), y = value_of(high);
       near |= high != 0 && !(x - y > 4 * err + 0x1p-21f * (fabsf(x) + fabsf(y)));
     }
-    if (!keep) {
-#pragma unroll
-      for (int j = 0; j < J; j++) key[j] = 0;
-    }
   }
-  uint32_t before = 0;
+  const uint64_t left = ((1ull << sub) - 1) << tok * LPT;  // the token's lanes before this one
+  uint32_t before = 0, mine = ~0u;
+  int again = 0;
   const int rounds = n.K + (with_bias ? 1 : 0);  // one more for the key that just missed
   for (int k = 0; k < rounds; k++) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < J; j++) m = max(m, key[j]);
-    const uint32_t best = max_of<LPT>(m);
+    const uint32_t m = keep ? key[0] : 0, best = max_of<LPT>(m);
     if (with_bias && k > 0 && best != 0) {
       const float x = value_of(before), y = value_of(best);
       near |= !(x - y > 2 * err + 0x1p-23f * (fabsf(x) + fabsf(y)));
     }
     before = best;
     if (k == n.K) break;
-    const int winner = min_of<LPT>(m == best ? sub : LPT);  // the lowest lane that has it
-    bool open = winner == sub && best != 0;
-    int at = 0;
+    const bool won = m == best && (__ballot(m == best) & left) == 0;  // the lowest lane that has it
+    if (won) {
+      again = best == mine ? again + 1 : 0;
+      mine = best;
+      room->pick[tok][k] = u32x2{(uint32_t)sub << 8 | (uint32_t)again, best};
+    }
 #pragma unroll
     for (int j = 0; j < J; j++) {
-      const bool hit = open && key[j] == best;
-      key[j] = hit ? 0 : key[j];
-      at = hit ? j : at;
-      open = open && !hit;
+      uint32_t here = key[j], next = j + 1 < J ? key[j + 1] : 0;
+      asm("" : "+v"(here), "+v"(next));  // two numbers: as two places to load from they made the array an indexed one
+      key[j] = won ? next : here;
     }
-    if (winner == sub) out[tok][k] = best == 0 ? kNone : (uint32_t)(sub * J + at) << 16 | (uint32_t)(e0 + at);
   }
   wave_sync();
+  if (sub < n.K) {
+    const u32x2 p = room->pick[tok][sub];
+    const int from = (int)(p[0] >> 8);
+    int skip = (int)(p[0] & 255), j = -1;
+#pragma unroll
+    for (int v = 0; v < J; v += 4) {
+      const dev::u32x4 x = *reinterpret_cast<const dev::u32x4*>(&room->of_place[tok][Room<LPT, J>::at(from, v)]);
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const bool same = x[i] == p[1];
+        j = same && skip == 0 ? v + i : j;
+        skip -= same;
+      }
+    }
+    room->chosen[tok][sub] = p[1] == 0 ? kNone : (uint32_t)(from * J + j) << 16 |
+                                                     (uint32_t)((from >> at.log_q) * at.eg + (from & ((1 << at.log_q) - 1)) * J + j);
+  }
   return near;
 }
 
@@ -335,22 +444,19 @@ __device__ __forceinline__ bool choose(const float* l, const float* s, const flo
 // step of its rank's tokens.  STATS: it counts its tokens' choices and sums their
 // scores, in its slot of the work array or, alone, in the results.
 template <int LPT, int J, bool GROUPS, bool STATS>
-__global__ __launch_bounds__(kBlock) void route_kernel(const RouteArgs a, const RouteShape n, const Layout at,
+__global__ __launch_bounds__(kBlock, LPT == 16 ? 4 : 2) void route_kernel(const RouteArgs a, const RouteShape n, const Layout at,
                                                        bool exact, int slots, float* work) {
   constexpr int kTok = 64 / LPT, kWaves = kBlock / 64, kPlaces = LPT * J;
   constexpr int kExactJ = (kPlaces + 63) / 64;
-  __shared__ uint32_t chosen[kWaves][kTok][16];
-  __shared__ __align__(16) float score[kWaves][kTok][kPlaces];
+  __shared__ Room<LPT, J> all_rooms[kWaves];
   __shared__ ExactRoom<GROUPS ? 64 * kExactJ : 1> rooms[GROUPS ? kWaves : 1];
   __shared__ int count[STATS ? kPlaces : 1];
   const int rank = blockIdx.x / slots, slot = blockIdx.x % slots;
-  const int wave = threadIdx.x >> 6, sub = threadIdx.x % LPT, tok = (threadIdx.x & 63) / LPT;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Room<LPT, J>& room = all_rooms[wave];
   const float* logits = a.logits[rank];
   const bool with_bias = a.bias[rank] != nullptr;
-  const int g = sub / at.q, i0 = sub % at.q * J, e0 = g * at.eg + i0;
-  const int mine = g * at.eg < n.E ? max(0, min(J, at.eg - i0)) : 0;
-  float bias[J], sums[J];
-  if (with_bias) load_some<J>(a.bias[rank] + (mine > 0 ? e0 : 0), mine, 0.0f, bias);
+  float sums[J];
   if constexpr (STATS) {
 #pragma unroll
     for (int j = 0; j < J; j++) sums[j] = 0;
@@ -358,28 +464,33 @@ __global__ __launch_bounds__(kBlock) void route_kernel(const RouteArgs a, const 
     __syncthreads();
   }
   for (int64_t t0 = ((int64_t)slot * kWaves + wave) * kTok; t0 < n.T; t0 += (int64_t)slots * kWaves * kTok) {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));  // what follows from it costs less anew than registers between the steps
+    const int sub = lane % LPT, tok = lane / LPT;
+    const int g = sub >> at.log_q, i0 = (sub & ((1 << at.log_q) - 1)) * J, e0 = g * at.eg + i0;
+    const int mine = g * at.eg < n.E ? max(0, min(J, at.eg - i0)) : 0;
     const int64_t t = t0 + tok;
     const bool live = t < n.T;
-    float l[J], s[J];
+    float l[J], s[J], bias[J];
     load_some<J>(logits + (live && mine > 0 ? t * n.E + e0 : 0), live ? mine : 0, kNegInf, l);
+    if (with_bias) load_some<J>(a.bias[rank] + (mine > 0 ? e0 : 0), mine, 0.0f, bias);
     scores<LPT, J, float>(l, n.sigmoid, s);
-#pragma unroll
-    for (int j = 0; j < J; j += 4)
-      *reinterpret_cast<dev::f32x4*>(&score[wave][tok][sub * J + j]) = dev::f32x4{s[j], s[j + 1], s[j + 2], s[j + 3]};
     if constexpr (STATS) {
 #pragma unroll
-      for (int j = 0; j < J; j++) sums[j] += l[j] == kNegInf ? 0.0f : s[j];
+      for (int j = 0; j < J; j++) sums[j] += s[j];
     }
     bool near = exact;
-    if (!exact) near = choose<LPT, J, GROUPS>(l, s, bias, with_bias, e0, n, at.q, chosen[wave]);
+    if (!exact) near = choose<LPT, J, GROUPS>(l, s, bias, with_bias, n, at, lane, &room);
     for (uint64_t todo = __ballot(near && live && sub == 0); todo; todo &= todo - 1) {
       const int k = (__ffsll((unsigned long long)todo) - 1) / LPT;
       choose_exactly<kExactJ, GROUPS>(logits + (t0 + k) * n.E, a.bias[rank], n, &rooms[GROUPS ? wave : 0], at, J,
-                                      chosen[wave][k]);
+                                      room.chosen[k]);
     }
     wave_sync();
-    const uint32_t c = live && sub < n.K ? chosen[wave][tok][sub & 15] : kNone;
-    float w = c != kNone ? score[wave][tok][c >> 16] : 0.0f;
+    room.put(tok, sub, s);
+    wave_sync();
+    const uint32_t c = live && sub < n.K ? room.chosen[tok][sub & 15] : kNone;
+    float w = c != kNone ? __builtin_bit_cast(float, room.of_place[tok][room.at((int)(c >> 16) / J, (int)(c >> 16) % J)]) : 0.0f;
     if (n.renorm) {
       const float total = sum_of<LPT>(w);
       w = total == 0.0f ? 0.0f : w / total;
@@ -394,14 +505,15 @@ __global__ __launch_bounds__(kBlock) void route_kernel(const RouteArgs a, const 
     wave_sync();
   }
   if constexpr (STATS) {
-#pragma unroll
-    for (int j = 0; j < J; j++) score[wave][tok][sub * J + j] = sums[j];
+    const int lane = threadIdx.x & 63;
+    room.put(lane / LPT, lane % LPT, sums);
     __syncthreads();
     for (int e = threadIdx.x; e < n.E; e += kBlock) {
-      const int eg = e / at.eg, i = e - eg * at.eg, p = (eg * at.q + i / J) * J + i % J;
+      const int eg = e / at.eg, i = e - eg * at.eg, of = (eg << at.log_q) + i / J, p = of * J + i % J;
       float s = 0;
 #pragma unroll
-      for (int k = 0; k < kWaves * kTok; k++) s += score[k / kTok][k % kTok][p];
+      for (int k = 0; k < kWaves * kTok; k++)
+        s += __builtin_bit_cast(float, all_rooms[k / kTok].of_place[k % kTok][room.at(of, i % J)]);
       if (slots == 1) {
         if (a.sums[rank]) a.sums[rank][e] = s;
         if (a.counts[rank]) a.counts[rank][e] = count[p];
@@ -414,27 +526,32 @@ __global__ __launch_bounds__(kBlock) void route_kernel(const RouteArgs a, const 
   }
 }
 
-// The slots' counts and sums, in the slots' order: a workgroup takes 64 experts,
-// a wave of it every fourth slot.
-__global__ __launch_bounds__(kBlock) void route_stats_kernel(const RouteArgs a, const float* work, int slots, int E) {
-  __shared__ double sum_part[kBlock / 64][64];
-  __shared__ int64_t count_part[kBlock / 64][64];
+// The slots' counts and sums, in an order of their own: a workgroup takes 64
+// experts, a wave of it every 16th slot (with 4 waves the reads of the slots were
+// most of the kernel: 9.8 us at 8 ranks of 128 slots and 256 experts).
+constexpr int kStatsBlock = 1024;
+__global__ __launch_bounds__(kStatsBlock) void route_stats_kernel(const RouteArgs a, const float* work, int slots, int E) {
+  constexpr int kWaves = kStatsBlock / 64;
+  __shared__ double sum_part[kWaves][64];
+  __shared__ int64_t count_part[kWaves][64];
   const int rank = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int e = blockIdx.x * 64 + lane;
   const float* from = work + (int64_t)rank * slots * 2 * E;
   double s = 0;
   int64_t c = 0;
-  if (e < E)
-    for (int k = wave; k < slots; k += kBlock / 64) {
+  if (e < E) {
+#pragma unroll 4
+    for (int k = wave; k < slots; k += kWaves) {
       s += (double)from[(int64_t)k * 2 * E + e];
       c += reinterpret_cast<const int*>(from)[((int64_t)k * 2 + 1) * E + e];
     }
+  }
   sum_part[wave][lane] = s;
   count_part[wave][lane] = c;
   __syncthreads();
   if (wave == 0 && e < E) {
 #pragma unroll
-    for (int k = 1; k < kBlock / 64; k++) {
+    for (int k = 1; k < kWaves; k++) {
       s += sum_part[k][lane];
       c += count_part[k][lane];
     }
@@ -537,7 +654,7 @@ __global__ __launch_bounds__(kBlock) void route_bwd_kernel(const RouteBwdArgs a,
 }
 
 hipError_t launch_stats(const RouteArgs& a, const RouteShape& n, const float* work, int slots, hipStream_t stream) {
-  route_stats_kernel<<<dim3((unsigned)((n.E + 63) / 64), (unsigned)n.R), kBlock, 0, stream>>>(a, work, slots, n.E);
+  route_stats_kernel<<<dim3((unsigned)((n.E + 63) / 64), (unsigned)n.R), kStatsBlock, 0, stream>>>(a, work, slots, n.E);
   return hipGetLastError();
 }
 
@@ -579,12 +696,12 @@ hipError_t launch_route(const RouteArgs& a, const RouteShape& n, float* work, hi
   for (int r = 0; r < n.R; r++) stats |= a.counts[r] || a.sums[r];
   if (n.T <= 0) return stats ? launch_stats(a, n, work, 0, stream) : hipSuccess;  // no slot: zeros
   const int groups = n.kept < n.groups ? n.groups : 1, eg = n.E / groups;
-  if (const int q = lanes_of(16, 4, groups, eg)) return launch_route_as<16, 4>(a, n, Layout{eg, q}, false, stats, work, stream);
-  if (const int q = lanes_of(16, 16, groups, eg)) return launch_route_as<16, 16>(a, n, Layout{eg, q}, false, stats, work, stream);
-  if (const int q = lanes_of(64, 4, groups, eg)) return launch_route_as<64, 4>(a, n, Layout{eg, q}, false, stats, work, stream);
-  if (const int q = lanes_of(64, 16, groups, eg)) return launch_route_as<64, 16>(a, n, Layout{eg, q}, false, stats, work, stream);
+  if (const int q = lanes_of(16, 4, groups, eg)) return launch_route_as<16, 4>(a, n, Layout{eg, __builtin_ctz((unsigned)q)}, false, stats, work, stream);
+  if (const int q = lanes_of(16, 16, groups, eg)) return launch_route_as<16, 16>(a, n, Layout{eg, __builtin_ctz((unsigned)q)}, false, stats, work, stream);
+  if (const int q = lanes_of(64, 4, groups, eg)) return launch_route_as<64, 4>(a, n, Layout{eg, __builtin_ctz((unsigned)q)}, false, stats, work, stream);
+  if (const int q = lanes_of(64, 16, groups, eg)) return launch_route_as<64, 16>(a, n, Layout{eg, __builtin_ctz((unsigned)q)}, false, stats, work, stream);
   // groups that do not fit the lanes: every token by the whole wave, in 64 bits
-  return launch_route_as<64, 16>(a, n, Layout{n.E, 64}, true, stats, work, stream);
+  return launch_route_as<64, 16>(a, n, Layout{n.E, 6}, true, stats, work, stream);
 }
 
 hipError_t launch_route_bwd(const RouteBwdArgs& a, const RouteShape& n, hipStream_t stream) {
