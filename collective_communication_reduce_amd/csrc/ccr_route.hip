@@ -207,15 +207,18 @@ __device__ __forceinline__ void choose_exactly(const float* logits, const float*
   asm volatile("" : "+v"(lane), "+s"(eg), "+s"(size));
   size = n.E / size;
   const bool real = GROUPS && n.group_top == 2;  // values, not only their order, count
-  float l[J];
+  float l[J], with[J];
   double s[J], v[J];
 #pragma unroll
-  for (int j = 0; j < J; j++) l[j] = lane * J + j < n.E ? logits[lane * J + j] : kNegInf;
+  for (int j = 0; j < J; j++) {
+    l[j] = lane * J + j < n.E ? logits[lane * J + j] : kNegInf;
+    with[j] = bias && lane * J + j < n.E ? bias[lane * J + j] : 0.0f;
+  }
   if (bias || real) scores<64, J, double>(l, n.sigmoid, s);
   uint64_t key[J];
 #pragma unroll
   for (int j = 0; j < J; j++) {
-    v[j] = bias && lane * J + j < n.E ? s[j] + (double)bias[lane * J + j] : (double)l[j];
+    v[j] = bias ? s[j] + (double)with[j] : (double)l[j];
     key[j] = l[j] == kNegInf ? 0 : ordered(v[j]);
   }
   if constexpr (GROUPS) {
@@ -229,6 +232,7 @@ __device__ __forceinline__ void choose_exactly(const float* logits, const float*
     if (lane < n.groups) {
       double a = kNegInf, b = kNegInf;
       bool nan = false;
+#pragma unroll 8
       for (int i = 0; i < size; i++) {
         const double x = room->key[lane * size + i];
         nan |= x != x;
@@ -245,6 +249,7 @@ __device__ __forceinline__ void choose_exactly(const float* logits, const float*
     if (lane < n.groups) {
       const uint64_t o = ordered(room->value[lane]);
       int rank = 0;
+#pragma unroll 4
       for (int i = 0; i < n.groups; i++) {
         const uint64_t p = ordered(room->value[i]);
         rank += p > o || (p == o && i < lane);
@@ -337,9 +342,10 @@ __device__ __forceinline__ bool choose(const float* l, const float* s, const flo
 #pragma unroll
   for (int j = 0; j < J; j++) key[j] = l[j] == kNegInf ? 0 : ordered(with_bias ? s[j] + bias[j] : l[j]);
   room->put(tok, sub, key);
-  // fp32 scores are off by up to 2^-21 (sigmoid) or 2^-20 (softmax) of the
-  // largest one, the sum with the bias by 2^-24 of itself
-  float err = 0x1p-21f;
+  // fp32 scores are off by up to 2^-22 (sigmoid: the exponential's two units at a
+  // quarter, one each of the sum, the reciprocal and the product) or 2^-20 of the
+  // largest one (softmax), the sum with the bias by 2^-24 of itself
+  float err = 0x1p-22f;
   if (!n.sigmoid && (with_bias || of_scores)) {
     float top = 0;
 #pragma unroll
