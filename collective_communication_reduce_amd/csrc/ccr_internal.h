@@ -262,8 +262,11 @@ struct Q8Args {
 };
 // Pieces of a row that one wave makes (64 vectors of the row) or one thread
 // expands (16 values), and the workgroups for `rows` rows.
+// Vectors that a lane makes 8-bit values of: 4 in rows of more than 2 for each lane.
+constexpr int q8_unroll(int es, int64_t H) { return q8_values(H) * es / 16 > 128 ? 4 : 1; }
 constexpr int64_t q8_chunks(bool to_q8, int es, int64_t H) {
-  return to_q8 ? (q8_values(H) * es / 16 + 63) / 64 : (H + 15) / 16;
+  const int64_t wave = 64 * q8_unroll(es, H);
+  return to_q8 ? (q8_values(H) * es / 16 + wave - 1) / wave : (H + 15) / 16;
 }
 constexpr int64_t q8_grid(bool to_q8, int es, int64_t rows, int64_t H) {
   const int64_t per = to_q8 ? kBlock / 64 : kBlock;

@@ -359,23 +359,31 @@ __global__ __launch_bounds__(kDwBlock) void norm_dw_kernel(const NormBwdArgs a, 
 }
 
 // -------------------------------------------------------------- 8-bit rows
-// A wave takes 64 vectors of the padded row, whatever the row's length.
-template <int ES>
+// A wave takes U times 64 vectors of the padded row: 4 where they are there for
+// it, so that it has 4 loads on their way (2 x 11,264 rows of 2048 bf16: 39 us with
+// one and its place in 64-bit divisions by lanes, 29 so).
+template <int ES, int U>
 __global__ __launch_bounds__(kBlock) void quantize_kernel(const Q8Args a, int R, int64_t vpr, int64_t values,
                                                           int64_t q_bytes, int64_t chunks) {
   constexpr int P = kPer<ES>;
-  const int64_t unit = (int64_t)blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6);
+  const int64_t unit = (int64_t)blockIdx.x * (kBlock / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int rank = 0;
   while (rank < R && unit >= a.first[rank + 1] * chunks) rank++;
   if (rank == R) return;
-  const int64_t k = unit - a.first[rank] * chunks, t = k / chunks;
-  const int64_t i = (k % chunks) * 64 + (threadIdx.x & 63);
+  const int64_t k = unit - a.first[rank] * chunks, t = k / chunks, c = k - t * chunks;
+  const int64_t i0 = c * (64 * U) + (threadIdx.x & 63);
   const u32x4* x = reinterpret_cast<const u32x4*>(a.rows[rank]) + t * vpr;
   char* q = a.q[rank] + t * q_bytes;
-  float f[P] = {};
-  if (i < vpr) unpack<ES>(x[i], f);
-  store_q8<P>(q, i, values, f);
-  if (k % chunks == chunks - 1) pad_q8<64>(q, values, q_bytes, threadIdx.x & 63);
+  u32x4 v[U];
+#pragma unroll
+  for (int u = 0; u < U; u++) v[u] = i0 + u * 64 < vpr ? x[i0 + u * 64] : u32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int u = 0; u < U; u++) {
+    float f[P];
+    unpack<ES>(v[u], f);
+    store_q8<P>(q, i0 + u * 64, values, f);
+  }
+  if (c == chunks - 1) pad_q8<64>(q, values, q_bytes, threadIdx.x & 63);
 }
 
 // A thread expands 16 bytes.
@@ -494,8 +502,11 @@ hipError_t launch_q8(bool to_q8, int es, const Q8Args& a, int R, int64_t H, hipS
   if (grid64 > kMaxGridWorkgroups) return hipErrorInvalidValue;
   const unsigned grid = (unsigned)grid64;
   const int64_t vpr = H * es >> 4, values = q8_values(H), row = q8_row_bytes(H), chunks = q8_chunks(to_q8, es, H);
-  if (to_q8 && es == 4) quantize_kernel<4><<<grid, kBlock, 0, stream>>>(a, R, vpr, values, row, chunks);
-  else if (to_q8) quantize_kernel<2><<<grid, kBlock, 0, stream>>>(a, R, vpr, values, row, chunks);
+  const bool wide = q8_unroll(es, H) == 4;
+  if (to_q8 && es == 4 && wide) quantize_kernel<4, 4><<<grid, kBlock, 0, stream>>>(a, R, vpr, values, row, chunks);
+  else if (to_q8 && es == 4) quantize_kernel<4, 1><<<grid, kBlock, 0, stream>>>(a, R, vpr, values, row, chunks);
+  else if (to_q8 && wide) quantize_kernel<2, 4><<<grid, kBlock, 0, stream>>>(a, R, vpr, values, row, chunks);
+  else if (to_q8) quantize_kernel<2, 1><<<grid, kBlock, 0, stream>>>(a, R, vpr, values, row, chunks);
   else if (es == 4) dequantize_kernel<4><<<grid, kBlock, 0, stream>>>(a, R, H, values, row, chunks);
   else dequantize_kernel<2><<<grid, kBlock, 0, stream>>>(a, R, H, values, row, chunks);
   return hipGetLastError();

@@ -91,11 +91,12 @@ __device__ __forceinline__ void q8_pack(const float* f, uint32_t* bytes, int* sc
     const uint32_t m = __builtin_bit_cast(uint32_t, f[j]) & 0x7fffffff;
     top = top > m ? top : m;
   }
-#pragma unroll
-  for (int off = 1; off < 32 / P; off <<= 1) {
-    const uint32_t o = __shfl_xor(top, off);
-    top = top > o ? top : o;
-  }
+  // over the block's neighbouring lanes: pairs, quads, halves of a row mirrored
+  static_assert(P >= 4 && P <= 16, "two to eight lanes");
+  auto merge = [&](int o) { top = top > (uint32_t)o ? top : (uint32_t)o; };
+  merge(__builtin_amdgcn_mov_dpp((int)top, 0xb1, 0xf, 0xf, true));
+  if constexpr (P < 16) merge(__builtin_amdgcn_mov_dpp((int)top, 0x4e, 0xf, 0xf, true));
+  if constexpr (P < 8) merge(__builtin_amdgcn_mov_dpp((int)top, 0x141, 0xf, 0xf, true));
   const int b = q8_scale(top);
   *scale = b;
   const float inv = __builtin_bit_cast(float, (uint32_t)(b < 255 ? 254 - b : 0) << 23);  // 2^(127 - b)
