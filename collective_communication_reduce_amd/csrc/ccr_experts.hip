@@ -635,22 +635,39 @@ ExpertTileSize expert_tile_size(ExpertTile tile) {
 // (products in bf16).  fp32 products of 8 x 16 rows, 512 x 512: 3.9, 6.0, 11.2,
 // 32.3; of 1 row, 8192 x 1024: 17.8, 55.1; weight gradients (fp32 out) of 64 x 4
 // rows, 2048 x 1024, from tile 32 on: 268, 161, 181, 109.  Large fp32 products
-// run at the rate of the matrix units from tile 64 on.
+// run at the rate of the matrix units from tile 64 on.  8-bit rows have constants
+// of their own, fitted to the products of 22 shapes from 1 to 90,000 rows (their
+// rows are whole lines); where the choice matters, us of the whole call, of which
+// the host's part hides all below 8.5:
+//   us at tile                        16     32     64    128    256
+//   1 row, 8192 x 1024              11.3   13.5   15.2   29.3   73.2
+//   64 x 5 rows, 2048 x 1024        36.2   27.7   25.5   30.8   31.2
+//   8 x 16 rows, 4096 x 4096        27.0   28.5   24.5   28.2   44.0
+//   64 x 100 rows, 2048 x 1024       208    110   53.4   42.4   34.4
+//   8 x 200 rows, 2048 x 2048        102   52.2   25.2   21.7   26.9
+//   4 x 500 rows, 1024 x 1024       47.4   18.2    9.3   10.8   17.4
+//   8 x 500 rows, 7168 x 2048        479    335    155    111   76.6
+//   16 x 700 rows, 2048 x 1024       325    148   68.1   58.4   31.7
 ExpertTile expert_tile(ExpertOp op, int es, int os, const ExpertShape& sh, const int64_t* rows, int n) {
   struct Cost {
     ExpertTile tile;
     double c0, c1, alone;
   };
   const bool f32 = es == 4;
-  const Cost costs[] = {{ExpertTile::k16, 0.3, op == ExpertOp::kProduct ? 0.07 : 0.09, f32 ? 0.058 : 0.03},
-                        {ExpertTile::k32, 0.25, f32 ? 0.15 : 0.09, f32 ? 0.2 : 0.11},
-                        {ExpertTile::k64, 0.4, f32 ? 0.52 : 0.2, f32 ? 0.52 : 0.2},
-                        {ExpertTile::k128, 2.0, f32 ? 2.0 : 0.5, f32 ? 2.0 : 0.44},
-                        {ExpertTile::k256, 1.0, 1.42, 1.1}};
-  const bool odd_lines = sh.H * es % 128 || (op != ExpertOp::kProduct && sh.F * es % 128);
+  const Cost of_rows8[] = {{ExpertTile::k16, 1.2, 0.06, 0.05},
+                           {ExpertTile::k32, 0.5, 0.176, 0.12},
+                           {ExpertTile::k64, 0.5, 0.33, 0.2},
+                           {ExpertTile::k128, 3.3, 0.89, 0.4},
+                           {ExpertTile::k256, 5.0, 1.3, 1.1}};
+  const Cost of_values[] = {{ExpertTile::k16, 0.3, op == ExpertOp::kProduct ? 0.07 : 0.09, f32 ? 0.058 : 0.03},
+                            {ExpertTile::k32, 0.25, f32 ? 0.15 : 0.09, f32 ? 0.2 : 0.11},
+                            {ExpertTile::k64, 0.4, f32 ? 0.52 : 0.2, f32 ? 0.52 : 0.2},
+                            {ExpertTile::k128, 2.0, f32 ? 2.0 : 0.5, f32 ? 2.0 : 0.44},
+                            {ExpertTile::k256, 1.0, 1.42, 1.1}};
+  const bool odd_lines = es > 1 && (sh.H * es % 128 || (op != ExpertOp::kProduct && sh.F * es % 128));
   ExpertTile best = ExpertTile::k16;
   double least = 0;
-  for (const Cost& c : costs) {
+  for (const Cost& c : es == 1 ? of_rows8 : of_values) {
     if (c.tile == ExpertTile::k256 && es == 4) continue;
     const ExpertTileSize x = expert_tile_size(c.tile);
     const int step = KB / es;
