@@ -43,10 +43,11 @@ __device__ __forceinline__ i32x8 fragment8(const char* lds, int x0, int i) {
 }
 
 // The scale that lane l gives for a fragment: of row l % 16, of values 32 g +
-// (0..31) of the step.  scales: four bytes per row.
+// (0..31) of the step.  scales: four bytes every STRIDE of them.
+template <int STRIDE>
 __device__ __forceinline__ int fragment_scale(const char* scales, int x0, int i) {
   const int l = threadIdx.x & 63;
-  return (uint8_t)scales[(x0 + i * 16 + (l & 15)) * 4 + (l >> 4)];
+  return (uint8_t)scales[(x0 + i * 16 + (l & 15)) * STRIDE + (l >> 4)];
 }
 
 // D (rows: a's, columns: b's) += a b^T over a K-step.
@@ -59,6 +60,13 @@ __device__ __forceinline__ f32x4 mma8(i32x8 a, i32x8 b, f32x4 d, int sa, int sb)
 // LDS, a step being the tile's lines of a, of b, and their scales.  Per round one
 // barrier: behind it the round's vectors are in LDS and the round before is read
 // by every wave, so its buffer takes the loads of the round NBUF - 1 ahead.
+//
+// Of a row's scales 16 bytes are loaded, of four steps: four of them alone in
+// every step asked the L2 for as many lines as the values do (8 x 200 rows, 2048 ->
+// 2048: 22.0 us, 15.6 so; 288 rows over 64 experts, 2048 -> 1024: 35.9 and 30.9).
+// They go in every fourth round to one of two places, and a wait leaves no more
+// loads on their way than lines have been loaded since.  The groups of WK = 4 are
+// in four steps at once and load each its own.
 template <int BM, int BN, int WM, int WN, int WK, int NBUF>
 __global__ __launch_bounds__(WM * WN * WK * 64) void experts8_ring_kernel(const ExpertTable tab,
                                                                           const ExpertShape sh, int64_t row_bytes) {
@@ -67,13 +75,17 @@ __global__ __launch_bounds__(WM * WN * WK * 64) void experts8_ring_kernel(const 
   constexpr int kABytes = BM * KB, kTile = (BM + BN) * KB;
   using LoadA = Loader<1, BM, false, false, NT>;
   using LoadB = Loader<1, BN, false, false, NT>;
-  constexpr int kScaleLoads = (BM + BN + NT - 1) / NT;  // of one dword per lane
-  constexpr int kStepBytes = kTile + kScaleLoads * NT * 4, kBuf = WK * kStepBytes;
-  constexpr int kLoads = LoadA::kLoads + LoadB::kLoads + kScaleLoads;
+  constexpr bool kFour = WK == 1;  // scales of four steps at a time
+  static_assert((BM + BN) <= NT || !kFour, "a row of scales to a lane");
+  static_assert((BM + BN) <= 64 || kFour, "a row of scales to a lane");
+  static_assert(NBUF <= 4, "a place for scales is read before it is loaded again");
+  constexpr int kStepBytes = kTile + (kFour ? 0 : NT * 4), kBuf = WK * kStepBytes;
+  constexpr int kPlace = kFour ? (BM + BN) * 16 : 0;
+  constexpr int kLoads = LoadA::kLoads + LoadB::kLoads + (kFour ? 0 : 1);
   static_assert(LoadA::kLoads * NT == BM * 8 && LoadB::kLoads * NT == BN * 8, "whole loads");
   static_assert((NBUF - 2) * kLoads <= 63, "the wait count has 6 bits");
   static_assert(WK == 1 || WK * BM * BN * 4 <= NBUF * kBuf, "the groups' sums fit the ring");
-  __shared__ __align__(1024) char lds[NBUF * kBuf];
+  __shared__ __align__(1024) char lds[NBUF * kBuf + 2 * kPlace];
   const Where at = place_of<ExpertOp::kProduct, BM, BN>(tab, sh, xcd_tile(blockIdx.x, gridDim.x));
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wk = w / (WM * WN), wg = w % (WM * WN);
@@ -84,26 +96,26 @@ __global__ __launch_bounds__(WM * WN * WK * 64) void experts8_ring_kernel(const 
   la.init(at.a, row_bytes, at.m0, at.M, thread);
   lb.init(at.b, row_bytes, at.n0, at.N, thread);
   const int nk = (int)((sh.H + KB - 1) / KB);
-  // this lane's rows of scales: those of a, then of b; past them the first ones again
-  const char* scale[kScaleLoads];
-#pragma unroll
-  for (int i = 0; i < kScaleLoads; i++) {
-    const int q = (i * NT + thread) % (BM + BN);
-    const int64_t r = q < BM ? q : q - BM, left = q < BM ? at.M - at.m0 : at.N - at.n0;
-    scale[i] = (q < BM ? la.base : lb.base) + (r < left ? r : left - 1) * row_bytes + (int64_t)nk * KB;
-  }
+  // this lane's row of scales: those of a, then of b; past them the first ones again
+  const int q = thread % (BM + BN);
+  const int64_t row = q < BM ? q : q - BM, left = q < BM ? at.M - at.m0 : at.N - at.n0;
+  const char* scale = (q < BM ? la.base : lb.base) + (row < left ? row : left - 1) * row_bytes + (int64_t)nk * KB;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(CCR_LDS char*)lds + wk * kStepBytes;
-  int j = wk < nk ? wk : nk - 1;  // the step that is loaded next; past the last one, that one again
+  int j = wk;  // the step that is loaded next; past the last one, that one again
   auto issue = [&](uint32_t to) {
-    const char *pa = la.base + (int64_t)j * KB, *pb = lb.base + (int64_t)j * KB;
+    const int s = j < nk ? j : nk - 1;
+    const char *pa = la.base + (int64_t)s * KB, *pb = lb.base + (int64_t)s * KB;
+    if constexpr (kFour) {
+      if (j % 4 == 0 && j < nk && wg < (BM + BN) / 64)
+        load_lds(lds0 + NBUF * kBuf + (j / 4 & 1) * kPlace + wg * 1024, scale + s * 4);
+    }
 #pragma unroll
     for (int i = 0; i < LoadA::kLoads; i++) load_lds(to + wg * 1024 + i * NT * 16, (uint32_t)la.off[i], pa);
 #pragma unroll
     for (int i = 0; i < LoadB::kLoads; i++)
       load_lds(to + kABytes + wg * 1024 + i * NT * 16, (uint32_t)lb.off[i], pb);
-#pragma unroll
-    for (int i = 0; i < kScaleLoads; i++) load_lds4(to + kTile + wg * 256 + i * NT * 4, scale[i] + j * 4);
-    j = j + WK < nk ? j + WK : nk - 1;
+    if constexpr (!kFour) load_lds4(to + kTile + wg * 256, scale + s * 4);
+    j += WK;
   };
 #pragma unroll
   for (int i = 0; i < NBUF - 1; i++) issue(lds0 + i * kBuf);
@@ -118,17 +130,19 @@ __global__ __launch_bounds__(WM * WN * WK * 64) void experts8_ring_kernel(const 
   for (int r = 0; r < rounds; r++) {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NBUF - 2) * kLoads) : "memory");
     const char* from = lds + cur + wk * kStepBytes;
+    const char* sc = kFour ? lds + NBUF * kBuf + (r / 4 & 1) * kPlace + r % 4 * 4 : from + kTile;
+    constexpr int kStride = kFour ? 16 : 4;
     i32x8 a[TM], b[TN];
     int sa[TM], sb[TN];
 #pragma unroll
     for (int i = 0; i < TM; i++) {
       a[i] = fragment8<BM>(from, wm, i);
-      sa[i] = fragment_scale(from + kTile, wm, i);
+      sa[i] = fragment_scale<kStride>(sc, wm, i);
     }
 #pragma unroll
     for (int n = 0; n < TN; n++) {
       b[n] = fragment8<BN>(from + kABytes, wn, n);
-      sb[n] = fragment_scale(from + kTile, BM + wn, n);
+      sb[n] = fragment_scale<kStride>(sc, BM + wn, n);
     }
     issue(lds0 + free);
     free = cur;
