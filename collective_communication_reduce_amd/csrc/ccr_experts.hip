@@ -640,14 +640,14 @@ ExpertTileSize expert_tile_size(ExpertTile tile) {
 // rows are whole lines); where the choice matters, us of the whole call, of which
 // the host's part hides all below 8.5:
 //   us at tile                        16     32     64    128    256
-//   1 row, 8192 x 1024              11.3   13.5   15.2   29.3   73.2
-//   64 x 5 rows, 2048 x 1024        36.2   27.7   25.5   30.8   31.2
-//   8 x 16 rows, 4096 x 4096        27.0   28.5   24.5   28.2   44.0
-//   64 x 100 rows, 2048 x 1024       208    110   53.4   42.4   34.4
-//   8 x 200 rows, 2048 x 2048        102   52.2   25.2   21.7   26.9
-//   4 x 500 rows, 1024 x 1024       47.4   18.2    9.3   10.8   17.4
-//   8 x 500 rows, 7168 x 2048        479    335    155    111   76.6
-//   16 x 700 rows, 2048 x 1024       325    148   68.1   58.4   31.7
+//   1 row, 8192 x 1024              10.7   13.3   18.4   34.4   73.3
+//   64 x 5 rows, 2048 x 1024        36.5   23.4   25.4   27.4   31.3
+//   8 x 16 rows, 4096 x 4096        27.4   22.3   21.8   23.5   43.5
+//   64 x 100 rows, 2048 x 1024       208   63.4   36.2   33.4   34.5
+//   8 x 200 rows, 2048 x 2048        103   30.9   22.5   16.2   26.6
+//   4 x 500 rows, 1024 x 1024       47.6   12.2    8.5    9.9   16.9
+//   8 x 500 rows, 7168 x 2048        480    183    107   73.8   77.6
+//   16 x 700 rows, 2048 x 1024       327   82.0   50.2   40.9   31.5
 ExpertTile expert_tile(ExpertOp op, int es, int os, const ExpertShape& sh, const int64_t* rows, int n) {
   struct Cost {
     ExpertTile tile;
@@ -655,9 +655,9 @@ ExpertTile expert_tile(ExpertOp op, int es, int os, const ExpertShape& sh, const
   };
   const bool f32 = es == 4;
   const Cost of_rows8[] = {{ExpertTile::k16, 1.2, 0.06, 0.05},
-                           {ExpertTile::k32, 0.5, 0.176, 0.12},
-                           {ExpertTile::k64, 0.5, 0.33, 0.2},
-                           {ExpertTile::k128, 3.3, 0.89, 0.4},
+                           {ExpertTile::k32, 0.22, 0.096, 0.12},
+                           {ExpertTile::k64, 0.6, 0.22, 0.2},
+                           {ExpertTile::k128, 2.6, 0.58, 0.45},
                            {ExpertTile::k256, 5.0, 1.3, 1.1}};
   const Cost of_values[] = {{ExpertTile::k16, 0.3, op == ExpertOp::kProduct ? 0.07 : 0.09, f32 ? 0.058 : 0.03},
                             {ExpertTile::k32, 0.25, f32 ? 0.15 : 0.09, f32 ? 0.2 : 0.11},
