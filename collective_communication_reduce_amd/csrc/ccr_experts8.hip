@@ -211,7 +211,7 @@ __global__ __launch_bounds__(WM * WN * WK * 64) void experts8_ring_kernel(const 
 // With one wave to a SIMD nothing hides an instruction that stalls, so reads and
 // loads are placed one by one between the products, no branch of the loop is taken
 // but its own, and a tile's first step is code of its own, whose products start the
-// sums: no pass over the accumulators sets them to zero (434 us before, 417 with
+// sums: no pass over the accumulators sets them to zero (434 us before, 412 with
 // all of it; 196,608 rows of 2048 over 64 experts of 1024 rows).
 //
 // The products are 32 x 32 x 64: half as many instructions as 16 x 16 x 128 for
