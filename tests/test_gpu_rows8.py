@@ -172,6 +172,29 @@ def test_whole_numbers_are_exact(ccr_mod, R, rows, H, F):
             at += n
 
 
+@pytest.mark.parametrize("H", [72, 200, 344, 520, 1160])
+def test_many_rows_are_exact(ccr_mod, H):
+    """The same over several rounds of the largest tiles, of 1 to 10 steps, with rows
+    and columns that end inside a tile: rows of -1, 0 and 1 against at most 60 values
+    of up to 4, in blocks of different powers of two."""
+    import torch
+    rng = np.random.default_rng(H)
+    rows, F = [12000, 0, 9001, 130, 257, 5000], 2040
+    counts = counts_of(rows, 1, len(rows), rng)
+    say(f"experts8 rows={rows} H={H} F={F}")
+    scale = np.repeat(rng.integers(-3, 4, size=-(-H // 32)), 32)[:H]
+    x = rng.integers(-1, 2, size=(sum(rows), H)).astype(np.float32)
+    w = np.zeros((len(rows), F, H), np.float32)
+    at = rng.integers(0, H, size=(len(rows), F, 60))
+    np.put_along_axis(w, at, rng.integers(-4, 5, size=at.shape).astype(np.float32), 2)
+    got, = run_experts(ccr_mod, [packed(np.ldexp(x, scale))], [packed(np.ldexp(w, -scale))], counts, H, F, more=3)
+    first = 0
+    for e, n in enumerate(rows):
+        want = torch.from_numpy(x[first:first + n]).cuda() @ torch.from_numpy(w[e]).cuda().t()  # whole numbers
+        assert torch.equal(got[first:first + n].float(), want)
+        first += n
+
+
 @pytest.mark.parametrize("R,rows,H,F", CASES)
 def test_against_the_reference(ccr_mod, R, rows, H, F):
     import torch
