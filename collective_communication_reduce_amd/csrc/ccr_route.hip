@@ -99,6 +99,9 @@ __device__ __forceinline__ uint64_t ordered(double x) {
 __device__ __forceinline__ float value_of(uint32_t k) {
   return __builtin_bit_cast(float, k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
+__device__ __forceinline__ double value_of(uint64_t k) {
+  return __builtin_bit_cast(double, k >> 63 ? k & ~(1ull << 63) : ~k);
+}
 
 // exp(x), x <= 0: 2^n 2^f with n + f = x log2(e), whose last bits the second
 // product adds; off by two units of its 24 bits at most.
@@ -192,8 +195,8 @@ __device__ __forceinline__ void load_some(const float* p, int n, float none, flo
 // One token's choice by a whole wave, keys in fp64.
 template <int E>
 struct ExactRoom {
-  double key[E];
-  double value[kRouteGroups];
+  uint64_t key[E];
+  uint64_t value[kRouteGroups];
   uint8_t keep[kRouteGroups];
 };
 
@@ -223,35 +226,28 @@ __device__ __forceinline__ void choose_exactly(const float* logits, const float*
   }
   if constexpr (GROUPS) {
     // a group's value: of one key that key, of two their sum (of scores, where
-    // the keys are logits); a group's masked experts add nothing
+    // the keys are logits); an expert that cannot be chosen is none of the two
 #pragma unroll
     for (int j = 0; j < J; j++)
-      if (lane * J + j < n.E)
-        room->key[lane * J + j] = l[j] == kNegInf ? (double)kNegInf : real && !bias ? s[j] : v[j];
+      if (lane * J + j < n.E) room->key[lane * J + j] = key[j] != 0 && real && !bias ? ordered(s[j]) : key[j];
     wave_sync();
     if (lane < n.groups) {
-      double a = kNegInf, b = kNegInf;
-      bool nan = false;
+      uint64_t a = 0, b = 0;
 #pragma unroll 8
       for (int i = 0; i < size; i++) {
-        const double x = room->key[lane * size + i];
-        nan |= x != x;
-        if (x > a) {
-          b = a;
-          a = x;
-        } else if (x > b) {
-          b = x;
-        }
+        const uint64_t x = room->key[lane * size + i], low = a < x ? a : x;
+        b = b > low ? b : low;
+        a = a > x ? a : x;
       }
-      room->value[lane] = nan ? __builtin_nan("") : n.group_top == 2 && b != (double)kNegInf ? a + b : a;
+      room->value[lane] = n.group_top == 2 && b != 0 ? ordered(value_of(a) + value_of(b)) : a;
     }
     wave_sync();
     if (lane < n.groups) {
-      const uint64_t o = ordered(room->value[lane]);
+      const uint64_t o = room->value[lane];
       int rank = 0;
 #pragma unroll 4
       for (int i = 0; i < n.groups; i++) {
-        const uint64_t p = ordered(room->value[i]);
+        const uint64_t p = room->value[i];
         rank += p > o || (p == o && i < lane);
       }
       room->keep[lane] = rank < n.kept;

@@ -196,6 +196,37 @@ def test_masked_experts_and_tokens(ccr_mod, E, groups, kept, top, score, with_bi
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,kept", [(64, 8, 2), (12, 4, 2), (256, 8, 3)])
+def test_a_bias_of_minus_infinity_counts_in_its_group(ccr_mod, E, groups, kept, score):
+    """The sum of a group's two largest keys is -infinity if the second one is, however
+    near other groups are to each other; only masked logits are left out."""
+    import torch
+    g = gen(E + 5)
+    T, K, eg = 40, 3, E // groups
+    l = torch.randn(T, E, generator=g, device="cuda")
+    bias = 0.1 * torch.randn(E, generator=g, device="cuda")
+    bias[1:eg] = NINF                       # the first group: one key is not -infinity,
+    bias[0] = 5.0                           # and it is the largest of all
+    l[::2, -eg:] = l[::2, -2 * eg:-eg]      # two groups of the same value: decided in 64 bits
+    bias[-eg:] = bias[-2 * eg:-eg]
+    l[5, :eg] = NINF
+    l[6, eg:] = NINF                        # the first group's value -infinity is above none at all
+    topk = torch.empty(T, K, dtype=torch.int32, device="cuda")
+    w = torch.empty(T, K, device="cuda")
+    with ccr_mod.Context(0) as c:
+        ccr_mod.ccr_moe_route(c, [l], [topk], [w], bias=[bias], score=score, groups=groups, kept=kept, group_top=2)
+        torch.cuda.synchronize()
+    keys = (scores_ref(l, score) + bias.double()).cpu()
+    for t in range(T):
+        open_ = [[e for e in range(i * eg, (i + 1) * eg) if float(l[t, e]) != NINF] for i in range(groups)]
+        value = [sum(sorted((float(keys[t, e]) for e in o), reverse=True)[:2]) for o in open_]
+        order = sorted((i for i in range(groups) if open_[i]), key=lambda i: (-value[i], i))[:kept]
+        order += [i for i in range(groups) if not open_[i]][:kept - len(order)]
+        chosen = sorted((e for i in order for e in open_[i]), key=lambda e: (-float(keys[t, e]), e))[:K]
+        assert topk[t].tolist() == chosen + [-1] * (K - len(chosen)), t
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_nan_shows_in_its_token_alone(ccr_mod, score):
     import torch
     l = torch.randn(6, 40, generator=gen(1), device="cuda")
