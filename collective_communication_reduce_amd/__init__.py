@@ -681,12 +681,16 @@ def ccr_q8_row_bytes(H: int) -> int:
 def _q8_lists(ctx, rows, q, what):
     """(row pointers, 8-bit row pointers, counts, H, dtype code) of lists of
     [..., H] tensors and of uint8 ones of the same rows."""
-    import torch
-    H = rows[0].shape[-1]
-    code, nbytes = _dtype_code(rows[0]), ccr_q8_row_bytes(H)
-    return (_buffers(ctx, rows, rows[0].dtype, [(*t.shape[:-1], H) for t in rows], what),
-            _buffers(ctx, q, torch.uint8, [(*t.shape[:-1], nbytes) for t in rows], "q"),
-            (ctypes.c_int64 * len(rows))(*[t.shape[:-1].numel() for t in rows]), H, code)
+    x = rows[0]
+    H, code = x.shape[-1], _dtype_code(x)
+    nbytes = ccr_q8_row_bytes(H)
+    r = _marshal().row_lists(rows, q, x.dtype, ctx.device, H, nbytes)
+    if r is None:
+        import torch
+        _buffers(ctx, rows, x.dtype, [(*t.shape[:-1], H) for t in rows], what)
+        _buffers(ctx, q, torch.uint8, [(*t.shape[:-1], nbytes) for t in rows], "q")
+        raise ValueError(f"{what} and q: rows do not match")
+    return (*r, H, code)
 
 
 def ccr_quantize_rows(ctx: Context, x: Sequence, q: Sequence, stream=None):

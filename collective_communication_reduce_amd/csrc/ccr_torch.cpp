@@ -8,6 +8,10 @@
 //       the index of the first tensor that is not a contiguous tensor of `dtype`
 //       on GPU `device` with its entry of `shapes` as its shape (if `room`, the
 //       first dimension may be larger)
+//   row_lists(rows, q, dtype, device, H, row_bytes) -> (data pointers of rows, of
+//       q, rows of each) as bytes (uint64, uint64, int64), or None where one is
+//       not a contiguous tensor [..., H] of `dtype`, or uint8 [..., row_bytes] of
+//       the same rows, on GPU `device`
 //   grad_list(tensors) -> (data pointers, element counts, dtype codes) as bytes
 //       (uint64, int64, int32), or the index of the first tensor that is not a
 //       contiguous GPU tensor of float32 (code 0) or bfloat16 (code 1)
@@ -83,6 +87,47 @@ PyObject* pointers(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     p[static_cast<size_t>(i)] = reinterpret_cast<uint64_t>(t.data_ptr());
   }
   return as_bytes(p);
+}
+
+PyObject* row_lists(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  if (nargs != 6 || !THPDtype_Check(args[2])) {
+    PyErr_SetString(PyExc_TypeError, "row_lists(rows, q, dtype, device, H, row_bytes)");
+    return nullptr;
+  }
+  Items rows(args[0], "a list of tensors"), q(args[1], "a list of tensors");
+  if (!rows.ok() || !q.ok()) return nullptr;
+  const at::ScalarType dtype = reinterpret_cast<THPDtype*>(args[2])->scalar_type;
+  const long device = PyLong_AsLong(args[3]);
+  const long long H = PyLong_AsLongLong(args[4]), row_bytes = PyLong_AsLongLong(args[5]);
+  if (PyErr_Occurred()) return nullptr;
+  const size_t n = static_cast<size_t>(rows.size());
+  if (static_cast<size_t>(q.size()) != n) Py_RETURN_NONE;
+  std::vector<uint64_t> p(n), pq(n);
+  std::vector<int64_t> count(n);
+  for (size_t i = 0; i < n; i++) {
+    PyObject *a = rows[static_cast<Py_ssize_t>(i)], *b = q[static_cast<Py_ssize_t>(i)];
+    if (!THPVariable_Check(a) || !THPVariable_Check(b)) Py_RETURN_NONE;
+    const at::Tensor &x = THPVariable_Unpack(a), &y = THPVariable_Unpack(b);
+    const int64_t d = x.dim();
+    if (x.scalar_type() != dtype || y.scalar_type() != at::kByte || !x.is_cuda() || !y.is_cuda() ||
+        x.get_device() != device || y.get_device() != device || !x.is_contiguous() || !y.is_contiguous() ||
+        d < 1 || y.dim() != d || x.size(d - 1) != H || y.size(d - 1) != row_bytes)
+      Py_RETURN_NONE;
+    int64_t c = 1;
+    for (int64_t k = 0; k + 1 < d; k++) {
+      if (x.size(k) != y.size(k)) Py_RETURN_NONE;
+      c *= x.size(k);
+    }
+    p[i] = reinterpret_cast<uint64_t>(x.data_ptr());
+    pq[i] = reinterpret_cast<uint64_t>(y.data_ptr());
+    count[i] = c;
+  }
+  PyObject *a = as_bytes(p), *b = as_bytes(pq), *c = as_bytes(count);
+  PyObject* r = a && b && c ? PyTuple_Pack(3, a, b, c) : nullptr;
+  Py_XDECREF(a);
+  Py_XDECREF(b);
+  Py_XDECREF(c);
+  return r;
 }
 
 PyObject* grad_list(PyObject*, PyObject* arg) {
@@ -162,6 +207,9 @@ PyObject* no_throw(F&& f) {
 PyObject* py_pointers(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   return no_throw([&] { return pointers(self, args, n); });
 }
+PyObject* py_row_lists(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  return no_throw([&] { return row_lists(self, args, n); });
+}
 PyObject* py_grad_list(PyObject* self, PyObject* arg) {
   return no_throw([&] { return grad_list(self, arg); });
 }
@@ -172,6 +220,8 @@ PyObject* py_expert_rows(PyObject* self, PyObject* const* args, Py_ssize_t n) {
 
 PyMethodDef methods[] = {
     {"pointers", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_pointers)), METH_FASTCALL,
+     nullptr},
+    {"row_lists", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_row_lists)), METH_FASTCALL,
      nullptr},
     {"expert_rows", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_expert_rows)),
      METH_FASTCALL, nullptr},
