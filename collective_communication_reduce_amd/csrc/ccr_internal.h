@@ -260,16 +260,21 @@ struct Q8Args {
   char* q[kRingHopMaxRanks];
   int64_t first[kRingHopMaxRanks + 1];
 };
-// Pieces of a row that one wave makes (64 vectors of the row) or one thread
-// expands (16 values), and the workgroups for `rows` rows.
-// Vectors that a lane makes 8-bit values of: 4 in rows of more than 2 for each lane.
+// Vectors that a lane makes 8-bit values of: 4 in rows of more than 2 for each lane;
+// whole rows of a wave: as many as fit, of 16 and 32 vectors; the pieces of a row
+// that one wave makes or one thread expands (16 values); and the workgroups for
+// `rows` rows.
 constexpr int q8_unroll(int es, int64_t H) { return q8_values(H) * es / 16 > 128 ? 4 : 1; }
+constexpr int q8_rows(int es, int64_t H) {
+  const int64_t vectors = q8_values(H) * es / 16;  // a multiple of 16 (bf16) or 32
+  return vectors == 16 ? 4 : vectors == 32 ? 2 : 1;
+}
 constexpr int64_t q8_chunks(bool to_q8, int es, int64_t H) {
   const int64_t wave = 64 * q8_unroll(es, H);
   return to_q8 ? (q8_values(H) * es / 16 + wave - 1) / wave : (H + 15) / 16;
 }
 constexpr int64_t q8_grid(bool to_q8, int es, int64_t rows, int64_t H) {
-  const int64_t per = to_q8 ? kBlock / 64 : kBlock;
+  const int64_t per = to_q8 ? kBlock / 64 * q8_rows(es, H) : kBlock;
   return (rows * q8_chunks(to_q8, es, H) + per - 1) / per;
 }
 // To 8 bits, or back (rows is written then).

@@ -53,10 +53,11 @@ __device__ __forceinline__ u32x4 pack(const float* f) {
   return v;
 }
 
-template <typename T>
-__device__ __forceinline__ T wave_sum(T x) {
+// The sum over each N neighbouring lanes, in all of them.
+template <int N, typename T>
+__device__ __forceinline__ T lanes_sum(T x) {
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) x += __shfl_xor(x, off);
+  for (int off = N / 2; off >= 1; off >>= 1) x += __shfl_xor(x, off);
   return x;
 }
 
@@ -65,7 +66,7 @@ __device__ __forceinline__ T wave_sum(T x) {
 // after the next barrier.
 template <typename T>
 __device__ __forceinline__ T block_sum(T x, T* part) {
-  x = wave_sum(x);
+  x = lanes_sum<64>(x);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
   __syncthreads();
   T s = 0;

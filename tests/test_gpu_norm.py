@@ -249,6 +249,16 @@ def test_backward_against_differences(ccr_mod):
         assert abs(float(dw[i]) - float(diff)) <= 100 * U * float(mag.sum()) + 1e-9
 
 
+@pytest.mark.parametrize("add", [False, True])
+@pytest.mark.parametrize("dt,wdt", [("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("R,T,H", [(3, 37, 56), (2, 50, 200), (2, 41, 384), (1, 33, 960), (1, 19, 2040), (1, 6, 16384)])
+def test_rows_of_every_length(ccr_mod, R, T, H, dt, wdt, add):
+    """Numbers of rows that end inside a wave and a workgroup, in rows of sixteenths of
+    a wave's lanes up to several vectors to each lane of a workgroup."""
+    test_forward(ccr_mod, R, T, H, dt, wdt, add)
+    test_backward(ccr_mod, R, T, H, dt, wdt, add)
+
+
 @pytest.mark.parametrize("H", [64, 2048, 16392])
 def test_dx_in_the_place_of_dh(ccr_mod, H):
     import torch
