@@ -446,7 +446,7 @@ __device__ __forceinline__ bool choose(const float* l, const float* s, const flo
 // step of its rank's tokens.  STATS: it counts its tokens' choices and sums their
 // scores, in its slot of the work array or, alone, in the results.
 template <int LPT, int J, bool GROUPS, bool STATS>
-__global__ __launch_bounds__(kBlock, LPT == 16 ? 4 : 2) void route_kernel(const RouteArgs a, const RouteShape n, const Layout at,
+__global__ __launch_bounds__(kBlock, LPT == 16 ? 4 : LPT == 32 ? 3 : 2) void route_kernel(const RouteArgs a, const RouteShape n, const Layout at,
                                                        bool exact, int slots, float* work) {
   constexpr int kTok = 64 / LPT, kWaves = kBlock / 64, kPlaces = LPT * J;
   constexpr int kExactJ = (kPlaces + 63) / 64;
@@ -697,10 +697,14 @@ hipError_t launch_route(const RouteArgs& a, const RouteShape& n, float* work, hi
   bool stats = false;
   for (int r = 0; r < n.R; r++) stats |= a.counts[r] || a.sums[r];
   if (n.T <= 0) return stats ? launch_stats(a, n, work, 0, stream) : hipSuccess;  // no slot: zeros
+  // As few lanes to a token as hold its experts: what all lanes do for a choice is
+  // shared by more tokens (65,536 tokens, us; 16 lanes with 4 and 16 experts each, 32
+  // and 64 with 16; E = 64: 18, 41; 256: 45, 89, 228; 512: 83, 234; 256 in 32
+  // groups, which 32 lanes hold: 105, 281).
   const int groups = n.kept < n.groups ? n.groups : 1, eg = n.E / groups;
   if (const int q = lanes_of(16, 4, groups, eg)) return launch_route_as<16, 4>(a, n, Layout{eg, __builtin_ctz((unsigned)q)}, false, stats, work, stream);
   if (const int q = lanes_of(16, 16, groups, eg)) return launch_route_as<16, 16>(a, n, Layout{eg, __builtin_ctz((unsigned)q)}, false, stats, work, stream);
-  if (const int q = lanes_of(64, 4, groups, eg)) return launch_route_as<64, 4>(a, n, Layout{eg, __builtin_ctz((unsigned)q)}, false, stats, work, stream);
+  if (const int q = lanes_of(32, 16, groups, eg)) return launch_route_as<32, 16>(a, n, Layout{eg, __builtin_ctz((unsigned)q)}, false, stats, work, stream);
   if (const int q = lanes_of(64, 16, groups, eg)) return launch_route_as<64, 16>(a, n, Layout{eg, __builtin_ctz((unsigned)q)}, false, stats, work, stream);
   // groups that do not fit the lanes: every token by the whole wave, in 64 bits
   return launch_route_as<64, 16>(a, n, Layout{n.E, 6}, true, stats, work, stream);
@@ -708,8 +712,10 @@ hipError_t launch_route(const RouteArgs& a, const RouteShape& n, float* work, hi
 
 hipError_t launch_route_bwd(const RouteBwdArgs& a, const RouteShape& n, hipStream_t stream) {
   if (n.T <= 0) return hipSuccess;
+  // likewise (E = 64: 12 us, 29; 256: 51, 50; 512: 90, 119)
   if (n.E <= 64) return launch_route_bwd_as<16, 4>(a, n, stream);
   if (n.E <= 256) return launch_route_bwd_as<16, 16>(a, n, stream);
+  if (n.E <= 512) return launch_route_bwd_as<32, 16>(a, n, stream);
   return launch_route_bwd_as<64, 16>(a, n, stream);
 }
 

@@ -195,6 +195,19 @@ def test_masked_experts_and_tokens(ccr_mod, E, groups, kept, top, score, with_bi
     assert topk[0][1].tolist() == [E - 1] + [-1] * (K - 1) and float(w[0][1, 0]) == 1.0
 
 
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("score,group_top", [("softmax", 1), ("sigmoid", 2)])
+@pytest.mark.parametrize("E,K,groups,kept", [(257, 4, 1, 1), (384, 8, 1, 1), (512, 16, 16, 5), (300, 7, 30, 6),
+                                             (256, 8, 32, 8), (64, 3, 32, 2), (512, 8, 2, 1), (192, 8, 48, 10)])
+def test_tokens_on_half_a_wave(ccr_mod, E, K, groups, kept, group_top, score, with_bias):
+    import torch
+    g = gen(E + groups)
+    l = [1.5 * torch.randn(67, E, generator=g, device="cuda") for _ in range(2)]
+    l[1][::3, 5] = NINF
+    bs = [0.1 * torch.randn(E, generator=g, device="cuda")] * 2 if with_bias else None
+    check(ccr_mod, l, bs, K, how_(score, groups, kept, group_top))
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("E,groups,kept", [(64, 8, 2), (12, 4, 2), (256, 8, 3)])
 def test_a_bias_of_minus_infinity_counts_in_its_group(ccr_mod, E, groups, kept, score):
