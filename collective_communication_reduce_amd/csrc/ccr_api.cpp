@@ -2566,7 +2566,7 @@ ccr_status_t run_q8(ccr_ctx* ctx, bool to_q8, const void* const* rows, const voi
     args.first[r + 1] = args.first[r] + counts[r];
   }
   CCR_TRY(b.disjoint());
-  if (q8_grid(to_q8, es, args.first[R], H) > kMaxGridWorkgroups)
+  if (q8_grid(es, args.first[R], H) > kMaxGridWorkgroups)
     return fail(CCR_ERR_UNSUPPORTED, "too many rows for one launch");
   HIP_TRY(launch_q8(to_q8, es, args, R, H, s));
   return CCR_OK;

@@ -260,22 +260,19 @@ struct Q8Args {
   char* q[kRingHopMaxRanks];
   int64_t first[kRingHopMaxRanks + 1];
 };
-// Vectors that a lane makes 8-bit values of: 4 in rows of more than 2 for each lane;
-// whole rows of a wave: as many as fit, of 16 and 32 vectors; the pieces of a row
-// that one wave makes or one thread expands (16 values); and the workgroups for
-// `rows` rows.
-constexpr int q8_unroll(int es, int64_t H) { return q8_values(H) * es / 16 > 128 ? 4 : 1; }
-constexpr int q8_rows(int es, int64_t H) {
-  const int64_t vectors = q8_values(H) * es / 16;  // a multiple of 16 (bf16) or 32
-  return vectors == 16 ? 4 : vectors == 32 ? 2 : 1;
-}
-constexpr int64_t q8_chunks(bool to_q8, int es, int64_t H) {
+// How waves take rows of 16-byte vectors to or from 8 bits: vectors to a lane, 4 in
+// rows of more than 2 for each lane; whole rows to a wave, as many as fit, of 16 and
+// 32 vectors; a row's pieces, one to a wave; and the workgroups for `rows` rows.
+constexpr int64_t q8_vectors(int es, int64_t H) { return q8_values(H) * es / 16; }  // a multiple of 16 (bf16) or 32
+constexpr int q8_unroll(int es, int64_t H) { return q8_vectors(es, H) > 128 ? 4 : 1; }
+constexpr int q8_rows(int es, int64_t H) { return q8_vectors(es, H) <= 32 ? (int)(64 / q8_vectors(es, H)) : 1; }
+constexpr int64_t q8_chunks(int es, int64_t H) {
   const int64_t wave = 64 * q8_unroll(es, H);
-  return to_q8 ? (q8_values(H) * es / 16 + wave - 1) / wave : (H + 15) / 16;
+  return (q8_vectors(es, H) + wave - 1) / wave;
 }
-constexpr int64_t q8_grid(bool to_q8, int es, int64_t rows, int64_t H) {
-  const int64_t per = to_q8 ? kBlock / 64 * q8_rows(es, H) : kBlock;
-  return (rows * q8_chunks(to_q8, es, H) + per - 1) / per;
+constexpr int64_t q8_grid(int es, int64_t rows, int64_t H) {
+  const int64_t per = kBlock / 64 * q8_rows(es, H);
+  return (rows * q8_chunks(es, H) + per - 1) / per;
 }
 // To 8 bits, or back (rows is written then).
 hipError_t launch_q8(bool to_q8, int es, const Q8Args& a, int R, int64_t H, hipStream_t stream);

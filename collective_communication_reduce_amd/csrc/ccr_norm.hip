@@ -361,22 +361,25 @@ __global__ __launch_bounds__(kDwBlock) void norm_dw_kernel(const NormBwdArgs a, 
 }
 
 // -------------------------------------------------------------- 8-bit rows
-// A wave takes U times 64 vectors of the padded row: 4 where they are there for
-// it, so that it has 4 loads on their way (2 x 11,264 rows of 2048 bf16: 39 us with
-// one and its place in 64-bit divisions by lanes, 29 so); or ROWS whole rows of 64 /
-// ROWS vectors (1,048,576 rows of 64 bf16: 237 us with one row to a wave, 117 so).
-template <int ES, int U, int ROWS>
-__global__ __launch_bounds__(kBlock) void quantize_kernel(const Q8Args a, int R, int64_t vpr, int64_t values,
-                                                          int64_t q_bytes, int64_t chunks) {
+// To 8 bits or back: a wave takes U times 64 vectors of a row's values, 4 where
+// they are there for it, so that it has 4 loads on their way (2 x 11,264 rows of
+// 2048 bf16: 39 us with one and its place in 64-bit divisions by lanes, 29 so); or
+// ROWS whole rows of up to 64 / ROWS vectors (1,048,576 rows of 64 bf16: 237 us with
+// one row to a wave, 117 so).  Back, a lane reads as many bytes as make a vector (16
+// bytes and four stores of 64 bytes' distance to fp32 rows of 2048: 103 us for 2^26
+// values, 60 so).
+template <int ES, int U, int ROWS, bool BACK>
+__global__ __launch_bounds__(kBlock) void q8_kernel(const Q8Args a, int R, int64_t vpr, int64_t values,
+                                                    int64_t q_bytes, int64_t chunks) {
   constexpr int P = kPer<ES>, kLanes = 64 / ROWS;
   const int lane = threadIdx.x & (kLanes - 1), row = (threadIdx.x & 63) / kLanes;
   const int64_t unit = (int64_t)blockIdx.x * (kBlock / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int rank = 0;
-  int64_t k, t, c = 0;
+  int64_t t, c = 0;
   if constexpr (ROWS == 1) {
     while (rank < R && unit >= a.first[rank + 1] * chunks) rank++;
     if (rank == R) return;
-    k = unit - a.first[rank] * chunks;
+    const int64_t k = unit - a.first[rank] * chunks;
     t = k / chunks;
     c = k - t * chunks;
   } else {
@@ -386,88 +389,106 @@ __global__ __launch_bounds__(kBlock) void quantize_kernel(const Q8Args a, int R,
     t -= a.first[rank];
   }
   const int64_t i0 = c * (64 * U) + lane;
-  const u32x4* x = reinterpret_cast<const u32x4*>(a.rows[rank]) + t * vpr;
+  u32x4* x = reinterpret_cast<u32x4*>(const_cast<char*>(a.rows[rank])) + t * vpr;
   char* q = a.q[rank] + t * q_bytes;
-  u32x4 v[U];
+  if constexpr (!BACK) {
+    u32x4 v[U];
 #pragma unroll
-  for (int u = 0; u < U; u++) v[u] = i0 + u * 64 < vpr ? x[i0 + u * 64] : u32x4{0, 0, 0, 0};
+    for (int u = 0; u < U; u++) v[u] = i0 + u * 64 < vpr ? x[i0 + u * 64] : u32x4{0, 0, 0, 0};
 #pragma unroll
-  for (int u = 0; u < U; u++) {
-    float f[P];
-    unpack<ES>(v[u], f);
-    store_q8<P>(q, i0 + u * 64, values, f);
+    for (int u = 0; u < U; u++) {
+      float f[P];
+      unpack<ES>(v[u], f);
+      store_q8<P>(q, i0 + u * 64, values, f);
+    }
+    if (c == chunks - 1) pad_q8<kLanes>(q, values, q_bytes, lane);
+  } else {
+    uint32_t bytes[U][P / 4];
+    uint8_t scale[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int64_t i = i0 + u * 64 < vpr ? i0 + u * 64 : 0;
+      __builtin_memcpy(bytes[u], __builtin_assume_aligned(q + i * P, P), P);
+      scale[u] = (uint8_t)q[values + i / (32 / P)];
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const float s = q8_factor(scale[u]);
+      float f[P];
+#pragma unroll
+      for (int j = 0; j < P / 4; j++) {
+        const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)bytes[u][j], false);
+        const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)bytes[u][j], true);
+        f[4 * j] = lo[0] * s;
+        f[4 * j + 1] = lo[1] * s;
+        f[4 * j + 2] = hi[0] * s;
+        f[4 * j + 3] = hi[1] * s;
+      }
+      if (i0 + u * 64 < vpr) x[i0 + u * 64] = pack<ES>(f);
+    }
   }
-  if (c == chunks - 1) pad_q8<kLanes>(q, values, q_bytes, lane);
 }
 
-// A thread expands 16 bytes (2 x 24,571 rows of 2048 to bf16: 61 us, 5.0 TB/s).
-template <int ES>
-__global__ __launch_bounds__(kBlock) void dequantize_kernel(const Q8Args a, int R, int64_t H, int64_t values,
-                                                            int64_t q_bytes, int64_t chunks) {
-  const int64_t unit = (int64_t)blockIdx.x * kBlock + threadIdx.x;
-  int rank = 0;
-  while (rank < R && unit >= a.first[rank + 1] * chunks) rank++;
-  if (rank == R) return;
-  const int64_t k = unit - a.first[rank] * chunks, t = k / chunks, i = k % chunks;
-  const char* q = a.q[rank] + t * q_bytes;
-  const u32x4 v = *reinterpret_cast<const u32x4*>(q + i * 16);
-  const float s = q8_factor((uint8_t)q[values + i / 2]);
-  char* y = const_cast<char*>(a.rows[rank]) + (t * H + i * 16) * ES;
-  float f[16];
-#pragma unroll
-  for (int j = 0; j < 4; j++) {
-    const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)v[j], false);
-    const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)v[j], true);
-    f[4 * j] = lo[0] * s;
-    f[4 * j + 1] = lo[1] * s;
-    f[4 * j + 2] = hi[0] * s;
-    f[4 * j + 3] = hi[1] * s;
+template <int ES, bool BACK>
+hipError_t launch_q8_as(const Q8Args& a, int R, int64_t H, hipStream_t stream) {
+  const int64_t grid64 = q8_grid(ES, a.first[R], H);
+  if (grid64 == 0) return hipSuccess;
+  if (grid64 > kMaxGridWorkgroups) return hipErrorInvalidValue;
+  const unsigned grid = (unsigned)grid64;
+  const int64_t vpr = H * ES >> 4, values = q8_values(H), row = q8_row_bytes(H), chunks = q8_chunks(ES, H);
+  if constexpr (ES == 2) {
+    if (q8_rows(ES, H) == 4) {
+      q8_kernel<ES, 1, 4, BACK><<<grid, kBlock, 0, stream>>>(a, R, vpr, values, row, chunks);
+      return hipGetLastError();
+    }
   }
-  constexpr int P = kPer<ES>;
-#pragma unroll
-  for (int j = 0; j < 16 / P; j++)  // rows are whole vectors
-    if (i * 16 + j * P < H) reinterpret_cast<u32x4*>(y)[j] = pack<ES>(f + j * P);
+  if (q8_rows(ES, H) == 2) q8_kernel<ES, 1, 2, BACK><<<grid, kBlock, 0, stream>>>(a, R, vpr, values, row, chunks);
+  else if (q8_unroll(ES, H) == 4) q8_kernel<ES, 4, 1, BACK><<<grid, kBlock, 0, stream>>>(a, R, vpr, values, row, chunks);
+  else q8_kernel<ES, 1, 1, BACK><<<grid, kBlock, 0, stream>>>(a, R, vpr, values, row, chunks);
+  return hipGetLastError();
 }
 
-template <int ES, int WES, int TPR, int NV>
+template <int ES, int WES, bool ADD, int TPR, int NV>
 hipError_t launch_norm_as(const NormArgs& a, const NormShape& n, hipStream_t stream) {
   constexpr int kRows = kBlock / TPR;
   const int64_t vpr = n.H * ES >> 4, per_rank = (n.T + kRows - 1) / kRows;
   if (per_rank * n.R > kMaxGridWorkgroups) return hipErrorInvalidValue;
   const unsigned grid = (unsigned)(per_rank * n.R);
-  const int64_t values = q8_values(n.H), row = q8_row_bytes(n.H);
-  if (n.add)
-    norm_kernel<ES, WES, TPR, NV, true><<<grid, kBlock, 0, stream>>>(a, n.T, vpr, values, row, (float)n.H, n.eps, per_rank);
-  else
-    norm_kernel<ES, WES, TPR, NV, false><<<grid, kBlock, 0, stream>>>(a, n.T, vpr, values, row, (float)n.H, n.eps, per_rank);
+  norm_kernel<ES, WES, TPR, NV, ADD><<<grid, kBlock, 0, stream>>>(a, n.T, vpr, q8_values(n.H), q8_row_bytes(n.H),
+                                                                  (float)n.H, n.eps, per_rank);
   return hipGetLastError();
 }
 
 // v: vectors that a row's registers have to hold, up to the end of the 8-bit row
-// where there is one.  Short rows share a wave, long ones leave the registers; us
-// for 2^26 bf16 values with residual, of this rule and its neighbours:
-//   rows of            64    256    512   1024   2048   8192   16384
-//   16 lanes          147     98    104
-//   a wave            441    136     92     96
-//   the workgroup    1183    325    177    106     91    102     108
-//   read twice       1265    335    186    119    106    114     120
+// where there is one.  Short rows share a wave, long ones leave the registers; a
+// lane has one vector on its way where the residual makes that two loads and two
+// stores, else four.  us for 2^26 bf16 values, with residual / to 8 bits without:
+//   rows of            64        256       512       1024      2048      8192     16384
+//   16 lanes       147/128     97/41    105/41
+//   a wave         441         136       92/55     96/41    101/40
+//   the workgroup  1183        325      177       106        90/54    102/40   108
+//   read twice     1265        335      186       119       106       114      120
 // The gradients':
-//   16 lanes           89     83     80
-//   a wave            266     91     81     83
-//   the workgroup    1022    283    161     96     81     86     110
-//   read twice       1325    359    206    145    138    157     168
-template <int ES, int WES>
+//   16 lanes        89          83       79
+//   a wave         266          91       81        84        81
+//   the workgroup  1022        283      161        96        80        86      110
+//   read twice     1325        359      206       145       138       157      168
+template <int ES, int WES, bool ADD>
 hipError_t launch_norm_w(const NormArgs& a, const NormShape& n, hipStream_t stream) {
   const int64_t v = q8_values(n.H) * ES >> 4;
-  if (v <= 16) return launch_norm_as<ES, WES, 16, 1>(a, n, stream);
-  if (v <= 32) return launch_norm_as<ES, WES, 16, 2>(a, n, stream);
-  if (v <= 64) return launch_norm_as<ES, WES, 64, 1>(a, n, stream);
-  if (v <= 128) return launch_norm_as<ES, WES, 64, 2>(a, n, stream);
-  if (v <= kBlock) return launch_norm_as<ES, WES, kBlock, 1>(a, n, stream);
-  if (v <= 2 * kBlock) return launch_norm_as<ES, WES, kBlock, 2>(a, n, stream);
-  if (v <= 4 * kBlock) return launch_norm_as<ES, WES, kBlock, 4>(a, n, stream);
-  if (v <= 8 * kBlock) return launch_norm_as<ES, WES, kBlock, 8>(a, n, stream);
-  return launch_norm_as<ES, WES, kBlock, 0>(a, n, stream);
+  if (v <= 16) return launch_norm_as<ES, WES, ADD, 16, 1>(a, n, stream);
+  if (v <= 32) return launch_norm_as<ES, WES, ADD, 16, 2>(a, n, stream);
+  if (v <= 64) return launch_norm_as<ES, WES, ADD, ADD ? 64 : 16, ADD ? 1 : 4>(a, n, stream);
+  if (v <= 128) return launch_norm_as<ES, WES, ADD, 64, 2>(a, n, stream);
+  if (v <= kBlock) return launch_norm_as<ES, WES, ADD, ADD ? kBlock : 64, ADD ? 1 : 4>(a, n, stream);
+  if (v <= 2 * kBlock) return launch_norm_as<ES, WES, ADD, kBlock, 2>(a, n, stream);
+  if (v <= 4 * kBlock) return launch_norm_as<ES, WES, ADD, kBlock, 4>(a, n, stream);
+  if (v <= 8 * kBlock) return launch_norm_as<ES, WES, ADD, kBlock, 8>(a, n, stream);
+  return launch_norm_as<ES, WES, ADD, kBlock, 0>(a, n, stream);
+}
+template <int ES, int WES>
+hipError_t launch_norm_of(const NormArgs& a, const NormShape& n, hipStream_t stream) {
+  return n.add ? launch_norm_w<ES, WES, true>(a, n, stream) : launch_norm_w<ES, WES, false>(a, n, stream);
 }
 
 template <int ES, int WES, int TPR, int NV>
@@ -516,8 +537,8 @@ hipError_t launch_norm_bwd_w(const NormBwdArgs& a, const NormShape& n, float* wo
 }  // namespace
 
 hipError_t launch_norm(const NormArgs& a, const NormShape& n, hipStream_t stream) {
-  if (n.es == 4) return n.wes == 4 ? launch_norm_w<4, 4>(a, n, stream) : launch_norm_w<4, 2>(a, n, stream);
-  return n.wes == 4 ? launch_norm_w<2, 4>(a, n, stream) : launch_norm_w<2, 2>(a, n, stream);
+  if (n.es == 4) return n.wes == 4 ? launch_norm_of<4, 4>(a, n, stream) : launch_norm_of<4, 2>(a, n, stream);
+  return n.wes == 4 ? launch_norm_of<2, 4>(a, n, stream) : launch_norm_of<2, 2>(a, n, stream);
 }
 
 hipError_t launch_norm_bwd(const NormBwdArgs& a, const NormShape& n, float* work, hipStream_t stream) {
@@ -531,26 +552,8 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a, const NormShape& n, float* work
 }
 
 hipError_t launch_q8(bool to_q8, int es, const Q8Args& a, int R, int64_t H, hipStream_t stream) {
-  const int64_t rows = a.first[R], grid64 = q8_grid(to_q8, es, rows, H);
-  if (rows == 0) return hipSuccess;
-  if (grid64 > kMaxGridWorkgroups) return hipErrorInvalidValue;
-  const unsigned grid = (unsigned)grid64;
-  const int64_t vpr = H * es >> 4, values = q8_values(H), row = q8_row_bytes(H), chunks = q8_chunks(to_q8, es, H);
-  const int64_t vectors = values * es / 16;
-  if (!to_q8) {
-    if (es == 4) dequantize_kernel<4><<<grid, kBlock, 0, stream>>>(a, R, H, values, row, chunks);
-    else dequantize_kernel<2><<<grid, kBlock, 0, stream>>>(a, R, H, values, row, chunks);
-  } else if (es == 4) {
-    if (vectors == 32) quantize_kernel<4, 1, 2><<<grid, kBlock, 0, stream>>>(a, R, vpr, values, row, chunks);
-    else if (q8_unroll(es, H) == 4) quantize_kernel<4, 4, 1><<<grid, kBlock, 0, stream>>>(a, R, vpr, values, row, chunks);
-    else quantize_kernel<4, 1, 1><<<grid, kBlock, 0, stream>>>(a, R, vpr, values, row, chunks);
-  } else {
-    if (vectors == 16) quantize_kernel<2, 1, 4><<<grid, kBlock, 0, stream>>>(a, R, vpr, values, row, chunks);
-    else if (vectors == 32) quantize_kernel<2, 1, 2><<<grid, kBlock, 0, stream>>>(a, R, vpr, values, row, chunks);
-    else if (q8_unroll(es, H) == 4) quantize_kernel<2, 4, 1><<<grid, kBlock, 0, stream>>>(a, R, vpr, values, row, chunks);
-    else quantize_kernel<2, 1, 1><<<grid, kBlock, 0, stream>>>(a, R, vpr, values, row, chunks);
-  }
-  return hipGetLastError();
+  if (to_q8) return es == 4 ? launch_q8_as<4, false>(a, R, H, stream) : launch_q8_as<2, false>(a, R, H, stream);
+  return es == 4 ? launch_q8_as<4, true>(a, R, H, stream) : launch_q8_as<2, true>(a, R, H, stream);
 }
 
 }  // namespace ccr
