@@ -67,7 +67,7 @@ __device__ __forceinline__ void pad_q8(char* q, int64_t values, int64_t row_byte
 // rows of 2048 bf16 with residual: 92 us, 5.8 TB/s; to 8 bits 88.
 template <int ES, int WES, int TPR, int NV, bool ADD>
 __global__ __launch_bounds__(kBlock) void norm_kernel(const NormArgs a, int64_t T, int64_t vpr, int64_t values,
-                                                      int64_t q_bytes, float H, float eps,
+                                                      int64_t q_bytes, double inv_H, float eps,
                                                       int64_t blocks_per_rank) {
   constexpr int P = kPer<ES>, kRows = kBlock / TPR;
   __shared__ double part[kBlock / 64];
@@ -99,8 +99,12 @@ __global__ __launch_bounds__(kBlock) void norm_kernel(const NormArgs a, int64_t 
   auto finish = [&]() {
     if constexpr (TPR == kBlock) sum = block_sum(sum, part);
     else sum = lanes_sum<TPR>(sum);
-    // in fp64, where the mean of any finite values has a root
-    return (float)(1.0 / sqrt(sum / (double)H + (double)eps));
+    // In fp64, where the mean of any finite values has a root: the instruction's 2^-23
+    // and a Newton step, which 0 and infinity do without (a division, a root and
+    // another division were most of a short row's instructions).
+    const double m = __builtin_fma(sum, inv_H, (double)eps), y = __builtin_amdgcn_rsq(m);
+    const double half = 0.5 * m * y, better = __builtin_fma(y, __builtin_fma(-half, y, 0.5), y);
+    return (float)(m > 0.0 && m < __builtin_inf() ? better : y);
   };
   auto emit = [&](int64_t i, u32x4 v, float r) {  // of every vector up to the 8-bit row's end
     float f[P], g[P];
@@ -455,7 +459,7 @@ hipError_t launch_norm_as(const NormArgs& a, const NormShape& n, hipStream_t str
   if (per_rank * n.R > kMaxGridWorkgroups) return hipErrorInvalidValue;
   const unsigned grid = (unsigned)(per_rank * n.R);
   norm_kernel<ES, WES, TPR, NV, ADD><<<grid, kBlock, 0, stream>>>(a, n.T, vpr, q8_values(n.H), q8_row_bytes(n.H),
-                                                                  (float)n.H, n.eps, per_rank);
+                                                                  1.0 / (double)n.H, n.eps, per_rank);
   return hipGetLastError();
 }
 
@@ -464,8 +468,9 @@ hipError_t launch_norm_as(const NormArgs& a, const NormShape& n, hipStream_t str
 // lane has one vector on its way where the residual makes that two loads and two
 // stores, else four.  us for 2^26 bf16 values, with residual / to 8 bits without:
 //   rows of            64        256       512       1024      2048      8192     16384
-//   16 lanes       147/128     97/41    105/41
-//   a wave         441         136       92/55     96/41    101/40
+//   8 lanes         97
+//   16 lanes       147/122     97/40    105/40
+//   a wave         441         136       92/55     96/38    101/39
 //   the workgroup  1183        325      177       106        90/54    102/40   108
 //   read twice     1265        335      186       119       106       114      120
 // The gradients':
@@ -475,7 +480,8 @@ hipError_t launch_norm_as(const NormArgs& a, const NormShape& n, hipStream_t str
 //   read twice     1325        359      206       145       138       157      168
 template <int ES, int WES, bool ADD>
 hipError_t launch_norm_w(const NormArgs& a, const NormShape& n, hipStream_t stream) {
-  const int64_t v = q8_values(n.H) * ES >> 4;
+  const int64_t v = (a.q[0] ? q8_values(n.H) : n.H) * ES >> 4;
+  if (v <= 8) return launch_norm_as<ES, WES, ADD, 8, 1>(a, n, stream);
   if (v <= 16) return launch_norm_as<ES, WES, ADD, 16, 1>(a, n, stream);
   if (v <= 32) return launch_norm_as<ES, WES, ADD, 16, 2>(a, n, stream);
   if (v <= 64) return launch_norm_as<ES, WES, ADD, ADD ? 64 : 16, ADD ? 1 : 4>(a, n, stream);

@@ -249,6 +249,28 @@ def test_backward_against_differences(ccr_mod):
         assert abs(float(dw[i]) - float(diff)) <= 100 * U * float(mag.sum()) + 1e-9
 
 
+@pytest.mark.parametrize("H", [32, 64, 2048, 16392])
+def test_roots_over_the_whole_range(ccr_mod, H):
+    """rstd of rows of every magnitude of fp32, of zeros and of infinities, without an
+    eps, and of one: off by its rounding to fp32 and 2^-40 before."""
+    import torch
+    sizes = [0.0, 1.4e-45, 1e-38, 3e-20, 1.0, 7e19, 3.4e38, float("inf")]
+    x = torch.tensor(sizes, device="cuda")[:, None] * torch.ones(H, device="cuda")
+    x[3:6] *= 0.5 + torch.rand(3, H, generator=gen(H), device="cuda")
+    w, y, rstd = torch.ones(H, device="cuda"), torch.empty_like(x), torch.empty(len(sizes), device="cuda")
+    with ccr_mod.Context(0) as c:
+        for eps in (0.0, 1e-6):
+            ccr_mod.ccr_rms_norm(c, [x], [w], y=[y], rstd=[rstd], eps=eps)
+            torch.cuda.synchronize()
+            want = 1.0 / (x.double().square().mean(1) + float(torch.tensor(eps))).sqrt()
+            big = want > torch.finfo(torch.float32).max  # infinite in fp32
+            got = rstd.double()
+            assert bool((got[big] == float("inf")).all())
+            # 1 / 3.4e38 = 2.9e-39 lies below 2^-126 = 1.2e-38, where fp32's steps are all
+            # 2^-149 and half a step is 2^-150
+            assert bool(((got - want).abs() <= want * U * (1 + 2.0 ** -15) + 2.0 ** -150)[~big].all())
+
+
 @pytest.mark.parametrize("add", [False, True])
 @pytest.mark.parametrize("dt,wdt", [("bf16", "f32"), ("f32", "f32")])
 @pytest.mark.parametrize("R,T,H", [(3, 37, 56), (2, 50, 200), (2, 41, 384), (1, 33, 960), (1, 19, 2040), (1, 6, 16384)])
