@@ -180,9 +180,9 @@ __global__ __launch_bounds__(kBlock) void norm_bwd_kernel(const NormBwdArgs a, i
     for (int j = 0; j < P; j++) w[n][j] = dw[n][j] = 0.0f;
     if (i < vpr) load_weight<P, WES>(a.w[rank], i, w[n]);
   }
-  // A row is loaded while the one before is summed: short rows leave the
-  // registers for it.
-  constexpr bool kAhead = NV <= 2;
+  // A row is loaded while the one before is summed, where a lane has one vector of
+  // it; with more it has loads enough on their way.
+  constexpr bool kAhead = NV == 1;
   struct Row {
     u32x4 d[NV], h[NV], e[NV];
     float r;
@@ -475,6 +475,7 @@ hipError_t launch_norm_as(const NormArgs& a, const NormShape& n, hipStream_t str
 //   read twice     1265        335      186       119       106       114      120
 // The gradients':
 //   16 lanes        89          83       79
+//   32 lanes                    81        83        80        81
 //   a wave         266          91       81        84        81
 //   the workgroup  1022        283      161        96        80        86      110
 //   read twice     1325        359      206       145       138       157      168
@@ -530,9 +531,9 @@ template <int ES, int WES>
 hipError_t launch_norm_bwd_w(const NormBwdArgs& a, const NormShape& n, float* work, hipStream_t stream) {
   const int64_t v = n.H * ES >> 4;
   if (v <= 16) return launch_norm_bwd_as<ES, WES, 16, 1>(a, n, work, stream);
-  if (v <= 32) return launch_norm_bwd_as<ES, WES, 16, 2>(a, n, work, stream);
+  if (v <= 32) return launch_norm_bwd_as<ES, WES, 32, 1>(a, n, work, stream);
   if (v <= 64) return launch_norm_bwd_as<ES, WES, 64, 1>(a, n, work, stream);
-  if (v <= 128) return launch_norm_bwd_as<ES, WES, 64, 2>(a, n, work, stream);
+  if (v <= 128) return launch_norm_bwd_as<ES, WES, 32, 4>(a, n, work, stream);
   if (v <= kBlock) return launch_norm_bwd_as<ES, WES, kBlock, 1>(a, n, work, stream);
   if (v <= 2 * kBlock) return launch_norm_bwd_as<ES, WES, kBlock, 2>(a, n, work, stream);
   if (v <= 4 * kBlock) return launch_norm_bwd_as<ES, WES, kBlock, 4>(a, n, work, stream);
