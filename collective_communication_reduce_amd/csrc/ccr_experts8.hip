@@ -205,13 +205,13 @@ __global__ __launch_bounds__(WM * WN * WK * 64) void experts8_ring_kernel(const 
 // second b's (each half behind its last product) and a's first two of the next
 // step.  So a line is loaded a step and a half before it is read, into the place of
 // the one that has just been read: behind a barrier a little into the first phase,
-// b, the first half of a and the scales of the step after next; behind one a little
-// into the second, the second half of a.
+// half of b, the first half of a; behind one a little into the second, the other
+// half of b, the scales and the second half of a, of the step after next.
 //
 // With one wave to a SIMD nothing hides an instruction that stalls, so reads and
 // loads are placed one by one between the products, no branch of the loop is taken
 // but its own, and a tile's first step is code of its own, whose products start the
-// sums: no pass over the accumulators sets them to zero (434 us before, 412 with
+// sums: no pass over the accumulators sets them to zero (434 us before, 417 with
 // all of it; 196,608 rows of 2048 over 64 experts of 1024 rows).
 //
 // The products are 32 x 32 x 64: half as many instructions as 16 x 16 x 128 for
@@ -335,9 +335,10 @@ __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable 
     aimed_step = 0;
     aimed_group = aimed_group == 2 ? 0 : aimed_group + 1;
   };
-  // Load k of a step's 18: the first half of a's (of each wave's 128 rows), b's,
-  // the scales; then the second half of a's.
-  constexpr int kFirst = 14, kAll = 18;
+  // Load k of a step's 18: the first half of a's (of each wave's 128 rows), b's, the
+  // scales: 14 that the step's first phase needs; then the second half of a's.  9 go
+  // out in each phase (14 and 4 kept the waves waiting to issue: 422 us, 412 so).
+  constexpr int kHalf = 14, kAll = 18, kFirst = 9;
   auto load_at = [&](int i, uint32_t to, const int* off, u32x4 from) {
     asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds"
                  ::"s"(to), "n"(i * NT * 16), "v"(off[i]), "s"(from) : "memory", "scc");
@@ -411,11 +412,12 @@ __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable 
     const char* sc1 = scales + group * kScales + in1 * 4;
     // after: the full tile before left its results on their way, which the first
     // step counts with the loads; the step behind waits for them
-    auto wait = [&]() {
+    auto wait = [&](auto loads) {
+      constexpr int kLeft = decltype(loads)::value;
       if (kFirstStep && after)
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kAll + kStores) : "memory");
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLeft + kStores) : "memory");
       else
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kAll) : "memory");
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLeft) : "memory");
     };
     auto product = [&](int n, int half_of_a) {
       const int i = half_of_a * 2 + n % 2, j = n % 8 / 2;
@@ -439,7 +441,7 @@ __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable 
       // end (in the very first step read again)
       if (n < 3) b[3].read<kPaired>(lines + 2 * kSlot, sc + kScales / 2, wn, 3, 2 + n);
       // b and the first half of a are read by every wave; the second half is there
-      if (n == kBarrier) wait();
+      if (n == kBarrier) wait(std::integral_constant<int, kAll>{});
       spread(n, 10, [&](int u) { a[2 + u % 2].read<false>(lines, sc, wm, 2 + u % 2, u < 2 ? 4 : u / 2 - 1); });
       spread(n, kFirst, [&](int k) { load(k, g); });
       __builtin_amdgcn_sched_barrier(0);
@@ -451,7 +453,7 @@ __global__ __launch_bounds__(256, 1) void experts8_big_kernel(const ExpertTable 
       product(n, 1);
       // the second half of a is read by every wave; the next step is there but for
       // its second half of a
-      if (n == kBarrier) wait();
+      if (n == kBarrier) wait(std::integral_constant<int, kAll - kHalf + kFirst>{});
       spread(n, 10, [&](int u) { a[u % 2].read<false>(lines1, sc1, wm, u % 2, u < 2 ? 4 : u / 2 - 1); });
       // b's parts, each behind its last product: 0 and 1 of fragment j, 2 and 3 and
       // the scales
