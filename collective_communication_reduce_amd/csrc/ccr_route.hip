@@ -379,7 +379,14 @@ __device__ __forceinline__ bool choose(const float* l, const float* s, const flo
     if constexpr (LPT == 64) {
       if (q > 16) merge(__shfl_xor(a, 16), __shfl_xor(b, 16));
     }
-    if (n.group_top == 2 && b != 0) a = ordered(value_of(a) + value_of(b));
+    // The group's value, of one key or two, and what it may be off by: its keys'
+    // scores, and the roundings of the keys and of their sum, which are shares of the
+    // keys themselves: they may cancel.  Infinite keys are exact.
+    const bool two = n.group_top == 2 && b != 0;
+    const float first = value_of(a), second = two ? value_of(b) : 0.0f, parts = fabsf(first) + fabsf(second);
+    float off = fmaxf(fabsf(first), fabsf(second)) == -kNegInf ? 0.0f : 2 * err + 0x1p-21f * parts;
+    asm volatile("" : "+v"(off));  // one register over the loop below, not its parts
+    if (two) a = ordered(first + second);
     if ((sub & (q - 1)) == 0) room->group[tok][g] = g < n.groups ? a : 0;
     wave_sync();
     // how many groups are before this one: a larger value, or as large and left
@@ -391,9 +398,13 @@ __device__ __forceinline__ bool choose(const float* l, const float* s, const flo
     }
     keep = rank < n.kept && g < n.groups;
     if (with_bias || n.group_top == 2) {
-      const uint32_t low = min_of<LPT>(keep ? a : ~0u), high = max_of<LPT>(keep || g >= n.groups ? 0u : a);
-      const float x = value_of(low), y = value_of(high);
-      near |= high != 0 && !(x - y > 4 * err + 0x1p-21f * (fabsf(x) + fabsf(y)));
+      // Every kept group's least value against the others' largest; a sum beyond fp32
+      // and NaN are undecided.  A group of no expert that can be chosen (0) is kept
+      // only if all others are such groups.
+      const float least = value_of(a) - off, most = value_of(a) + off;
+      const float low = min_of<LPT>(!keep || a == 0 ? -kNegInf : least == least ? least : kNegInf);
+      const float high = max_of<LPT>(keep || a == 0 || g >= n.groups ? kNegInf : most == most ? most : -kNegInf);
+      near |= high != kNegInf && !(low > high);  // -infinity: no group is left out that could stay
     }
   }
   const uint64_t left = ((1ull << sub) - 1) << tok * LPT;  // the token's lanes before this one

@@ -1,0 +1,51 @@
+"""GPU parity of the router and its gradient with 64-bit references where fp32 is
+short of range or of digits."""
+import pytest
+
+from gpu_helpers import torch_cuda
+from test_gpu_route import check, gen, how_
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ccr_mod():
+    torch_cuda()
+    import collective_communication_reduce_amd as ccr
+    return ccr
+
+
+@pytest.mark.parametrize("size", [64.0, 1000.0])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,kept,K", [(4, 2, 1, 2), (64, 8, 3, 6), (256, 8, 4, 8), (512, 16, 5, 8), (1024, 16, 4, 16)])
+def test_groups_whose_two_keys_cancel(ccr_mod, E, groups, kept, K, score, size):
+    """Biases of both signs: a group's value, the sum of its two best keys, is far
+    smaller than they are, and what fp32 drops of the keys decides between groups
+    of nearly the same value."""
+    import torch
+    g = gen(E + int(size))
+    T, eg = 600, E // groups
+    l = torch.randn(T, 1, eg, generator=g, device="cuda") + 1e-5 * torch.randn(T, groups, eg, generator=g, device="cuda")
+    bias = torch.full((groups, eg), -size, device="cuda")
+    bias[:, 0] = size
+    check(ccr_mod, [l.view(T, E)], [bias.view(E)], K, how_(score, groups, kept, 2))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("top", [1, 2])
+@pytest.mark.parametrize("kept", [5, 9, 15])
+def test_groups_with_biases_of_every_size(ccr_mod, score, kept, top):
+    """From 1e-30 to 3e38, and sums past fp32's range: every group twice, alike but
+    for what is added to their logits."""
+    import torch
+    g = gen(top)
+    T, E, groups = 300, 64, 16
+    l = torch.randn(T, E, generator=g, device="cuda")
+    l[:, 32:] = l[:, :32] + 1e-5 * torch.randn(T, 32, generator=g, device="cuda")
+    size = torch.tensor([0.0, 1e-30, 0.1, 3.0, 1e4, 1e15, 3e38, 2.9e38], device="cuda")
+    half = size[:, None] * torch.tensor([1.0, -1.0, -1.0, -1.0], device="cuda")
+    half[-1] = 2.9e38
+    half[0] = -2.9e38
+    bias = torch.cat([half, half]).view(E)
+    bias[:4] = -2.901e38
+    check(ccr_mod, [l], [bias], 5, how_(score, groups, kept, top))
