@@ -573,11 +573,32 @@ __global__ __launch_bounds__(kStatsBlock) void route_stats_kernel(const RouteArg
   }
 }
 
+// A choice's share of the sum of its token's chosen scores, 0 without one (have):
+// c / sum c, or where a chosen score is below fp32's normal numbers from its logit
+// lk (m: the row's largest) in 64 bits.
+template <int LPT>
+__device__ __forceinline__ float share(float c, float lk, float m, bool have, bool sig) {
+  const float total = sum_of<LPT>(c);
+  float w = total == 0.0f ? 0.0f : c / total;
+  const uint64_t tiny = __ballot(have && c < 0x1p-126f);
+  if (tiny) {
+    const double x = !have ? 0.0 : sig ? sigmoid((double)lk).s : exp((double)lk - (double)m);
+    const double sum = sum_of<LPT>(x);
+    const int first = (threadIdx.x & 63) / LPT * LPT;  // the token's lanes
+    if (tiny << (64 - LPT - first) >> (64 - LPT)) w = sum == 0.0 ? 0.0f : (float)(x / sum);
+  }
+  return w;
+}
+
 // ---------------------------------------------------------------- backward
 // With c_k the chosen scores and u_k = scale dw_k, the gradient of the scores
-// is, at the k-th choice, u_k, or renormalised (u_k - sum u c / C) / C with
-// C = sum c; at every expert, that of the sums of scores; and that of the logits
-// s (ds - sum s ds) for a softmax, s (1 - s) ds for sigmoids.
+// is u_k at the k-th choice and, at every expert, that of the sums of scores; that
+// of the logits is s (ds - sum s ds) for a softmax, s (1 - s) ds for sigmoids.
+//
+// Renormalised, the choices' part is (u_k - sum w u) / C with C = sum c and w = c /
+// C, and adds to the logits' gradient w_k (u_k - sum w u), for sigmoids times 1 - c_k
+// (a softmax's own sum over it is 0).  So no score divides another's: 1 / C may be
+// beyond fp32.  Of choices with scores below its normal numbers w is that of 64 bits.
 template <int LPT, int J>
 __global__ __launch_bounds__(kBlock) void route_bwd_kernel(const RouteBwdArgs a, const RouteShape n,
                                                            int64_t blocks_per_rank) {
@@ -614,11 +635,11 @@ __global__ __launch_bounds__(kBlock) void route_bwd_kernel(const RouteBwdArgs a,
   }
   // lane k < K: the k-th choice and its score
   int id = -1;
-  float c = 0, u = 0;
+  float c = 0, u = 0, lk = kNegInf;
   if (live && sub < n.K) {
     id = a.topk[rank][t * n.K + sub];
     if (id < 0 || id >= n.E) id = -1;
-    const float lk = id >= 0 ? logits[id] : kNegInf;
+    if (id >= 0) lk = logits[id];
     if (lk == kNegInf) id = -1;
     if (id >= 0) {
       c = n.sigmoid ? sigmoid(lk).s : expf(lk - m) * inv;
@@ -626,17 +647,25 @@ __global__ __launch_bounds__(kBlock) void route_bwd_kernel(const RouteBwdArgs a,
     }
   }
   if (n.renorm) {
-    const float total = sum_of<LPT>(c), dot = sum_of<LPT>(u * c);
-    u = id < 0 || total == 0.0f ? 0.0f : (u - dot / total) / total;
+    float w = share<LPT>(c, lk, m, id >= 0, n.sigmoid);
+    w *= u - sum_of<LPT>(w * u);
+    u = n.sigmoid ? w * sigmoid(lk).rest : w;
   }
   if (sub < 16) back[wave][tok][sub] = Part{id, u};
   wave_sync();
   const float* dsums = a.dsums[rank];
   load_some<J>(dsums ? dsums + (mine > 0 ? e0 : 0) : nullptr, dsums ? mine : 0, 0.0f, ds);
+  float chosen[J];
+#pragma unroll
+  for (int j = 0; j < J; j++) chosen[j] = 0.0f;
   for (int k = 0; k < n.K; k++) {
     const Part b = back[wave][tok][k];
 #pragma unroll
-    for (int j = 0; j < J; j++) ds[j] += b.id == e0 + j ? b.u : 0.0f;
+    for (int j = 0; j < J; j++) chosen[j] += b.id == e0 + j ? b.u : 0.0f;
+  }
+  if (!n.renorm) {
+#pragma unroll
+    for (int j = 0; j < J; j++) ds[j] += chosen[j];
   }
   float dot = 0;
   if (!n.sigmoid) {
@@ -653,6 +682,7 @@ __global__ __launch_bounds__(kBlock) void route_bwd_kernel(const RouteBwdArgs a,
     } else {
       d[j] = s[j] * (ds[j] - dot);
     }
+    if (n.renorm) d[j] += chosen[j];
     if (l[j] == kNegInf) d[j] = 0.0f;
   }
   float* out = a.dlogits[rank] + t * n.E + e0;

@@ -3,7 +3,7 @@ short of range or of digits."""
 import pytest
 
 from gpu_helpers import torch_cuda
-from test_gpu_route import check, gen, how_
+from test_gpu_route import check, check_backward, gen, how_
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,23 @@ def test_groups_with_biases_of_every_size(ccr_mod, score, kept, top):
     bias = torch.cat([half, half]).view(E)
     bias[:4] = -2.901e38
     check(ccr_mod, [l], [bias], 5, how_(score, groups, kept, top))
+
+
+@pytest.mark.parametrize("with_sums", [False, True])
+@pytest.mark.parametrize("E,K", [(3, 2), (64, 6), (200, 16), (300, 8), (1024, 16)])
+def test_renormalised_gradient_of_tiny_scores(ccr_mod, E, K, with_sums):
+    """Choices whose scores, or the quotients by their sum, are beyond fp32: sigmoids
+    of logits down to -600, softmax choices as far below the largest logit."""
+    import torch
+    g = gen(E)
+    below = torch.tensor([0.0, -40.0, -80.0, -88.0, -91.0, -95.0, -100.0, -104.0, -120.0, -300.0, -600.0], device="cuda")
+    T = 3 * len(below)
+    l = torch.randn(T, E, generator=g, device="cuda") + below.repeat(3)[:, None]
+    l[-1, 1] = -30.0  # next to choices that vanish
+    dw, dsum = torch.randn(T, K, generator=g, device="cuda"), torch.randn(E, generator=g, device="cuda")
+    top = (1 + torch.argsort(torch.rand(T, E - 1, generator=g, device="cuda"), dim=1)[:, :K]).int()
+    top[-1, 0] = 1
+    dsums = [dsum] if with_sums else None
+    check_backward(ccr_mod, [l], [top], [dw], dsums, "sigmoid", True, 2.5)
+    l[:, 0] = 1.0  # in no choice
+    check_backward(ccr_mod, [l], [top], [dw], dsums, "softmax", True, 2.5)
