@@ -453,6 +453,31 @@ __device__ __forceinline__ bool choose(const float* l, const float* s, const flo
   return near;
 }
 
+// The renormalised weights of a wave's tokens from t0 on in 64 bits, where a chosen
+// score, or a softmax's exponential before its division by at most 1024, is below
+// 2^-116: scores in fp32 lose their digits from 2^-126 on.  (Behind the tokens' loop,
+// by the lanes that wrote topk; within it, it cost registers.)
+template <int LPT>
+__device__ __forceinline__ void precise_weights(const float* logits, const RouteShape& n, int64_t t0,
+                                                const int32_t* topk, float* weights) {
+  const int lane = threadIdx.x & 63, sub = lane % LPT;
+  const int64_t t = t0 + lane / LPT;
+  const bool here = t < n.T && sub < n.K;
+  const int e = here ? topk[t * n.K + sub] : -1;
+  double x = 0;
+  if (e >= 0) {
+    const float* row = logits + t * n.E;
+    float m = kNegInf;  // the row's largest, NaN with one
+    if (!n.sigmoid)
+      for (int i = 0; i < n.E; i++) m = row[i] > m || row[i] != row[i] ? row[i] : m;
+    const double l = (double)row[e];
+    x = n.sigmoid ? sigmoid(l).s : m < -kNegInf ? exp(l - (double)m) : __builtin_nan("");
+  }
+  const bool tiny = max_of<LPT>(e >= 0 && x < 0x1p-116 ? 1 : 0) != 0;
+  const double sum = sum_of<LPT>(x);
+  if (here && tiny) weights[t * n.K + sub] = (sum == 0.0 ? 0.0f : (float)(x / sum)) * n.scale;
+}
+
 // A token per LPT lanes, J experts to a lane; a workgroup takes every slots-th
 // step of its rank's tokens.  STATS: it counts its tokens' choices and sums their
 // scores, in its slot of the work array or, alone, in the results.
@@ -476,6 +501,7 @@ __global__ __launch_bounds__(kBlock, LPT == 16 ? 4 : LPT == 32 ? 3 : 2) void rou
     for (int e = threadIdx.x; e < kPlaces; e += kBlock) count[e] = 0;
     __syncthreads();
   }
+  uint64_t tiny = 0;
   for (int64_t t0 = ((int64_t)slot * kWaves + wave) * kTok; t0 < n.T; t0 += (int64_t)slots * kWaves * kTok) {
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));  // what follows from it costs less anew than registers between the steps
@@ -506,6 +532,7 @@ __global__ __launch_bounds__(kBlock, LPT == 16 ? 4 : LPT == 32 ? 3 : 2) void rou
     float w = c != kNone ? __builtin_bit_cast(float, room.of_place[tok][room.at((int)(c >> 16) / J, (int)(c >> 16) % J)]) : 0.0f;
     if (n.renorm) {
       const float total = sum_of<LPT>(w);
+      tiny |= __ballot(c != kNone && w < 0x1p-115f);
       w = total == 0.0f ? 0.0f : w / total;
     }
     if (live && sub < n.K) {
@@ -517,6 +544,9 @@ __global__ __launch_bounds__(kBlock, LPT == 16 ? 4 : LPT == 32 ? 3 : 2) void rou
     }
     wave_sync();
   }
+  if (tiny)
+    for (int64_t t0 = ((int64_t)slot * kWaves + wave) * kTok; t0 < n.T; t0 += (int64_t)slots * kWaves * kTok)
+      precise_weights<LPT>(logits, n, t0, a.topk[rank], a.weights[rank]);
   if constexpr (STATS) {
     const int lane = threadIdx.x & 63;
     room.put(lane / LPT, lane % LPT, sums);

@@ -667,7 +667,10 @@ ccr_status_t ccr_rms_norm_bwd(ccr_ctx_t ctx, const void *const *dy, const void *
  * Keys are compared as if computed in 64 bits.  An expert whose logit is
  * -infinity has s = 0 and is never chosen, and adds nothing to its group; where
  * fewer than K can be chosen the last entries are -1 with weight 0.  A NaN key is
- * above all others and shows in the weights.  A sum of 0 gives weights 0.
+ * above all others and shows in the weights.  Renormalised weights (and the
+ * gradient through them) are those of 64 bits where the chosen scores are below
+ * fp32's normal numbers; a sum that is 0 even so (sigmoids of logits below -745)
+ * gives weights 0.
  *   counts[r] (device int64 [E]; counts may be NULL): the tokens that chose e;
  *   score_sums[r] (device fp32 [E]; may be NULL): the sum over the tokens of s_e,
  *            from which a loss for balance is made.

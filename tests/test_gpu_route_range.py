@@ -3,7 +3,7 @@ short of range or of digits."""
 import pytest
 
 from gpu_helpers import torch_cuda
-from test_gpu_route import check, check_backward, gen, how_
+from test_gpu_route import NINF, check, check_backward, gen, how_
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +69,50 @@ def test_renormalised_gradient_of_tiny_scores(ccr_mod, E, K, with_sums):
     check_backward(ccr_mod, [l], [top], [dw], dsums, "sigmoid", True, 2.5)
     l[:, 0] = 1.0  # in no choice
     check_backward(ccr_mod, [l], [top], [dw], dsums, "softmax", True, 2.5)
+
+
+@pytest.mark.parametrize("E,K", [(3, 2), (64, 6), (200, 16), (300, 8), (1024, 16)])
+def test_renormalised_weights_of_tiny_scores(ccr_mod, E, K):
+    """Weights of choices whose scores are below fp32's normal numbers are those of 64
+    bits: sigmoids of logits down to -600, and 0 at -800; softmax choices as far
+    below an expert that the bias keeps out."""
+    import torch
+    g = gen(E)
+    below = torch.tensor([0.0, -40.0, -80.0, -88.0, -91.0, -95.0, -100.0, -104.0, -120.0, -300.0, -600.0, -800.0],
+                         device="cuda")
+    T = 3 * len(below)
+    l = torch.randn(T, E, generator=g, device="cuda") + below.repeat(3)[:, None]
+    l[5, 1] = -30.0  # next to choices that vanish
+    check(ccr_mod, [l], None, K, how_("sigmoid"))
+    l[:, 0] = 1.0
+    bias = torch.zeros(E, device="cuda")
+    bias[0] = -10.0
+    check(ccr_mod, [l], [bias], K, how_("softmax", scale=2.5))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [12, 256, 1024])
+def test_tokens_with_tiny_scores_leave_others_alone(ccr_mod, E, score):
+    """A token's results do not hang on the tokens beside it: infinities and NaN that
+    the bias keeps out of the choices, scores around 2^-126 and ordinary ones."""
+    import torch
+    K, g = 3, gen(E)
+    l = torch.randn(40, E, generator=g, device="cuda")
+    l[:, 4:] -= torch.linspace(0, 100, 40, device="cuda")[:, None]
+    l[3, 0], l[8, 1], l[13, 2] = float("inf"), float("nan"), NINF
+    bias = torch.zeros(E, device="cuda")
+    bias[:4] = -10.0
+    far = l.clone()
+    far[::2, 4:] = -200.0
+    far[::2, :4] = 0.0
+    out = []
+    with ccr_mod.Context(0) as c:
+        for v in (l, far):
+            topk, w = torch.empty(40, K, dtype=torch.int32, device="cuda"), torch.empty(40, K, device="cuda")
+            dl, dw = torch.empty(40, E, device="cuda"), torch.ones(40, K, device="cuda")
+            dw[:, 1] = 0.5
+            ccr_mod.ccr_moe_route(c, [v], [topk], [w], bias=[bias], score=score)
+            ccr_mod.ccr_moe_route_bwd(c, [v], [topk], [dw], [dl], score=score)
+            torch.cuda.synchronize()
+            out.append([t[1::2].nan_to_num(7.0) for t in (topk, w, dl)])
+    assert all(torch.equal(a, b) for a, b in zip(*out))
