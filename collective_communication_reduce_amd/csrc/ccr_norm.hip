@@ -155,9 +155,13 @@ __global__ __launch_bounds__(kBlock) void norm_kernel(const NormArgs a, int64_t 
 
 // ---------------------------------------------------------------- backward
 // Every workgroup takes every slots-th row (or, of short rows, as many as it
-// holds at a time) of its rank, so that it can add up dw in its registers; what it
-// has goes to its slot of the work array, and norm_dw_kernel adds the slots (8 x
-// 4096 rows of 2048 bf16 with dh: 115 and 5 us, 4.7 TB/s).
+// holds at a time) of its rank, so that it can add up dw in its registers; after
+// every kPiece of its rows, and at the end, what it has goes to its slot of the work
+// array, and norm_dw_kernel adds the slots (8 x 4096 rows of 2048 bf16 with dh: 115
+// and 5 us, 4.7 TB/s).  So no sum of dw is a chain of more than kPiece rows, however
+// many there are (of R T < 2^24 rows a slot has up to 136 pieces): chains of 4096
+// were off by 980 units of 2^-24.
+constexpr int kPiece = 128;
 template <int ES, int WES, int TPR, int NV, bool ADD>
 __global__ __launch_bounds__(kBlock) void norm_bwd_kernel(const NormBwdArgs a, int64_t T, int64_t vpr, float H,
                                                           int slots, float* work) {
@@ -202,72 +206,84 @@ __global__ __launch_bounds__(kBlock) void norm_bwd_kernel(const NormBwdArgs a, i
   };
   int turn = 0;
   const int64_t step = (int64_t)slots * kRows;
-  int64_t t = (int64_t)slot * kRows + sub;
+  const int64_t first = (int64_t)slot * kRows;
+  int64_t t = first + sub;
+  float* out = work + (int64_t)blockIdx.x * vpr * P;
   Row x, next;
   if (kAhead) load(t, next);
-  for (; t < T; t += step) {
-    if (kAhead) {
-      x = next;
-      load(t + step, next);
+  for (int64_t from = first; from < T; from += kPiece * step) {  // uniform over the workgroup
+    const int64_t to = T < from + kPiece * step ? T : from + kPiece * step;
+    for (; t < to; t += step) {
+      if (kAhead) {
+        x = next;
+        load(t + step, next);
+      } else {
+        load(t, x);
+      }
+      const float r = x.r;
+      float s = 0;
+#pragma unroll
+      for (int n = 0; n < NV; n++) {
+        float d[P], f[P];
+        unpack<ES>(x.d[n], d);
+        unpack<ES>(x.h[n], f);
+#pragma unroll
+        for (int j = 0; j < P; j++) {
+          const float hh = f[j] * r;
+          s = __builtin_fmaf(w[n][j] * d[j], hh, s);
+          dw[n][j] = __builtin_fmaf(d[j], hh, dw[n][j]);
+        }
+      }
+      // two arrays in turn: a wave may be a row ahead of one that still reads
+      if constexpr (TPR == kBlock) s = block_sum(s, part[turn]);
+      else s = lanes_sum<TPR>(s);
+      turn ^= 1;
+      s /= H;
+#pragma unroll
+      for (int n = 0; n < NV; n++) {
+        const int64_t i = tid + n * TPR;
+        float d[P], f[P], e[P], o[P];
+        unpack<ES>(x.d[n], d);
+        unpack<ES>(x.h[n], f);
+        if (ADD) unpack<ES>(x.e[n], e);
+#pragma unroll
+        for (int j = 0; j < P; j++) {
+          o[j] = r * (w[n][j] * d[j] - f[j] * r * s);
+          if (ADD) o[j] += e[j];
+        }
+        if (i < vpr) dx[t * vpr + i] = pack<ES>(o);
+      }
+    }
+    if constexpr (TPR == kBlock) {
+#pragma unroll
+      for (int n = 0; n < NV; n++) {
+        const int64_t i = tid + n * TPR;
+        if (i >= vpr) continue;
+#pragma unroll
+        for (int j = 0; j < P; j += 4) {
+          f32x4* o = reinterpret_cast<f32x4*>(out + i * P + j);
+          const f32x4 v = {dw[n][j], dw[n][j + 1], dw[n][j + 2], dw[n][j + 3]};
+          *o = from == first ? v : *o + v;
+        }
+      }
     } else {
-      load(t, x);
-    }
-    const float r = x.r;
-    float s = 0;
+      if (from != first) __syncthreads();  // the piece before is read
 #pragma unroll
-    for (int n = 0; n < NV; n++) {
-      float d[P], f[P];
-      unpack<ES>(x.d[n], d);
-      unpack<ES>(x.h[n], f);
+      for (int n = 0; n < NV; n++)
 #pragma unroll
-      for (int j = 0; j < P; j++) {
-        const float hh = f[j] * r;
-        s = __builtin_fmaf(w[n][j] * d[j], hh, s);
-        dw[n][j] = __builtin_fmaf(d[j], hh, dw[n][j]);
+        for (int j = 0; j < P; j++) wave_dw[sub][(tid + n * TPR) * P + j] = dw[n][j];
+      __syncthreads();
+      for (int64_t c = threadIdx.x; c < vpr * P; c += kBlock) {
+        float v = 0;
+#pragma unroll
+        for (int k = 0; k < kRows; k++) v += wave_dw[k][c];
+        out[c] = from == first ? v : out[c] + v;
       }
     }
-    // two arrays in turn: a wave may be a row ahead of one that still reads
-    if constexpr (TPR == kBlock) s = block_sum(s, part[turn]);
-    else s = lanes_sum<TPR>(s);
-    turn ^= 1;
-    s /= H;
-#pragma unroll
-    for (int n = 0; n < NV; n++) {
-      const int64_t i = tid + n * TPR;
-      float d[P], f[P], e[P], o[P];
-      unpack<ES>(x.d[n], d);
-      unpack<ES>(x.h[n], f);
-      if (ADD) unpack<ES>(x.e[n], e);
-#pragma unroll
-      for (int j = 0; j < P; j++) {
-        o[j] = r * (w[n][j] * d[j] - f[j] * r * s);
-        if (ADD) o[j] += e[j];
-      }
-      if (i < vpr) dx[t * vpr + i] = pack<ES>(o);
-    }
-  }
-  float* out = work + (int64_t)blockIdx.x * vpr * P;
-  if constexpr (TPR == kBlock) {
-#pragma unroll
-    for (int n = 0; n < NV; n++) {
-      const int64_t i = tid + n * TPR;
-      if (i >= vpr) continue;
-#pragma unroll
-      for (int j = 0; j < P; j += 4)
-        *reinterpret_cast<f32x4*>(out + i * P + j) = f32x4{dw[n][j], dw[n][j + 1], dw[n][j + 2], dw[n][j + 3]};
-    }
-  } else {
 #pragma unroll
     for (int n = 0; n < NV; n++)
 #pragma unroll
-      for (int j = 0; j < P; j++) wave_dw[sub][(tid + n * TPR) * P + j] = dw[n][j];
-    __syncthreads();
-    for (int64_t c = threadIdx.x; c < vpr * P; c += kBlock) {
-      float v = 0;
-#pragma unroll
-      for (int k = 0; k < kRows; k++) v += wave_dw[k][c];
-      out[c] = v;
-    }
+      for (int j = 0; j < P; j++) dw[n][j] = 0.0f;
   }
 }
 
@@ -320,18 +336,23 @@ __global__ __launch_bounds__(kBlock) void norm_dw_long_kernel(const NormBwdArgs 
   if (i >= vpr) return;
   const u32x4* dy = reinterpret_cast<const u32x4*>(a.dy[rank]);
   const u32x4* h = reinterpret_cast<const u32x4*>(a.h[rank]);
-  float dw[P] = {};
-  for (int64_t t = slot; t < T; t += slots) {
-    const float r = a.rstd[rank][t];
-    float d[P], f[P];
-    unpack<ES>(dy[t * vpr + i], d);
-    unpack<ES>(h[t * vpr + i], f);
+  float sum[P] = {};
+  for (int64_t from = slot; from < T; from += (int64_t)kPiece * slots) {  // in pieces, as above
+    float dw[P] = {};
+    for (int64_t k = 0, t = from; k < kPiece && t < T; k++, t += slots) {
+      const float r = a.rstd[rank][t];
+      float d[P], f[P];
+      unpack<ES>(dy[t * vpr + i], d);
+      unpack<ES>(h[t * vpr + i], f);
 #pragma unroll
-    for (int j = 0; j < P; j++) dw[j] = __builtin_fmaf(d[j], f[j] * r, dw[j]);
+      for (int j = 0; j < P; j++) dw[j] = __builtin_fmaf(d[j], f[j] * r, dw[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < P; j++) sum[j] += dw[j];
   }
   float* out = work + ((int64_t)blockIdx.x * vpr + i) * P;
 #pragma unroll
-  for (int j = 0; j < P; j++) out[j] = dw[j];
+  for (int j = 0; j < P; j++) out[j] = sum[j];
 }
 
 // dw (+)= the slots' sums, in a fixed order: a workgroup takes 64 columns, 16

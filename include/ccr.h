@@ -628,8 +628,10 @@ ccr_status_t ccr_moe_experts_q8(ccr_ctx_t ctx, const void *const *exp, const voi
  *   residual alike.  accumulate = 1 adds to what dw holds.  The ranks' dw are
  *   sums over their own rows: ccr_allreduce joins them.
  *
- * Squares are summed in fp64 (no finite row overflows), all else in fp32, each
- * result is rounded once, and dw has the same bits on every run.  work: device
+ * Squares are summed in fp64 (no finite row overflows), all else in fp32; h, y, q
+ * and dx are rounded once.  dw is an fp32 sum over the rows in a fixed order (the
+ * same bits on every run), none of whose values passes more than 330 roundings
+ * however many rows there are.  work: device
  * fp32 [ccr_rms_norm_work(R, T, H)] (host only), the call's alone until it
  * completes, contents of no meaning before and after: two calls that may run at
  * the same time, captured graphs included, need one each.  H: 1 .. 2^20 with
