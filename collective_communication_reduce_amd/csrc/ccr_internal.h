@@ -339,9 +339,12 @@ struct RouteShape {
   float scale;
 };
 constexpr int kRouteGroups = 64;  // at most
-// Workgroups of a rank that count, each with a slot of 2 E words of the work array.
+// Workgroups of a rank that count, each with a slot of 2 E words of the work array:
+// as many as the chip holds, and of many tokens one for every 512, which a workgroup
+// takes at least 4 at a time, so that no sum of scores is a chain of more than 128
+// tokens (one of 4096 was off by 980 units of 2^-24) before it goes on in fp64.
 constexpr int route_slots(int R, int64_t T) {
-  const int64_t most = 1024 / R, of = (T + 15) / 16;
+  const int64_t chip = 1024 / R, many = (T + 511) / 512, most = chip > many ? chip : many, of = (T + 15) / 16;
   return (int)(of < most ? of : most);
 }
 hipError_t launch_route(const RouteArgs& a, const RouteShape& n, float* work, hipStream_t stream);

@@ -675,7 +675,8 @@ ccr_status_t ccr_rms_norm_bwd(ccr_ctx_t ctx, const void *const *dy, const void *
  * gives weights 0.
  *   counts[r] (device int64 [E]; counts may be NULL): the tokens that chose e;
  *   score_sums[r] (device fp32 [E]; may be NULL): the sum over the tokens of s_e,
- *            from which a loss for balance is made.
+ *            from which a loss for balance is made: in a fixed order, of parts of
+ *            at most 128 x 16 tokens in fp32, then in fp64.
  * ccr_moe_route_bwd: dlogits[r] (fp32 [T x E], every entry written) from
  *   dweights[r] (fp32 [T x K]) at the choices topk[r] and dscore_sums[r] (fp32
  *   [E]; dscore_sums may be NULL).  Choices themselves have no gradient, nor has

@@ -1,9 +1,11 @@
 """GPU parity of the router and its gradient with 64-bit references where fp32 is
 short of range or of digits."""
+import math
+
 import pytest
 
-from gpu_helpers import torch_cuda
-from test_gpu_route import NINF, check, check_backward, gen, how_
+from gpu_helpers import say, torch_cuda
+from test_gpu_route import NINF, U, check, check_backward, gen, how_, weight_units
 
 pytestmark = pytest.mark.gpu
 
@@ -116,3 +118,33 @@ def test_tokens_with_tiny_scores_leave_others_alone(ccr_mod, E, score):
             torch.cuda.synchronize()
             out.append([t[1::2].nan_to_num(7.0) for t in (topk, w, dl)])
     assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+@pytest.mark.parametrize("E,chain", [(64, 1024), (256, 1024), (512, 2048), (1024, 4096)])
+def test_sums_of_scores_over_many_tokens(ccr_mod, E, chain):
+    """Every token the same score, 0.49 units above a multiple of what a sum of `chain`
+    of them resolves, so that it would drift apart from the true one: chains of at
+    most 128 additions each."""
+    import torch
+    R, T = 64, 262143
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("needs 8 GiB")
+    say(f"route sums over {R} x {T} tokens E={E}")
+    unit = 2.0 ** (math.floor(math.log2(0.24 * chain)) - 23)
+    score = (math.floor(0.24 / unit) + 0.49) * unit
+    l = torch.full((T, E), math.log(score / (1 - score)), device="cuda")
+    topk = [torch.empty(T, 1, dtype=torch.int32, device="cuda") for _ in range(R)]
+    w = [torch.empty(T, 1, device="cuda") for _ in range(R)]
+    counts = [torch.empty(E, dtype=torch.int64, device="cuda") for _ in range(R)]
+    sums = [torch.empty(E, device="cuda") for _ in range(R)]
+    work = torch.empty(ccr_mod.ccr_moe_route_work(R, T, E), device="cuda")
+    with ccr_mod.Context(0) as c:
+        ccr_mod.ccr_moe_route(c, [l] * R, topk, w, score="sigmoid", counts=counts, score_sums=sums, work=work)
+        torch.cuda.synchronize()
+    want = T / (1 + math.exp(-float(l[0, 0])))
+    # 128 tokens to a lane, the lanes of four waves; then fp64, and its rounding
+    units = weight_units("sigmoid", E, 1) + 128 + 16 + 1
+    worst = max(float((v.double() - want).abs().max()) for v in sums) / (U * want)
+    assert worst <= units, f"{worst} units"
+    for r in range(R):
+        assert counts[r].tolist() == [T] + [0] * (E - 1)
