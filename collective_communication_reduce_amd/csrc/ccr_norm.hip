@@ -104,20 +104,36 @@ __global__ __launch_bounds__(kBlock) void norm_kernel(const NormArgs a, int64_t 
     // another division were most of a short row's instructions).
     const double m = __builtin_fma(sum, inv_H, (double)eps), y = __builtin_amdgcn_rsq(m);
     const double half = 0.5 * m * y, better = __builtin_fma(y, __builtin_fma(-half, y, 0.5), y);
-    return (float)(m > 0.0 && m < __builtin_inf() ? better : y);
+    return m > 0.0 && m < __builtin_inf() ? better : y;
   };
-  auto emit = [&](int64_t i, u32x4 v, float r) {  // of every vector up to the 8-bit row's end
+  // Where the root is beyond fp32 or among its subnormal numbers (rows below 2^-128,
+  // above 2^126) values and root are multiplied at other scales, which changes
+  // neither's digits: `up` on the one side, its inverse on the other.
+  float r, up = 1.0f;
+  auto emit = [&](int64_t i, u32x4 v) {  // of every vector up to the 8-bit row's end
     float f[P], g[P];
     if (i < vpr) {
       unpack<ES>(v, f);
       load_weight<P, WES>(w, i, g);
+    }
+    if (__builtin_expect(up != 1.0f, 0)) {
+#pragma unroll
+      for (int j = 0; j < P; j++) f[j] *= up;
     }
 #pragma unroll
     for (int j = 0; j < P; j++) f[j] = i < vpr ? f[j] * r * g[j] : 0.0f;
     if (y && i < vpr) y[i] = pack<ES>(f);
     if (q) store_q8<P>(q, i, values, f);
   };
-  float r;
+  auto root = [&]() {
+    const double d = finish();
+    r = (float)d;
+    if (a.rstd[rank] && tid == 0) a.rstd[rank][t] = r;
+    if (!(r >= 0x1p-126f && r < __builtin_inff())) {
+      up = r < 1.0f ? 0x1p-64f : 0x1p64f;
+      r = (float)(d * (r < 1.0f ? 0x1p64 : 0x1p-64));
+    }
+  };
   const int64_t end = q ? values / P : vpr;
   if constexpr (NV > 0) {
     u32x4 v[NV];
@@ -132,25 +148,24 @@ __global__ __launch_bounds__(kBlock) void norm_kernel(const NormArgs a, int64_t 
       if (ADD && i < vpr) h[i] = v[n];
       squares(v[n]);
     }
-    r = finish();
+    root();
 #pragma unroll
     for (int n = 0; n < NV; n++)
-      if (n * TPR < end) emit(tid + n * TPR, v[n], r);
+      if (n * TPR < end) emit(tid + n * TPR, v[n]);
   } else {
     for (int64_t i = tid; i < vpr; i += TPR) {
       const u32x4 v = joined(i);
       if (ADD) h[i] = v;
       squares(v);
     }
-    r = finish();
+    root();
     const u32x4* from = ADD ? h : x;
     for (int64_t n = 0; n < end; n += TPR) {
       const int64_t i = n + tid;
-      emit(i, i < vpr ? from[i] : u32x4{0, 0, 0, 0}, r);
+      emit(i, i < vpr ? from[i] : u32x4{0, 0, 0, 0});
     }
   }
   if (q) pad_q8<TPR>(q, values, q_bytes, tid);
-  if (a.rstd[rank] && tid == 0) a.rstd[rank][t] = r;
 }
 
 // ---------------------------------------------------------------- backward

@@ -629,7 +629,9 @@ ccr_status_t ccr_moe_experts_q8(ccr_ctx_t ctx, const void *const *exp, const voi
  *   sums over their own rows: ccr_allreduce joins them.
  *
  * Squares are summed in fp64 (no finite row overflows), all else in fp32; h, y, q
- * and dx are rounded once.  dw is an fp32 sum over the rows in a fixed order (the
+ * and dx are rounded once.  y and q hold for rows of every magnitude; with eps = 0
+ * rstd is infinite for rows below 2^-128 (and zero rows are NaN), and has fewer
+ * digits for rows above 2^126: the gradients, made from it, share that.  dw is an fp32 sum over the rows in a fixed order (the
  * same bits on every run), none of whose values passes more than 330 roundings
  * however many rows there are.  work: device
  * fp32 [ccr_rms_norm_work(R, T, H)] (host only), the call's alone until it
@@ -676,7 +678,7 @@ ccr_status_t ccr_rms_norm_bwd(ccr_ctx_t ctx, const void *const *dy, const void *
  *   counts[r] (device int64 [E]; counts may be NULL): the tokens that chose e;
  *   score_sums[r] (device fp32 [E]; may be NULL): the sum over the tokens of s_e,
  *            from which a loss for balance is made: in a fixed order, of parts of
- *            at most 128 x 16 tokens in fp32, then in fp64.
+ *            at most 512 tokens in fp32, then in fp64.
  * ccr_moe_route_bwd: dlogits[r] (fp32 [T x E], every entry written) from
  *   dweights[r] (fp32 [T x K]) at the choices topk[r] and dscore_sums[r] (fp32
  *   [E]; dscore_sums may be NULL).  Choices themselves have no gradient, nor has

@@ -50,3 +50,37 @@ def test_weight_gradient_over_many_rows(ccr_mod, R, T, H, dt, rows):
     units = 128 + 128 + 32 + 16 + 2 + 16 + 2
     worst = max(float((v.double() - want).abs().max()) for v in dw) / (U * want)
     assert worst <= units, f"{worst} units"
+
+
+@pytest.mark.parametrize("add", [False, True])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("H", [32, 64, 104, 200, 1000, 2048, 8192, 16392])
+def test_results_over_the_whole_range(ccr_mod, H, dt, add):
+    """Rows of every magnitude without an eps, with zeros among their values: y and its
+    8-bit rows, also where 1 / root is beyond fp32 or among its subnormal numbers."""
+    import torch
+    say(f"norm over the whole range H={H} {dt} add={add}")
+    g = gen(H)
+    d = tdtype(dt)
+    sizes = [1.4e-45, 1e-43, 1e-40, 2.9e-39, 1e-38, 3e-20, 1.0, 7e19, 8e37, 1.7e38]
+    x = torch.tensor(sizes, device="cuda")[:, None] * (2 * torch.rand(len(sizes), H, generator=g, device="cuda") - 1)
+    x[:, 0] = torch.tensor(sizes, device="cuda")
+    x[:, 3] = 0.0
+    x[-1, 5] = 3.3e38
+    x = x.to(d)
+    if dt == "bf16":
+        x[:2, 0] = 2.0 ** -133  # its smallest number
+    w = (1 + 0.2 * torch.randn(H, generator=g, device="cuda")).to(d)
+    y = torch.empty_like(x)
+    q = torch.empty(len(sizes), r8.row_bytes(H), dtype=torch.uint8, device="cuda")
+    more = dict(residual=[torch.zeros_like(x)], h=[torch.empty_like(x)]) if add else {}
+    with ccr_mod.Context(0) as c:
+        ccr_mod.ccr_rms_norm(c, [x], [w], y=[y], q=[q], eps=0.0, **more)
+        torch.cuda.synchronize()
+    h = x.double()
+    want = h * h.square().mean(1, keepdim=True).rsqrt() * w.double()
+    # as for other rows: the root and two products, then the rounding; below the
+    # smallest normal number three roundings of half the smallest step
+    least = 2.0 ** -149 * 3 + (2.0 ** -134 if dt == "bf16" else 0)
+    assert bool(((y.double() - want).abs() <= (HALF[dt] + 3.1 * U) * want.abs() + least).all())
+    check_q8(q, want, 3.1 * U)
