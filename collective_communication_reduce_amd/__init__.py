@@ -727,7 +727,7 @@ def ccr_rms_norm(ctx: Context, x: Sequence, w: Sequence, y=None, q=None, residua
                  eps: float = 1e-6, stream=None):
     """h[r] = x[r] + residual[r] (x[r] itself without them), and its norm times
     w[r], to y[r] (x's dtype), q[r] (8-bit rows) or both.  x, residual, h, y: [T,
-    H]; w: [H], float32 or x's dtype; rstd: float32 [T], for the gradients.  h[r]
+    H]; w: [H], float32 or bfloat16; rstd: float32 [T], for the gradients.  h[r]
     may be x[r] or residual[r]."""
     import torch
     R = len(x)

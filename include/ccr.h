@@ -577,7 +577,7 @@ ccr_status_t ccr_moe_gate_sum_bwd(ccr_ctx_t ctx, const void *const *dy, const vo
  * b is the smallest byte whose scale times 448 reaches the block's largest
  * magnitude (0 for zeros), so nothing saturates, and each value is rounded once
  * to the nearest multiple (ties to even).  A block with an infinity or a NaN gets
- * b = 255 and stands for NaN.  Rows are plain bytes to the exchange: row_bytes =
+ * b = 255 and 32 bytes 0x7f (those behind the H values too) and stands for NaN.  Rows are plain bytes to the exchange: row_bytes =
  * ccr_q8_row_bytes(H) in ccr_moe_dispatch, ccr_moe_dispatch_fused,
  * ccr_alltoall_rows and ccr_permute_rows.
  *
